@@ -99,6 +99,9 @@ typedef enum {
  * zigzag needs its chunk L / 2N to be a multiple of 128 (RA_ERR_UNSUPPORTED
  * otherwise).  There is no Ulysses split in this form (U = 1).            */
 #define RA_FLAG_SEQ_ORDER 4u
+/* ra_window_attn_bwd: dq, dk and dv are bf16 (rounded once, to nearest even,
+ * from the fp32 accumulators) instead of fp32. */
+#define RA_FLAG_GRAD_BF16 8u
 /* Test hook for the timeout path: the first CTA of the fused sweep (or of
  * the first step of ra_ring_attn_fwd_stepwise_noalloc) never loads one key tile, so the waits that depend on it run out after about two
  * seconds; the kernel records RA_ERR_TIMEOUT in the status word, releases what
@@ -319,6 +322,55 @@ RA_API ra_status ra_ring_attn_bwd(const void *q, const void *k, const void *v, c
 
 /* Workspace bytes ra_ring_attn_bwd needs (0 on bad arguments). */
 RA_API size_t ra_ring_attn_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int d, int N);
+
+/*
+ * ra_window_attn_fwd -- causal attention with a sliding window and sinks over
+ * whole sequences in token order.  A query at position p of a sequence that
+ * starts at token s0 sees the keys t of its own sequence with
+ *     s0 <= t <= p  and  (t > p - window  or  t < s0 + sinks):
+ * the last `window` tokens, itself included, and the sequence's first `sinks`
+ * tokens, which stay visible.  O = softmax(Q K^T * scale) V over those keys,
+ * LSE the natural log of the sum of exponentials.
+ * q: bf16 [B, L, H, d]; k, v: bf16 [B, L, H_kv, d], H_kv dividing H (query
+ * head h reads head h / (H / H_kv)); o: fp32 [B, L, H, d], or bf16 with
+ * RA_FLAG_O_BF16; lse: fp32 [B, H, L].  d in {64, 128}; window >= 1 (L or more:
+ * no window); sinks >= 0 (0: none); scale <= 0: 1 / sqrt(d).
+ * cu_seqlens / n_seqs: packed sequences, n_seqs + 1 int32 boundaries on the
+ * device from 0 up (B = 1), or NULL / 0 for B sequences of L tokens.  Tokens
+ * past the last boundary form one more sequence.  Boundaries that do not
+ * increase give wrong masks, never an access out of range.
+ * Every element of q, k and v must be finite: tiles are multiplied whole, and
+ * an infinity or NaN in V reaches the rows of the same tile that mask it.
+ * workspace: RA_WORKSPACE_MIN_BYTES bytes, zero-filled before its first use.
+ */
+RA_API ra_status ra_window_attn_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
+                                    const int32_t *cu_seqlens, int n_seqs, int64_t B, int64_t L,
+                                    int64_t H, int64_t H_kv, int d, int64_t window, int64_t sinks,
+                                    float scale, unsigned flags, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/*
+ * ra_window_attn_bwd -- gradients of ra_window_attn_fwd (the formulas of
+ * ra_ring_attn_bwd under the windowed mask).  o: the forward's output, fp32, or
+ * bf16 with RA_FLAG_O_BF16; dout: bf16 like q; lse: from the forward.  dq like
+ * q, dk and dv like k: fp32, or bf16 with RA_FLAG_GRAD_BF16; every element is
+ * written.  Deterministic (no atomics).  The sinks' gradient from the queries
+ * past their windows is taken in chunks of queries and added in their order.
+ * workspace: ra_window_attn_bwd_workspace_bytes() bytes (the status word, D and
+ * the sinks' partial gradients), zero-filled before its first use; calls that
+ * may overlap on the GPU need one each.
+ */
+RA_API ra_status ra_window_attn_bwd(const void *q, const void *k, const void *v, const void *o,
+                                    const void *dout, const float *lse, void *dq, void *dk, void *dv,
+                                    const int32_t *cu_seqlens, int n_seqs, int64_t B, int64_t L,
+                                    int64_t H, int64_t H_kv, int d, int64_t window, int64_t sinks,
+                                    float scale, unsigned flags, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/* Workspace bytes ra_window_attn_bwd needs (0 on bad arguments); n_seqs as in
+ * the call. */
+RA_API size_t ra_window_attn_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t H_kv, int d,
+                                                 int64_t window, int64_t sinks, int n_seqs);
 
 /*
  * ra_check_status -- synchronise `stream`, read the status word at the start

@@ -23,6 +23,7 @@ RA_SEQ_TO_SHARDS, RA_SHARDS_TO_SEQ, RA_ULYSSES_SEQ_TO_HEAD, RA_ULYSSES_HEAD_TO_S
 RA_FLAG_STEPWISE = 1
 RA_FLAG_O_BF16 = 2
 RA_FLAG_SEQ_ORDER = 4
+RA_FLAG_GRAD_BF16 = 8
 RA_FLAG_INJECT_STALL = 0x80000000
 RA_WORKSPACE_MIN_BYTES = 256
 LAYOUTS = {"contiguous": RA_CONTIGUOUS, "striped": RA_STRIPED, "zigzag": RA_ZIGZAG}
@@ -52,6 +53,11 @@ SIGNATURES = {
     "ra_ring_attn_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I, _I,
                               _I, _I, _F, _U, _P, _SZ, _P]),
     "ra_ring_attn_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I, _I]),
+    "ra_window_attn_fwd": (_I, [_P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I, _I64, _I64, _F, _U, _P,
+                                _SZ, _P]),
+    "ra_window_attn_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I, _I64,
+                                _I64, _F, _U, _P, _SZ, _P]),
+    "ra_window_attn_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I, _I64, _I64, _I]),
     "ra_check_status": (_I, [_P, _P]),
     "ra_last_error": (ctypes.c_char_p, []),
     "ra_version": (ctypes.c_char_p, []),
@@ -270,6 +276,79 @@ def ra_ring_attn_bwd(q, k, v, o, dout, lse, dq, dk, dv, B, L, H, H_kv, d, N, lay
                                   d, N, _layout(layout), int(bool(causal)), float(scale), int(flags),
                                   _ptr(workspace, "workspace"),
                                   workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+_DTYPE_NAMES = {torch.bfloat16: "bf16", torch.float32: "fp32", torch.int32: "int32", torch.uint8: "uint8"}
+
+
+def _tensors(first, named):
+    """Check (name, tensor, dtypes, shape) entries -- None for a tensor that may be left out (a
+    workspace may not) and for a type or shape that is not fixed -- and that all lie, contiguous,
+    on the current CUDA device."""
+    dev = first.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device, not %s" % dev)
+    for name, t, dtypes, shape in named:
+        if t is None:
+            if name == "workspace":
+                raise ValueError("workspace is needed (see new_workspace)")
+            continue
+        if dtypes is not None and t.dtype not in dtypes:
+            raise TypeError("%s must be %s, not %s" % (name, " or ".join(_DTYPE_NAMES[x] for x in dtypes), t.dtype))
+        if t.device != dev:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
+        if shape is not None and t.shape != shape:
+            raise ValueError("%s must be %s, not %s" % (name, list(shape), list(t.shape)))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+
+
+_BF16, _FP32, _INT32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+_ANY_FLOAT = (torch.bfloat16, torch.float32)
+
+
+def _cu_seqlens(cu_seqlens):
+    return (None, 0) if cu_seqlens is None else (cu_seqlens.data_ptr(), cu_seqlens.numel() - 1)
+
+
+def _nbytes(workspace):
+    return workspace.numel() * workspace.element_size()
+
+
+def ra_window_attn_fwd(q, k, v, o, lse, B, L, H, H_kv, d, window, sinks=0, scale=0.0, cu_seqlens=None, workspace=None,
+                       stream=None):
+    """Causal attention of each token to the last ``window`` tokens of its sequence and its first
+    ``sinks``; o fp32 or bf16.  ``cu_seqlens``: int32 boundaries of packed sequences (B = 1)."""
+    _tensors(q, (("q", q, _BF16, (B, L, H, d)), ("k", k, _BF16, (B, L, H_kv, d)), ("v", v, _BF16, (B, L, H_kv, d)),
+                 ("o", o, _ANY_FLOAT, (B, L, H, d)), ("lse", lse, _FP32, (B, H, L)),
+                 ("cu_seqlens", cu_seqlens, _INT32, None), ("workspace", workspace, None, None)))
+    cu, n_seqs = _cu_seqlens(cu_seqlens)
+    _check(lib().ra_window_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), cu, n_seqs,
+                                    B, L, H, H_kv, d, window, sinks, scale,
+                                    RA_FLAG_O_BF16 if o.dtype == torch.bfloat16 else 0, workspace.data_ptr(),
+                                    _nbytes(workspace), _stream(stream)))
+
+
+def ra_window_attn_bwd_workspace_bytes(B, L, H, H_kv, d, window, sinks=0, n_seqs=0):
+    return int(lib().ra_window_attn_bwd_workspace_bytes(B, L, H, H_kv, d, window, sinks, n_seqs))
+
+
+def ra_window_attn_bwd(q, k, v, o, dout, lse, dq, dk, dv, B, L, H, H_kv, d, window, sinks=0, scale=0.0,
+                       cu_seqlens=None, workspace=None, stream=None):
+    """Gradients of ra_window_attn_fwd; o fp32 or bf16 (as the forward wrote it), dq / dk / dv all
+    fp32 or all bf16."""
+    _tensors(q, (("q", q, _BF16, (B, L, H, d)), ("k", k, _BF16, (B, L, H_kv, d)), ("v", v, _BF16, (B, L, H_kv, d)),
+                 ("o", o, _ANY_FLOAT, (B, L, H, d)), ("dout", dout, _BF16, (B, L, H, d)),
+                 ("lse", lse, _FP32, (B, H, L)), ("dq", dq, _ANY_FLOAT, (B, L, H, d)),
+                 ("dk", dk, (dq.dtype,), (B, L, H_kv, d)), ("dv", dv, (dq.dtype,), (B, L, H_kv, d)),
+                 ("cu_seqlens", cu_seqlens, _INT32, None), ("workspace", workspace, None, None)))
+    cu, n_seqs = _cu_seqlens(cu_seqlens)
+    flags = (RA_FLAG_O_BF16 if o.dtype == torch.bfloat16 else 0) | \
+        (RA_FLAG_GRAD_BF16 if dq.dtype == torch.bfloat16 else 0)
+    _check(lib().ra_window_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
+                                    lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu, n_seqs, B, L, H,
+                                    H_kv, d, window, sinks, scale, flags, workspace.data_ptr(), _nbytes(workspace),
+                                    _stream(stream)))
 
 
 def ra_check_status(workspace, stream=None):

@@ -1,0 +1,163 @@
+// ra_window.cuh -- which keys a row of windowed attention sees, and the key
+// tiles a block of rows visits; the paged form's units and splits.
+//
+// Plain integer arithmetic callable from host and device, as in
+// ra_positions.cuh, so that a CPU test can run what the kernels run
+// (tests/window_probe.cu).
+//
+// A query at position p of a sequence that starts at `start` sees the keys t
+// of its sequence with t <= p and (t > p - window or t < start + sinks): an
+// interval that ends at the query, and the sinks it has left behind.
+#pragma once
+#include <cstdint>
+
+#include "ra_positions.cuh"
+
+namespace ra {
+
+// Boundary i of the packed sequences, i in [0, n_seqs + 1]: the tokens past
+// the last boundary are one more sequence.  Every read stays inside the
+// n_seqs + 1 boundaries and every value inside [0, S], whatever they hold.
+RA_HD int seq_bound(const int *cu, int n_seqs, int S, int i) {
+    return i > n_seqs ? S : (int)clamp64(cu[i], 0, S);
+}
+
+// The number of the sequence holding position p, and its bounds; without
+// packing (cu null) number 0, [0, S).
+RA_HD int seq_of(const int *cu, int n_seqs, int S, int p, int &start, int &end) {
+    start = 0;
+    end = S;
+    if (!cu) return 0;
+    int lo = 0, hi = n_seqs + 1;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (seq_bound(cu, n_seqs, S, mid) <= p) lo = mid;
+        else hi = mid;
+    }
+    start = seq_bound(cu, n_seqs, S, lo);
+    end = seq_bound(cu, n_seqs, S, lo + 1);
+    if (start > p) start = p;
+    if (end < p + 1) end = p + 1;
+    return lo;
+}
+
+// The keys of one row: [lo, hi) and, when the window has left the sinks
+// behind, [slo, shi) with shi < lo; otherwise slo = shi = 0 and [lo, hi) holds
+// both.  hi <= lo for a row that sees nothing (a negative position).
+struct RowKeys {
+    int lo, hi, slo, shi;
+};
+
+// window <= 0 means no window.  Everything lies in [0, 2^30], so no sum here
+// leaves 32 bits.
+RA_HD RowKeys window_row_keys(int start, int p, int window, int sinks) {
+    RowKeys r;
+    r.hi = p + 1;
+    r.lo = window > 0 && p - window + 1 > start ? p - window + 1 : start;
+    r.slo = r.shi = 0;
+    const int s_end = start + sinks < p + 1 ? start + sinks : p + 1;
+    if (r.lo > start && s_end > start) {
+        if (s_end >= r.lo) {
+            r.lo = start;
+        } else {
+            r.slo = start;
+            r.shi = s_end;
+        }
+    }
+    return r;
+}
+
+// The key tiles (128 keys) a block of rows visits, in order: n_sink tiles from
+// s0 on, then tiles from m0 on; tile number i of `end` in all, from `i` on.
+// The rows' positions increase and `first` is the first row's keys, so that
+// the main tiles run from first.lo to the last row's position: a later row's
+// window starts no earlier, a later sequence's sinks lie after first.lo, and
+// sinks left behind by a row of the first sequence are first's (or lie after
+// first.lo = start).
+struct RangeWalk {
+    int i, end, n_sink, s0, m0;
+    int tile, j;
+
+    RA_HD_STEP void seek() { tile = i < n_sink ? s0 + i : m0 + (i - n_sink); }
+    RA_HD_STEP void start_step() { seek(); }
+    RA_HD_STEP bool valid() const { return i < end; }
+    RA_HD_STEP void next() {
+        ++i;
+        seek();
+    }
+};
+
+RA_HD RangeWalk range_walk(const RowKeys &first, int last_hi) {
+    RangeWalk w;
+    w.j = 0;
+    w.i = 0;
+    w.m0 = first.lo / 128;
+    const int m1 = (last_hi + 127) / 128;
+    w.s0 = first.slo / 128;
+    int s1 = (first.shi + 127) / 128;
+    if (s1 > w.m0) s1 = w.m0;
+    w.n_sink = first.shi > first.slo && s1 > w.s0 ? s1 - w.s0 : 0;
+    w.end = w.n_sink + (m1 > w.m0 ? m1 - w.m0 : 0);
+    w.tile = 0;
+    return w;
+}
+
+// The walk of a unit of windowed rows [row0, row_end) of one batch element of
+// S tokens (packed sequences: cu, n_seqs).
+RA_HD RowKeys window_row(const int *cu, int n_seqs, int S, int p, int window, int sinks) {
+    int start, end;
+    seq_of(cu, n_seqs, S, p, start, end);
+    return window_row_keys(start, p, window, sinks);
+}
+
+RA_HD RangeWalk window_unit_walk(const int *cu, int n_seqs, int S, int row0, int row_end, int window, int sinks) {
+    return range_walk(window_row(cu, n_seqs, S, row0, window, sinks), row_end);
+}
+
+// The queries that meet a key at position t inside the window: rows [t, hi),
+// hi = t + window but not past the end of t's sequence.
+RA_HD int window_col_end(int t, int end, int window) {
+    return window > 0 && end - t > window ? t + window : end;
+}
+
+// The far part of a sink's gradient: the queries past its window.  They are
+// cut at multiples of kSinkChunk rows and each (sequence, chunk) is a unit of
+// its own, so that the few keys every query sees do not become one long block.
+// Unit u belongs to the last sequence s whose first unit, start / kSinkChunk + s,
+// is not past u, and is chunk u - s of the rows; the chunks of a sequence
+// [start, end) are start / kSinkChunk .. (end - 1) / kSinkChunk, one more than
+// the next sequence's start is on at most, which the "+ s" has room for.
+constexpr int kSinkChunk = 2048;
+
+struct SinkUnit {
+    int start, end;     // the sequence's tokens
+    int lo, hi;         // the chunk's query rows inside it; lo >= hi: no such unit
+};
+
+RA_HD int64_t sink_units(int64_t S, int n_seqs) { return S / kSinkChunk + n_seqs + 1; }
+
+// The number of the first unit of sequence s, which starts at `start`.
+RA_HD int sink_first_unit(int start, int s) { return start / kSinkChunk + s; }
+
+RA_HD SinkUnit sink_unit(const int *cu, int n_seqs, int S, int u) {
+    SinkUnit k;
+    int s = 0;
+    k.start = 0;
+    k.end = S;
+    if (cu) {
+        int hi = n_seqs + 1;
+        while (hi - s > 1) {
+            const int mid = (s + hi) >> 1;
+            if (sink_first_unit(seq_bound(cu, n_seqs, S, mid), mid) <= u) s = mid;
+            else hi = mid;
+        }
+        k.start = seq_bound(cu, n_seqs, S, s);
+        k.end = seq_bound(cu, n_seqs, S, s + 1);
+    }
+    const int64_t at = (int64_t)(u - s) * kSinkChunk;   // unit start / kSinkChunk + s + i is chunk start / kSinkChunk + i
+    k.lo = (int)clamp64(at, k.start, k.end);
+    k.hi = (int)clamp64(at + kSinkChunk, k.start, k.end);
+    return k;
+}
+
+}  // namespace ra
