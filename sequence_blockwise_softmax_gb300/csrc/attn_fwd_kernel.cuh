@@ -101,9 +101,14 @@ struct AttnSmem {
     static constexpr uint32_t kRing = 2 * kTile;
     static constexpr uint32_t kP = kRing + kSlots * kTile;   // P_g: 128 rows x 128 keys bf16, two boxes each
     static constexpr uint32_t kBars = kP + 2 * 2 * kBox;
-    // barriers: Q full, slot full[3], slot empty[3], S full[2], S free[2],
-    // P full[2], PV done[2], final, tile count posted
-    static constexpr int kNumBars = 1 + 2 * kSlots + 2 + 2 + 2 + 2 + 1 + 1;
+    // barriers: Q full, K full[3], V full[3], slot empty[3], S full[2],
+    // S free[2], P full[2], PV done[2], final, tile count posted.  A slot holds
+    // K and V loads in turn but has a full barrier for each: the S and the PV
+    // issuer then see every phase of the barriers they wait on.  On one shared
+    // barrier each would see every other phase, and a wait two phases ahead of
+    // the barrier passes at once (the parities agree): products would read a
+    // tile still on its way whenever loads lag or overtake one another.
+    static constexpr int kNumBars = 1 + 3 * kSlots + 2 + 2 + 2 + 2 + 1 + 1;
     static constexpr uint32_t kMisc = kBars + kNumBars * 8;
     // the tile-skipping variant's step table: per ring step (at most
     // kMaxSteps) the unit's key-tile range and each Q tile's own range inside
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(384, 1)
     }
     const uint32_t bar0 = s_base + L::kBars;
     auto BAR = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
-    const int B_QFULL = 0, B_SLOTF = 1, B_SLOTE = 1 + NSL, B_SFULL = 1 + 2 * NSL, B_SFREE = B_SFULL + 2,
+    const int B_QFULL = 0, B_KF = 1, B_VF = 1 + NSL, B_SLOTE = 1 + 2 * NSL, B_SFULL = 1 + 3 * NSL, B_SFREE = B_SFULL + 2,
               B_PFULL = B_SFREE + 2, B_PVDONE = B_PFULL + 2, B_FINAL = B_PVDONE + 2, B_TCOUNT = B_FINAL + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
@@ -236,7 +241,8 @@ __global__ void __launch_bounds__(384, 1)
     if (threadIdx.x == 0) {
         mbar_init(BAR(B_QFULL), 1);
         for (int s = 0; s < NSL; ++s) {
-            mbar_init(BAR(B_SLOTF + s), 1);
+            mbar_init(BAR(B_KF + s), 1);
+            mbar_init(BAR(B_VF + s), 1);
             mbar_init(BAR(B_SLOTE + s), 1);
         }
         for (int g = 0; g < 2; ++g) {
@@ -295,19 +301,23 @@ __global__ void __launch_bounds__(384, 1)
         wk.start_step();
         int vj = 0, vtile = 0;
         int i = 0, withheld = -1;
+        uint32_t k_loads = 0, v_loads = 0;   // bit s: slot s has had a load of the kind, bit 8 + s: the parity of its last
         bool ok = true;
         auto load = [&](int wj, int wtile, bool is_k) -> bool {
             const int sl = i % NSL;
             if (i >= NSL && !warp_wait(BAR(B_SLOTE + sl), ((i / NSL) - 1) & 1, abort_flag)) return false;
             const bool withhold = args.inject_stall && blockIdx.x == 0 && i == 1;
+            const uint32_t full = BAR((is_k ? B_KF : B_VF) + sl);
+            uint32_t &loads = is_k ? k_loads : v_loads;
+            loads = (loads & (1u << sl)) ? loads ^ (256u << sl) : loads | (1u << sl);
             if (lane == 0 && !withhold) {
                 const uint32_t dst = s_base + L::kRing + sl * L::kTile;
                 int c1, c2, c3;
                 tile_coords(args.seq_order, args.layout, args.S, args.N, ring ? wj : 0, b, wtile * 128, c1, c2, c3);
-                mbar_arrive_expect_tx(BAR(B_SLOTF + sl), L::kTile);
+                mbar_arrive_expect_tx(full, L::kTile);
                 for (int c = 0; c < HALVES; ++c) {
-                    if (is_k) tma_load_4d(dst + c * L::kBox, &tmk, BAR(B_SLOTF + sl), xkv + 64 * c, c1, c2, c3);
-                    else tma_load_4d(dst + c * L::kBox, &tmv, BAR(B_SLOTF + sl), xkv + 64 * c, c1, c2, c3);
+                    if (is_k) tma_load_4d(dst + c * L::kBox, &tmk, full, xkv + 64 * c, c1, c2, c3);
+                    else tma_load_4d(dst + c * L::kBox, &tmv, full, xkv + 64 * c, c1, c2, c3);
                 }
             }
             __syncwarp();
@@ -334,8 +344,11 @@ __global__ void __launch_bounds__(384, 1)
             // let the copies already issued land before the CTA exits
             volatile int never = 0;
             mbar_wait(BAR(B_QFULL), 0, &never);
-            for (int u = (i > NSL ? i - NSL : 0); u < i; ++u)
-                if (u != withheld) mbar_wait(BAR(B_SLOTF + u % NSL), (u / NSL) & 1, &never);
+            for (int sl = 0; sl < NSL; ++sl) {
+                if (((k_loads >> sl) & 1u) && !(withheld == 1 && sl == 1))   // (load 1 is a K tile)
+                    mbar_wait(BAR(B_KF + sl), (k_loads >> (8 + sl)) & 1u, &never);
+                if ((v_loads >> sl) & 1u) mbar_wait(BAR(B_VF + sl), (v_loads >> (8 + sl)) & 1u, &never);
+            }
         }
     } else if (warp == 1 && !TWO_ISSUERS) {
         // ================================================= MMA issuer (d = 64)
@@ -399,12 +412,24 @@ __global__ void __launch_bounds__(384, 1)
             }
             tc_commit_elect(BAR(B_PVDONE + g));
         };
+        uint32_t k_parity = 0;   // bit s: parity of the next K load of slot s
+        auto k_wait = [&](int sl) -> bool {
+            const bool got = warp_wait(BAR(B_KF + sl), (k_parity >> sl) & 1u, abort_flag);
+            k_parity ^= 1u << sl;
+            return got;
+        };
+        uint32_t v_parity = 0;   // bit s: parity of the next V load of slot s
+        auto v_wait = [&](int sl) -> bool {
+            const bool got = warp_wait(BAR(B_VF + sl), (v_parity >> sl) & 1u, abort_flag);
+            v_parity ^= 1u << sl;
+            return got;
+        };
         bool ok = warp_wait(BAR(B_QFULL), 0, abort_flag);
         Walk w = walk0;
         w.start_step();
         int t = 0;
         if (ok && w.valid()) {
-            ok = warp_wait(BAR(B_SLOTF + 0), 0, abort_flag);   // K(0) is load 0
+            ok = k_wait(0);   // K(0) is load 0
             tc_fence_after();
             if (ok) {
                 issue_s(0, 0);
@@ -418,14 +443,14 @@ __global__ void __launch_bounds__(384, 1)
             const bool has_next = w.valid();
             const int ki = 2 * t + 1;                        // load index of K(t+1)
             const int vi = has_next ? 2 * t + 2 : 2 * t + 1; // load index of V(t)
-            if (has_next && !(ok = warp_wait(BAR(B_SLOTF + ki % NSL), (ki / NSL) & 1, abort_flag))) break;
+            if (has_next && !(ok = k_wait(ki % NSL))) break;
             if (has_next) {
                 if (!(ok = warp_wait(BAR(B_SFREE + 0), t & 1, abort_flag))) break;
                 tc_fence_after();
                 issue_s(0, ki % NSL);
                 __syncwarp();
             }
-            if (!(ok = warp_wait(BAR(B_SLOTF + vi % NSL), (vi / NSL) & 1, abort_flag))) break;
+            if (!(ok = v_wait(vi % NSL))) break;
             if (!(ok = warp_wait(BAR(B_PFULL + 0), t & 1, abort_flag))) break;
             tc_fence_after();
             issue_pv(0, vi % NSL, t == 0);
@@ -486,6 +511,12 @@ __global__ void __launch_bounds__(384, 1)
             }
             tc_commit_elect(BAR(B_SFULL + g));
         };
+        uint32_t k_parity = 0;   // bit s: parity of the next K load of slot s
+        auto k_wait = [&](int sl) -> bool {
+            const bool got = warp_wait(BAR(B_KF + sl), (k_parity >> sl) & 1u, abort_flag);
+            k_parity ^= 1u << sl;
+            return got;
+        };
         // the issuers need only the number of key tiles the walk visits,
         // which warp 4 counts (and, when skipping, its step table)
         bool ok = warp_wait(BAR(B_TCOUNT), 0, abort_flag);
@@ -494,7 +525,7 @@ __global__ void __launch_bounds__(384, 1)
         if constexpr (!SKIP) {
             int t = 0;
             if (ok && T > 0) {
-                ok = warp_wait(BAR(B_SLOTF + 0), 0, abort_flag);   // K(0) is load 0
+                ok = k_wait(0);   // K(0) is load 0
                 tc_fence_after();
                 if (ok) {
                     issue_s(0, 0);
@@ -506,7 +537,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
             for (; ok && t + 1 < T; ++t) {
                 const int ki = 2 * t + 1;                    // load index of K(t+1)
-                if (!(ok = warp_wait(BAR(B_SLOTF + ki % NSL), (ki / NSL) & 1, abort_flag))) break;
+                if (!(ok = k_wait(ki % NSL))) break;
                 if (!(ok = warp_wait(BAR(B_SFREE + 0), t & 1, abort_flag))) break;
                 tc_fence_after();
                 issue_s(0, ki % NSL);
@@ -525,7 +556,7 @@ __global__ void __launch_bounds__(384, 1)
             cs.start((ok && *tab_ok) ? step_tab : nullptr, args.num_steps);
             int ks0 = 0, ks1 = 0;         // S products issued per Q tile
             if (ok && T > 0) {
-                ok = warp_wait(BAR(B_SLOTF + 0), 0, abort_flag);   // K(0) is load 0
+                ok = k_wait(0);   // K(0) is load 0
                 tc_fence_after();
                 if (ok) {
                     if (cs.need(0)) {
@@ -544,7 +575,7 @@ __global__ void __launch_bounds__(384, 1)
             for (int t = 0; ok && t + 1 < T; ++t) {
                 cs.next();
                 const int ki = 2 * t + 1;                    // load index of K(t+1)
-                if (!(ok = warp_wait(BAR(B_SLOTF + ki % NSL), (ki / NSL) & 1, abort_flag))) break;
+                if (!(ok = k_wait(ki % NSL))) break;
                 if (cs.need(0)) {
                     if (ks0 > 0 && !(ok = warp_wait(BAR(B_SFREE + 0), (ks0 - 1) & 1, abort_flag))) break;
                     tc_fence_after();
@@ -589,6 +620,12 @@ __global__ void __launch_bounds__(384, 1)
             mma_ss_elect<hb + 6, 896>(d, a0, b0, IDESC_O, 1u);
             tc_commit_elect(BAR(B_PVDONE + g));
         };
+        uint32_t v_parity = 0;   // bit s: parity of the next V load of slot s
+        auto v_wait = [&](int sl) -> bool {
+            const bool got = warp_wait(BAR(B_VF + sl), (v_parity >> sl) & 1u, abort_flag);
+            v_parity ^= 1u << sl;
+            return got;
+        };
         // the issuers need only the number of key tiles the walk visits,
         // which warp 4 counts (and, when skipping, its step table)
         bool ok = warp_wait(BAR(B_TCOUNT), 0, abort_flag);
@@ -600,7 +637,7 @@ __global__ void __launch_bounds__(384, 1)
             for (; ok && t < T; ++t) {
                 const bool has_next = t + 1 < T;
                 const int vi = has_next ? 2 * t + 2 : 2 * t + 1; // load index of V(t)
-                if (!(ok = warp_wait(BAR(B_SLOTF + vi % NSL), (vi / NSL) & 1, abort_flag))) break;
+                if (!(ok = v_wait(vi % NSL))) break;
                 if (!(ok = warp_wait(BAR(B_PFULL + 0), t & 1, abort_flag))) break;
                 tc_fence_after();
                 issue_pv(0, vi % NSL, t == 0);
@@ -621,7 +658,7 @@ __global__ void __launch_bounds__(384, 1)
             for (int t = 0; ok && t < T; ++t) {
                 const bool has_next = t + 1 < T;
                 const int vi = has_next ? 2 * t + 2 : 2 * t + 1; // load index of V(t)
-                if (!(ok = warp_wait(BAR(B_SLOTF + vi % NSL), (vi / NSL) & 1, abort_flag))) break;
+                if (!(ok = v_wait(vi % NSL))) break;
                 if (cv.need(0)) {
                     if (!(ok = warp_wait(BAR(B_PFULL + 0), kv0 & 1, abort_flag))) break;
                     tc_fence_after();
