@@ -373,11 +373,79 @@ RA_API size_t ra_window_attn_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H
                                                  int64_t window, int64_t sinks, int n_seqs);
 
 /*
+ * Paged cache.  Keys and values of a running batch lie in pages of page_size
+ * tokens: k_pages, v_pages: bf16, page p at p * page_stride elements, inside it
+ * [page_size, H_kv, d] without gaps (one pool of each, or K and V, or several
+ * layers, interleaved by the stride).  page_size is a power of two from 16 to
+ * 65536.  block_table: int32 [n_seqs, max_pages], entry [s, i] the page of
+ * sequence s's tokens i * page_size and on; entries past a sequence's last
+ * token, and of pages no query of the call sees, are not read.  seq_lens: int32
+ * [n_seqs], each sequence's tokens in the cache, the call's new ones among
+ * them.  cu_q / cu_new: int32 [n_seqs + 1], increasing: sequence s has the rows
+ * [cu[s], cu[s + 1]) of the T rows of q (k_new, v_new); row i of its n stands
+ * at position seq_lens[s] - n + i.  A sequence may have no new row; rows before
+ * cu[0] and from cu[n_seqs] on are not read and their outputs left as they were.
+ * All of these lie on the device and may change between replays of a captured
+ * call; T, n_seqs and the bounds may not.  What they may not hold -- a page
+ * outside the pool, more new tokens than max_new or than the sequence's length,
+ * a length over max_pages * page_size -- never leads out of range: the page
+ * reads as zeros (or the token is not written), the rows past a bound are left
+ * out, and ra_check_status() returns RA_ERR_INVALID_ARG.
+ */
+
+/*
+ * ra_paged_attn_fwd -- causal attention of new tokens over the cache, which
+ * holds their own keys and values already (ra_paged_append): a chunk of a
+ * prompt, single tokens, or both in one batch.  The query at position p sees
+ * the keys t <= p; with window > 0 those with t > p - window or t < sinks.
+ * q: bf16 [T, H, d] with q_stride elements from token to token (at least H * d,
+ * a multiple of 8); o: fp32 [T, H, d], or bf16 with RA_FLAG_O_BF16; lse: fp32
+ * [H, T], natural log, or NULL.  d in {64, 128}; H_kv divides H, at most 128
+ * query heads to one key/value head.  A token at a negative position gets
+ * O = 0 and LSE = -inf.  What lies in a page behind a sequence's last token may
+ * be anything, NaN included; what a sequence's tokens hold must be finite.
+ * max_new: no sequence has more new tokens.  max_len: how long the sequences
+ * get; it only guides how the keys are split (any value gives the same results
+ * up to the rounding of the join).  scale <= 0: 1 / sqrt(d).
+ * workspace: ra_paged_attn_workspace_bytes() bytes, zero-filled before its
+ * first use; calls that may overlap on the GPU need one each.
+ */
+RA_API ra_status ra_paged_attn_fwd(const void *q, const void *k_pages, const void *v_pages,
+                                   const int32_t *block_table, const int32_t *seq_lens,
+                                   const int32_t *cu_q, void *o, float *lse, int64_t T, int64_t n_seqs,
+                                   int64_t H, int64_t H_kv, int d, int64_t n_pages, int64_t page_size,
+                                   int64_t page_stride, int64_t max_pages, int64_t q_stride,
+                                   int64_t max_new, int64_t max_len, int64_t window, int64_t sinks,
+                                   float scale, unsigned flags, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/* Workspace bytes ra_paged_attn_fwd needs (0 on bad arguments); at most 64 MiB. */
+RA_API size_t ra_paged_attn_workspace_bytes(int64_t T, int64_t n_seqs, int64_t H, int64_t H_kv, int d,
+                                            int64_t max_new, int64_t max_len, int64_t window,
+                                            int64_t sinks);
+
+/*
+ * ra_paged_append -- copy new keys and values into the cache.  k_new, v_new:
+ * bf16 [T, H_kv, d] with new_stride elements from token to token (at least
+ * H_kv * d, a multiple of 8); they must not overlap the pools.  Tokens of two
+ * sequences must not share a place in a page (a forked sequence has its own
+ * page to write to).  workspace: RA_WORKSPACE_MIN_BYTES bytes, zero-filled
+ * before its first use.
+ */
+RA_API ra_status ra_paged_append(const void *k_new, const void *v_new, void *k_pages, void *v_pages,
+                                 const int32_t *block_table, const int32_t *seq_lens,
+                                 const int32_t *cu_new, int64_t T, int64_t n_seqs, int64_t H_kv, int d,
+                                 int64_t n_pages, int64_t page_size, int64_t page_stride,
+                                 int64_t max_pages, int64_t new_stride, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
  * ra_check_status -- synchronise `stream`, read the status word at the start
  * of `workspace`, clear it, and return RA_ERR_TIMEOUT if a kernel recorded a
  * timeout since the last check, RA_ERR_ALIGNMENT if a kernel found its
  * dynamic shared memory base not 1024-byte aligned (it then computed
- * nothing), RA_OK otherwise.
+ * nothing), RA_ERR_INVALID_ARG if a paged call met a page outside the pool or
+ * counts outside its bounds, RA_OK otherwise.
  */
 RA_API ra_status ra_check_status(void *workspace, void *stream);
 

@@ -58,6 +58,11 @@ SIGNATURES = {
     "ra_window_attn_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I, _I64,
                                 _I64, _F, _U, _P, _SZ, _P]),
     "ra_window_attn_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I, _I64, _I64, _I]),
+    "ra_paged_attn_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _I64, _I64, _I64, _I64,
+                               _I64, _I64, _I64, _I64, _I64, _F, _U, _P, _SZ, _P]),
+    "ra_paged_attn_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I, _I64, _I64, _I64, _I64]),
+    "ra_paged_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I64, _I64, _I64, _I64, _I64, _P, _SZ,
+                             _P]),
     "ra_check_status": (_I, [_P, _P]),
     "ra_last_error": (ctypes.c_char_p, []),
     "ra_version": (ctypes.c_char_p, []),
@@ -349,6 +354,74 @@ def ra_window_attn_bwd(q, k, v, o, dout, lse, dq, dk, dv, B, L, H, H_kv, d, wind
                                     lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu, n_seqs, B, L, H,
                                     H_kv, d, window, sinks, scale, flags, workspace.data_ptr(), _nbytes(workspace),
                                     _stream(stream)))
+
+
+def _pool(k_pages, v_pages):
+    """[n_pages, page, H_kv, d] views of one shape and page stride, each page without gaps."""
+    n_pages, page, H_kv, d = k_pages.shape
+    for name, x in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if x.dtype != torch.bfloat16:
+            raise TypeError("%s must be bf16, not %s" % (name, x.dtype))
+        if x.shape != k_pages.shape or x.device != k_pages.device:
+            raise ValueError("k_pages and v_pages must have one shape and device")
+        if not (x.is_contiguous() or x[:1].is_contiguous()) or x.stride(0) != k_pages.stride(0):
+            raise ValueError("%s: a page must be contiguous, and both pools have one page stride" % name)
+    return n_pages, page, H_kv, d, k_pages.stride(0) if n_pages > 1 else page * H_kv * d
+
+
+def _rows(name, x, heads, d):
+    """The token stride of a bf16 [T, heads, d] view whose tokens are contiguous."""
+    if x.dtype != torch.bfloat16:
+        raise TypeError("%s must be bf16, not %s" % (name, x.dtype))
+    if x.dim() != 3 or x.shape[1:] != (heads, d):
+        raise ValueError("%s must be [T, %d, %d], not %s" % (name, heads, d, list(x.shape)))
+    if not (x.is_contiguous() or x[:1].is_contiguous()):
+        raise ValueError("%s: a token's heads must be contiguous" % name)
+    return x.stride(0) if x.shape[0] > 1 else heads * d
+
+
+def ra_paged_attn_workspace_bytes(T, n_seqs, H, H_kv, d, max_new, max_len, window=0, sinks=0):
+    return int(lib().ra_paged_attn_workspace_bytes(T, n_seqs, H, H_kv, d, max_new, max_len, window, sinks))
+
+
+def ra_paged_attn_fwd(q, k_pages, v_pages, block_table, seq_lens, cu_q, o, lse, max_new, max_len, window=0, sinks=0,
+                      scale=0.0, workspace=None, stream=None):
+    """Attention of the new tokens q [T, H, d] (tokens may be strided) over a paged cache [n_pages,
+    page, H_kv, d] (pages may be strided), which holds their keys and values already; o [T, H, d]
+    fp32 or bf16, lse [H, T] or None."""
+    T, H, d = q.shape
+    n_pages, page, H_kv, _, page_stride = _pool(k_pages, v_pages)
+    q_stride = _rows("q", q, H, k_pages.shape[3])
+    n_seqs, max_pages = block_table.shape
+    _tensors(q, (("block_table", block_table, _INT32, None), ("seq_lens", seq_lens, _INT32, (n_seqs,)),
+                 ("cu_q", cu_q, _INT32, (n_seqs + 1,)), ("o", o, _ANY_FLOAT, (T, H, d)), ("lse", lse, _FP32, (H, T)),
+                 ("workspace", workspace, None, None)))
+    if k_pages.device != q.device:
+        raise ValueError("the pages are on %s, not on %s" % (k_pages.device, q.device))
+    _check(lib().ra_paged_attn_fwd(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                                   seq_lens.data_ptr(), cu_q.data_ptr(), o.data_ptr(),
+                                   None if lse is None else lse.data_ptr(), T, n_seqs, H, H_kv, d, n_pages, page,
+                                   page_stride, max_pages, q_stride, max_new, max_len, window, sinks, scale,
+                                   RA_FLAG_O_BF16 if o.dtype == torch.bfloat16 else 0, workspace.data_ptr(),
+                                   _nbytes(workspace), _stream(stream)))
+
+
+def ra_paged_append(k_new, v_new, k_pages, v_pages, block_table, seq_lens, cu_new, workspace=None, stream=None):
+    """Copy new keys and values [T, H_kv, d] (tokens may be strided) to their places in the cache."""
+    n_pages, page, H_kv, d, page_stride = _pool(k_pages, v_pages)
+    new_stride = _rows("k_new", k_new, H_kv, d)
+    T = k_new.shape[0]
+    if v_new.shape != k_new.shape or _rows("v_new", v_new, H_kv, d) != new_stride:
+        raise ValueError("k_new and v_new must have one shape and token stride")
+    n_seqs, max_pages = block_table.shape
+    _tensors(k_new, (("block_table", block_table, _INT32, None), ("seq_lens", seq_lens, _INT32, (n_seqs,)),
+                     ("cu_new", cu_new, _INT32, (n_seqs + 1,)), ("workspace", workspace, None, None)))
+    if v_new.device != k_new.device or k_pages.device != k_new.device:
+        raise ValueError("k_new, v_new and the pages must be on one device")
+    _check(lib().ra_paged_append(k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                 block_table.data_ptr(), seq_lens.data_ptr(), cu_new.data_ptr(), T, n_seqs, H_kv, d,
+                                 n_pages, page, page_stride, max_pages, new_stride, workspace.data_ptr(),
+                                 _nbytes(workspace), _stream(stream)))
 
 
 def ra_check_status(workspace, stream=None):

@@ -55,6 +55,7 @@
 
 #include "ra_device.cuh"
 #include "ra_internal.h"
+#include "ra_paged.cuh"
 #include "ra_positions.cuh"
 #include "ra_window.cuh"
 
@@ -80,12 +81,34 @@ struct AttnArgs {
     int bh_chunk;       // (batch, head) pairs whose units are interleaved heavy-first
     int seq_order;      // q/k/v/o in sequence order [B, L, H, d], LSE [B, H, L] (ring mode)
     int window, sinks;  // windowed keys (KEYS_WINDOW)
+    // KEYS_PAGED: the sequences and pages; the parts' rows when the keys are
+    // split, [units, H_kv, num_splits, rows of a unit, d], and their LSE
+    PagedSeqs seqs;
+    int n_units, tile_tokens, page_box;
+    float *part_o, *part_lse;
 };
 
 // Which keys a unit's rows see.  KEYS_RING: the shards of a ring sweep, by
 // position.  KEYS_WINDOW: one batch element's own tokens (N = 1), a causal
-// window and the sequence's first tokens (window_row_keys).
-enum KeySet { KEYS_RING = 0, KEYS_WINDOW = 1 };
+// window and the sequence's first tokens (window_row_keys).  KEYS_PAGED: new
+// tokens over a paged cache (ra_paged.cuh): a unit's rows are the group of
+// query heads of up to 2 * tile_tokens tokens, its key tiles are gathered from
+// the block table's pages, and its tiles may be split over several CTAs.
+enum KeySet { KEYS_RING = 0, KEYS_WINDOW = 1, KEYS_PAGED = 2 };
+
+// The sequence of unit u, searched by a whole warp: 32 probes at a time.
+__device__ __forceinline__ int paged_find_seq_warp(const PagedSeqs &q, int u, int lane) {
+    int lo = 0, hi = q.n_seqs;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int at = lo + lane * step;
+        const bool below = at < hi && (lane == 0 || paged_first_unit(q, at) <= u);
+        const int last = 31 - __clz(__ballot_sync(0xffffffffu, below));
+        lo += last * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
+}
 
 __device__ __forceinline__ void record_timeout(unsigned *status, volatile int *abort) {
     *abort = 1;
@@ -170,6 +193,22 @@ struct StepCursor {
 // reference never moves at all.
 constexpr float kSumLo = 0x1p-32f, kSumHi = 0x1p32f;
 
+// Zero rows [from, 128) of a V tile in shared memory (nothing for from >= 128),
+// by one warp before it issues the products that read them: what lies behind a
+// sequence's last token was never written and may hold NaN, which P = 0 would
+// not remove.
+template <int D>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int from, int lane) {
+    if (from >= 128) return;
+    for (int e = max(from, 0) * 8 + lane; e < 128 * 8; e += 32)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + c * 128 * 128 + e * 16), "r"(0)
+                         : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+
 // SKIP: each Q tile of a unit skips the key tiles none of its own rows sees
 // (packed sequences in the striped layout, where a unit's 256 rows span many
 // short sequences); the MMA issuers skip those tiles' S and PV.
@@ -221,8 +260,26 @@ __global__ void __launch_bounds__(384, 1)
     // ---- unit decode: heavy units first, in L2-sized chunks of (batch, head)
     // pairs (decode_unit)
     const int S = args.S, H = args.H, N = args.N;
-    const UnitId unit = decode_unit(blockIdx.x, args.bh_chunk, args.B, H, args.num_q_ranks, args.n_units_seq,
-                                    args.layout);
+    UnitId unit{};
+    PagedUnit pu{};
+    int part = 0;             // KEYS_PAGED: which part of the unit's keys
+    int unit_no = 0;
+    if constexpr (KEYS == KEYS_PAGED) {
+        // blockIdx.x = (hk * num_splits + part) * n_units + unit, a sequence's
+        // last (longest) unit first; the CTAs of one head and part stand
+        // together and share its keys in L2
+        unit_no = args.n_units - 1 - blockIdx.x % args.n_units;
+        const int rest = blockIdx.x / args.n_units;
+        part = rest % args.seqs.num_splits;
+        unit.h = rest / args.seqs.num_splits;    // the key/value head
+        const int sq = paged_find_seq_warp(args.seqs, unit_no, lane);
+        pu = paged_unit(args.seqs, sq, unit_no - paged_first_unit(args.seqs, sq));
+        if (part == 0 && unit.h == 0 && threadIdx.x == 0 && pu.first == 0 && paged_bad_counts(args.seqs, sq))
+            atomicOr(args.status, RA_DEV_PAGE_BIT);
+        if (pu.n <= 0) return;
+    } else {
+        unit = decode_unit(blockIdx.x, args.bh_chunk, args.B, H, args.num_q_ranks, args.n_units_seq, args.layout);
+    }
     const int b = unit.b, h = unit.h, qi = unit.qi, qt = unit.qt;
     const bool ring = args.q_rank_fixed < 0;
     const int q_rank = ring ? qi : args.q_rank_fixed;
@@ -234,8 +291,20 @@ __global__ void __launch_bounds__(384, 1)
     if constexpr (KEYS == KEYS_RING)
         walk0 = unit_walk(args.layout, N, S, q_rank, args.kv_rank_fixed, args.num_steps, args.step_base, row0,
                           row_end, args.causal, args.cu_seqlens, args.n_seqs);
-    else
+    else if constexpr (KEYS == KEYS_WINDOW)
         walk0 = window_unit_walk(args.cu_seqlens, args.n_seqs, S, row0, row_end, args.window, args.sinks);
+    else {
+        walk0 = paged_walk(args.seqs, pu);
+        if (args.seqs.num_splits > 1) {
+            if (part >= paged_split_count(args.seqs, walk0.end)) return;
+            const int per = paged_split_tiles(args.seqs, walk0.end);
+            walk0.i = part * per;
+            walk0.end = min(walk0.end, walk0.i + per);
+        }
+    }
+    // KEYS_PAGED: a unit of few tokens has no second Q tile; its products and
+    // softmax are left out
+    const bool two_tiles = KEYS != KEYS_PAGED || pu.n > args.tile_tokens;
 
     // ---- setup
     if (threadIdx.x == 0) {
@@ -279,8 +348,19 @@ __global__ void __launch_bounds__(384, 1)
         // ================================================= TMA producer
         regs_shrink<LOW_REGS>();
         const int xh = h * D;                        // Q columns of head h
-        const int xkv = (h / args.kv_group) * D;     // K/V columns of its key/value head
-        if (lane == 0) {
+        const int xkv = KEYS == KEYS_PAGED ? h * D : (h / args.kv_group) * D;   // K/V columns of its key/value head
+        if constexpr (KEYS == KEYS_PAGED) {
+            // a box of the group's heads by tile_tokens tokens: rows in the
+            // packed order; rows of later tokens of q are loaded but not used
+            if (lane == 0) {
+                const int tiles = two_tiles ? 2 : 1;
+                mbar_arrive_expect_tx(BAR(B_QFULL), tiles * HALVES * args.tile_tokens * args.seqs.group * 128);
+                for (int g = 0; g < tiles; ++g)
+                    for (int c = 0; c < HALVES; ++c)
+                        tma_load_3d(s_base + L::kQ + g * L::kTile + c * L::kBox, &tmq, BAR(B_QFULL), 64 * c,
+                                    h * args.seqs.group, pu.t0 + g * args.tile_tokens);
+            }
+        } else if (lane == 0) {
             mbar_arrive_expect_tx(BAR(B_QFULL), 2 * L::kTile);
             for (int g = 0; g < 2; ++g) {
                 int c1, c2, c3;
@@ -303,6 +383,23 @@ __global__ void __launch_bounds__(384, 1)
         int i = 0, withheld = -1;
         uint32_t k_loads = 0, v_loads = 0;   // bit s: slot s has had a load of the kind, bit 8 + s: the parity of its last
         bool ok = true;
+        // KEYS_PAGED: lane i's page of a key tile (its box of page_box keys), or
+        // one past the last page, which reads as zeros, where the unit sees none
+        // of its keys
+        const RowKeys first = KEYS == KEYS_PAGED ? paged_row(args.seqs, pu.p0) : RowKeys{};
+        auto page_of = [&](int wtile) -> int {
+            int z = args.seqs.n_pages;
+            const int k0 = wtile * 128 + lane * args.page_box;
+            if (lane * args.page_box < 128 && paged_needed(first, pu.p0 + pu.n, pu.len, k0, args.page_box)) {
+                z = args.seqs.table[(size_t)pu.s * args.seqs.max_pages + k0 / args.seqs.page];
+                if ((unsigned)z >= (unsigned)args.seqs.n_pages) {
+                    atomicOr(args.status, RA_DEV_PAGE_BIT);
+                    z = args.seqs.n_pages;
+                }
+            }
+            return z;
+        };
+        // (for KEYS_PAGED wj is the lane's page)
         auto load = [&](int wj, int wtile, bool is_k) -> bool {
             const int sl = i % NSL;
             if (i >= NSL && !warp_wait(BAR(B_SLOTE + sl), ((i / NSL) - 1) & 1, abort_flag)) return false;
@@ -310,7 +407,17 @@ __global__ void __launch_bounds__(384, 1)
             const uint32_t full = BAR((is_k ? B_KF : B_VF) + sl);
             uint32_t &loads = is_k ? k_loads : v_loads;
             loads = (loads & (1u << sl)) ? loads ^ (256u << sl) : loads | (1u << sl);
-            if (lane == 0 && !withhold) {
+            if constexpr (KEYS == KEYS_PAGED) {
+                const uint32_t dst = s_base + L::kRing + sl * L::kTile;
+                if (lane == 0) mbar_arrive_expect_tx(full, L::kTile);
+                __syncwarp();
+                if (lane * args.page_box < 128) {
+                    const int y = (wtile * 128 + lane * args.page_box) & (args.seqs.page - 1);
+                    for (int c = 0; c < HALVES; ++c)
+                        tma_load_3d(dst + c * L::kBox + lane * args.page_box * 128, is_k ? &tmk : &tmv, full,
+                                    xkv + 64 * c, y, wj);
+                }
+            } else if (lane == 0 && !withhold) {
                 const uint32_t dst = s_base + L::kRing + sl * L::kTile;
                 int c1, c2, c3;
                 tile_coords(args.seq_order, args.layout, args.S, args.N, ring ? wj : 0, b, wtile * 128, c1, c2, c3);
@@ -325,7 +432,19 @@ __global__ void __launch_bounds__(384, 1)
             ++i;
             return true;
         };
-        if (wk.valid()) {
+        if constexpr (KEYS == KEYS_PAGED) {
+            if (wk.valid()) wk.j = page_of(wk.tile);
+            // the next tile's table entries are read a tile ahead
+            while (ok && wk.valid()) {
+                if (!(ok = load(wk.j, wk.tile, true))) break;
+                if (i > 1 && !(ok = load(vj, vtile, false))) break;
+                vj = wk.j;
+                vtile = wk.tile;
+                wk.next();
+                if (wk.valid()) wk.j = page_of(wk.tile);
+            }
+            if (ok && i > 0) ok = load(vj, vtile, false);
+        } else if (wk.valid()) {
             ok = load(wk.j, wk.tile, true);
             vj = wk.j;
             vtile = wk.tile;
@@ -433,12 +552,13 @@ __global__ void __launch_bounds__(384, 1)
             tc_fence_after();
             if (ok) {
                 issue_s(0, 0);
-                issue_s(1, 0);
+                if (two_tiles) issue_s(1, 0);
                 tc_commit_elect(BAR(B_SLOTE + 0));
             }
             __syncwarp();
         }
         while (ok && w.valid()) {
+            const int v_tile = w.tile;
             w.next();
             const bool has_next = w.valid();
             const int ki = 2 * t + 1;                        // load index of K(t+1)
@@ -451,20 +571,26 @@ __global__ void __launch_bounds__(384, 1)
                 __syncwarp();
             }
             if (!(ok = v_wait(vi % NSL))) break;
+            if constexpr (KEYS == KEYS_PAGED)
+                zero_rows<D>(s_base + L::kRing + (vi % NSL) * L::kTile, pu.len - v_tile * 128, lane);
             if (!(ok = warp_wait(BAR(B_PFULL + 0), t & 1, abort_flag))) break;
             tc_fence_after();
             issue_pv(0, vi % NSL, t == 0);
             __syncwarp();
             if (has_next) {
-                if (!(ok = warp_wait(BAR(B_SFREE + 1), t & 1, abort_flag))) break;
-                tc_fence_after();
-                issue_s(1, ki % NSL);
+                if (two_tiles) {
+                    if (!(ok = warp_wait(BAR(B_SFREE + 1), t & 1, abort_flag))) break;
+                    tc_fence_after();
+                    issue_s(1, ki % NSL);
+                }
                 tc_commit_elect(BAR(B_SLOTE + ki % NSL));
                 __syncwarp();
             }
-            if (!(ok = warp_wait(BAR(B_PFULL + 1), t & 1, abort_flag))) break;
-            tc_fence_after();
-            issue_pv(1, vi % NSL, t == 0);
+            if (two_tiles) {
+                if (!(ok = warp_wait(BAR(B_PFULL + 1), t & 1, abort_flag))) break;
+                tc_fence_after();
+                issue_pv(1, vi % NSL, t == 0);
+            }
             tc_commit_elect(BAR(B_SLOTE + vi % NSL));
             __syncwarp();
             ++t;
@@ -529,7 +655,7 @@ __global__ void __launch_bounds__(384, 1)
                 tc_fence_after();
                 if (ok) {
                     issue_s(0, 0);
-                    issue_s(1, 0);
+                    if (two_tiles) issue_s(1, 0);
                     tc_commit_elect(BAR(B_SLOTE + 0));
                 }
                 __syncwarp();
@@ -542,9 +668,11 @@ __global__ void __launch_bounds__(384, 1)
                 tc_fence_after();
                 issue_s(0, ki % NSL);
                 __syncwarp();
-                if (!(ok = warp_wait(BAR(B_SFREE + 1), t & 1, abort_flag))) break;
-                tc_fence_after();
-                issue_s(1, ki % NSL);
+                if (two_tiles) {
+                    if (!(ok = warp_wait(BAR(B_SFREE + 1), t & 1, abort_flag))) break;
+                    tc_fence_after();
+                    issue_s(1, ki % NSL);
+                }
                 tc_commit_elect(BAR(B_SLOTE + ki % NSL));
                 __syncwarp();
             }
@@ -633,18 +761,26 @@ __global__ void __launch_bounds__(384, 1)
         ok = ok && warp_wait(BAR(B_QFULL), 0, abort_flag);
         if constexpr (!SKIP) {
             int t = 0;
+            Walk wv = walk0;
+            if constexpr (KEYS == KEYS_PAGED) wv.start_step();
 #pragma unroll 1
             for (; ok && t < T; ++t) {
                 const bool has_next = t + 1 < T;
                 const int vi = has_next ? 2 * t + 2 : 2 * t + 1; // load index of V(t)
                 if (!(ok = v_wait(vi % NSL))) break;
+                if constexpr (KEYS == KEYS_PAGED) {
+                    zero_rows<D>(s_base + L::kRing + (vi % NSL) * L::kTile, pu.len - wv.tile * 128, lane);
+                    wv.next();
+                }
                 if (!(ok = warp_wait(BAR(B_PFULL + 0), t & 1, abort_flag))) break;
                 tc_fence_after();
                 issue_pv(0, vi % NSL, t == 0);
                 __syncwarp();
-                if (!(ok = warp_wait(BAR(B_PFULL + 1), t & 1, abort_flag))) break;
-                tc_fence_after();
-                issue_pv(1, vi % NSL, t == 0);
+                if (two_tiles) {
+                    if (!(ok = warp_wait(BAR(B_PFULL + 1), t & 1, abort_flag))) break;
+                    tc_fence_after();
+                    issue_pv(1, vi % NSL, t == 0);
+                }
                 tc_commit_elect(BAR(B_SLOTE + vi % NSL));
                 __syncwarp();
             }
@@ -770,8 +906,21 @@ __global__ void __launch_bounds__(384, 1)
         RowKeys rk{};
         if constexpr (KEYS == KEYS_RING)
             row_key_bounds(args.cu_seqlens, args.n_seqs, (int64_t)N * S, my_pos, args.causal, my_lo_pos, my_hi_pos);
-        else
+        else if constexpr (KEYS == KEYS_WINDOW)
             rk = window_row(args.cu_seqlens, args.n_seqs, S, a_c, args.window, args.sinks);
+        // KEYS_PAGED: row r is token r / group of the Q tile; rows past the
+        // tile's tokens or the unit's take the last token's keys, so that no
+        // tile is masked for their sake, and are not stored
+        bool live = true;           // the row is stored
+        bool warp_live = true;      // some row of the warp is
+        int my_tok = 0;
+        if constexpr (KEYS == KEYS_PAGED) {
+            const int tok = r / args.seqs.group;
+            my_tok = g * args.tile_tokens + tok;
+            live = tok < args.tile_tokens && my_tok < pu.n;
+            warp_live = __any_sync(0xffffffffu, live);
+            rk = paged_row(args.seqs, pu.p0 + min(my_tok, pu.n - 1));
+        }
         Walk w = walk0;
         w.start_step();
         int t = 0;              // key tiles this Q tile has processed
@@ -785,6 +934,17 @@ __global__ void __launch_bounds__(384, 1)
         int klo = 0, khi = S;   // this row's visible local keys [klo, khi) of shard w.j
         // (t counts the tiles processed: without skipping, every tile the walk visits)
         for (; (!SKIP || ok) && w.valid(); w.next(), t += SKIP ? 0 : 1) {
+            if constexpr (KEYS == KEYS_PAGED) {
+                if (g == 1 && !two_tiles) break;
+                if (!warp_live) {
+                    // no row here is stored: its P may be anything
+                    if (!(ok = warp_wait(BAR(B_SFULL + g), t & 1, abort_flag))) break;
+                    mbar_arrive(BAR(B_SFREE + g));
+                    if (t > 0 && !(ok = warp_wait(BAR(B_PVDONE + g), (t - 1) & 1, abort_flag))) break;
+                    mbar_arrive(BAR(B_PFULL + g));
+                    continue;
+                }
+            }
             if constexpr (KEYS != KEYS_RING) {
                 klo = rk.lo;
                 khi = rk.hi;
@@ -884,7 +1044,7 @@ __global__ void __launch_bounds__(384, 1)
                 // a windowed row may see no column of a tile its unit visits:
                 // nothing is added and nothing has to move
                 if constexpr (KEYS != KEYS_RING)
-                    bad = bad && (max(lim_lo, 0) < min(lim, 128) || max(sk_lo, 0) < min(sk_hi, 128));
+                    bad = bad && live && (max(lim_lo, 0) < min(lim, 128) || max(sk_lo, 0) < min(sk_hi, 128));
                 if (__builtin_expect(__any_sync(0xffffffffu, bad), 0)) {
                     load_s();
                     const float *s = reinterpret_cast<const float *>(&sr[0][0]);
@@ -1029,9 +1189,44 @@ __global__ void __launch_bounds__(384, 1)
                 }
             }
         }
+        if constexpr (KEYS == KEYS_PAGED) {
+            // each warp copies its own rows out: final rows of [T, H, d], or
+            // this part's rows for the join
+            const bool split = args.seqs.num_splits > 1;
+            const float lse = l > 0.f ? (m_ref + lg2(l)) * 0.6931471805599453f : -INFINITY;
+            const int head = h * args.seqs.group + r % args.seqs.group;
+            long long at = -1;       // the row's first element
+            if (ok && live && (g == 0 || two_tiles)) {
+                const size_t part_row = (((size_t)unit_no * args.seqs.Hkv + h) * args.seqs.num_splits + part) *
+                                            paged_unit_rows(args.seqs) +
+                                        my_tok * args.seqs.group + r % args.seqs.group;
+                const size_t tok = (size_t)(pu.t0 + my_tok);
+                at = (long long)((split ? part_row : tok * args.seqs.H + head) * D);
+                if (split) args.part_lse[part_row] = lse;
+                else if (args.lse) args.lse[(size_t)head * args.seqs.T + tok] = lse;
+            }
+            __syncwarp();
+            uint8_t *out = split ? reinterpret_cast<uint8_t *>(args.part_o) : static_cast<uint8_t *>(args.o);
+            constexpr int ESZ = OUT_F32 ? 4 : 2;
+            constexpr int CPR = D * ESZ / 16;        // 16-byte chunks per row
+            if (warp_live && *abort_flag == 0) {
+#pragma unroll 4
+                for (int e = lane; e < 32 * CPR; e += 32) {
+                    const int row = e / CPR, ch = e % CPR;
+                    const long long dst = __shfl_sync(0xffffffffu, at, row);
+                    const int rr = wq * 32 + row;
+                    const uint32_t src = box_addr(ch >> 3) + (rr >> 3) * 1024 + (rr & 7) * 128 + (((ch & 7) ^ (rr & 7)) << 4);
+                    uint32_t x0, x1, x2, x3;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3) : "r"(src) : "memory");
+                    if (dst >= 0)
+                        *reinterpret_cast<uint4 *>(out + (size_t)dst * ESZ + ch * 16) = make_uint4(x0, x1, x2, x3);
+                }
+            }
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        named_barrier_sync(1 + g, 128);
-        if (wq == 0 && lane == 0 && *abort_flag == 0) {
+        if constexpr (KEYS != KEYS_PAGED) named_barrier_sync(1 + g, 128);
+        if (KEYS != KEYS_PAGED && wq == 0 && lane == 0 && *abort_flag == 0) {
             // rows past the shard's end fall outside the tensor and are not written
             int c1, c2, c3;
             tile_coords(args.seq_order, args.layout, args.S, args.N, ring ? qi : 0, b, row0 + 128 * g, c1, c2, c3);
@@ -1040,7 +1235,7 @@ __global__ void __launch_bounds__(384, 1)
             tma_store_commit();
             tma_store_wait_read();
         }
-        if (ok && a < S) {
+        if (KEYS != KEYS_PAGED && ok && a < S) {
             // shard stacks: [N or 1, B, H, S]; sequence order: [B, H, L] at the row's position
             const size_t at = args.seq_order ? ((size_t)b * H + h) * ((size_t)N * S) + (size_t)my_pos
                                              : ((size_t)zq * H + h) * S + a;

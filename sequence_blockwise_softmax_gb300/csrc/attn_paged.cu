@@ -1,0 +1,427 @@
+// attn_paged.cu -- attention of new tokens over a paged key/value cache: the
+// entry points, their checks and launches, the join of split keys, and the
+// copy of new keys and values into the cache.
+//
+// ra_paged_attn_fwd runs the tensor-core forward (attn_fwd_kernel.cuh,
+// KEYS_PAGED): units of up to 256 rows (the query heads of one key/value head
+// by consecutive new tokens), key tiles of 128 gathered page by page with TMA.
+// Where there are few units, each unit's key tiles are cut into parts that run
+// as CTAs of their own and are joined by their LSE.
+#include <cmath>
+
+#include "attn_fwd_kernel.cuh"
+#include "ra_tensor_map.h"
+
+namespace ra {
+namespace {
+
+constexpr size_t kHeader = RA_WORKSPACE_MIN_BYTES;
+constexpr int kSms = 152;               // GB300; only the choice of a split depends on it
+constexpr size_t kPartBytes = 48u << 20;   // most bytes of a call's parts
+
+size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+ra_status launch_error() {
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
+}
+
+// ------------------------------------------------------------------ join
+// One warp per (token, head): O = sum_i w_i O_i, w_i = exp(LSE_i - LSE).  The
+// parts are read in order, so the result does not depend on timing.  Bound by
+// the parts' bytes, most of which are still in L2.
+struct JoinArgs {
+    PagedSeqs seqs;
+    const float *part_o, *part_lse;
+    void *o;
+    float *lse;
+    int o_bf16;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) paged_join_kernel(const JoinArgs a) {
+    const PagedSeqs &q = a.seqs;
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= (int64_t)q.T * q.H) return;
+    const int tok = (int)(row / q.H), head = (int)(row % q.H);
+    // the last sequence starting at or before the token
+    int lo = 0, hi = q.n_seqs;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (paged_bound(q, mid) <= tok) lo = mid;
+        else hi = mid;
+    }
+    const int i = tok - paged_bound(q, lo);
+    if (i < 0 || i >= q.max_new || tok >= paged_bound(q, lo + 1)) return;    // behind the last sequence
+    const int local = i / q.unit_tokens;
+    const PagedUnit u = paged_unit(q, lo, local);
+    const int parts = paged_split_count(q, paged_walk(q, u).end);
+    const size_t rows = paged_unit_rows(q);
+    const size_t unit = (size_t)paged_first_unit(q, lo) + local;
+    const size_t first = ((unit * q.Hkv + head / q.group) * q.num_splits) * rows +
+                         (size_t)(i - u.first) * q.group + head % q.group;
+    float m = -INFINITY;
+    for (int p = 0; p < parts; ++p) m = fmaxf(m, a.part_lse[first + p * rows]);
+    constexpr int PER = D / 32;
+    float acc[PER] = {};
+    float sum = 0.f;
+    if (m > -INFINITY) {
+        for (int p = 0; p < parts; ++p) {
+            const float w = ex2((a.part_lse[first + p * rows] - m) * 1.4426950408889634f);
+            const float *src = a.part_o + (first + p * rows) * D + lane * PER;
+            sum += w;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] += w * src[e];
+        }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    if (a.o_bf16) {
+        uint32_t *dst = static_cast<uint32_t *>(a.o) + (row * D + lane * PER) / 2;
+#pragma unroll
+        for (int e = 0; e < PER; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    } else {
+        float *dst = static_cast<float *>(a.o) + row * D + lane * PER;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) dst[e] = acc[e] * inv;
+    }
+    if (lane == 0 && a.lse) a.lse[(size_t)head * q.T + tok] = sum > 0.f ? m + lg2(sum) * 0.6931471805599453f : -INFINITY;
+}
+
+// ------------------------------------------------------------------ plan
+struct Paged {
+    int64_t T, n_seqs, H, H_kv, n_pages, page, page_stride, max_pages, q_stride, max_new, max_len, window, sinks;
+    int d;
+    float scale;
+};
+
+// How a call is cut: tokens per unit, the most parts per unit, the parts' bytes.
+struct Plan {
+    int tile_tokens, splits;
+    int64_t units;
+    size_t part_o, part_lse, total;
+};
+
+Plan plan(const Paged &a) {
+    Plan p;
+    const int64_t group = a.H / a.H_kv;
+    p.tile_tokens = (int)(128 / group);
+    const int unit = 2 * p.tile_tokens;
+    p.units = paged_units(a.T, a.n_seqs, unit);
+    const int64_t rows = (a.max_new < unit ? a.max_new : unit) * group;
+    const size_t part = (size_t)p.units * a.H_kv * rows * (a.d + 1) * 4;     // one part of every unit
+    // The time of s parts: waves of CTAs, about 7 us and 1.3 us per key tile
+    // each, and the join's launch.
+    const int64_t full = (a.T + unit - 1) / unit, active = a.n_seqs < a.T ? a.n_seqs : a.T;
+    const int64_t ctas = (full > active ? full : active) * a.H_kv;
+    int64_t keys = a.max_len;
+    if (a.window > 0 && a.window + a.max_new + a.sinks < keys) keys = a.window + (a.max_new < unit ? a.max_new : unit) + a.sinks;
+    const int64_t tiles = (keys + 127) / 128 + 1;
+    p.splits = 1;
+    double best = 0;
+    for (int s = 1; s <= 64 && (s == 1 || (tiles / s >= kSplitTiles && part * s <= kPartBytes)); ++s) {
+        const double t = (double)((ctas * s + kSms - 1) / kSms) * (7.0 + 1.3 * (double)((tiles + s - 1) / s)) +
+                         (s > 1 ? 4.0 : 0.0);
+        if (s == 1 || t < best) {
+            best = t;
+            p.splits = s;
+        }
+    }
+    p.part_o = kHeader;
+    p.part_lse = p.part_o;
+    p.total = kHeader;
+    if (p.splits > 1) {
+        p.part_lse = p.part_o + round256((size_t)p.units * a.H_kv * p.splits * rows * a.d * 4);
+        p.total = p.part_lse + round256((size_t)p.units * a.H_kv * p.splits * rows * 4);
+    }
+    return p;
+}
+
+ra_status check_heads(int64_t H, int64_t H_kv, int d) {
+    if (d != 64 && d != 128) return set_error(RA_ERR_UNSUPPORTED, "head dimension d must be 64 or 128");
+    if (H_kv < 1 || H_kv > H || H % H_kv)
+        return set_error(RA_ERR_SHAPE, "the key/value head count must divide the query head count");
+    if (H / H_kv > 128) return set_error(RA_ERR_UNSUPPORTED, "at most 128 query heads per key/value head");
+    if (H > (int64_t)1 << 16) return set_error(RA_ERR_UNSUPPORTED, "H beyond the supported range");
+    return RA_OK;
+}
+
+ra_status check_cache(int64_t T, int64_t n_seqs, int64_t H_kv, int d, int64_t n_pages, int64_t page,
+                      int64_t page_stride, int64_t max_pages) {
+    if (T < 0 || n_seqs < 0 || n_pages < 0 || max_pages < 0) return set_error(RA_ERR_SHAPE, "sizes must be non-negative");
+    if (page < 16 || page > 65536 || (page & (page - 1)))
+        return set_error(RA_ERR_UNSUPPORTED, "page_size must be a power of two, at least 16 and at most 65536");
+    if (T > (int64_t)1 << 24 || n_seqs > (int64_t)1 << 24 || n_pages > (int64_t)1 << 30)
+        return set_error(RA_ERR_UNSUPPORTED, "tokens, sequences or pages beyond the supported range");
+    if (max_pages * page > (int64_t)1 << 29)
+        return set_error(RA_ERR_UNSUPPORTED, "max_pages * page_size beyond the supported range (2^29 tokens)");
+    if (page_stride < page * H_kv * d) return set_error(RA_ERR_SHAPE, "page_stride is smaller than a page: pages would overlap");
+    if (page_stride % 8) return set_error(RA_ERR_ALIGNMENT, "page_stride must be a multiple of 8 elements (16 bytes)");
+    if (page_stride * 2 >= ((int64_t)1 << 40)) return set_error(RA_ERR_UNSUPPORTED, "page_stride beyond the supported range");
+    return RA_OK;
+}
+
+ra_status check(const Paged &a) {
+    ra_status st = check_heads(a.H, a.H_kv, a.d);
+    if (st != RA_OK) return st;
+    if ((st = check_cache(a.T, a.n_seqs, a.H_kv, a.d, a.n_pages, a.page, a.page_stride, a.max_pages)) != RA_OK) return st;
+    if (std::isnan(a.scale) || std::isinf(a.scale)) return set_error(RA_ERR_INVALID_ARG, "scale must be finite");
+    if (a.q_stride < a.H * a.d) return set_error(RA_ERR_SHAPE, "q_stride is smaller than H * d: tokens would overlap");
+    if (a.q_stride % 8) return set_error(RA_ERR_ALIGNMENT, "q_stride must be a multiple of 8 elements (16 bytes)");
+    if (a.q_stride * 2 >= ((int64_t)1 << 40)) return set_error(RA_ERR_UNSUPPORTED, "q_stride beyond the supported range");
+    if (a.max_new < 0 || a.max_len < 0) return set_error(RA_ERR_SHAPE, "max_new and max_len must be non-negative");
+    if (a.window < 0) return set_error(RA_ERR_INVALID_ARG, "window must not be negative (0: none)");
+    if (a.sinks < 0) return set_error(RA_ERR_INVALID_ARG, "sinks must not be negative");
+    return RA_OK;
+}
+
+// ------------------------------------------------------------------ launch
+bool page_map(CUtensorMap *map, const void *base, const Paged &a, int box) {
+    EncodeTiledFn enc = get_encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)(a.H_kv * a.d), (cuuint64_t)a.page, (cuuint64_t)a.n_pages};
+    cuuint64_t strides[2] = {(cuuint64_t)(a.H_kv * a.d * 2), (cuuint64_t)(a.page_stride * 2)};
+    cuuint32_t bx[3] = {64, (cuuint32_t)box, 1}, estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, bx, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [T, H, d] with a token stride, in boxes of 64 columns by a group's heads by tile_tokens tokens
+bool query_map(CUtensorMap *map, const void *base, const Paged &a, int tile_tokens) {
+    EncodeTiledFn enc = get_encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.H, (cuuint64_t)a.T};
+    cuuint64_t strides[2] = {(cuuint64_t)(a.d * 2), (cuuint64_t)(a.q_stride * 2)};
+    cuuint32_t bx[3] = {64, (cuuint32_t)(a.H / a.H_kv), (cuuint32_t)tile_tokens}, estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, bx, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+PagedSeqs sequences(const Paged &a, const int *table, const int *seq_lens, const int *cu_q) {
+    PagedSeqs s{};
+    s.table = table;
+    s.seq_lens = seq_lens;
+    s.cu_q = cu_q;
+    s.n_seqs = (int)a.n_seqs;
+    s.T = (int)a.T;
+    s.max_pages = (int)a.max_pages;
+    s.page = (int)a.page;
+    s.n_pages = (int)a.n_pages;
+    s.H = (int)a.H;
+    s.Hkv = (int)a.H_kv;
+    s.group = (int)(a.H / a.H_kv);
+    s.max_new = (int)(a.max_new < a.T ? a.max_new : a.T);
+    const int64_t cap = (int64_t)1 << 29;      // at least as long as any cache
+    s.window = (int)(a.window < cap ? a.window : cap);
+    s.sinks = (int)(a.sinks < cap ? a.sinks : cap);
+    return s;
+}
+
+template <int D, bool F32>
+ra_status launch_chunks(const Paged &a, const Plan &p, const AttnArgs &args, const void *q, const void *k,
+                        const void *v, cudaStream_t stream) {
+    CUtensorMap mq, mk, mv;
+    if (!query_map(&mq, q, a, p.tile_tokens) || !page_map(&mk, k, a, args.page_box) || !page_map(&mv, v, a, args.page_box))
+        return set_error(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the q and page maps");
+    auto kern = attn_fwd_kernel<D, F32, false, KEYS_PAGED>;
+    const int smem = (int)AttnSmem<D>::kBytes;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
+    const int64_t grid = p.units * a.H_kv * p.splits;
+    if (grid > 0x7fffffffLL) return set_error(RA_ERR_UNSUPPORTED, "too many query tiles for one launch");
+    kern<<<(unsigned)grid, 384, smem, stream>>>(mq, mk, mv, mq, args);
+    return launch_error();
+}
+
+template <int D>
+ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, const int *cu_q, const void *q,
+                       const void *k, const void *v, void *o, float *lse, bool o_bf16, uint8_t *workspace,
+                       cudaStream_t stream) {
+    const Plan p = plan(a);
+    AttnArgs args{};
+    args.o = o;
+    args.lse = lse;
+    args.status = reinterpret_cast<unsigned *>(workspace);
+    args.B = args.H = args.N = 1;
+    args.layout = RA_CONTIGUOUS;
+    args.causal = 1;
+    args.scale_log2 = (a.scale > 0.f ? a.scale : 1.0f / std::sqrt((float)a.d)) * 1.4426950408889634f;
+    args.num_q_ranks = 1;
+    args.q_rank_fixed = args.kv_rank_fixed = -1;
+    args.num_steps = 1;
+    args.kv_group = 1;
+    args.seqs = sequences(a, table, seq_lens, cu_q);
+    args.seqs.unit_tokens = 2 * p.tile_tokens;
+    args.seqs.num_splits = p.splits;
+    args.n_units = (int)p.units;
+    args.tile_tokens = p.tile_tokens;
+    args.page_box = (int)(a.page < 128 ? a.page : 128);
+    args.part_o = reinterpret_cast<float *>(workspace + p.part_o);
+    args.part_lse = reinterpret_cast<float *>(workspace + p.part_lse);
+    const bool f32 = p.splits > 1 || !o_bf16;
+    const ra_status st = f32 ? launch_chunks<D, true>(a, p, args, q, k, v, stream)
+                             : launch_chunks<D, false>(a, p, args, q, k, v, stream);
+    if (st != RA_OK || p.splits == 1) return st;
+    JoinArgs j{args.seqs, args.part_o, args.part_lse, o, lse, o_bf16 ? 1 : 0};
+    const int64_t blocks = (a.T * a.H + 7) / 8;
+    paged_join_kernel<D><<<(unsigned)blocks, 256, 0, stream>>>(j);
+    return launch_error();
+}
+
+// ------------------------------------------------------------------ append
+// Row i of sequence s's n new rows goes to position seq_lens[s] - n + i.  One
+// thread per 16 bytes of a token's keys and of its values; a token's bytes are
+// one run on both sides.  Bound by HBM: 4 * H_kv * d * 2 bytes per token.
+struct AppendArgs {
+    PagedSeqs seqs;
+    const uint4 *k_new, *v_new;
+    uint4 *k_pages, *v_pages;
+    int64_t new_stride, page_stride;   // in 16-byte chunks
+    int chunks;                        // per token
+    unsigned *status;
+};
+
+constexpr int kAppendThreads = 256, kAppendPer = 4;   // tokens a block copies at a time
+
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendArgs a) {
+    const PagedSeqs &q = a.seqs;
+    __shared__ int64_t dst_of[kAppendPer];
+    for (int64_t t0 = (int64_t)blockIdx.x * kAppendPer; t0 < q.T; t0 += (int64_t)gridDim.x * kAppendPer) {
+        if (threadIdx.x < kAppendPer) {
+            const int64_t t = t0 + threadIdx.x;
+            int64_t dst = -1;
+            if (t < q.T) {
+                int lo = 0, hi = q.n_seqs;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (paged_bound(q, mid) <= t) lo = mid;
+                    else hi = mid;
+                }
+                const int c0 = paged_bound(q, lo), c1 = paged_bound(q, lo + 1);
+                if (t >= c0 && t < c1) {
+                    const int64_t pos = (int64_t)q.seq_lens[lo] - (c1 - t);
+                    int id = -1;
+                    if (pos >= 0 && pos / q.page < q.max_pages) id = q.table[(size_t)lo * q.max_pages + pos / q.page];
+                    if (id >= 0 && id < q.n_pages)
+                        dst = (int64_t)id * a.page_stride + (pos & (q.page - 1)) * a.chunks;
+                    else
+                        atomicOr(a.status, RA_DEV_PAGE_BIT);
+                }
+            }
+            dst_of[threadIdx.x] = dst;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < kAppendPer * a.chunks; e += kAppendThreads) {
+            const int i = e / a.chunks, c = e - i * a.chunks;
+            if (dst_of[i] < 0) continue;
+            const int64_t src = (t0 + i) * a.new_stride + c;
+            const uint4 kv = a.k_new[src], vv = a.v_new[src];
+            a.k_pages[dst_of[i] + c] = kv;
+            a.v_pages[dst_of[i] + c] = vv;
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+}  // namespace ra
+
+extern "C" {
+
+size_t ra_paged_attn_workspace_bytes(int64_t T, int64_t n_seqs, int64_t H, int64_t H_kv, int d, int64_t max_new,
+                                     int64_t max_len, int64_t window, int64_t sinks) {
+    if (T < 0 || n_seqs < 0 || max_new < 0 || max_len < 0 || window < 0 || sinks < 0 || H_kv < 1 || H < H_kv ||
+        H % H_kv || H / H_kv > 128 || H > (int64_t)1 << 16 || (d != 64 && d != 128) || T > (int64_t)1 << 24 ||
+        n_seqs > (int64_t)1 << 24)
+        return 0;
+    ra::Paged a{};
+    a.T = T, a.n_seqs = n_seqs, a.H = H, a.H_kv = H_kv, a.d = d, a.max_new = max_new, a.max_len = max_len;
+    a.window = window, a.sinks = sinks;
+    return ra::plan(a).total;
+}
+
+ra_status ra_paged_attn_fwd(const void *q, const void *k_pages, const void *v_pages, const int32_t *block_table,
+                            const int32_t *seq_lens, const int32_t *cu_q, void *o, float *lse, int64_t T,
+                            int64_t n_seqs, int64_t H, int64_t H_kv, int d, int64_t n_pages, int64_t page_size,
+                            int64_t page_stride, int64_t max_pages, int64_t q_stride, int64_t max_new,
+                            int64_t max_len, int64_t window, int64_t sinks, float scale, unsigned flags,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+    using namespace ra;
+    if (flags & ~RA_FLAG_O_BF16) return set_error(RA_ERR_INVALID_ARG, "unknown flag bits");
+    Paged a{T, n_seqs, H, H_kv, n_pages, page_size, page_stride, max_pages, q_stride, max_new, max_len, window, sinks,
+            d, scale};
+    const ra_status st = check(a);
+    if (st != RA_OK) return st;
+    if (T == 0 || n_seqs == 0 || max_new == 0) return RA_OK;
+    if (n_pages == 0 || max_pages == 0) return set_error(RA_ERR_SHAPE, "new tokens need pages to lie in");
+    const void *ptrs[] = {q, k_pages, v_pages, o, workspace};
+    for (const void *p : ptrs) {
+        if (!p) return set_error(RA_ERR_INVALID_ARG, "null pointer argument");
+        if (!aligned(p, 16)) return set_error(RA_ERR_ALIGNMENT, "every tensor pointer must be 16-byte aligned");
+    }
+    const void *ints[] = {block_table, seq_lens, cu_q};
+    for (const void *p : ints) {
+        if (!p) return set_error(RA_ERR_INVALID_ARG, "null pointer argument");
+        if (!aligned(p, 4)) return set_error(RA_ERR_ALIGNMENT, "block_table, seq_lens and cu_q must be 4-byte aligned");
+    }
+    if (!aligned(lse, 4)) return set_error(RA_ERR_ALIGNMENT, "lse must be 4-byte aligned");
+    if (workspace_bytes < plan(a).total)
+        return set_error(RA_ERR_INVALID_ARG, "workspace smaller than ra_paged_attn_workspace_bytes()");
+    auto launch = d == 128 ? launch_paged<128> : launch_paged<64>;
+    return launch(a, block_table, seq_lens, cu_q, q, k_pages, v_pages, o, lse, (flags & RA_FLAG_O_BF16) != 0,
+                  static_cast<uint8_t *>(workspace), static_cast<cudaStream_t>(stream));
+}
+
+ra_status ra_paged_append(const void *k_new, const void *v_new, void *k_pages, void *v_pages,
+                          const int32_t *block_table, const int32_t *seq_lens, const int32_t *cu_new, int64_t T,
+                          int64_t n_seqs, int64_t H_kv, int d, int64_t n_pages, int64_t page_size,
+                          int64_t page_stride, int64_t max_pages, int64_t new_stride, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+    using namespace ra;
+    ra_status st = check_heads(H_kv, H_kv, d);
+    if (st != RA_OK) return st;
+    if ((st = check_cache(T, n_seqs, H_kv, d, n_pages, page_size, page_stride, max_pages)) != RA_OK) return st;
+    if (new_stride < H_kv * d) return set_error(RA_ERR_SHAPE, "new_stride is smaller than H_kv * d: tokens would overlap");
+    if (new_stride % 8) return set_error(RA_ERR_ALIGNMENT, "new_stride must be a multiple of 8 elements (16 bytes)");
+    if (new_stride * 2 >= ((int64_t)1 << 40)) return set_error(RA_ERR_UNSUPPORTED, "new_stride beyond the supported range");
+    if (T == 0 || n_seqs == 0) return RA_OK;
+    if (n_pages == 0 || max_pages == 0) return set_error(RA_ERR_SHAPE, "new tokens need pages to lie in");
+    const void *ptrs[] = {k_new, v_new, k_pages, v_pages, workspace};
+    for (const void *p : ptrs) {
+        if (!p) return set_error(RA_ERR_INVALID_ARG, "null pointer argument");
+        if (!aligned(p, 16)) return set_error(RA_ERR_ALIGNMENT, "every tensor pointer must be 16-byte aligned");
+    }
+    const void *ints[] = {block_table, seq_lens, cu_new};
+    for (const void *p : ints) {
+        if (!p) return set_error(RA_ERR_INVALID_ARG, "null pointer argument");
+        if (!aligned(p, 4)) return set_error(RA_ERR_ALIGNMENT, "block_table, seq_lens and cu_new must be 4-byte aligned");
+    }
+    if (workspace_bytes < RA_WORKSPACE_MIN_BYTES)
+        return set_error(RA_ERR_INVALID_ARG, "workspace smaller than RA_WORKSPACE_MIN_BYTES");
+    AppendArgs a{};
+    a.seqs.table = block_table;
+    a.seqs.seq_lens = seq_lens;
+    a.seqs.cu_q = cu_new;
+    a.seqs.n_seqs = (int)n_seqs;
+    a.seqs.T = (int)T;
+    a.seqs.max_pages = (int)max_pages;
+    a.seqs.page = (int)page_size;
+    a.seqs.n_pages = (int)n_pages;
+    a.k_new = static_cast<const uint4 *>(k_new);
+    a.v_new = static_cast<const uint4 *>(v_new);
+    a.k_pages = static_cast<uint4 *>(k_pages);
+    a.v_pages = static_cast<uint4 *>(v_pages);
+    a.new_stride = new_stride / 8;
+    a.page_stride = page_stride / 8;
+    a.chunks = (int)(H_kv * d / 8);
+    a.status = static_cast<unsigned *>(workspace);
+    int64_t blocks = (T + kAppendPer - 1) / kAppendPer;
+    if (blocks > kSms * 8) blocks = kSms * 8;
+    paged_append_kernel<<<(unsigned)blocks, kAppendThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    return launch_error();
+}
+
+}  // extern "C"

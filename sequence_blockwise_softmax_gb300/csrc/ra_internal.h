@@ -13,6 +13,9 @@ constexpr unsigned RA_DEV_TIMEOUT_BIT = 1u;
 // A kernel that lays out its shared memory from a 1024-byte-aligned dynamic
 // base found the base unaligned, and returned before touching it.
 constexpr unsigned RA_DEV_SMEM_ALIGN_BIT = 2u;
+// A block table named a page outside the pool (it read as zeros, or the token
+// was not written), or a sequence is longer than its row of the table.
+constexpr unsigned RA_DEV_PAGE_BIT = 4u;
 
 // One attention launch: every query unit of `num_q_ranks` ranks sweeps its
 // key/value shards.  Ring mode: q/k/v are [N, B, S, H, d] stacks, each query
