@@ -2,7 +2,9 @@
 
 Argument marshalling only: every function here checks that it was given CUDA
 tensors, takes their device pointers and the current CUDA stream, and calls
-the C entry point of the same name declared in ``include/ra.h``.  All work
+the C entry point of the same name declared in ``include/ra.h`` -- the windowed
+and paged attention calls, whose host time counts, through the compiled
+``ra_torch.so`` (``csrc/torch_binding.cpp``).  All work
 runs in the library's kernels; there is no fallback of any kind -- if the
 library is missing, the first call raises.
 
@@ -10,6 +12,7 @@ Layouts (see ``include/ra.h``): full sequences are ``[B, L, H, d]``; shard
 stacks ``[N, B, S, H, d]``; LSE ``[.., H, S]`` fp32 in natural log.
 """
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -98,6 +101,25 @@ def lib():
             fn.argtypes = args
         _lib = L
     return _lib
+
+
+_native = None
+
+
+def native():
+    """The compiled tensor marshalling (ra_torch.so), bound to the loaded library; raise if it is missing."""
+    global _native
+    if _native is None:
+        path = _build.BINDING
+        if not os.path.exists(path):
+            raise RuntimeError("ra_torch.so is not built (%s); run __graft_entry__.build()" % path)
+        spec = importlib.util.spec_from_file_location("ra_torch", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*[ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
+                      for name in ("ra_window_attn_fwd", "ra_window_attn_bwd", "ra_paged_attn_fwd", "ra_paged_append")])
+        _native = module
+    return _native
 
 
 def _check(st):
@@ -283,55 +305,17 @@ def ra_ring_attn_bwd(q, k, v, o, dout, lse, dq, dk, dv, B, L, H, H_kv, d, N, lay
                                   workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
-_DTYPE_NAMES = {torch.bfloat16: "bf16", torch.float32: "fp32", torch.int32: "int32", torch.uint8: "uint8"}
-
-
-def _tensors(first, named):
-    """Check (name, tensor, dtypes, shape) entries -- None for a tensor that may be left out (a
-    workspace may not) and for a type or shape that is not fixed -- and that all lie, contiguous,
-    on the current CUDA device."""
-    dev = first.device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError("tensors must be on the current CUDA device, not %s" % dev)
-    for name, t, dtypes, shape in named:
-        if t is None:
-            if name == "workspace":
-                raise ValueError("workspace is needed (see new_workspace)")
-            continue
-        if dtypes is not None and t.dtype not in dtypes:
-            raise TypeError("%s must be %s, not %s" % (name, " or ".join(_DTYPE_NAMES[x] for x in dtypes), t.dtype))
-        if t.device != dev:
-            raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
-        if shape is not None and t.shape != shape:
-            raise ValueError("%s must be %s, not %s" % (name, list(shape), list(t.shape)))
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-
-
-_BF16, _FP32, _INT32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
-_ANY_FLOAT = (torch.bfloat16, torch.float32)
-
-
-def _cu_seqlens(cu_seqlens):
-    return (None, 0) if cu_seqlens is None else (cu_seqlens.data_ptr(), cu_seqlens.numel() - 1)
-
-
-def _nbytes(workspace):
-    return workspace.numel() * workspace.element_size()
+def _raw_stream(stream):
+    """None for the current stream (the compiled binding looks it up), else the stream's handle."""
+    return stream if stream is None else _stream(stream)
 
 
 def ra_window_attn_fwd(q, k, v, o, lse, B, L, H, H_kv, d, window, sinks=0, scale=0.0, cu_seqlens=None, workspace=None,
                        stream=None):
     """Causal attention of each token to the last ``window`` tokens of its sequence and its first
     ``sinks``; o fp32 or bf16.  ``cu_seqlens``: int32 boundaries of packed sequences (B = 1)."""
-    _tensors(q, (("q", q, _BF16, (B, L, H, d)), ("k", k, _BF16, (B, L, H_kv, d)), ("v", v, _BF16, (B, L, H_kv, d)),
-                 ("o", o, _ANY_FLOAT, (B, L, H, d)), ("lse", lse, _FP32, (B, H, L)),
-                 ("cu_seqlens", cu_seqlens, _INT32, None), ("workspace", workspace, None, None)))
-    cu, n_seqs = _cu_seqlens(cu_seqlens)
-    _check(lib().ra_window_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), cu, n_seqs,
-                                    B, L, H, H_kv, d, window, sinks, scale,
-                                    RA_FLAG_O_BF16 if o.dtype == torch.bfloat16 else 0, workspace.data_ptr(),
-                                    _nbytes(workspace), _stream(stream)))
+    _check((_native or native()).window_fwd(q, k, v, o, lse, B, L, H, H_kv, d, window, sinks, scale, cu_seqlens,
+                                            workspace, _raw_stream(stream)))
 
 
 def ra_window_attn_bwd_workspace_bytes(B, L, H, H_kv, d, window, sinks=0, n_seqs=0):
@@ -342,42 +326,8 @@ def ra_window_attn_bwd(q, k, v, o, dout, lse, dq, dk, dv, B, L, H, H_kv, d, wind
                        cu_seqlens=None, workspace=None, stream=None):
     """Gradients of ra_window_attn_fwd; o fp32 or bf16 (as the forward wrote it), dq / dk / dv all
     fp32 or all bf16."""
-    _tensors(q, (("q", q, _BF16, (B, L, H, d)), ("k", k, _BF16, (B, L, H_kv, d)), ("v", v, _BF16, (B, L, H_kv, d)),
-                 ("o", o, _ANY_FLOAT, (B, L, H, d)), ("dout", dout, _BF16, (B, L, H, d)),
-                 ("lse", lse, _FP32, (B, H, L)), ("dq", dq, _ANY_FLOAT, (B, L, H, d)),
-                 ("dk", dk, (dq.dtype,), (B, L, H_kv, d)), ("dv", dv, (dq.dtype,), (B, L, H_kv, d)),
-                 ("cu_seqlens", cu_seqlens, _INT32, None), ("workspace", workspace, None, None)))
-    cu, n_seqs = _cu_seqlens(cu_seqlens)
-    flags = (RA_FLAG_O_BF16 if o.dtype == torch.bfloat16 else 0) | \
-        (RA_FLAG_GRAD_BF16 if dq.dtype == torch.bfloat16 else 0)
-    _check(lib().ra_window_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
-                                    lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu, n_seqs, B, L, H,
-                                    H_kv, d, window, sinks, scale, flags, workspace.data_ptr(), _nbytes(workspace),
-                                    _stream(stream)))
-
-
-def _pool(k_pages, v_pages):
-    """[n_pages, page, H_kv, d] views of one shape and page stride, each page without gaps."""
-    n_pages, page, H_kv, d = k_pages.shape
-    for name, x in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if x.dtype != torch.bfloat16:
-            raise TypeError("%s must be bf16, not %s" % (name, x.dtype))
-        if x.shape != k_pages.shape or x.device != k_pages.device:
-            raise ValueError("k_pages and v_pages must have one shape and device")
-        if not (x.is_contiguous() or x[:1].is_contiguous()) or x.stride(0) != k_pages.stride(0):
-            raise ValueError("%s: a page must be contiguous, and both pools have one page stride" % name)
-    return n_pages, page, H_kv, d, k_pages.stride(0) if n_pages > 1 else page * H_kv * d
-
-
-def _rows(name, x, heads, d):
-    """The token stride of a bf16 [T, heads, d] view whose tokens are contiguous."""
-    if x.dtype != torch.bfloat16:
-        raise TypeError("%s must be bf16, not %s" % (name, x.dtype))
-    if x.dim() != 3 or x.shape[1:] != (heads, d):
-        raise ValueError("%s must be [T, %d, %d], not %s" % (name, heads, d, list(x.shape)))
-    if not (x.is_contiguous() or x[:1].is_contiguous()):
-        raise ValueError("%s: a token's heads must be contiguous" % name)
-    return x.stride(0) if x.shape[0] > 1 else heads * d
+    _check((_native or native()).window_bwd(q, k, v, o, dout, lse, dq, dk, dv, B, L, H, H_kv, d, window, sinks, scale,
+                                            cu_seqlens, workspace, _raw_stream(stream)))
 
 
 def ra_paged_attn_workspace_bytes(T, n_seqs, H, H_kv, d, max_new, max_len, window=0, sinks=0):
@@ -389,39 +339,14 @@ def ra_paged_attn_fwd(q, k_pages, v_pages, block_table, seq_lens, cu_q, o, lse, 
     """Attention of the new tokens q [T, H, d] (tokens may be strided) over a paged cache [n_pages,
     page, H_kv, d] (pages may be strided), which holds their keys and values already; o [T, H, d]
     fp32 or bf16, lse [H, T] or None."""
-    T, H, d = q.shape
-    n_pages, page, H_kv, _, page_stride = _pool(k_pages, v_pages)
-    q_stride = _rows("q", q, H, k_pages.shape[3])
-    n_seqs, max_pages = block_table.shape
-    _tensors(q, (("block_table", block_table, _INT32, None), ("seq_lens", seq_lens, _INT32, (n_seqs,)),
-                 ("cu_q", cu_q, _INT32, (n_seqs + 1,)), ("o", o, _ANY_FLOAT, (T, H, d)), ("lse", lse, _FP32, (H, T)),
-                 ("workspace", workspace, None, None)))
-    if k_pages.device != q.device:
-        raise ValueError("the pages are on %s, not on %s" % (k_pages.device, q.device))
-    _check(lib().ra_paged_attn_fwd(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
-                                   seq_lens.data_ptr(), cu_q.data_ptr(), o.data_ptr(),
-                                   None if lse is None else lse.data_ptr(), T, n_seqs, H, H_kv, d, n_pages, page,
-                                   page_stride, max_pages, q_stride, max_new, max_len, window, sinks, scale,
-                                   RA_FLAG_O_BF16 if o.dtype == torch.bfloat16 else 0, workspace.data_ptr(),
-                                   _nbytes(workspace), _stream(stream)))
+    _check((_native or native()).paged_fwd(q, k_pages, v_pages, block_table, seq_lens, cu_q, o, lse, max_new, max_len,
+                                           window, sinks, scale, workspace, _raw_stream(stream)))
 
 
 def ra_paged_append(k_new, v_new, k_pages, v_pages, block_table, seq_lens, cu_new, workspace=None, stream=None):
     """Copy new keys and values [T, H_kv, d] (tokens may be strided) to their places in the cache."""
-    n_pages, page, H_kv, d, page_stride = _pool(k_pages, v_pages)
-    new_stride = _rows("k_new", k_new, H_kv, d)
-    T = k_new.shape[0]
-    if v_new.shape != k_new.shape or _rows("v_new", v_new, H_kv, d) != new_stride:
-        raise ValueError("k_new and v_new must have one shape and token stride")
-    n_seqs, max_pages = block_table.shape
-    _tensors(k_new, (("block_table", block_table, _INT32, None), ("seq_lens", seq_lens, _INT32, (n_seqs,)),
-                     ("cu_new", cu_new, _INT32, (n_seqs + 1,)), ("workspace", workspace, None, None)))
-    if v_new.device != k_new.device or k_pages.device != k_new.device:
-        raise ValueError("k_new, v_new and the pages must be on one device")
-    _check(lib().ra_paged_append(k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                                 block_table.data_ptr(), seq_lens.data_ptr(), cu_new.data_ptr(), T, n_seqs, H_kv, d,
-                                 n_pages, page, page_stride, max_pages, new_stride, workspace.data_ptr(),
-                                 _nbytes(workspace), _stream(stream)))
+    _check((_native or native()).append(k_new, v_new, k_pages, v_pages, block_table, seq_lens, cu_new, workspace,
+                                        _raw_stream(stream)))
 
 
 def ra_check_status(workspace, stream=None):

@@ -2,8 +2,9 @@
 
 Each CUDA translation unit is compiled in parallel, then linked into
 ``sequence_blockwise_softmax_gb300/_lib/libra_gb300.so`` with the CUDA runtime
-linked statically.  Rebuilds only when a source or header is newer than the
-library.
+linked statically.  Beside it g++ builds ``_lib/ra_torch.so``, the marshalling
+of torch tensors for the calls whose host time counts.  Rebuilds only when a
+source or header is newer than the libraries.
 """
 import concurrent.futures
 import glob
@@ -17,6 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libra_gb300.so")
+BINDING = os.path.join(OUT_DIR, "ra_torch.so")
+BINDING_SOURCE = os.path.join(CSRC, "torch_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
@@ -39,10 +42,34 @@ def _deps():
 
 
 def up_to_date():
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
     t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    header = os.path.join(ROOT, "include", "ra.h")
+    return all(os.path.getmtime(p) <= t for p in _deps()) and \
+        all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in (BINDING_SOURCE, header))
+
+
+def build_binding():
+    """Compile the torch binding against the installed torch's headers and libraries."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = BINDING + ".%d.tmp" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), BINDING_SOURCE, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s%s" % (BINDING_SOURCE, r.stdout, r.stderr))
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force=False, verbose=False, extra_flags=()):
@@ -64,8 +91,10 @@ def build(force=False, verbose=False, extra_flags=()):
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(sources()))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(9, len(sources()) + 1)) as ex:
+        binding = ex.submit(build_binding)
         objs = list(ex.map(compile_one, sources()))
+        binding.result()
     tmp = LIB + ".%d.tmp" % os.getpid()
     cmd = [exe, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
