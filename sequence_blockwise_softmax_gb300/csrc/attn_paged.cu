@@ -10,6 +10,7 @@
 #include <cmath>
 
 #include "attn_fwd_kernel.cuh"
+#include "paged_launch.h"
 #include "ra_tensor_map.h"
 
 namespace ra {
@@ -17,7 +18,11 @@ namespace {
 
 constexpr size_t kHeader = RA_WORKSPACE_MIN_BYTES;
 constexpr int kSms = 152;               // GB300; only the choice of a split depends on it
-constexpr size_t kPartBytes = 48u << 20;   // most bytes of a call's parts
+constexpr size_t kPartBytes = (64u << 20) - (16u << 10);   // most bytes of a call's parts
+// The few-row kernel's counters, in a place of their own: they are zero
+// between calls, whatever form the calls take.
+constexpr size_t kCounters = kHeader, kCounterBytes = 4096;
+static_assert(kPagedTokensCtas * 4 <= kCounterBytes, "one counter per CTA");
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -98,14 +103,29 @@ struct Paged {
 
 // How a call is cut: tokens per unit, the most parts per unit, the parts' bytes.
 struct Plan {
-    int tile_tokens, splits;
+    int tile_tokens, splits;    // the tensor-core form
     int64_t units;
+    bool tokens;                // the few-row form, with this many CTAs
+    int ctas;
     size_t part_o, part_lse, total;
 };
 
 Plan plan(const Paged &a) {
-    Plan p;
+    Plan p{};
     const int64_t group = a.H / a.H_kv;
+    const int64_t active0 = a.n_seqs < a.T ? a.n_seqs : a.T;
+    p.part_o = kCounters + kCounterBytes;
+    // Few rows per key/value head: bound by the cache's bytes (see attn_paged_tokens.cu)
+    if (a.max_new * group <= kPagedTokensRows) {
+        p.tokens = true;
+        int64_t seen = a.max_len;
+        if (a.window > 0 && a.window + a.max_new + a.sinks < seen) seen = a.window + a.max_new + a.sinks;
+        p.ctas = paged_tokens_ctas(active0 * a.H_kv, seen);
+        const size_t rows = (size_t)2 * p.ctas * (a.max_new * group <= 16 ? 16 : 32);
+        p.part_lse = p.part_o + round256(rows * a.d * 4);
+        p.total = p.part_lse + round256(rows * 8);
+        return p;
+    }
     p.tile_tokens = (int)(128 / group);
     const int unit = 2 * p.tile_tokens;
     p.units = paged_units(a.T, a.n_seqs, unit);
@@ -113,8 +133,8 @@ Plan plan(const Paged &a) {
     const size_t part = (size_t)p.units * a.H_kv * rows * (a.d + 1) * 4;     // one part of every unit
     // The time of s parts: waves of CTAs, about 7 us and 1.3 us per key tile
     // each, and the join's launch.
-    const int64_t full = (a.T + unit - 1) / unit, active = a.n_seqs < a.T ? a.n_seqs : a.T;
-    const int64_t ctas = (full > active ? full : active) * a.H_kv;
+    const int64_t full = (a.T + unit - 1) / unit;
+    const int64_t ctas = (full > active0 ? full : active0) * a.H_kv;
     int64_t keys = a.max_len;
     if (a.window > 0 && a.window + a.max_new + a.sinks < keys) keys = a.window + (a.max_new < unit ? a.max_new : unit) + a.sinks;
     const int64_t tiles = (keys + 127) / 128 + 1;
@@ -128,9 +148,7 @@ Plan plan(const Paged &a) {
             p.splits = s;
         }
     }
-    p.part_o = kHeader;
-    p.part_lse = p.part_o;
-    p.total = kHeader;
+    p.part_lse = p.total = p.part_o;
     if (p.splits > 1) {
         p.part_lse = p.part_o + round256((size_t)p.units * a.H_kv * p.splits * rows * a.d * 4);
         p.total = p.part_lse + round256((size_t)p.units * a.H_kv * p.splits * rows * 4);
@@ -241,6 +259,28 @@ ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, co
                        const void *k, const void *v, void *o, float *lse, bool o_bf16, uint8_t *workspace,
                        cudaStream_t stream) {
     const Plan p = plan(a);
+    const float scale_log2 = (a.scale > 0.f ? a.scale : 1.0f / std::sqrt((float)a.d)) * 1.4426950408889634f;
+    if (p.tokens) {
+        TokensLaunch t{};
+        t.seqs = sequences(a, table, seq_lens, cu_q);
+        t.seqs.unit_tokens = t.seqs.max_new;        // a sequence's tokens are one unit
+        t.q = q;
+        t.k = k;
+        t.v = v;
+        t.q_stride = a.q_stride;
+        t.page_stride = a.page_stride;
+        t.o = o;
+        t.lse = lse;
+        t.o_bf16 = o_bf16;
+        t.d = D;
+        t.ctas = p.ctas;
+        t.scale_log2 = scale_log2;
+        t.status = reinterpret_cast<unsigned *>(workspace);
+        t.counters = reinterpret_cast<int *>(workspace + kCounters);
+        t.part_o = reinterpret_cast<float *>(workspace + p.part_o);
+        t.part_ml = reinterpret_cast<float *>(workspace + p.part_lse);
+        return launch_paged_tokens(t, stream);
+    }
     AttnArgs args{};
     args.o = o;
     args.lse = lse;
@@ -248,7 +288,7 @@ ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, co
     args.B = args.H = args.N = 1;
     args.layout = RA_CONTIGUOUS;
     args.causal = 1;
-    args.scale_log2 = (a.scale > 0.f ? a.scale : 1.0f / std::sqrt((float)a.d)) * 1.4426950408889634f;
+    args.scale_log2 = scale_log2;
     args.num_q_ranks = 1;
     args.q_rank_fixed = args.kv_rank_fixed = -1;
     args.num_steps = 1;

@@ -1,0 +1,502 @@
+// attn_paged_tokens.cu -- paged attention of few rows: single tokens, or a few
+// tokens of each sequence, up to 32 rows (tokens x query heads) per key/value
+// head.
+//
+// Bound by the cache's bytes: each key and value is used by a handful of rows,
+// so the kernel is a stream of loads with small products beside it.  The work
+// is one flat list of 16-key chunks -- sequence by sequence, key/value head by
+// head, key by key -- cut into equal runs, one per CTA (two CTAs per SM): a
+// batch of very different lengths leaves no CTA with more than its share, and
+// one long sequence is spread over the whole GPU.  A CTA's run may begin and
+// end inside a head's keys; such pieces leave O (unnormalised, fp32), the
+// reference and the sum of exponentials in the workspace, and the CTA that
+// counts the last piece of a head adds them in the order of their keys, so the
+// result does not depend on which one it is.
+//
+// Inside a run the four warps take the chunks in turn and share nothing until
+// the end of a head: each has its own ring of cp.async stages (96 KB per CTA in
+// flight), its own m, l and O.  mma.sync m16n8k16 with the rows padded to 16:
+// at 6.8 TB/s an SM sees a chunk (8 KB at d = 128) every 0.18 us and needs 48
+// such products for it, a few per cent of the pipe, so the tensor pipe is not
+// what bounds this; 128-row tcgen05 tiles would spend their time on padding.
+// P enters its product as the sum of two bf16 values (about 16 bits), which
+// costs a second product and leaves the output's own rounding as the only one.
+//
+// Measured on a GB300 (64 sequences of 200-16000 keys, 32 / 8 heads, d = 128):
+// see the design doc's table of the operators.
+#include <cmath>
+
+#include "paged_launch.h"
+#include "ra_device.cuh"
+#include "ra_paged.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kChunk = kPagedChunk;
+constexpr int kMinRun = 16;         // chunks: below it a CTA's start and join cost more than its share saves
+
+struct TokensArgs {
+    PagedSeqs seqs;
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, page_stride;  // elements
+    void *o;
+    float *lse;
+    int o_bf16;
+    float scale_log2;
+    unsigned *status;
+    int *counters;                  // one per CTA, zero between calls
+    float *part_o, *part_ml;        // [2 * CTAs, 16 * MT, d], [2 * CTAs, 16 * MT, 2]
+};
+
+template <int D>
+struct TokensSmem {
+    static constexpr int kStages = 384 / D;                       // 3 at d = 128, 6 at d = 64
+    static constexpr uint32_t kHalf = kChunk * D * 2;             // a chunk's keys; its values follow
+    static constexpr uint32_t kStage = 2 * kHalf;
+    static constexpr uint32_t kWarp = kStages * kStage;
+    static constexpr uint32_t kBytes = kWarps * kWarp;            // 96 KB
+    static constexpr int kRow = D + 8;                            // floats per row of the warps' O at the end
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const TokensArgs a) {
+    using L = TokensSmem<D>;
+    constexpr int NS = L::kStages, KS = D / 16, CPR = D / 8;   // k-steps, 16-byte pieces per row
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long s_sum[kWarps];
+    __shared__ long long s_at;                 // the run's first chunk inside its sequence
+    __shared__ int s_seq, s_last;
+    __shared__ float s_m[kWarps][16 * MT], s_l[kWarps][16 * MT];
+    const PagedSeqs &sq = a.seqs;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cta = blockIdx.x;
+
+    // ---- the flat list's length, and where this CTA's run starts
+    long long mine = 0;
+    for (int s = threadIdx.x; s < sq.n_seqs; s += blockDim.x) mine += paged_chunks(sq, s).count;
+    long long sum = mine;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += s_sum[w];
+    total *= sq.Hkv;
+    long long per = (total + gridDim.x - 1) / gridDim.x;
+    if (per < kMinRun) per = kMinRun;
+    long long pos = (long long)cta * per;
+    const long long end = pos + per < total ? pos + per : total;
+    if (cta == 0) {
+        for (int s = threadIdx.x; s < sq.n_seqs; s += blockDim.x)
+            if (paged_bad_counts(sq, s)) atomicOr(a.status, RA_DEV_PAGE_BIT);
+    }
+    if (pos >= end) return;
+    long long base = 0;
+    for (int s0 = 0; s0 < sq.n_seqs; s0 += blockDim.x) {
+        const int s = s0 + threadIdx.x;
+        const long long c = s < sq.n_seqs ? (long long)paged_chunks(sq, s).count * sq.Hkv : 0;
+        long long inc = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += up;
+        }
+        __syncthreads();
+        if (lane == 31) s_sum[warp] = inc;
+        __syncthreads();
+        long long before = base;
+        for (int w = 0; w < warp; ++w) before += s_sum[w];
+        inc += before;
+        if (c > 0 && inc - c <= pos && pos < inc) {
+            s_seq = s;
+            s_at = pos - (inc - c);
+        }
+        for (int w = 0; w < kWarps; ++w) base += s_sum[w];
+        if (base > pos) break;
+    }
+    __syncthreads();
+    int seq = s_seq;
+    PagedChunks cl = paged_chunks(sq, seq);
+    int hk = (int)(s_at / cl.count);
+    int c_at = (int)(s_at - (long long)hk * cl.count);
+
+    const uint32_t ring = smem_u32(smem) + warp * L::kWarp;
+    const int g = lane >> 2, t4 = lane & 3;
+
+    // ---- one head's keys (or this run's part of them) after another
+    while (pos < end) {
+        const long long unit_begin = pos - c_at, unit_end = unit_begin + cl.count;
+        const int c_end = (int)(unit_end < end ? cl.count : end - unit_begin);
+        const int rows = cl.n * sq.group;
+
+        // Q fragments, straight from global memory; rows past the unit's are zero
+        uint32_t qf[MT][KS][4];
+        RowKeys keys[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = mt * 16 + h * 8 + g;
+                const bool live = r < rows;
+                const int tok = live ? r / sq.group : 0, head = live ? r - tok * sq.group : 0;
+                keys[mt][h] = paged_row(sq, cl.p0 + (live ? tok : cl.n - 1));
+                const uint16_t *src = a.q + (size_t)(cl.t0 + tok) * a.q_stride + (size_t)(hk * sq.group + head) * D + 2 * t4;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    qf[mt][ks][h] = live ? *reinterpret_cast<const uint32_t *>(src + ks * 16) : 0u;
+                    qf[mt][ks][2 + h] = live ? *reinterpret_cast<const uint32_t *>(src + ks * 16 + 8) : 0u;
+                }
+            }
+        // chunks inside [all_lo, all_hi) or [0, all_shi) are seen whole by every row
+        const RowKeys first = paged_row(sq, cl.p0), last = paged_row(sq, cl.p0 + cl.n - 1);
+        const int all_lo = last.lo, all_hi = first.hi, all_shi = first.shi > first.slo ? first.shi : 0;
+
+        float acc[MT][D / 8][4];
+        float m[MT][2], l[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[mt][n][e] = 0.f;
+            m[mt][0] = m[mt][1] = -INFINITY;
+            l[mt][0] = l[mt][1] = 0.f;
+        }
+
+        auto key_of = [&](int c) { return paged_chunk_key(cl, c); };
+        const int *row_table = sq.table + (size_t)seq * sq.max_pages;
+        auto page_of = [&](int c) -> int {
+            const int k0 = key_of(c);
+            return c < c_end && k0 < cl.len ? row_table[k0 / sq.page] : 0;
+        };
+        // load chunk c (of page id) into its stage; every call commits one group
+        auto load = [&](int c, int stage, int id) {
+            if (c < c_end) {
+                const int k0 = key_of(c);
+                bool ok = k0 < cl.len;
+                if (ok && (unsigned)id >= (unsigned)sq.n_pages) {
+                    ok = false;
+                    if (lane == 0) atomicOr(a.status, RA_DEV_PAGE_BIT);
+                }
+                const size_t off = ok ? (size_t)id * a.page_stride + ((size_t)(k0 & (sq.page - 1)) * sq.Hkv + hk) * D : 0;
+                const uint32_t dst = ring + stage * L::kStage;
+                constexpr int ROWS = 32 / CPR;       // keys per pass of the warp
+                const int key = lane / CPR, pc = lane % CPR;
+#pragma unroll
+                for (int i = 0; i < kChunk / ROWS; ++i) {
+                    const int kk = i * ROWS + key;
+                    const bool in = ok && k0 + kk < cl.len;
+                    const size_t at = in ? off + (size_t)kk * sq.Hkv * D + pc * 8 : 0;
+                    const uint32_t to = dst + kk * (D * 2) + ((pc ^ (kk & 7)) << 4);
+                    cp_async16(to, a.k + at, in);
+                    cp_async16(to + L::kHalf, a.v + at, in);
+                }
+            }
+            cp_async_commit();
+        };
+
+        int c = c_at + warp;
+        int next_id = page_of(c);
+#pragma unroll
+        for (int s = 0; s < NS - 1; ++s) {
+            const int id = next_id;
+            next_id = page_of(c + (s + 1) * kWarps);
+            load(c + s * kWarps, s, id);
+        }
+        int stage = 0;
+        for (; c < c_end; c += kWarps) {
+            cp_async_wait<NS - 2>();
+            __syncwarp();
+            {
+                const int id = next_id;
+                next_id = page_of(c + NS * kWarps);
+                load(c + (NS - 1) * kWarps, stage == 0 ? NS - 1 : stage - 1, id);
+            }
+            const uint32_t sk = ring + stage * L::kStage, sv = sk + L::kHalf;
+            const int k0 = key_of(c);
+            // S: 16 rows x 16 keys per row tile
+            float sc[MT][2][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.f;
+            {
+                // matrices: keys 0-7 / 8-15 by d 0-7 / 8-15 of the k-step
+                const int kk = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+                const uint32_t row = sk + kk * (D * 2);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    uint32_t b[4];
+                    ldmatrix4(b, row + (((ks * 2 + half) ^ (kk & 7)) << 4));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        mma16816(sc[mt][0], qf[mt][ks], b[0], b[1]);
+                        mma16816(sc[mt][1], qf[mt][ks], b[2], b[3]);
+                    }
+                }
+            }
+            const bool whole = (k0 >= all_lo && k0 + kChunk <= all_hi) || k0 + kChunk <= all_shi;
+            bool raise = false;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = sc[mt][n][e] * a.scale_log2;
+                        if (!whole) {
+                            const RowKeys &rk = keys[mt][e >> 1];
+                            const int key = k0 + n * 8 + 2 * t4 + (e & 1);
+                            if (!((key >= rk.lo && key < rk.hi) || (key >= rk.slo && key < rk.shi))) x = -INFINITY;
+                        }
+                        sc[mt][n][e] = x;
+                        raise = raise || x > m[mt][e >> 1] + 8.f;
+                    }
+            // The reference m of a row moves only when a score passes it by
+            // 2^8 (at the row's first key, then rarely): exponentials stay
+            // below 2^8 and their sums far inside 32 bits.
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float x = fmaxf(fmaxf(sc[mt][0][2 * h], sc[mt][0][2 * h + 1]),
+                                        fmaxf(sc[mt][1][2 * h], sc[mt][1][2 * h + 1]));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                        const float m_new = fmaxf(m[mt][h], x);
+                        const float f = m[mt][h] > -INFINITY ? ex2(m[mt][h] - m_new) : 0.f;
+                        m[mt][h] = m_new;
+                        l[mt][h] *= f;
+#pragma unroll
+                        for (int n = 0; n < D / 8; ++n) {
+                            acc[mt][n][2 * h] *= f;
+                            acc[mt][n][2 * h + 1] *= f;
+                        }
+                    }
+            }
+            uint32_t hi[MT][4], lo[MT][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float ref = m[mt][h] > -INFINITY ? m[mt][h] : 0.f;
+                        const float p0 = ex2(sc[mt][n][2 * h] - ref), p1 = ex2(sc[mt][n][2 * h + 1] - ref);
+                        l[mt][h] += p0 + p1;
+                        const uint32_t top = pack_bf16x2(p0, p1);
+                        hi[mt][2 * n + h] = top;
+                        lo[mt][2 * n + h] = pack_bf16x2(p0 - __uint_as_float(top << 16),
+                                                        p1 - __uint_as_float(top & 0xffff0000u));
+                    }
+            {
+                // matrices: keys 0-7 / 8-15 by d 0-7 / 8-15 of a pair of column tiles
+                const int kk = (lane & 7) + (((lane >> 3) & 1) << 3), half = lane >> 4;
+                const uint32_t row = sv + kk * (D * 2);
+#pragma unroll
+                for (int n = 0; n < D / 16; ++n) {
+                    uint32_t b[4];
+                    ldmatrix4_trans(b, row + (((n * 2 + half) ^ (kk & 7)) << 4));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        mma16816(acc[mt][2 * n], hi[mt], b[0], b[1]);
+                        mma16816(acc[mt][2 * n + 1], hi[mt], b[2], b[3]);
+                        mma16816(acc[mt][2 * n], lo[mt], b[0], b[1]);
+                        mma16816(acc[mt][2 * n + 1], lo[mt], b[2], b[3]);
+                    }
+                }
+            }
+            __syncwarp();
+            stage = stage + 1 == NS ? 0 : stage + 1;
+        }
+        cp_async_wait<0>();
+        // ---- the four warps' rows become one
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 1);
+                l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 2);
+                if (t4 == 0) {
+                    s_m[warp][mt * 16 + h * 8 + g] = m[mt][h];
+                    s_l[warp][mt * 16 + h * 8 + g] = l[mt][h];
+                }
+            }
+        __syncthreads();     // every warp is past its ring too
+        float *warp_o = reinterpret_cast<float *>(smem);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = mt * 16 + h * 8 + g;
+                const float top = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+                const float f = m[mt][h] > -INFINITY ? ex2(m[mt][h] - top) : 0.f;
+                float *dst = warp_o + ((size_t)warp * 16 * MT + r) * L::kRow + 2 * t4;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+                    *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(acc[mt][n][2 * h] * f, acc[mt][n][2 * h + 1] * f);
+            }
+        __syncthreads();
+        const bool begins = c_at == 0, ends = c_end == cl.count;
+        const int first_cta = (int)(unit_begin / per), last_cta = (int)((unit_end - 1) / per);
+        auto store = [&](int r, int col, const float (&x)[4], float inv) {
+            const int tok = r / sq.group, head = hk * sq.group + r - tok * sq.group;
+            const size_t at = ((size_t)(cl.t0 + tok) * sq.H + head) * D + col;
+            if (a.o_bf16)
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + at) =
+                    make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+            else
+                *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + at) =
+                    make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+        };
+        auto store_lse = [&](int r, float top, float lsum) {
+            const int tok = r / sq.group, head = hk * sq.group + r - tok * sq.group;
+            if (a.lse)
+                a.lse[(size_t)head * sq.T + cl.t0 + tok] = lsum > 0.f ? (top + lg2(lsum)) * 0.6931471805599453f : -INFINITY;
+        };
+        const size_t slot = (size_t)cta * 2 + (begins ? 1 : 0);
+        for (int e = threadIdx.x; e < rows * (D / 4); e += blockDim.x) {
+            const int r = e / (D / 4), col = (e % (D / 4)) * 4;
+            float x[4] = {};
+            float top = -INFINITY, lsum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float4 f = *reinterpret_cast<const float4 *>(warp_o + ((size_t)w * 16 * MT + r) * L::kRow + col);
+                x[0] += f.x, x[1] += f.y, x[2] += f.z, x[3] += f.w;
+                top = fmaxf(top, s_m[w][r]);
+            }
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) lsum += s_m[w][r] > -INFINITY ? s_l[w][r] * ex2(s_m[w][r] - top) : 0.f;
+            if (begins && ends) {
+                store(r, col, x, lsum > 0.f ? 1.f / lsum : 0.f);
+                if (col == 0) store_lse(r, top, lsum);
+            } else {
+                *reinterpret_cast<float4 *>(a.part_o + (slot * 16 * MT + r) * D + col) = make_float4(x[0], x[1], x[2], x[3]);
+                if (col == 0)
+                    *reinterpret_cast<float2 *>(a.part_ml + (slot * 16 * MT + r) * 2) = make_float2(top, lsum);
+            }
+        }
+        if (!(begins && ends)) {
+            // the head's last piece to arrive joins them, in order
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                const int n = atomicAdd(a.counters + first_cta, 1);
+                s_last = n == last_cta - first_cta;
+                if (s_last) a.counters[first_cta] = 0;
+            }
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                for (int e = threadIdx.x; e < rows * (D / 4); e += blockDim.x) {
+                    const int r = e / (D / 4), col = (e % (D / 4)) * 4;
+                    float x[4] = {};
+                    float top = -INFINITY, lsum = 0.f;
+                    for (int p = first_cta; p <= last_cta; ++p) {
+                        const size_t at = ((size_t)p * 2 + (p == first_cta ? 1 : 0)) * 16 * MT + r;
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + at * 2));
+                        const float4 f = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * D + col));
+                        if (!(ml.x > -INFINITY)) continue;
+                        const float t2 = fmaxf(top, ml.x);
+                        const float old = top > -INFINITY ? ex2(top - t2) : 0.f, now = ex2(ml.x - t2);
+                        x[0] = x[0] * old + f.x * now;
+                        x[1] = x[1] * old + f.y * now;
+                        x[2] = x[2] * old + f.z * now;
+                        x[3] = x[3] * old + f.w * now;
+                        lsum = lsum * old + ml.y * now;
+                        top = t2;
+                    }
+                    store(r, col, x, lsum > 0.f ? 1.f / lsum : 0.f);
+                    if (col == 0) store_lse(r, top, lsum);
+                }
+            }
+        }
+        __syncthreads();     // the rows in shared memory have been read
+        // ---- the next head, or the next sequence with new tokens
+        pos = unit_begin + c_end;
+        c_at = 0;
+        if (pos < end && ++hk == sq.Hkv) {
+            hk = 0;
+            do cl = paged_chunks(sq, ++seq);
+            while (cl.count == 0);
+        }
+    }
+}
+
+template <int D, int MT>
+ra_status launch(const TokensLaunch &t, const TokensArgs &args, cudaStream_t stream) {
+    auto kern = paged_tokens_kernel<D, MT>;
+    const int smem = (int)TokensSmem<D>::kBytes;
+    static_assert(kWarps * 16 * MT * TokensSmem<D>::kRow * 4 <= TokensSmem<D>::kBytes, "the warps' rows fit in the rings");
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
+    kern<<<(unsigned)t.ctas, 32 * kWarps, smem, stream>>>(args);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
+}
+
+}  // namespace
+
+int paged_tokens_ctas(int64_t pairs, int64_t keys) {
+    const int64_t chunks = pairs * ((keys + kChunk - 1) / kChunk + 1);
+    const int64_t n = (chunks + kMinRun - 1) / kMinRun;
+    return (int)(n < 1 ? 1 : n > kPagedTokensCtas ? kPagedTokensCtas : n);
+}
+
+ra_status launch_paged_tokens(const TokensLaunch &t, cudaStream_t stream) {
+    TokensArgs a{};
+    a.seqs = t.seqs;
+    a.q = static_cast<const uint16_t *>(t.q);
+    a.k = static_cast<const uint16_t *>(t.k);
+    a.v = static_cast<const uint16_t *>(t.v);
+    a.q_stride = t.q_stride;
+    a.page_stride = t.page_stride;
+    a.o = t.o;
+    a.lse = t.lse;
+    a.o_bf16 = t.o_bf16;
+    a.scale_log2 = t.scale_log2;
+    a.status = t.status;
+    a.counters = t.counters;
+    a.part_o = t.part_o;
+    a.part_ml = t.part_ml;
+    const int rows = t.seqs.max_new * t.seqs.group;
+    if (t.d == 128) return rows <= 16 ? launch<128, 1>(t, a, stream) : launch<128, 2>(t, a, stream);
+    return rows <= 16 ? launch<64, 1>(t, a, stream) : launch<64, 2>(t, a, stream);
+}
+
+}  // namespace ra

@@ -1,0 +1,33 @@
+// paged_launch.h -- the launch of paged attention's few-row form, shared
+// between its kernel (attn_paged_tokens.cu) and the entry point
+// (attn_paged.cu).
+#pragma once
+#include "ra_internal.h"
+#include "ra_paged.cuh"
+
+namespace ra {
+
+constexpr int kPagedTokensRows = 32;        // most rows (new tokens x query heads) per key/value head
+constexpr int kPagedTokensCtas = 2 * 152;   // two resident CTAs on each SM of a GB300
+
+struct TokensLaunch {
+    PagedSeqs seqs;
+    const void *q, *k, *v;
+    int64_t q_stride, page_stride;
+    void *o;
+    float *lse;
+    bool o_bf16;
+    int d, ctas;
+    float scale_log2;
+    unsigned *status;
+    int *counters;              // kPagedTokensCtas, zero between calls
+    float *part_o, *part_ml;    // [2 * ctas, rows up to 16 or 32, d], [.., 2]
+};
+
+// CTAs for `pairs` (sequence, key/value head) pairs of up to `keys` keys: the
+// grid, not the split, which the kernel takes from the lengths it finds.
+int paged_tokens_ctas(int64_t pairs, int64_t keys);
+
+ra_status launch_paged_tokens(const TokensLaunch &t, cudaStream_t stream);
+
+}  // namespace ra

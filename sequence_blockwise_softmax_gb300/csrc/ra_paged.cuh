@@ -117,4 +117,40 @@ RA_HD bool paged_needed(const RowKeys &first, int last_hi, int len, int k0, int 
     return (k0 < last_hi && k0 + n > first.lo) || (k0 < first.shi && k0 + n > first.slo);
 }
 
+constexpr int kPagedChunk = 16;
+
+// The few-row form (attn_paged_tokens.cu): the 16-key chunks of sequence s's keys that its new tokens see, in order:
+// n_sink chunks from 0 on, then chunks from m0 on.  A sequence with new tokens
+// that see nothing keeps one (masked) chunk, so that its rows are written.
+struct PagedChunks {
+    int n_sink, m0, count;
+    int t0, n, p0, len;      // its new tokens, their first position, its length
+};
+RA_HD PagedChunks paged_chunks(const PagedSeqs &q, int s) {
+    PagedChunks c;
+    const PagedUnit u = paged_unit(q, s, 0);
+    c.t0 = u.t0;
+    c.n = u.n;
+    c.p0 = u.p0;
+    c.len = u.len;
+    c.n_sink = c.m0 = c.count = 0;
+    if (u.n <= 0) return c;
+    const RowKeys first = paged_row(q, u.p0);
+    const int last = u.p0 + u.n;
+    c.m0 = first.lo / kPagedChunk;
+    const int m1 = (last + kPagedChunk - 1) / kPagedChunk;
+    if (first.shi > first.slo) {
+        const int s1 = (first.shi + kPagedChunk - 1) / kPagedChunk;
+        c.n_sink = s1 < c.m0 ? s1 : c.m0;
+    }
+    c.count = c.n_sink + (m1 > c.m0 ? m1 - c.m0 : 0);
+    if (c.count == 0) c.count = 1;
+    return c;
+}
+
+// The first key of chunk number c.
+RA_HD int paged_chunk_key(const PagedChunks &l, int c) {
+    return (c < l.n_sink ? c : l.m0 + (c - l.n_sink)) * kPagedChunk;
+}
+
 }  // namespace ra

@@ -70,4 +70,40 @@ int ra_test_paged(const int *seq_lens, const int *cu_q, int n_seqs, int T, int m
     }
     return 0;
 }
+
+// The same for the few-row form's chunks.
+int ra_test_paged_chunks(const int *seq_lens, const int *cu_q, int n_seqs, int T, int max_pages, int page, int max_new,
+                         int window, int sinks, int *cnt) {
+    ra::PagedSeqs q{};
+    q.seq_lens = seq_lens;
+    q.cu_q = cu_q;
+    q.n_seqs = n_seqs;
+    q.T = T;
+    q.max_pages = max_pages;
+    q.page = page;
+    q.H = q.Hkv = q.group = 1;
+    q.max_new = q.unit_tokens = max_new;
+    q.window = window;
+    q.sinks = sinks;
+    const size_t cap = (size_t)max_pages * page;
+    for (int s = 0; s < n_seqs; ++s) {
+        const ra::PagedChunks l = ra::paged_chunks(q, s);
+        if ((l.n > 0) != (l.count > 0)) return 1;
+        if (l.n > 0 && (l.t0 < 0 || l.t0 + l.n > T)) return 2;
+        for (int c = 0; c < l.count; ++c) {
+            const int k0 = ra::paged_chunk_key(l, c);
+            if (k0 < 0 || k0 % ra::kPagedChunk) return 3;
+            if (c > 0 && k0 <= ra::paged_chunk_key(l, c - 1)) return 4;
+            for (int i = 0; i < l.n; ++i) {
+                const ra::RowKeys r = ra::paged_row(q, l.p0 + i);
+                for (int k = k0; k < k0 + ra::kPagedChunk; ++k)
+                    if ((k >= r.lo && k < r.hi) || (k >= r.slo && k < r.shi)) {
+                        if (k >= l.len || (size_t)k >= cap) return 5;
+                        ++cnt[(size_t)(l.t0 + i) * cap + k];
+                    }
+            }
+        }
+    }
+    return 0;
+}
 }

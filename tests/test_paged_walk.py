@@ -67,6 +67,9 @@ def test_every_pair_once(probe, new, lens, page, max_pages, group, unit, window,
         if new[s] and window and length > 4 * (window + unit + sinks + page + 256):
             assert loaded[s].sum() < held
     assert np.array_equal(cnt, want)
+    cnt[:] = 0
+    assert probe.ra_test_paged_chunks(p(sl), p(cu), n, T, max_pages, page, max(new), window, sinks, p(cnt)) == 0
+    assert np.array_equal(cnt, want)
     if splits > 1 and max(min(x, cap, window or cap) for x in lens) >= 1536:
         assert seen.value > 1
 
@@ -85,6 +88,7 @@ def test_bad_boundaries_stay_inside(probe):
         assert probe.ra_test_paged(p(sl), p(cu), n, T, max_pages, page, 4, 1, 64, int(rng.randint(1, 300)),
                                    int(rng.randint(0, 200)), int(rng.randint(0, 200)), 4, p(cnt), p(loaded),
                                    ctypes.byref(seen)) == 0
+        assert probe.ra_test_paged_chunks(p(sl), p(cu), n, T, max_pages, page, int(rng.randint(1, 300)), 50, 20, p(cnt)) == 0
 
 
 FAKE = 0x10000
