@@ -7,11 +7,13 @@
 // is one flat list of 16-key chunks -- sequence by sequence, key/value head by
 // head, key by key -- cut into equal runs, one per CTA (two CTAs per SM): a
 // batch of very different lengths leaves no CTA with more than its share, and
-// one long sequence is spread over the whole GPU.  A CTA's run may begin and
-// end inside a head's keys; such pieces leave O (unnormalised, fp32), the
-// reference and the sum of exponentials in the workspace, and the CTA that
-// counts the last piece of a head adds them in the order of their keys, so the
-// result does not depend on which one it is.
+// one long sequence is spread over the whole GPU.  With few (sequence, head)
+// pairs each pair is cut into pieces of its own instead, so that no CTA meets
+// two of them and pays the end of a pair (about 3 us) twice.  A piece that is
+// not a whole pair leaves O (unnormalised, fp32), the reference and the sum of
+// exponentials in the workspace, and the CTA that counts the last piece of a
+// pair adds them in the order of their keys, so the result does not depend on
+// which one it is.
 //
 // Inside a run the four warps take the chunks in turn and share nothing until
 // the end of a head: each has its own ring of cp.async stages (96 KB per CTA in
@@ -25,6 +27,7 @@
 // Measured on a GB300 (64 sequences of 200-16000 keys, 32 / 8 heads, d = 128):
 // see the design doc's table of the operators.
 #include <cmath>
+#include <type_traits>
 
 #include "paged_launch.h"
 #include "ra_device.cuh"
@@ -35,7 +38,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kChunk = kPagedChunk;
-constexpr int kMinRun = 16;         // chunks: below it a CTA's start and join cost more than its share saves
+constexpr int kWholeKeys = 1024;    // many pairs of at most so many keys: one CTA each, no pieces
+constexpr int kMinRun = 4;          // chunks of a piece at least: one per warp
 
 struct TokensArgs {
     PagedSeqs seqs;
@@ -43,7 +47,7 @@ struct TokensArgs {
     int64_t q_stride, page_stride;  // elements
     void *o;
     float *lse;
-    int o_bf16;
+    int o_bf16, whole_pairs;
     float scale_log2;
     unsigned *status;
     int *counters;                  // one per CTA, zero between calls
@@ -95,39 +99,18 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
     constexpr int NS = L::kStages, KS = D / 16, CPR = D / 8;   // k-steps, 16-byte pieces per row
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long s_sum[kWarps];
-    __shared__ long long s_at;                 // the run's first chunk inside its sequence
+    __shared__ long long s_at;                 // the first chunk (or piece) inside its sequence
+    __shared__ PagedChunks s_list;
     __shared__ int s_seq, s_last;
     __shared__ float s_m[kWarps][16 * MT], s_l[kWarps][16 * MT];
     const PagedSeqs &sq = a.seqs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
 
-    // ---- the flat list's length, and where this CTA's run starts
-    long long mine = 0;
-    for (int s = threadIdx.x; s < sq.n_seqs; s += blockDim.x) mine += paged_chunks(sq, s).count;
-    long long sum = mine;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) s_sum[warp] = sum;
-    __syncthreads();
-    long long total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += s_sum[w];
-    total *= sq.Hkv;
-    long long per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < kMinRun) per = kMinRun;
-    long long pos = (long long)cta * per;
-    const long long end = pos + per < total ? pos + per : total;
-    if (cta == 0) {
-        for (int s = threadIdx.x; s < sq.n_seqs; s += blockDim.x)
-            if (paged_bad_counts(sq, s)) atomicOr(a.status, RA_DEV_PAGE_BIT);
-    }
-    if (pos >= end) return;
-    long long base = 0;
-    for (int s0 = 0; s0 < sq.n_seqs; s0 += blockDim.x) {
-        const int s = s0 + threadIdx.x;
-        const long long c = s < sq.n_seqs ? (long long)paged_chunks(sq, s).count * sq.Hkv : 0;
-        long long inc = c;
+    // ---- how the work is cut, from the lengths the call finds
+    // An inclusive scan of x over the block (its total added to `base`).
+    auto scan = [&](long long x, long long &base) -> long long {
+        long long inc = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long up = __shfl_up_sync(0xffffffffu, inc, o);
@@ -136,49 +119,83 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
         __syncthreads();
         if (lane == 31) s_sum[warp] = inc;
         __syncthreads();
-        long long before = base;
-        for (int w = 0; w < warp; ++w) before += s_sum[w];
-        inc += before;
-        if (c > 0 && inc - c <= pos && pos < inc) {
-            s_seq = s;
-            s_at = pos - (inc - c);
+        inc += base;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) inc += s_sum[w];
+            base += s_sum[w];
         }
-        for (int w = 0; w < kWarps; ++w) base += s_sum[w];
-        if (base > pos) break;
+        return inc;
+    };
+    const int blocks = (sq.n_seqs + blockDim.x - 1) / blockDim.x;    // of sequences, one to a thread
+    const PagedChunks none{};
+    auto list_of = [&](int s) { return s < sq.n_seqs ? paged_chunks(sq, s) : none; };
+    PagedChunks mine = list_of(threadIdx.x);
+    // total chunks, and (sequence, head) pairs with new tokens in the high half
+    long long total = 0;
+    for (int i = 0; i < blocks; ++i) {
+        const PagedChunks l = i == 0 ? mine : list_of(i * blockDim.x + threadIdx.x);
+        scan(l.count + (l.count > 0 ? 1ll << 40 : 0ll), total);
+    }
+    const long long pairs = (total >> 40) * sq.Hkv;
+    total = (total & ((1ll << 40) - 1)) * sq.Hkv;
+    const int grid = gridDim.x;
+    // Few pairs: each is cut into pieces of its own, at most one to a CTA.
+    // Many: equal runs of the flat list, whose ends fall anywhere.
+    const bool flat = !a.whole_pairs && pairs * 2 > grid;
+    const long long room = flat ? grid : max(grid - pairs, 1ll);
+    const long long per64 = total < 0x7fffffff ? (long long)(((unsigned)total + (unsigned)room - 1) / (unsigned)room)
+                                               : (total + room - 1) / room;
+    // A piece of n chunks costs its CTA about 0.09 n us, each piece its pair's
+    // join about 0.07 us: n is at least the square root that balances them.
+    const int balanced = (int)sqrtf(0.8f * (float)total / (float)(pairs > 0 ? pairs : 1));
+    int per = max((int)per64, max(balanced, kMinRun));
+    if (a.whole_pairs) per = 0x3fffffff;       // one CTA to a pair
+    if (cta == 0) {
+        for (int s = threadIdx.x; s < sq.n_seqs; s += blockDim.x)
+            if (paged_bad_counts(sq, s)) atomicOr(a.status, RA_DEV_PAGE_BIT);
+    }
+    // where this CTA begins: chunk (or piece) number `at` of the list
+    const long long at = flat ? (long long)cta * per : cta;
+    {
+        long long base = 0;
+        for (int i = 0; i < blocks; ++i) {
+            if (i > 0) mine = list_of(i * blockDim.x + threadIdx.x);
+            const long long n = (long long)(flat ? mine.count : (mine.count + per - 1) / per) * sq.Hkv;
+            const long long inc = scan(n, base);
+            if (n > 0 && inc - n <= at && at < inc) {
+                s_seq = i * blockDim.x + threadIdx.x;
+                s_list = mine;
+                s_at = at - (inc - n);
+            }
+            if (base > at) break;
+        }
+        if (at >= base) return;
     }
     __syncthreads();
     int seq = s_seq;
-    PagedChunks cl = paged_chunks(sq, seq);
-    int hk = (int)(s_at / cl.count);
-    int c_at = (int)(s_at - (long long)hk * cl.count);
+    PagedChunks cl = s_list;
+    int hk, c_at, first_cta = 0, last_cta = 0;
+    long long pos = at;
+    const long long end = at + per < total ? at + per : total;    // of a flat run
+    {
+        const unsigned each = flat ? cl.count : (cl.count + per - 1) / per;
+        hk = s_at < 0x7fffffff ? (int)((unsigned)s_at / each) : (int)(s_at / each);
+        const int in = (int)(s_at - (long long)hk * each);
+        c_at = flat ? in : in * per;
+        first_cta = cta - in;             // of a pair in pieces
+        last_cta = first_cta + (int)each - 1;
+    }
 
     const uint32_t ring = smem_u32(smem) + warp * L::kWarp;
     const int g = lane >> 2, t4 = lane & 3;
 
     // ---- one head's keys (or this run's part of them) after another
-    while (pos < end) {
+    while (true) {
         const long long unit_begin = pos - c_at, unit_end = unit_begin + cl.count;
-        const int c_end = (int)(unit_end < end ? cl.count : end - unit_begin);
+        const int c_end = flat ? (int)(unit_end < end ? cl.count : end - unit_begin) : (int)min((long long)cl.count, (long long)c_at + per);
         const int rows = cl.n * sq.group;
 
-        // Q fragments, straight from global memory; rows past the unit's are zero
-        uint32_t qf[MT][KS][4];
-        RowKeys keys[MT][2];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = mt * 16 + h * 8 + g;
-                const bool live = r < rows;
-                const int tok = live ? r / sq.group : 0, head = live ? r - tok * sq.group : 0;
-                keys[mt][h] = paged_row(sq, cl.p0 + (live ? tok : cl.n - 1));
-                const uint16_t *src = a.q + (size_t)(cl.t0 + tok) * a.q_stride + (size_t)(hk * sq.group + head) * D + 2 * t4;
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    qf[mt][ks][h] = live ? *reinterpret_cast<const uint32_t *>(src + ks * 16) : 0u;
-                    qf[mt][ks][2 + h] = live ? *reinterpret_cast<const uint32_t *>(src + ks * 16 + 8) : 0u;
-                }
-            }
         // chunks inside [all_lo, all_hi) or [0, all_shi) are seen whole by every row
         const RowKeys first = paged_row(sq, cl.p0), last = paged_row(sq, cl.p0 + cl.n - 1);
         const int all_lo = last.lo, all_hi = first.hi, all_shi = first.shi > first.slo ? first.shi : 0;
@@ -235,6 +252,24 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
             next_id = page_of(c + (s + 1) * kWarps);
             load(c + s * kWarps, s, id);
         }
+        // Q fragments, straight from global memory; rows past the unit's are zero
+        uint32_t qf[MT][KS][4];
+        RowKeys keys[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = mt * 16 + h * 8 + g;
+                const bool live = r < rows;
+                const int tok = live ? r / sq.group : 0, head = live ? r - tok * sq.group : 0;
+                keys[mt][h] = paged_row(sq, cl.p0 + (live ? tok : cl.n - 1));
+                const uint16_t *src = a.q + (size_t)(cl.t0 + tok) * a.q_stride + (size_t)(hk * sq.group + head) * D + 2 * t4;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    qf[mt][ks][h] = live ? *reinterpret_cast<const uint32_t *>(src + ks * 16) : 0u;
+                    qf[mt][ks][2 + h] = live ? *reinterpret_cast<const uint32_t *>(src + ks * 16 + 8) : 0u;
+                }
+            }
         int stage = 0;
         for (; c < c_end; c += kWarps) {
             cp_async_wait<NS - 2>();
@@ -373,7 +408,10 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
             }
         __syncthreads();
         const bool begins = c_at == 0, ends = c_end == cl.count;
-        const int first_cta = (int)(unit_begin / per), last_cta = (int)((unit_end - 1) / per);
+        if (flat && !(begins && ends)) {
+            first_cta = (int)(unit_begin / per);
+            last_cta = (int)((unit_end - 1) / per);
+        }
         auto store = [&](int r, int col, const float (&x)[4], float inv) {
             const int tok = r / sq.group, head = hk * sq.group + r - tok * sq.group;
             const size_t at = ((size_t)(cl.t0 + tok) * sq.H + head) * D + col;
@@ -388,6 +426,59 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
             const int tok = r / sq.group, head = hk * sq.group + r - tok * sq.group;
             if (a.lse)
                 a.lse[(size_t)head * sq.T + cl.t0 + tok] = lsum > 0.f ? (top + lg2(lsum)) * 0.6931471805599453f : -INFINITY;
+        };
+        // NI four-column items of the pair's rows per thread, from item e0 on,
+        // summed over the pieces; 16 / NI pieces at a time
+        auto join = [&](auto ni, int e0) {
+            constexpr int NI = decltype(ni)::value, B = 16 / NI;
+            float x[NI][4] = {}, top[NI], lsum[NI] = {};
+#pragma unroll
+            for (int i = 0; i < NI; ++i) top[i] = -INFINITY;
+            for (int p0 = first_cta; p0 <= last_cta; p0 += B) {
+                float2 ml[B][NI];
+                float4 f[B][NI];
+#pragma unroll
+                for (int j = 0; j < B; ++j)
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) {
+                        const int e = e0 + threadIdx.x + i * 32 * kWarps, r = e / (D / 4), col = (e % (D / 4)) * 4;
+                        const int p = p0 + j;
+                        const size_t row = ((size_t)p * 2 + (p == first_cta ? 1 : 0)) * 16 * MT + r;
+                        ml[j][i] = make_float2(-INFINITY, 0.f);
+                        f[j][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (p <= last_cta && r < rows) {
+                            ml[j][i] = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + row * 2));
+                            f[j][i] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + row * D + col));
+                        }
+                    }
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    float t2 = top[i];
+#pragma unroll
+                    for (int j = 0; j < B; ++j) t2 = fmaxf(t2, ml[j][i].x);
+                    if (!(t2 > -INFINITY)) continue;
+                    const float old = ex2(top[i] - t2);
+                    x[i][0] *= old, x[i][1] *= old, x[i][2] *= old, x[i][3] *= old;
+                    lsum[i] *= old;
+#pragma unroll
+                    for (int j = 0; j < B; ++j) {
+                        const float now = ex2(ml[j][i].x - t2);
+                        x[i][0] += f[j][i].x * now;
+                        x[i][1] += f[j][i].y * now;
+                        x[i][2] += f[j][i].z * now;
+                        x[i][3] += f[j][i].w * now;
+                        lsum[i] += ml[j][i].y * now;
+                    }
+                    top[i] = t2;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int e = e0 + threadIdx.x + i * 32 * kWarps, r = e / (D / 4), col = (e % (D / 4)) * 4;
+                if (r >= rows) continue;
+                store(r, col, x[i], lsum[i] > 0.f ? 1.f / lsum[i] : 0.f);
+                if (col == 0) store_lse(r, top[i], lsum[i]);
+            }
         };
         const size_t slot = (size_t)cta * 2 + (begins ? 1 : 0);
         for (int e = threadIdx.x; e < rows * (D / 4); e += blockDim.x) {
@@ -412,45 +503,34 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
             }
         }
         if (!(begins && ends)) {
-            // the head's last piece to arrive joins them, in order
-            __threadfence();
+            // the head's last piece to arrive joins them, in order: the
+            // barrier and the release order every thread's rows before the
+            // count, the acquire the other pieces' rows after it
             __syncthreads();
             if (threadIdx.x == 0) {
-                const int n = atomicAdd(a.counters + first_cta, 1);
+                int n;
+                asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(n) : "l"(a.counters + first_cta) : "memory");
                 s_last = n == last_cta - first_cta;
                 if (s_last) a.counters[first_cta] = 0;
             }
             __syncthreads();
             if (s_last) {
-                __threadfence();
-                for (int e = threadIdx.x; e < rows * (D / 4); e += blockDim.x) {
-                    const int r = e / (D / 4), col = (e % (D / 4)) * 4;
-                    float x[4] = {};
-                    float top = -INFINITY, lsum = 0.f;
-                    for (int p = first_cta; p <= last_cta; ++p) {
-                        const size_t at = ((size_t)p * 2 + (p == first_cta ? 1 : 0)) * 16 * MT + r;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + at * 2));
-                        const float4 f = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * D + col));
-                        if (!(ml.x > -INFINITY)) continue;
-                        const float t2 = fmaxf(top, ml.x);
-                        const float old = top > -INFINITY ? ex2(top - t2) : 0.f, now = ex2(ml.x - t2);
-                        x[0] = x[0] * old + f.x * now;
-                        x[1] = x[1] * old + f.y * now;
-                        x[2] = x[2] * old + f.z * now;
-                        x[3] = x[3] * old + f.w * now;
-                        lsum = lsum * old + ml.y * now;
-                        top = t2;
-                    }
-                    store(r, col, x, lsum > 0.f ? 1.f / lsum : 0.f);
-                    if (col == 0) store_lse(r, top, lsum);
+                // 16 loads of each thread on their way at once
+                const int items = rows * (D / 4);
+                for (int e0 = 0; e0 < items; e0 += 4 * 32 * kWarps) {
+                    const int left = (items - e0 + 32 * kWarps - 1) / (32 * kWarps);
+                    if (left == 1) join(std::integral_constant<int, 1>(), e0);
+                    else if (left == 2) join(std::integral_constant<int, 2>(), e0);
+                    else join(std::integral_constant<int, 4>(), e0);
                 }
             }
         }
-        __syncthreads();     // the rows in shared memory have been read
         // ---- the next head, or the next sequence with new tokens
         pos = unit_begin + c_end;
+        if (!flat || pos >= end) break;
+        __syncthreads();     // the rows in shared memory have been read
         c_at = 0;
-        if (pos < end && ++hk == sq.Hkv) {
+        if (++hk == sq.Hkv) {
             hk = 0;
             do cl = paged_chunks(sq, ++seq);
             while (cl.count == 0);
@@ -472,9 +552,15 @@ ra_status launch(const TokensLaunch &t, const TokensArgs &args, cudaStream_t str
 
 }  // namespace
 
+bool paged_tokens_whole(int64_t pairs, int64_t keys) {
+    return 2 * pairs > kPagedTokensCtas && keys <= kWholeKeys && pairs < (int64_t)1 << 30;
+}
+
 int paged_tokens_ctas(int64_t pairs, int64_t keys) {
+    if (paged_tokens_whole(pairs, keys)) return (int)pairs;
     const int64_t chunks = pairs * ((keys + kChunk - 1) / kChunk + 1);
-    const int64_t n = (chunks + kMinRun - 1) / kMinRun;
+    int64_t n = (chunks + kMinRun - 1) / kMinRun;
+    if (n < 2 * pairs) n = 2 * pairs;      // so that few pairs are cut on their own
     return (int)(n < 1 ? 1 : n > kPagedTokensCtas ? kPagedTokensCtas : n);
 }
 
@@ -489,6 +575,7 @@ ra_status launch_paged_tokens(const TokensLaunch &t, cudaStream_t stream) {
     a.o = t.o;
     a.lse = t.lse;
     a.o_bf16 = t.o_bf16;
+    a.whole_pairs = t.whole_pairs;
     a.scale_log2 = t.scale_log2;
     a.status = t.status;
     a.counters = t.counters;

@@ -16,13 +16,17 @@ struct TokensLaunch {
     int64_t q_stride, page_stride;
     void *o;
     float *lse;
-    bool o_bf16;
+    bool o_bf16, whole_pairs;
     int d, ctas;
     float scale_log2;
     unsigned *status;
     int *counters;              // kPagedTokensCtas, zero between calls
     float *part_o, *part_ml;    // [2 * ctas, rows up to 16 or 32, d], [.., 2]
 };
+
+// Whether every (sequence, key/value head) pair gets one CTA and is never cut:
+// there are enough of them and they are short.
+bool paged_tokens_whole(int64_t pairs, int64_t keys);
 
 // CTAs for `pairs` (sequence, key/value head) pairs of up to `keys` keys: the
 // grid, not the split, which the kernel takes from the lengths it finds.
