@@ -980,7 +980,14 @@ __global__ void __launch_bounds__(384, 1)
                     float x0, x1;
                     f32x2_split(fma_f32x2(f32x2(__uint_as_float(pv[j][c]), __uint_as_float(pv[j][c + 1])),
                                           sl2x2, nl2[c >> 1]), x0, x1);
-                    pk[j][c >> 1] = pack_bf16x2(ex2(x0), ex2(x1));
+                    const float p0 = ex2(x0), p1 = ex2(x1);
+                    pk[j][c >> 1] = pack_bf16x2(p0, p1);
+                    if constexpr (KEYS != BWD_RING) {
+                        // dS^T takes P^T unrounded: dK then has one rounding (of
+                        // dS^T) before its own instead of two
+                        pv[j][c] = __float_as_uint(p0);
+                        pv[j][c + 1] = __float_as_uint(p1);
+                    }
                 }
             }
             // P^T(t) goes where dV reads it once dV(t-1) has read P^T(t-1): at
@@ -1014,9 +1021,10 @@ __global__ void __launch_bounds__(384, 1)
                 const uint64_t *dd2 = reinterpret_cast<const uint64_t *>(vec + 128 + 64 * hh + 32 * j);
 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
-                    // the rounded P the dV product used: bf16 halves widened exactly
+                    // (ring) the rounded P the dV product used: bf16 halves widened exactly
                     const uint32_t w = pk[j][c >> 1];
-                    const float p0 = __uint_as_float(w << 16), p1 = __uint_as_float(w & 0xffff0000u);
+                    const float p0 = KEYS == BWD_RING ? __uint_as_float(w << 16) : __uint_as_float(pv[j][c]);
+                    const float p1 = KEYS == BWD_RING ? __uint_as_float(w & 0xffff0000u) : __uint_as_float(pv[j][c + 1]);
                     float d0, d1;
                     f32x2_split(mul_f32x2(f32x2(p0, p1),
                                           sub_f32x2(f32x2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])),
