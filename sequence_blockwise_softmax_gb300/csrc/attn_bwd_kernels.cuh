@@ -75,16 +75,29 @@ struct BwdArgs {
     // windowed attention (BWD_WINDOW, BWD_SINKS; N = 1)
     int window, sinks;
     int grad_bf16;          // dq, dk, dv are bf16 (rounded once from the accumulators)
-    int sink_units;         // (sequence, query chunk) units of the sinks' far part
-    float *sink_part;       // their partial dK and dV: [2, B, H_kv, sink_units, sinks, d]
+    // The sinks' far part: every query past a sink's window sees it too.  The
+    // dK / dV pass takes it in units (sequence, chunk of sink_chunk queries),
+    // in n_far blocks of their own before the n_kv key blocks; these and the
+    // key blocks leave the sinks' rows in sink_part, [2 (dK, dV), B, H_kv,
+    // sink_units + n_seqs + 1, sinks, d] unscaled -- the units', then each
+    // sequence's own from the key blocks -- and bwd_sink_join adds them.
+    int sink_units, sink_chunk, n_far, n_kv;
+    float *sink_part;
 };
 
 // BWD_RING: the ring sweep's masks.  BWD_WINDOW: a causal window and sinks
-// inside each sequence (ra_window.cuh); the dK / dV pass meets each key with
-// the queries of its window and adds what BWD_SINKS left in sink_part.
-// BWD_SINKS (dK / dV pass only): one 128-key block of a sequence's sinks
-// against one chunk of the queries past their windows, fp32 partials.
-enum BwdKeys { BWD_RING = 0, BWD_WINDOW = 1, BWD_SINKS = 2 };
+// inside each sequence (ra_window.cuh).
+enum BwdKeys { BWD_RING = 0, BWD_WINDOW = 1 };
+
+// First element of a sink's row in dK's half of sink_part; slot: a unit, or
+// sink_units + the sequence's number.
+__device__ __forceinline__ size_t sink_row(const BwdArgs &a, int b, int hk, int slot, int row, int d) {
+    const size_t slots = (size_t)a.sink_units + a.n_seqs + 1;
+    return ((((size_t)b * a.Hkv + hk) * slots + slot) * a.sinks + row) * d;
+}
+__device__ __forceinline__ size_t sink_half(const BwdArgs &a, int d) {
+    return (size_t)a.B * a.Hkv * ((size_t)a.sink_units + a.n_seqs + 1) * a.sinks * d;
+}
 
 __device__ __forceinline__ uint8_t *bwd_align1024(uint8_t *p) {
     return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
@@ -195,8 +208,8 @@ __device__ __forceinline__ void store_row32_bf16(uint16_t *dst, const uint32_t (
 // at its token position, and its LSE ([B, H, L]) is copied to the same
 // stack-order index of lse_stack, so that both passes read D and LSE of a
 // tile's rows as one contiguous run.
-template <int D, bool O_BF16 = false>
-__global__ void __launch_bounds__(256) bwd_dot_kernel(const uint16_t *dout, const void *o, float *dvec,
+template <int D>
+__global__ void __launch_bounds__(256) bwd_dot_kernel(const uint16_t *dout, const float *o, float *dvec,
                                                       int64_t rows, int H, int64_t S, int seq_order, int layout,
                                                       int N, int B, const float *lse_tok, float *lse_stack) {
     const int lane = threadIdx.x & 31;
@@ -233,18 +246,7 @@ __global__ void __launch_bounds__(256) bwd_dot_kernel(const uint16_t *dout, cons
             }
             dst[u] = (z * H + h) * S + s;
             const uint16_t *dp = dout + src * D + lane * PER;
-            if constexpr (O_BF16) {
-                const uint16_t *op = static_cast<const uint16_t *>(o) + src * D + lane * PER;
-#pragma unroll
-                for (int e = 0; e < PER / 2; ++e) {
-                    dw[u][e] = reinterpret_cast<const uint32_t *>(dp)[e];
-                    const uint32_t w = reinterpret_cast<const uint32_t *>(op)[e];
-                    ov[u][2 * e] = __uint_as_float(w << 16);
-                    ov[u][2 * e + 1] = __uint_as_float(w & 0xffff0000u);
-                }
-                continue;
-            }
-            const float *op = static_cast<const float *>(o) + src * D + lane * PER;
+            const float *op = o + src * D + lane * PER;
             if constexpr (PER == 4) {
                 const uint2 w = *reinterpret_cast<const uint2 *>(dp);
                 const float4 f = *reinterpret_cast<const float4 *>(op);
@@ -300,15 +302,13 @@ struct BwdQSmem {
     static constexpr uint32_t kBytes = kMisc + 16 + 1024;
 };
 
-template <int D, int KEYS = BWD_RING>
-__global__ void __launch_bounds__(384, 1)
-    attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo,
-                       const BwdArgs args) {
+template <int D, int KEYS>
+__device__ __forceinline__ void bwd_dq_body(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                                            const CUtensorMap &tmdo, const BwdArgs &args, int block) {
     using L = BwdQSmem<D>;
     constexpr int NK = L::kKStages, NV = L::kVStages;
     constexpr int HALVES = D / 64;
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = bwd_align1024(smem_raw);
     const uint32_t s_base = smem_u32(smem);
     const uint32_t bar0 = s_base + L::kBars;
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(384, 1)
 
     const int S = args.S, H = args.H, N = args.N;
     // causal work grows with the query position: heaviest tiles first
-    const UnitId unit = decode_unit(blockIdx.x, args.bh_chunk_q, args.B, H, N, args.n_tiles_seq, args.layout);
+    const UnitId unit = decode_unit(block, args.bh_chunk_q, args.B, H, N, args.n_tiles_seq, args.layout);
     const int b = unit.b, h = unit.h, qi = unit.qi, qt = unit.qt;
     const int zq = qi * args.B + b;
     const int row0 = qt * 128;
@@ -632,6 +632,14 @@ __global__ void __launch_bounds__(384, 1)
     }
 }
 
+template <int D>
+__global__ void __launch_bounds__(384, 1)
+    attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo,
+                       const BwdArgs args) {
+    bwd_dq_body<D, BWD_RING>(tmq, tmk, tmv, tmdo, args, blockIdx.x);
+}
+
 // ---------------------------------------------------------------- pass A: dK, dV
 template <int D>
 struct BwdKVSmem {
@@ -654,11 +662,9 @@ struct BwdKVSmem {
     static constexpr uint32_t kBytes = kMisc + 16;
 };
 
-template <int D, int KEYS = BWD_RING>
-__global__ void __launch_bounds__(384, 1)
-    attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                        const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo,
-                        const BwdArgs args) {
+template <int D, int KEYS>
+__device__ __forceinline__ void bwd_dkv_body(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                                             const CUtensorMap &tmdo, const BwdArgs &args, int block) {
     using L = BwdKVSmem<D>;
     constexpr int NS = L::kStages;
     constexpr int HALVES = D / 64;
@@ -691,13 +697,15 @@ __global__ void __launch_bounds__(384, 1)
     // causal work shrinks with the key position: earliest keys first
     UnitId unit;
     SinkUnit su{};
-    int c0, c_end;      // this block's keys; c_end leaves out rows past the shard (or, BWD_SINKS, past the sinks)
-    if constexpr (KEYS == BWD_SINKS) {
-        // blockIdx.x = ((b * H_kv + hk) * sink blocks + block) * units + unit
+    int c0, c_end;      // this block's keys; c_end leaves out rows past the shard (far: past the sinks)
+    // a block of the sinks' far part (see BwdArgs)
+    const bool far = KEYS == BWD_WINDOW && block < args.n_far;
+    if (far) {
+        // block = ((b * H_kv + hk) * sink blocks + sink block) * units + unit
         const int n_blocks = (args.sinks + 127) / 128;
-        const int u = blockIdx.x % args.sink_units;
-        const int rest = blockIdx.x / args.sink_units;
-        su = sink_unit(args.cu_seqlens, args.n_seqs, S, u);
+        const int u = block % args.sink_units;
+        const int rest = block / args.sink_units;
+        su = sink_unit(args.cu_seqlens, args.n_seqs, S, args.sink_chunk, u);
         c0 = su.start + rest % n_blocks * 128;
         c_end = min(min(su.start + args.sinks, su.end), c0 + 128);
         unit.h = rest / n_blocks % Hkv;
@@ -707,7 +715,8 @@ __global__ void __launch_bounds__(384, 1)
         // no query of the chunk lies past the first key's window
         if (c_end <= c0 || max(su.lo, c0 + args.window) >= su.hi) return;
     } else {
-        unit = decode_key_block(blockIdx.x, args.bh_chunk_kv, args.B, Hkv, N, args.n_tiles_seq, args.layout);
+        unit = decode_key_block(KEYS == BWD_WINDOW ? block - args.n_far : block, args.bh_chunk_kv, args.B, Hkv, N,
+                                args.n_tiles_seq, args.layout);
         c0 = unit.qt * 128;
         c_end = min(S, c0 + 128);
     }
@@ -720,7 +729,7 @@ __global__ void __launch_bounds__(384, 1)
         walk0 = key_block_walk(args.layout, N, S, kj, group, c0, c_end, args.causal, args.cu_seqlens, args.n_seqs);
     } else {
         walk0 = QWalk{0, 0, 0, 0, 0, group, 1, 0, RA_CONTIGUOUS, S, 0, 0};
-        if constexpr (KEYS == BWD_WINDOW) {
+        if (!far) {
             int start, end;
             seq_of(args.cu_seqlens, args.n_seqs, S, c_end - 1, start, end);
             walk0.lo_pos = c0 - 1;
@@ -916,7 +925,7 @@ __global__ void __launch_bounds__(384, 1)
         const int r = wq * 32 + lane;
         const int kk = c0 + r;
         const int kk_c = kk < S ? kk : S - 1;
-        const int k_end = KEYS == BWD_SINKS ? c_end : S;   // rows past it are not written
+        const int k_end = far ? c_end : S;   // rows past it are not written
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
         const uint32_t tS = tmem + lane_off, tP = tmem + lane_off + 128;
         const uint32_t tV = tmem + lane_off + 256, tK = tmem + lane_off + 256 + D;
@@ -925,7 +934,7 @@ __global__ void __launch_bounds__(384, 1)
         int seq = 0, seq_start = 0, seq_end = S;
         if constexpr (KEYS == BWD_RING) {
             col_query_bounds(args.cu_seqlens, args.n_seqs, total, kpos, args.causal, lo_pos, hi_pos);
-        } else if constexpr (KEYS == BWD_WINDOW) {
+        } else if (!far) {
             seq = seq_of(args.cu_seqlens, args.n_seqs, S, kk_c, seq_start, seq_end);
             lo_pos = kk_c - 1;
             hi_pos = window_col_end(kk_c, seq_end, args.window) - 1;
@@ -1054,44 +1063,24 @@ __global__ void __launch_bounds__(384, 1)
                                               : (size_t)zk * S + kk_c) * Hkv + hk) * D;
                 float *out_dv = args.dv, *out_dk = args.dk;
                 float dk_mul = args.scale;
-                const size_t part = (size_t)args.B * Hkv * args.sink_units * args.sinks * D;   // dK's half of sink_part
-                if constexpr (KEYS == BWD_SINKS) {
-                    // unscaled, [b, hk, unit, key - start]
-                    row = ((((size_t)b * Hkv + hk) * args.sink_units + unit.qt) * args.sinks + (kk - su.start)) * D;
-                    out_dk = args.sink_part;
-                    out_dv = args.sink_part + part;
-                    dk_mul = 1.f;
-                }
-                // BWD_WINDOW: the units that met this key past its window, in order
-                int u0 = 0, u1 = 0;
+                bool bf16 = KEYS == BWD_WINDOW && args.grad_bf16;
                 if constexpr (KEYS == BWD_WINDOW) {
-                    const int far = kk_c + args.window;
-                    if (kk < S && args.window > 0 && kk_c - seq_start < args.sinks && far < seq_end) {
-                        u0 = seq + far / kSinkChunk;
-                        u1 = seq + (seq_end - 1) / kSinkChunk + 1;
+                    // a sink's rows, if queries past its window see it, go to sink_part
+                    const bool sink = far || (args.n_far > 0 && kk_c - seq_start < args.sinks &&
+                                              kk_c + args.window < seq_end);
+                    if (sink) {
+                        row = far ? sink_row(args, b, hk, unit.qt, kk - su.start, D)
+                                  : sink_row(args, b, hk, args.sink_units + seq, kk_c - seq_start, D);
+                        out_dk = args.sink_part;
+                        out_dv = args.sink_part + sink_half(args, D);
+                        dk_mul = 1.f;
+                        bf16 = false;
                     }
                 }
-                auto finish = [&](uint32_t (&v)[32], float *out, const float *far_part, int col, float mul) {
-                    if constexpr (KEYS == BWD_WINDOW) {
-                        for (int u = u0; u < u1; ++u) {
-                            const float4 *src = reinterpret_cast<const float4 *>(
-                                far_part + ((((size_t)b * Hkv + hk) * args.sink_units + u) * args.sinks +
-                                            (kk_c - seq_start)) * D + col);
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                const float4 f = src[c];
-                                v[4 * c] = __float_as_uint(__uint_as_float(v[4 * c]) + f.x);
-                                v[4 * c + 1] = __float_as_uint(__uint_as_float(v[4 * c + 1]) + f.y);
-                                v[4 * c + 2] = __float_as_uint(__uint_as_float(v[4 * c + 2]) + f.z);
-                                v[4 * c + 3] = __float_as_uint(__uint_as_float(v[4 * c + 3]) + f.w);
-                            }
-                        }
-                        if (args.grad_bf16) {
-                            if (kk < k_end) store_row32_bf16(reinterpret_cast<uint16_t *>(out) + row + col, v, mul);
-                            return;
-                        }
-                    }
-                    if (kk < k_end) store_row32(out + row + col, v, mul);
+                auto finish = [&](const uint32_t (&v)[32], float *out, int col, float mul) {
+                    if (kk >= k_end) return;
+                    if (bf16) store_row32_bf16(reinterpret_cast<uint16_t *>(out) + row + col, v, mul);
+                    else store_row32(out + row + col, v, mul);
                 };
 #pragma unroll
                 for (int q = hh * (D / 64); q < (hh + 1) * (D / 64); ++q) {
@@ -1103,15 +1092,12 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                         for (int c = 0; c < 32; ++c) v[c] = 0u;
                     }
-                    finish(v, out_dv, args.sink_part + part, 32 * q, 1.f);
+                    finish(v, out_dv, 32 * q, 1.f);
                     if (T > 0) {
                         tmem_ld32(tK + 32 * q, v);
                         tmem_wait_ld();
-                    } else if constexpr (KEYS != BWD_RING) {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) v[c] = 0u;
                     }
-                    finish(v, out_dk, args.sink_part, 32 * q, dk_mul);
+                    finish(v, out_dk, 32 * q, dk_mul);
                 }
             }
         }
@@ -1121,6 +1107,130 @@ __global__ void __launch_bounds__(384, 1)
     if (warp == 2) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(384, 1)
+    attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                        const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo,
+                        const BwdArgs args) {
+    bwd_dkv_body<D, BWD_RING>(tmq, tmk, tmv, tmdo, args, blockIdx.x);
+}
+
+// ---------------------------------------------------------------- windowed: both passes
+// One launch: the sinks' far blocks, the key blocks, then the query tiles.
+// The passes do not depend on one another, so the second fills the SMs that
+// the first leaves idle at its end.
+template <int D>
+struct BwdWindowSmem {
+    static constexpr uint32_t kBytes = BwdQSmem<D>::kBytes > BwdKVSmem<D>::kBytes ? BwdQSmem<D>::kBytes
+                                                                                 : BwdKVSmem<D>::kBytes;
+};
+template <int D>
+__global__ void __launch_bounds__(384, 1)
+    attn_bwd_window_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                           const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo,
+                           const BwdArgs args) {
+    const int n = args.n_far + args.n_kv;
+    if ((int)blockIdx.x < n) bwd_dkv_body<D, BWD_WINDOW>(tmq, tmk, tmv, tmdo, args, blockIdx.x);
+    else bwd_dq_body<D, BWD_WINDOW>(tmq, tmk, tmv, tmdo, args, blockIdx.x - n);
+}
+
+// dK and dV of the sinks that queries past their windows see: the key block's
+// part and the units', in order.  One warp per (b, hk, sequence, sink).
+template <int D>
+__global__ void __launch_bounds__(256) bwd_sink_join(const BwdArgs a) {
+    constexpr int PER = D / 32, AHEAD = 8;
+    const int lane = threadIdx.x & 31;
+    int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int r = (int)(w % a.sinks);
+    w /= a.sinks;
+    const int s = (int)(w % (a.n_seqs + 1));
+    w /= a.n_seqs + 1;
+    const int hk = (int)(w % a.Hkv), b = (int)(w / a.Hkv);
+    if (b >= a.B) return;
+    const int start = a.cu_seqlens ? seq_bound(a.cu_seqlens, a.n_seqs, a.S, s) : 0;
+    const int end = a.cu_seqlens ? seq_bound(a.cu_seqlens, a.n_seqs, a.S, s + 1) : a.S;
+    const int key = start + r, past = key + a.window;
+    if (past >= end) return;
+    const int u0 = s + past / a.sink_chunk, u1 = s + (end - 1) / a.sink_chunk + 1;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const float *part = a.sink_part + (half ? sink_half(a, D) : 0) + lane * PER;
+        float x[PER];
+        const float *own = part + sink_row(a, b, hk, a.sink_units + s, r, D);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) x[e] = own[e];
+        for (int u = u0; u < u1; u += AHEAD) {
+            float f[AHEAD][PER];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const float *src = part + sink_row(a, b, hk, min(u + i, u1 - 1), r, D);
+#pragma unroll
+                for (int e = 0; e < PER; ++e) f[i][e] = src[e];
+            }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (u + i < u1)
+#pragma unroll
+                    for (int e = 0; e < PER; ++e) x[e] += f[i][e];
+        }
+        const size_t at = (((size_t)b * a.S + key) * a.Hkv + hk) * D + lane * PER;
+        const float mul = half ? 1.f : a.scale;
+        if (a.grad_bf16) {
+            uint32_t *dst = reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(half ? a.dv : a.dk) + at);
+#pragma unroll
+            for (int e = 0; e < PER; e += 2) dst[e / 2] = pack_bf16x2(x[e] * mul, x[e + 1] * mul);
+        } else {
+            float *dst = (half ? a.dv : a.dk) + at;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) dst[e] = x[e] * mul;
+        }
+    }
+}
+
+// D = rowsum(dO * O) for one shard in its own order ([B, S, H, d] to
+// [B, H, S]), O fp32 or bf16: 16-byte loads, a row to D / 8 lanes, four rows
+// of each lane group on their way at once.
+template <int D, bool O_BF16>
+__global__ void __launch_bounds__(256) bwd_window_dot(const uint16_t *dout, const void *o, float *dvec, int64_t rows,
+                                                      int H, int64_t S) {
+    constexpr int LANES = D / 8, PER_WARP = 32 / LANES, R = 4;
+    const int lane = threadIdx.x & 31, sub = lane % LANES;
+    const int64_t r0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * PER_WARP * R + lane / LANES;
+    uint4 dv[R], ov[R][O_BF16 ? 1 : 2];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t r = min(r0 + i * PER_WARP, rows - 1);
+        dv[i] = *reinterpret_cast<const uint4 *>(dout + r * D + sub * 8);
+        if constexpr (O_BF16) {
+            ov[i][0] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(o) + r * D + sub * 8);
+        } else {
+            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(o) + r * D + sub * 8);
+            ov[i][0] = p[0];
+            ov[i][1] = p[1];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const uint32_t *d = &dv[i].x, *p = &ov[i][0].x;
+        float acc = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float d0 = __uint_as_float(d[e] << 16), d1 = __uint_as_float(d[e] & 0xffff0000u);
+            const float o0 = O_BF16 ? __uint_as_float(p[e] << 16) : __uint_as_float(p[2 * e]);
+            const float o1 = O_BF16 ? __uint_as_float(p[e] & 0xffff0000u) : __uint_as_float(p[2 * e + 1]);
+            acc += d0 * o0;
+            acc += d1 * o1;
+        }
+#pragma unroll
+        for (int off = LANES / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+        const int64_t r = r0 + i * PER_WARP;
+        if (sub == 0 && r < rows) {
+            const int64_t zs = r / H;
+            dvec[((zs / S) * H + r % H) * S + zs % S] = acc;
+        }
     }
 }
 

@@ -107,10 +107,11 @@ BwdSpace bwd_space(int64_t B, int64_t L, int64_t H, int64_t H_kv, int d, int64_t
     BwdSpace s;
     if (sinks > L) sinks = L;
     // no query lies past a window of L tokens: no far part
-    s.units = sinks > 0 && window < L ? sink_units(L, n_seqs) : 0;
+    s.units = sinks > 0 && window < L ? sink_units(L, n_seqs, sink_chunk(window)) : 0;
     s.dvec = kHeader;
     s.part = s.dvec + round256((size_t)B * L * H * 4);
-    s.total = s.part + round256((size_t)2 * B * H_kv * s.units * sinks * d * 4);
+    const size_t slots = s.units > 0 ? s.units + n_seqs + 1 : 0;
+    s.total = s.part + round256(2 * (size_t)B * H_kv * slots * sinks * d * 4);
     return s;
 }
 
@@ -149,29 +150,26 @@ ra_status launch_bwd(const Window &w, const void *q, const void *k, const void *
     a.grad_bf16 = grad_bf16 ? 1 : 0;
     a.sink_units = (int)space.units;
     a.sink_part = reinterpret_cast<float *>(workspace + space.part);
-    const int64_t rows = w.B * w.L * w.H;
-    int dev = 0, sms = 152;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    int64_t blocks = (rows + 31) / 32;   // 8 warps of 4 rows
-    if (blocks > (int64_t)sms * 8) blocks = (int64_t)sms * 8;
-    auto dot = o_bf16 ? bwd_dot_kernel<D, true> : bwd_dot_kernel<D, false>;
-    auto kkv = attn_bwd_dkv_kernel<D, BWD_WINDOW>;
-    auto ksink = attn_bwd_dkv_kernel<D, BWD_SINKS>;
-    auto kq = attn_bwd_dq_kernel<D, BWD_WINDOW>;
-    const int smem_kv = (int)BwdKVSmem<D>::kBytes, smem_q = (int)BwdQSmem<D>::kBytes;
-    if (cudaFuncSetAttribute(kkv, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv) != cudaSuccess ||
-        cudaFuncSetAttribute(ksink, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv) != cudaSuccess ||
-        cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q) != cudaSuccess)
+    a.sink_chunk = sink_chunk(w.window);
+    const int64_t n_far = w.B * w.H_kv * ((w.sinks + 127) / 128) * space.units;
+    const int64_t n_kv = w.B * w.H_kv * a.n_tiles_seq, n_q = w.B * w.H * a.n_tiles_seq;
+    const int64_t joins = space.units > 0 ? w.B * w.H_kv * (w.n_seqs + 1) * w.sinks : 0;   // warps
+    if (n_far + n_kv + n_q > 0x7fffffffLL || joins / 8 > 0x7ffffffeLL)
+        return set_error(RA_ERR_UNSUPPORTED, "too many tiles for one launch");
+    a.n_far = (int)n_far;
+    a.n_kv = (int)n_kv;
+    const int64_t rows = w.B * w.L * w.H, per_block = 8 * 4 * (256 / D);
+    auto dot = o_bf16 ? bwd_window_dot<D, true> : bwd_window_dot<D, false>;
+    auto kern = attn_bwd_window_kernel<D>;
+    const int smem = (int)BwdWindowSmem<D>::kBytes;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
-    const int64_t grid_sink = w.B * w.H_kv * ((w.sinks + 127) / 128) * space.units;
-    if (grid_sink > 0x7fffffffLL) return set_error(RA_ERR_UNSUPPORTED, "too many sink tiles for one launch");
-    dot<<<(unsigned)blocks, 256, 0, stream>>>(static_cast<const uint16_t *>(dout), o,
-                                              reinterpret_cast<float *>(workspace + space.dvec), rows, a.H, w.L, 0,
-                                              RA_CONTIGUOUS, 1, a.B, nullptr, nullptr);
-    if (grid_sink > 0) ksink<<<(unsigned)grid_sink, 384, smem_kv, stream>>>(mq, mk, mv, mdo, a);
-    kkv<<<(unsigned)(w.B * w.H_kv * a.n_tiles_seq), 384, smem_kv, stream>>>(mq, mk, mv, mdo, a);
-    kq<<<(unsigned)(w.B * w.H * a.n_tiles_seq), 384, smem_q, stream>>>(mq, mk, mv, mdo, a);
+    if ((rows + per_block - 1) / per_block > 0x7fffffffLL)
+        return set_error(RA_ERR_UNSUPPORTED, "too many rows for one launch");
+    dot<<<(unsigned)((rows + per_block - 1) / per_block), 256, 0, stream>>>(
+        static_cast<const uint16_t *>(dout), o, reinterpret_cast<float *>(workspace + space.dvec), rows, a.H, w.L);
+    kern<<<(unsigned)(n_far + n_kv + n_q), 384, smem, stream>>>(mq, mk, mv, mdo, a);
+    if (joins > 0) bwd_sink_join<D><<<(unsigned)((joins + 7) / 8), 256, 0, stream>>>(a);
     return launch_error();
 }
 

@@ -121,25 +121,29 @@ RA_HD int window_col_end(int t, int end, int window) {
 }
 
 // The far part of a sink's gradient: the queries past its window.  They are
-// cut at multiples of kSinkChunk rows and each (sequence, chunk) is a unit of
+// cut at multiples of `chunk` rows and each (sequence, chunk) is a unit of
 // its own, so that the few keys every query sees do not become one long block.
-// Unit u belongs to the last sequence s whose first unit, start / kSinkChunk + s,
+// Unit u belongs to the last sequence s whose first unit, start / chunk + s,
 // is not past u, and is chunk u - s of the rows; the chunks of a sequence
-// [start, end) are start / kSinkChunk .. (end - 1) / kSinkChunk, one more than
+// [start, end) are start / chunk .. (end - 1) / chunk, one more than
 // the next sequence's start is on at most, which the "+ s" has room for.
-constexpr int kSinkChunk = 2048;
+// A chunk is about as long as a key block's own queries (the window), so that
+// the two kinds of block take alike; from 512 to 2048 rows.
+RA_HD int sink_chunk(int64_t window) {
+    return window <= 512 ? 512 : window >= 2048 ? 2048 : (int)((window + 127) / 128 * 128);
+}
 
 struct SinkUnit {
     int start, end;     // the sequence's tokens
     int lo, hi;         // the chunk's query rows inside it; lo >= hi: no such unit
 };
 
-RA_HD int64_t sink_units(int64_t S, int n_seqs) { return S / kSinkChunk + n_seqs + 1; }
+RA_HD int64_t sink_units(int64_t S, int n_seqs, int chunk) { return S / chunk + n_seqs + 1; }
 
 // The number of the first unit of sequence s, which starts at `start`.
-RA_HD int sink_first_unit(int start, int s) { return start / kSinkChunk + s; }
+RA_HD int sink_first_unit(int start, int s, int chunk) { return start / chunk + s; }
 
-RA_HD SinkUnit sink_unit(const int *cu, int n_seqs, int S, int u) {
+RA_HD SinkUnit sink_unit(const int *cu, int n_seqs, int S, int chunk, int u) {
     SinkUnit k;
     int s = 0;
     k.start = 0;
@@ -148,15 +152,15 @@ RA_HD SinkUnit sink_unit(const int *cu, int n_seqs, int S, int u) {
         int hi = n_seqs + 1;
         while (hi - s > 1) {
             const int mid = (s + hi) >> 1;
-            if (sink_first_unit(seq_bound(cu, n_seqs, S, mid), mid) <= u) s = mid;
+            if (sink_first_unit(seq_bound(cu, n_seqs, S, mid), mid, chunk) <= u) s = mid;
             else hi = mid;
         }
         k.start = seq_bound(cu, n_seqs, S, s);
         k.end = seq_bound(cu, n_seqs, S, s + 1);
     }
-    const int64_t at = (int64_t)(u - s) * kSinkChunk;   // unit start / kSinkChunk + s + i is chunk start / kSinkChunk + i
+    const int64_t at = (int64_t)(u - s) * chunk;   // unit start / chunk + s + i is chunk start / chunk + i
     k.lo = (int)clamp64(at, k.start, k.end);
-    k.hi = (int)clamp64(at + kSinkChunk, k.start, k.end);
+    k.hi = (int)clamp64(at + chunk, k.start, k.end);
     return k;
 }
 

@@ -122,8 +122,9 @@ def test_backward_workspace(ralib):
     r = lambda n: (n + 255) // 256 * 256
     assert f(1, 1000, 4, 2, 64, 100) == 256 + r(16000)
     assert f(1, 1000, 4, 2, 64, 1000, 8) == 256 + r(16000)          # no query past a window of L
-    assert f(1, 5000, 4, 2, 64, 100, 8) == 256 + r(80000) + 2 * 2 * 3 * 8 * 64 * 4
-    assert f(1, 5000, 4, 2, 64, 100, 8, n_seqs=5) == 256 + r(80000) + 2 * 2 * 8 * 8 * 64 * 4
+    # chunks of 512 queries, one more for each sequence, and each sequence's own part
+    assert f(1, 5000, 4, 2, 64, 100, 8) == 256 + r(80000) + 2 * 2 * (10 + 1) * 8 * 64 * 4
+    assert f(1, 5000, 4, 2, 64, 100, 8, n_seqs=5) == 256 + r(80000) + 2 * 2 * (15 + 6) * 8 * 64 * 4
     assert f(1, 5000, 4, 2, 96, 100, 8) == 0 and f(1, 5000, 4, 2, 64, 0, 8) == 0
 
 

@@ -25,7 +25,8 @@ void ra_test_window_rows(int S, int window, int sinks, const int *cu, int n_seqs
 // its window; a unit's partial counts only if the key's sum reads it.
 // Returns 1 if a unit number leaves [0, sink_units).
 int ra_test_window_cols(int S, int window, int sinks, const int *cu, int n_seqs, int *cnt) {
-    const int64_t units = ra::sink_units(S, cu ? n_seqs : 0);
+    const int chunk = ra::sink_chunk(window);
+    const int64_t units = ra::sink_units(S, cu ? n_seqs : 0, chunk);
     for (int c0 = 0; c0 < S; c0 += 128) {
         const int c_end = c0 + 128 < S ? c0 + 128 : S;
         int start, end;
@@ -37,9 +38,9 @@ int ra_test_window_cols(int S, int window, int sinks, const int *cu, int n_seqs,
             for (int p = c0 / 128 * 128; p < (last + 127) / 128 * 128; ++p)
                 if (p >= t && p < hi) ++cnt[(size_t)p * S + t];
             if (t - start >= sinks || t + window >= end) continue;
-            for (int u = s + (t + window) / ra::kSinkChunk; u < s + (end - 1) / ra::kSinkChunk + 1; ++u) {
+            for (int u = s + (t + window) / chunk; u < s + (end - 1) / chunk + 1; ++u) {
                 if (u < 0 || u >= units) return 1;
-                const ra::SinkUnit k = ra::sink_unit(cu, n_seqs, S, u);
+                const ra::SinkUnit k = ra::sink_unit(cu, n_seqs, S, chunk, u);
                 if (k.start != start || k.end != end) return 2;
                 // the unit's block holding t must have run: its first key has a query in the chunk
                 const int b0 = start + (t - start) / 128 * 128;
