@@ -305,6 +305,17 @@ __global__ void __launch_bounds__(384, 1)
     // KEYS_PAGED: a unit of few tokens has no second Q tile; its products and
     // softmax are left out
     const bool two_tiles = KEYS != KEYS_PAGED || pu.n > args.tile_tokens;
+    // KEYS_WINDOW: a Q tile's products and softmax skip the key tiles that only
+    // the other one's rows see (its neighbour's diagonal, its window's start):
+    // one of 9 and more at a window of 1024, one of 4 at 128
+    constexpr bool EDGES = KEYS == KEYS_WINDOW;
+    auto w_tile = [](const auto &w) -> int { return w.tile; };
+    auto seen_by = [&](int g) -> SeenTiles {
+        const int fr = row0 + 128 * g;
+        if (!EDGES || fr >= row_end) return SeenTiles{0, 0, 0, 0};
+        return seen_tiles(window_row(args.cu_seqlens, args.n_seqs, S, fr, args.window, args.sinks),
+                          min(row_end, fr + 128));
+    };
 
     // ---- setup
     if (threadIdx.x == 0) {
@@ -546,13 +557,25 @@ __global__ void __launch_bounds__(384, 1)
         bool ok = warp_wait(BAR(B_QFULL), 0, abort_flag);
         Walk w = walk0;
         w.start_step();
+        const SeenTiles seen0 = seen_by(0), seen1 = seen_by(1);
+        auto need = [&](int g, int tile) -> bool {
+            if (EDGES) return g == 0 ? seen0.has(tile) : seen1.has(tile);
+            return g == 0 || two_tiles;
+        };
+        int n_s0 = 0, n_s1 = 0, n_p0 = 0, n_p1 = 0;   // products issued per Q tile
         int t = 0;
         if (ok && w.valid()) {
             ok = k_wait(0);   // K(0) is load 0
             tc_fence_after();
             if (ok) {
-                issue_s(0, 0);
-                if (two_tiles) issue_s(1, 0);
+                if (need(0, w.tile)) {
+                    issue_s(0, 0);
+                    ++n_s0;
+                }
+                if (need(1, w.tile)) {
+                    issue_s(1, 0);
+                    ++n_s1;
+                }
                 tc_commit_elect(BAR(B_SLOTE + 0));
             }
             __syncwarp();
@@ -564,32 +587,38 @@ __global__ void __launch_bounds__(384, 1)
             const int ki = 2 * t + 1;                        // load index of K(t+1)
             const int vi = has_next ? 2 * t + 2 : 2 * t + 1; // load index of V(t)
             if (has_next && !(ok = k_wait(ki % NSL))) break;
-            if (has_next) {
-                if (!(ok = warp_wait(BAR(B_SFREE + 0), t & 1, abort_flag))) break;
+            if (has_next && need(0, w.tile)) {
+                if (n_s0 > 0 && !(ok = warp_wait(BAR(B_SFREE + 0), (n_s0 - 1) & 1, abort_flag))) break;
                 tc_fence_after();
                 issue_s(0, ki % NSL);
+                ++n_s0;
                 __syncwarp();
             }
             if (!(ok = v_wait(vi % NSL))) break;
             if constexpr (KEYS == KEYS_PAGED)
                 zero_rows<D>(s_base + L::kRing + (vi % NSL) * L::kTile, pu.len - v_tile * 128, lane);
-            if (!(ok = warp_wait(BAR(B_PFULL + 0), t & 1, abort_flag))) break;
-            tc_fence_after();
-            issue_pv(0, vi % NSL, t == 0);
-            __syncwarp();
+            if (need(0, v_tile)) {
+                if (!(ok = warp_wait(BAR(B_PFULL + 0), n_p0 & 1, abort_flag))) break;
+                tc_fence_after();
+                issue_pv(0, vi % NSL, n_p0 == 0);
+                ++n_p0;
+                __syncwarp();
+            }
             if (has_next) {
-                if (two_tiles) {
-                    if (!(ok = warp_wait(BAR(B_SFREE + 1), t & 1, abort_flag))) break;
+                if (need(1, w.tile)) {
+                    if (n_s1 > 0 && !(ok = warp_wait(BAR(B_SFREE + 1), (n_s1 - 1) & 1, abort_flag))) break;
                     tc_fence_after();
                     issue_s(1, ki % NSL);
+                    ++n_s1;
                 }
                 tc_commit_elect(BAR(B_SLOTE + ki % NSL));
                 __syncwarp();
             }
-            if (two_tiles) {
-                if (!(ok = warp_wait(BAR(B_PFULL + 1), t & 1, abort_flag))) break;
+            if (need(1, v_tile)) {
+                if (!(ok = warp_wait(BAR(B_PFULL + 1), n_p1 & 1, abort_flag))) break;
                 tc_fence_after();
-                issue_pv(1, vi % NSL, t == 0);
+                issue_pv(1, vi % NSL, n_p1 == 0);
+                ++n_p1;
             }
             tc_commit_elect(BAR(B_SLOTE + vi % NSL));
             __syncwarp();
@@ -650,12 +679,22 @@ __global__ void __launch_bounds__(384, 1)
         ok = ok && warp_wait(BAR(B_QFULL), 0, abort_flag);
         if constexpr (!SKIP) {
             int t = 0;
+            Walk w = walk0;
+            if constexpr (EDGES) w.start_step();
+            const SeenTiles seen0 = seen_by(0), seen1 = seen_by(1);
+            int n0 = 0, n1 = 0;   // S products issued per Q tile
             if (ok && T > 0) {
                 ok = k_wait(0);   // K(0) is load 0
                 tc_fence_after();
                 if (ok) {
-                    issue_s(0, 0);
-                    if (two_tiles) issue_s(1, 0);
+                    if (!EDGES || seen0.has(w_tile(w))) {
+                        issue_s(0, 0);
+                        ++n0;
+                    }
+                    if (EDGES ? seen1.has(w_tile(w)) : two_tiles) {
+                        issue_s(1, 0);
+                        ++n1;
+                    }
                     tc_commit_elect(BAR(B_SLOTE + 0));
                 }
                 __syncwarp();
@@ -663,15 +702,22 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
             for (; ok && t + 1 < T; ++t) {
                 const int ki = 2 * t + 1;                    // load index of K(t+1)
+                if constexpr (EDGES) w.next();
                 if (!(ok = k_wait(ki % NSL))) break;
-                if (!(ok = warp_wait(BAR(B_SFREE + 0), t & 1, abort_flag))) break;
-                tc_fence_after();
-                issue_s(0, ki % NSL);
-                __syncwarp();
-                if (two_tiles) {
-                    if (!(ok = warp_wait(BAR(B_SFREE + 1), t & 1, abort_flag))) break;
+                if (!EDGES || seen0.has(w_tile(w))) {
+                    if ((!EDGES || n0 > 0) &&
+                        !(ok = warp_wait(BAR(B_SFREE + 0), (EDGES ? n0 - 1 : t) & 1, abort_flag))) break;
+                    tc_fence_after();
+                    issue_s(0, ki % NSL);
+                    ++n0;
+                    __syncwarp();
+                }
+                if (EDGES ? seen1.has(w_tile(w)) : two_tiles) {
+                    if ((!EDGES || n1 > 0) &&
+                        !(ok = warp_wait(BAR(B_SFREE + 1), (EDGES ? n1 - 1 : t) & 1, abort_flag))) break;
                     tc_fence_after();
                     issue_s(1, ki % NSL);
+                    ++n1;
                 }
                 tc_commit_elect(BAR(B_SLOTE + ki % NSL));
                 __syncwarp();
@@ -762,27 +808,32 @@ __global__ void __launch_bounds__(384, 1)
         if constexpr (!SKIP) {
             int t = 0;
             Walk wv = walk0;
-            if constexpr (KEYS == KEYS_PAGED) wv.start_step();
+            if constexpr (KEYS != KEYS_RING) wv.start_step();
+            const SeenTiles seen0 = seen_by(0), seen1 = seen_by(1);
+            int n0 = 0, n1 = 0;   // PV products issued per Q tile
 #pragma unroll 1
             for (; ok && t < T; ++t) {
                 const bool has_next = t + 1 < T;
                 const int vi = has_next ? 2 * t + 2 : 2 * t + 1; // load index of V(t)
                 if (!(ok = v_wait(vi % NSL))) break;
-                if constexpr (KEYS == KEYS_PAGED) {
+                if constexpr (KEYS == KEYS_PAGED)
                     zero_rows<D>(s_base + L::kRing + (vi % NSL) * L::kTile, pu.len - wv.tile * 128, lane);
-                    wv.next();
-                }
-                if (!(ok = warp_wait(BAR(B_PFULL + 0), t & 1, abort_flag))) break;
-                tc_fence_after();
-                issue_pv(0, vi % NSL, t == 0);
-                __syncwarp();
-                if (two_tiles) {
-                    if (!(ok = warp_wait(BAR(B_PFULL + 1), t & 1, abort_flag))) break;
+                if (!EDGES || seen0.has(w_tile(wv))) {
+                    if (!(ok = warp_wait(BAR(B_PFULL + 0), (EDGES ? n0 : t) & 1, abort_flag))) break;
                     tc_fence_after();
-                    issue_pv(1, vi % NSL, t == 0);
+                    issue_pv(0, vi % NSL, EDGES ? n0 == 0 : t == 0);
+                    ++n0;
+                    __syncwarp();
+                }
+                if (EDGES ? seen1.has(w_tile(wv)) : two_tiles) {
+                    if (!(ok = warp_wait(BAR(B_PFULL + 1), (EDGES ? n1 : t) & 1, abort_flag))) break;
+                    tc_fence_after();
+                    issue_pv(1, vi % NSL, EDGES ? n1 == 0 : t == 0);
+                    ++n1;
                 }
                 tc_commit_elect(BAR(B_SLOTE + vi % NSL));
                 __syncwarp();
+                if constexpr (KEYS != KEYS_RING) wv.next();
             }
         } else {
             // PV_g only for the tiles Q tile g needs; P-full waits and the
@@ -933,7 +984,12 @@ __global__ void __launch_bounds__(384, 1)
         int cur_step = -1;
         int klo = 0, khi = S;   // this row's visible local keys [klo, khi) of shard w.j
         // (t counts the tiles processed: without skipping, every tile the walk visits)
-        for (; (!SKIP || ok) && w.valid(); w.next(), t += SKIP ? 0 : 1) {
+        const SeenTiles seen_g = seen_by(g);
+        // (with EDGES, and with SKIP, t counts the tiles this Q tile took)
+        for (; (!(SKIP || EDGES) || ok) && w.valid(); w.next(), t += SKIP || EDGES ? 0 : 1) {
+            if constexpr (EDGES) {
+                if (!seen_g.has(w.tile)) continue;
+            }
             if constexpr (KEYS == KEYS_PAGED) {
                 if (g == 1 && !two_tiles) break;
                 if (!warp_live) {
@@ -995,9 +1051,12 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             if (32 * q >= lo_max && 32 * q + 32 <= hi_min) continue;
+                            // bit c: column 32 q + c is visible
+                            const uint32_t seen = (low_bits(lim - 32 * q) & ~low_bits(lim_lo - 32 * q)) |
+                                                  (low_bits(sk_hi - 32 * q) & ~low_bits(sk_lo - 32 * q));
 #pragma unroll
-                            for (int c = 32 * q; c < 32 * q + 32; ++c)
-                                if ((c >= lim || c < lim_lo) && (c >= sk_hi || c < sk_lo)) s[c] = -INFINITY;
+                            for (int c = 0; c < 32; ++c)
+                                if (!(seen & (1u << c))) s[32 * q + c] = -INFINITY;
                         }
                     }
                 }
@@ -1104,7 +1163,7 @@ __global__ void __launch_bounds__(384, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(BAR(B_PFULL + g));
-                if constexpr (SKIP) ++t;
+                if constexpr (SKIP || EDGES) ++t;
                 continue;
             }
             {
@@ -1127,7 +1186,7 @@ __global__ void __launch_bounds__(384, 1)
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_arrive(BAR(B_PFULL + g));
-            if constexpr (SKIP) ++t;
+            if constexpr (SKIP || EDGES) ++t;
         }
         const int T = t;
         if (!ok) {

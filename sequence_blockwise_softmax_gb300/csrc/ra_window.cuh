@@ -114,6 +114,22 @@ RA_HD RangeWalk window_unit_walk(const int *cu, int n_seqs, int S, int row0, int
     return range_walk(window_row(cu, n_seqs, S, row0, window, sinks), row_end);
 }
 
+// The key tiles that some row of a block of consecutive rows sees (its first
+// row's keys, one past its last row's position): tiles [m0, m1) and, of the
+// sinks left behind, [s0, s1).
+struct SeenTiles {
+    int m0, m1, s0, s1;
+    RA_HD bool has(int tile) const { return (tile >= m0 && tile < m1) || (tile >= s0 && tile < s1); }
+};
+RA_HD SeenTiles seen_tiles(const RowKeys &first, int last_hi) {
+    SeenTiles t;
+    t.m0 = first.lo / 128;
+    t.m1 = (last_hi + 127) / 128;
+    t.s0 = first.slo / 128;
+    t.s1 = first.shi > first.slo ? (first.shi + 127) / 128 : t.s0;
+    return t;
+}
+
 // The queries that meet a key at position t inside the window: rows [t, hi),
 // hi = t + window but not past the end of t's sequence.
 RA_HD int window_col_end(int t, int end, int window) {
