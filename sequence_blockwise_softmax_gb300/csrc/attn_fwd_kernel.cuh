@@ -144,6 +144,20 @@ struct AttnSmem {
     static constexpr uint32_t kBytesSkip = kTab + kMaxSteps * 6 * 4;
 };
 
+// How a K or V tile lies in its slot: eight rows of 128 bytes (64 columns) are
+// 1024 bytes; kGroup is the distance from one such group of rows to the next,
+// kHalf from columns 0-63 to 64-127.  A 2-D box per half gives all groups of a
+// half in a row.  Paged tiles at d = 128 interleave the halves, so that one box
+// brings a page's rows whole: half the copies of a tile of small pages (32 of
+// 2 KB at 16 tokens a page otherwise, whose issue held the tile back by 0.5 us).
+template <int D, bool INTERLEAVED>
+struct KvTile {
+    static constexpr uint32_t kGroup = INTERLEAVED ? 2048 : 1024;
+    static constexpr uint32_t kHalf = INTERLEAVED ? 1024 : 128 * 128;
+    static constexpr uint32_t kH = kHalf >> 4;            // descriptor units
+    static constexpr uint32_t kStep = 2 * kGroup >> 4;    // 16 rows
+};
+
 // The key tiles of a unit's walk as the tile-skipping variant sees them: the
 // walk visits tiles [lo, hi) of each step's shard in step order, and Q tile g
 // needs only tiles [glo_g, ghi_g) of them.  With no table (more steps than it
@@ -197,13 +211,15 @@ constexpr float kSumLo = 0x1p-32f, kSumHi = 0x1p32f;
 // by one warp before it issues the products that read them: what lies behind a
 // sequence's last token was never written and may hold NaN, which P = 0 would
 // not remove.
-template <int D>
+template <int D, class Tile>
 __device__ __forceinline__ void zero_rows(uint32_t tile, int from, int lane) {
     if (from >= 128) return;
     for (int e = max(from, 0) * 8 + lane; e < 128 * 8; e += 32)
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + c * 128 * 128 + e * 16), "r"(0)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             tile + c * Tile::kHalf + (e >> 6) * Tile::kGroup + (e & 63) * 16),
+                         "r"(0)
                          : "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
@@ -236,6 +252,7 @@ __global__ void __launch_bounds__(384, 1)
     static_assert(!SKIP || TWO_ISSUERS, "tile skipping is built on the two-issuer pipeline");
     static_assert(!SKIP || KEYS == KEYS_RING, "tile skipping is a variant of the ring sweep");
     using Walk = typename std::conditional<KEYS == KEYS_RING, TileWalk, RangeWalk>::type;
+    using KT = KvTile<D, KEYS == KEYS_PAGED && D == 128>;
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw;
@@ -424,9 +441,11 @@ __global__ void __launch_bounds__(384, 1)
                 __syncwarp();
                 if (lane * args.page_box < 128) {
                     const int y = (wtile * 128 + lane * args.page_box) & (args.seqs.page - 1);
-                    for (int c = 0; c < HALVES; ++c)
-                        tma_load_3d(dst + c * L::kBox + lane * args.page_box * 128, is_k ? &tmk : &tmv, full,
-                                    xkv + 64 * c, y, wj);
+                    const uint32_t to = dst + (lane * args.page_box >> 3) * KT::kGroup;
+                    if constexpr (HALVES == 2)
+                        tma_load_5d(to, is_k ? &tmk : &tmv, full, 0, 0, 2 * h, y >> 3, wj);
+                    else
+                        tma_load_3d(to, is_k ? &tmk : &tmv, full, xkv, y, wj);
                 }
             } else if (lane == 0 && !withhold) {
                 const uint32_t dst = s_base + L::kRing + sl * L::kTile;
@@ -497,8 +516,8 @@ __global__ void __launch_bounds__(384, 1)
                                 sdesc_sw128(s_base + L::kQ + L::kTile, 16, 1024)};
         const uint64_t dp[2] = {sdesc_sw128(s_base + L::kP, 16, 1024),
                                 sdesc_sw128(s_base + L::kP + 2 * L::kBox, 16, 1024)};
-        const uint64_t dk0 = sdesc_sw128(s_base + L::kRing, 16, 1024);
-        const uint64_t dv0 = sdesc_sw128(s_base + L::kRing, L::kBox, 1024);
+        const uint64_t dk0 = sdesc_sw128(s_base + L::kRing, 16, KT::kGroup);
+        const uint64_t dv0 = sdesc_sw128(s_base + L::kRing, KT::kHalf, KT::kGroup);
         auto issue_s = [&](int g, int slot) {
             const uint64_t a0 = dq[g], b0 = dk0 + (uint64_t)(slot * (L::kTile >> 4));
             const uint32_t d = tmem + g * 128;
@@ -507,11 +526,11 @@ __global__ void __launch_bounds__(384, 1)
             mma_ss_elect<4, 4>(d, a0, b0, IDESC_S, 1u);
             mma_ss_elect<6, 6>(d, a0, b0, IDESC_S, 1u);
             if (D == 128) {
-                constexpr uint32_t h = L::kBox >> 4;
-                mma_ss_elect<h, h>(d, a0, b0, IDESC_S, 1u);
-                mma_ss_elect<h + 2, h + 2>(d, a0, b0, IDESC_S, 1u);
-                mma_ss_elect<h + 4, h + 4>(d, a0, b0, IDESC_S, 1u);
-                mma_ss_elect<h + 6, h + 6>(d, a0, b0, IDESC_S, 1u);
+                constexpr uint32_t h = L::kBox >> 4, kh = KT::kH;
+                mma_ss_elect<h, kh>(d, a0, b0, IDESC_S, 1u);
+                mma_ss_elect<h + 2, kh + 2>(d, a0, b0, IDESC_S, 1u);
+                mma_ss_elect<h + 4, kh + 4>(d, a0, b0, IDESC_S, 1u);
+                mma_ss_elect<h + 6, kh + 6>(d, a0, b0, IDESC_S, 1u);
             }
             tc_commit_elect(BAR(B_SFULL + g));
         };
@@ -596,7 +615,7 @@ __global__ void __launch_bounds__(384, 1)
             }
             if (!(ok = v_wait(vi % NSL))) break;
             if constexpr (KEYS == KEYS_PAGED)
-                zero_rows<D>(s_base + L::kRing + (vi % NSL) * L::kTile, pu.len - v_tile * 128, lane);
+                zero_rows<D, KT>(s_base + L::kRing + (vi % NSL) * L::kTile, pu.len - v_tile * 128, lane);
             if (need(0, v_tile)) {
                 if (!(ok = warp_wait(BAR(B_PFULL + 0), n_p0 & 1, abort_flag))) break;
                 tc_fence_after();
@@ -649,7 +668,7 @@ __global__ void __launch_bounds__(384, 1)
         // elect.sync picks the issuing lane.
         const uint64_t dq[2] = {sdesc_sw128(s_base + L::kQ, 16, 1024),
                                 sdesc_sw128(s_base + L::kQ + L::kTile, 16, 1024)};
-        const uint64_t dk0 = sdesc_sw128(s_base + L::kRing, 16, 1024);
+        const uint64_t dk0 = sdesc_sw128(s_base + L::kRing, 16, KT::kGroup);
         auto issue_s = [&](int g, int slot) {
             const uint64_t a0 = dq[g], b0 = dk0 + (uint64_t)(slot * (L::kTile >> 4));
             const uint32_t d = tmem + g * 128;
@@ -658,11 +677,11 @@ __global__ void __launch_bounds__(384, 1)
             mma_ss_elect<4, 4>(d, a0, b0, IDESC_S, 1u);
             mma_ss_elect<6, 6>(d, a0, b0, IDESC_S, 1u);
             if (D == 128) {
-                constexpr uint32_t h = L::kBox >> 4;
-                mma_ss_elect<h, h>(d, a0, b0, IDESC_S, 1u);
-                mma_ss_elect<h + 2, h + 2>(d, a0, b0, IDESC_S, 1u);
-                mma_ss_elect<h + 4, h + 4>(d, a0, b0, IDESC_S, 1u);
-                mma_ss_elect<h + 6, h + 6>(d, a0, b0, IDESC_S, 1u);
+                constexpr uint32_t h = L::kBox >> 4, kh = KT::kH;
+                mma_ss_elect<h, kh>(d, a0, b0, IDESC_S, 1u);
+                mma_ss_elect<h + 2, kh + 2>(d, a0, b0, IDESC_S, 1u);
+                mma_ss_elect<h + 4, kh + 4>(d, a0, b0, IDESC_S, 1u);
+                mma_ss_elect<h + 6, kh + 6>(d, a0, b0, IDESC_S, 1u);
             }
             tc_commit_elect(BAR(B_SFULL + g));
         };
@@ -779,19 +798,20 @@ __global__ void __launch_bounds__(384, 1)
         regs_shrink<LOW_REGS>();
         const uint64_t dp[2] = {sdesc_sw128(s_base + L::kP, 16, 1024),
                                 sdesc_sw128(s_base + L::kP + 2 * L::kBox, 16, 1024)};
-        const uint64_t dv0 = sdesc_sw128(s_base + L::kRing, L::kBox, 1024);
+        const uint64_t dv0 = sdesc_sw128(s_base + L::kRing, KT::kHalf, KT::kGroup);
         auto issue_pv = [&](int g, int slot, bool first) {
             constexpr uint32_t hb = L::kBox >> 4;
             const uint64_t a0 = dp[g], b0 = dv0 + (uint64_t)(slot * (L::kTile >> 4));
             const uint32_t d = tmem + 256 + g * D;
+            constexpr uint32_t vs = KT::kStep;
             mma_ss_elect<0, 0>(d, a0, b0, IDESC_O, first ? 0u : 1u);
-            mma_ss_elect<2, 128>(d, a0, b0, IDESC_O, 1u);
-            mma_ss_elect<4, 256>(d, a0, b0, IDESC_O, 1u);
-            mma_ss_elect<6, 384>(d, a0, b0, IDESC_O, 1u);
-            mma_ss_elect<hb, 512>(d, a0, b0, IDESC_O, 1u);
-            mma_ss_elect<hb + 2, 640>(d, a0, b0, IDESC_O, 1u);
-            mma_ss_elect<hb + 4, 768>(d, a0, b0, IDESC_O, 1u);
-            mma_ss_elect<hb + 6, 896>(d, a0, b0, IDESC_O, 1u);
+            mma_ss_elect<2, vs>(d, a0, b0, IDESC_O, 1u);
+            mma_ss_elect<4, 2 * vs>(d, a0, b0, IDESC_O, 1u);
+            mma_ss_elect<6, 3 * vs>(d, a0, b0, IDESC_O, 1u);
+            mma_ss_elect<hb, 4 * vs>(d, a0, b0, IDESC_O, 1u);
+            mma_ss_elect<hb + 2, 5 * vs>(d, a0, b0, IDESC_O, 1u);
+            mma_ss_elect<hb + 4, 6 * vs>(d, a0, b0, IDESC_O, 1u);
+            mma_ss_elect<hb + 6, 7 * vs>(d, a0, b0, IDESC_O, 1u);
             tc_commit_elect(BAR(B_PVDONE + g));
         };
         uint32_t v_parity = 0;   // bit s: parity of the next V load of slot s
@@ -817,7 +837,7 @@ __global__ void __launch_bounds__(384, 1)
                 const int vi = has_next ? 2 * t + 2 : 2 * t + 1; // load index of V(t)
                 if (!(ok = v_wait(vi % NSL))) break;
                 if constexpr (KEYS == KEYS_PAGED)
-                    zero_rows<D>(s_base + L::kRing + (vi % NSL) * L::kTile, pu.len - wv.tile * 128, lane);
+                    zero_rows<D, KT>(s_base + L::kRing + (vi % NSL) * L::kTile, pu.len - wv.tile * 128, lane);
                 if (!EDGES || seen0.has(w_tile(wv))) {
                     if (!(ok = warp_wait(BAR(B_PFULL + 0), (EDGES ? n0 : t) & 1, abort_flag))) break;
                     tc_fence_after();

@@ -196,14 +196,24 @@ ra_status check(const Paged &a) {
 }
 
 // ------------------------------------------------------------------ launch
+// Pages of [page, H_kv, d], in boxes of `box` tokens of one head (KvTile).
+// d = 64: {columns, tokens, pages}.  d = 128: {64 columns, 8 tokens, halves of
+// all heads, groups of 8 tokens, pages}, a box holding both halves.
 bool page_map(CUtensorMap *map, const void *base, const Paged &a, int box) {
     EncodeTiledFn enc = get_encode_fn();
     if (!enc) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)(a.H_kv * a.d), (cuuint64_t)a.page, (cuuint64_t)a.n_pages};
-    cuuint64_t strides[2] = {(cuuint64_t)(a.H_kv * a.d * 2), (cuuint64_t)(a.page_stride * 2)};
-    cuuint32_t bx[3] = {64, (cuuint32_t)box, 1}, estr[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, bx, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint64_t token = (cuuint64_t)(a.H_kv * a.d * 2), page = (cuuint64_t)(a.page_stride * 2);
+    const cuuint64_t dims3[3] = {(cuuint64_t)(a.H_kv * a.d), (cuuint64_t)a.page, (cuuint64_t)a.n_pages};
+    const cuuint64_t strides3[2] = {token, page};
+    const cuuint32_t box3[3] = {64, (cuuint32_t)box, 1};
+    const cuuint64_t dims5[5] = {64, 8, (cuuint64_t)(2 * a.H_kv), (cuuint64_t)(a.page / 8), (cuuint64_t)a.n_pages};
+    const cuuint64_t strides5[4] = {token, 128, 8 * token, page};
+    const cuuint32_t box5[5] = {64, 8, 2, (cuuint32_t)(box / 8), 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    const bool halves = a.d == 128;
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, halves ? 5 : 3, const_cast<void *>(base), halves ? dims5 : dims3,
+               halves ? strides5 : strides3, halves ? box5 : box3, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
