@@ -562,12 +562,13 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &tmq, const CUtens
                         for (int c = 0; c < 32; ++c)
                             if (c0 + c >= lim || c0 + c < lim_lo) sv[c] = __float_as_uint(-INFINITY);
                     } else {
-                        // windowed rows also see the sink columns [sk_lo, sk_hi)
+                        // windowed rows also see the sink columns [sk_lo, sk_hi); bit c: column c0 + c is visible
                         const int sk_lo = rk.slo - w.tile * 128, sk_hi = rk.shi - w.tile * 128;
+                        const uint32_t seen = (low_bits(lim - c0) & ~low_bits(lim_lo - c0)) |
+                                              (low_bits(sk_hi - c0) & ~low_bits(sk_lo - c0));
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
-                            if ((c0 + c >= lim || c0 + c < lim_lo) && (c0 + c >= sk_hi || c0 + c < sk_lo))
-                                sv[c] = __float_as_uint(-INFINITY);
+                            if (!(seen & (1u << c))) sv[c] = __float_as_uint(-INFINITY);
                     }
                 }
 #pragma unroll
@@ -971,12 +972,21 @@ __device__ __forceinline__ void bwd_dkv_body(const CUtensorMap &tmq, const CUten
             // exponential loop below stays one block the compiler can schedule
             if (lim < 128 || lim_lo > 0) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < 2; ++j) {
+                    if constexpr (KEYS == BWD_RING) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const int col = 64 * hh + 32 * j + c;
-                        if (col >= lim || col < lim_lo) pv[j][c] = __float_as_uint(-INFINITY);
+                        for (int c = 0; c < 32; ++c) {
+                            const int col = 64 * hh + 32 * j + c;
+                            if (col >= lim || col < lim_lo) pv[j][c] = __float_as_uint(-INFINITY);
+                        }
+                    } else {
+                        const int first = 64 * hh + 32 * j;
+                        const uint32_t seen = low_bits(lim - first) & ~low_bits(lim_lo - first);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!(seen & (1u << c))) pv[j][c] = __float_as_uint(-INFINITY);
                     }
+                }
             }
             const uint64_t sl2x2 = f32x2(sl2, sl2);
             // P^T stays in registers only as the packed bf16 the dV product uses

@@ -84,7 +84,7 @@ struct AttnArgs {
     // KEYS_PAGED: the sequences and pages; the parts' rows when the keys are
     // split, [units, H_kv, num_splits, rows of a unit, d], and their LSE
     PagedSeqs seqs;
-    int n_units, tile_tokens, page_box;
+    int n_units, tile_tokens, page_box, o_bf16;
     float *part_o, *part_lse;
 };
 
@@ -280,6 +280,7 @@ __global__ void __launch_bounds__(384, 1)
     UnitId unit{};
     PagedUnit pu{};
     int part = 0;             // KEYS_PAGED: which part of the unit's keys
+    bool split = false;       // ... and whether there is more than one
     int unit_no = 0;
     if constexpr (KEYS == KEYS_PAGED) {
         // blockIdx.x = (hk * num_splits + part) * n_units + unit, a sequence's
@@ -313,7 +314,9 @@ __global__ void __launch_bounds__(384, 1)
     else {
         walk0 = paged_walk(args.seqs, pu);
         if (args.seqs.num_splits > 1) {
-            if (part >= paged_split_count(args.seqs, walk0.end)) return;
+            const int parts = paged_split_count(args.seqs, walk0.end);
+            if (part >= parts) return;
+            split = parts > 1;
             const int per = paged_split_tiles(args.seqs, walk0.end);
             walk0.i = part * per;
             walk0.end = min(walk0.end, walk0.i + per);
@@ -1270,8 +1273,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         if constexpr (KEYS == KEYS_PAGED) {
             // each warp copies its own rows out: final rows of [T, H, d], or
-            // this part's rows for the join
-            const bool split = args.seqs.num_splits > 1;
+            // this part's rows (fp32) for the join
             const float lse = l > 0.f ? (m_ref + lg2(l)) * 0.6931471805599453f : -INFINITY;
             const int head = h * args.seqs.group + r % args.seqs.group;
             long long at = -1;       // the row's first element
@@ -1285,21 +1287,35 @@ __global__ void __launch_bounds__(384, 1)
                 else if (args.lse) args.lse[(size_t)head * args.seqs.T + tok] = lse;
             }
             __syncwarp();
+            auto staged = [&](int row, int ch) -> uint4 {     // 16-byte chunk ch of the warp's row
+                const int rr = wq * 32 + row;
+                const uint32_t src = box_addr(ch >> 3) + (rr >> 3) * 1024 + (rr & 7) * 128 + (((ch & 7) ^ (rr & 7)) << 4);
+                uint4 x;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(src) : "memory");
+                return x;
+            };
+            // rows of the staged type, or (a unit of one part in a split call) rounded to bf16 here
+            const bool round = OUT_F32 && args.o_bf16 && !split;
             uint8_t *out = split ? reinterpret_cast<uint8_t *>(args.part_o) : static_cast<uint8_t *>(args.o);
-            constexpr int ESZ = OUT_F32 ? 4 : 2;
-            constexpr int CPR = D * ESZ / 16;        // 16-byte chunks per row
+            const int esz = OUT_F32 && !round ? 4 : 2;
+            const int cpr = D * esz / 16;            // 16-byte chunks per row
             if (warp_live && *abort_flag == 0) {
 #pragma unroll 4
-                for (int e = lane; e < 32 * CPR; e += 32) {
-                    const int row = e / CPR, ch = e % CPR;
+                for (int e = lane; e < 32 * cpr; e += 32) {
+                    const int row = e / cpr, ch = e % cpr;
                     const long long dst = __shfl_sync(0xffffffffu, at, row);
-                    const int rr = wq * 32 + row;
-                    const uint32_t src = box_addr(ch >> 3) + (rr >> 3) * 1024 + (rr & 7) * 128 + (((ch & 7) ^ (rr & 7)) << 4);
-                    uint32_t x0, x1, x2, x3;
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3) : "r"(src) : "memory");
-                    if (dst >= 0)
-                        *reinterpret_cast<uint4 *>(out + (size_t)dst * ESZ + ch * 16) = make_uint4(x0, x1, x2, x3);
+                    uint4 x;
+                    if (round) {
+                        const uint4 lo = staged(row, 2 * ch), hi = staged(row, 2 * ch + 1);
+                        x.x = pack_bf16x2(__uint_as_float(lo.x), __uint_as_float(lo.y));
+                        x.y = pack_bf16x2(__uint_as_float(lo.z), __uint_as_float(lo.w));
+                        x.z = pack_bf16x2(__uint_as_float(hi.x), __uint_as_float(hi.y));
+                        x.w = pack_bf16x2(__uint_as_float(hi.z), __uint_as_float(hi.w));
+                    } else {
+                        x = staged(row, ch);
+                    }
+                    if (dst >= 0) *reinterpret_cast<uint4 *>(out + (size_t)dst * esz + ch * 16) = x;
                 }
             }
         }

@@ -33,9 +33,10 @@ ra_status launch_error() {
 }
 
 // ------------------------------------------------------------------ join
-// One warp per (token, head): O = sum_i w_i O_i, w_i = exp(LSE_i - LSE).  The
-// parts are read in order, so the result does not depend on timing.  Bound by
-// the parts' bytes, most of which are still in L2.
+// O = sum_i w_i O_i, w_i = exp(LSE_i - LSE), over a row's parts in order, so
+// that the result does not depend on timing; rows of one part were written by
+// the forward itself.  D / 4 lanes per row, 8 parts on their way at once:
+// bound by the parts' bytes, most of which are still in L2.
 struct JoinArgs {
     PagedSeqs seqs;
     const float *part_o, *part_lse;
@@ -47,10 +48,11 @@ struct JoinArgs {
 template <int D>
 __global__ void __launch_bounds__(256) paged_join_kernel(const JoinArgs a) {
     const PagedSeqs &q = a.seqs;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    constexpr int LANES = D / 4, AHEAD = 8;
+    const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LANES;
+    const int col = threadIdx.x % LANES * 4;
     if (row >= (int64_t)q.T * q.H) return;
-    const int tok = (int)(row / q.H), head = (int)(row % q.H);
+    const int tok = (int)(row / q.H), head = (int)(row - (int64_t)tok * q.H);
     // the last sequence starting at or before the token
     int lo = 0, hi = q.n_seqs;
     while (hi - lo > 1) {
@@ -63,35 +65,49 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const JoinArgs a) {
     const int local = i / q.unit_tokens;
     const PagedUnit u = paged_unit(q, lo, local);
     const int parts = paged_split_count(q, paged_walk(q, u).end);
+    if (parts == 1) return;
     const size_t rows = paged_unit_rows(q);
     const size_t unit = (size_t)paged_first_unit(q, lo) + local;
     const size_t first = ((unit * q.Hkv + head / q.group) * q.num_splits) * rows +
                          (size_t)(i - u.first) * q.group + head % q.group;
-    float m = -INFINITY;
-    for (int p = 0; p < parts; ++p) m = fmaxf(m, a.part_lse[first + p * rows]);
-    constexpr int PER = D / 32;
-    float acc[PER] = {};
-    float sum = 0.f;
-    if (m > -INFINITY) {
-        for (int p = 0; p < parts; ++p) {
-            const float w = ex2((a.part_lse[first + p * rows] - m) * 1.4426950408889634f);
-            const float *src = a.part_o + (first + p * rows) * D + lane * PER;
-            sum += w;
+    float x[4] = {}, top = -INFINITY, sum = 0.f;
+    for (int p0 = 0; p0 < parts; p0 += AHEAD) {
+        float l[AHEAD];
+        float4 f[AHEAD];
 #pragma unroll
-            for (int e = 0; e < PER; ++e) acc[e] += w * src[e];
+        for (int j = 0; j < AHEAD; ++j) {
+            const size_t at = first + min(p0 + j, parts - 1) * rows;
+            l[j] = a.part_lse[at];
+            f[j] = *reinterpret_cast<const float4 *>(a.part_o + at * D + col);
         }
+        float t2 = top;
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) t2 = fmaxf(t2, l[j]);
+        if (!(t2 > -INFINITY)) continue;
+        const float old = ex2((top - t2) * 1.4426950408889634f);
+        x[0] *= old, x[1] *= old, x[2] *= old, x[3] *= old;
+        sum *= old;
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            if (p0 + j >= parts) break;
+            const float w = ex2((l[j] - t2) * 1.4426950408889634f);
+            x[0] += f[j].x * w;
+            x[1] += f[j].y * w;
+            x[2] += f[j].z * w;
+            x[3] += f[j].w * w;
+            sum += w;
+        }
+        top = t2;
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    if (a.o_bf16) {
-        uint32_t *dst = static_cast<uint32_t *>(a.o) + (row * D + lane * PER) / 2;
-#pragma unroll
-        for (int e = 0; e < PER; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    } else {
-        float *dst = static_cast<float *>(a.o) + row * D + lane * PER;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) dst[e] = acc[e] * inv;
-    }
-    if (lane == 0 && a.lse) a.lse[(size_t)head * q.T + tok] = sum > 0.f ? m + lg2(sum) * 0.6931471805599453f : -INFINITY;
+    if (a.o_bf16)
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + row * D + col) =
+            make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+    else
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + row * D + col) =
+            make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    if (col == 0 && a.lse)
+        a.lse[(size_t)head * q.T + tok] = sum > 0.f ? top + lg2(sum) * 0.6931471805599453f : -INFINITY;
 }
 
 // ------------------------------------------------------------------ plan
@@ -311,6 +327,7 @@ ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, co
     args.n_units = (int)p.units;
     args.tile_tokens = p.tile_tokens;
     args.page_box = (int)(a.page < 128 ? a.page : 128);
+    args.o_bf16 = o_bf16 ? 1 : 0;
     args.part_o = reinterpret_cast<float *>(workspace + p.part_o);
     args.part_lse = reinterpret_cast<float *>(workspace + p.part_lse);
     const bool f32 = p.splits > 1 || !o_bf16;
@@ -318,7 +335,7 @@ ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, co
                              : launch_chunks<D, false>(a, p, args, q, k, v, stream);
     if (st != RA_OK || p.splits == 1) return st;
     JoinArgs j{args.seqs, args.part_o, args.part_lse, o, lse, o_bf16 ? 1 : 0};
-    const int64_t blocks = (a.T * a.H + 7) / 8;
+    const int64_t per_block = 256 / (D / 4), blocks = (a.T * a.H + per_block - 1) / per_block;
     paged_join_kernel<D><<<(unsigned)blocks, 256, 0, stream>>>(j);
     return launch_error();
 }
