@@ -355,6 +355,23 @@ __global__ void __launch_bounds__(384, 1)
         mbar_init(BAR(B_TCOUNT), 1);
         *abort_flag = 0;
         fence_mbar_init();
+        if constexpr (KEYS == KEYS_WINDOW) {
+            // Q and K(0) are on their way before tensor memory is allocated and
+            // the roles start: short units live by their prologue
+            mbar_arrive_expect_tx(BAR(B_QFULL), 2 * L::kTile);
+            for (int g = 0; g < 2; ++g)
+                for (int c = 0; c < HALVES; ++c)
+                    tma_load_4d(s_base + L::kQ + g * L::kTile + c * L::kBox, &tmq, BAR(B_QFULL), h * D + 64 * c,
+                                row0 + 128 * g, b, 0);
+            if (walk0.valid()) {
+                Walk w0 = walk0;
+                w0.start_step();
+                mbar_arrive_expect_tx(BAR(B_KF), L::kTile);
+                for (int c = 0; c < HALVES; ++c)
+                    tma_load_4d(s_base + L::kRing + c * L::kBox, &tmk, BAR(B_KF), (h / args.kv_group) * D + 64 * c,
+                                w0.tile * 128, b, 0);
+            }
+        }
     }
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmq);
@@ -391,7 +408,7 @@ __global__ void __launch_bounds__(384, 1)
                         tma_load_3d(s_base + L::kQ + g * L::kTile + c * L::kBox, &tmq, BAR(B_QFULL), 64 * c,
                                     h * args.seqs.group, pu.t0 + g * args.tile_tokens);
             }
-        } else if (lane == 0) {
+        } else if (KEYS == KEYS_RING && lane == 0) {
             mbar_arrive_expect_tx(BAR(B_QFULL), 2 * L::kTile);
             for (int g = 0; g < 2; ++g) {
                 int c1, c2, c3;
@@ -450,7 +467,7 @@ __global__ void __launch_bounds__(384, 1)
                     else
                         tma_load_3d(to, is_k ? &tmk : &tmv, full, xkv, y, wj);
                 }
-            } else if (lane == 0 && !withhold) {
+            } else if (lane == 0 && !withhold && !(KEYS == KEYS_WINDOW && i == 0)) {   // (K(0): issued in the setup)
                 const uint32_t dst = s_base + L::kRing + sl * L::kTile;
                 int c1, c2, c3;
                 tile_coords(args.seq_order, args.layout, args.S, args.N, ring ? wj : 0, b, wtile * 128, c1, c2, c3);
