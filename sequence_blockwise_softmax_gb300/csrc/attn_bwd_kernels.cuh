@@ -371,6 +371,7 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &tmq, const CUtens
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if constexpr (KEYS == BWD_WINDOW) pdl_wait();   // D comes from the kernel before
 
     if (warp == 0) {
         // ------------------------------------------------ producer
@@ -714,7 +715,10 @@ __device__ __forceinline__ void bwd_dkv_body(const CUtensorMap &tmq, const CUten
         unit.qi = 0;
         unit.qt = u;
         // no query of the chunk lies past the first key's window
-        if (c_end <= c0 || max(su.lo, c0 + args.window) >= su.hi) return;
+        if (c_end <= c0 || max(su.lo, c0 + args.window) >= su.hi) {
+            pdl_wait();
+            return;
+        }
     } else {
         unit = decode_key_block(KEYS == BWD_WINDOW ? block - args.n_far : block, args.bh_chunk_kv, args.B, Hkv, N,
                                 args.n_tiles_seq, args.layout);
@@ -768,6 +772,7 @@ __device__ __forceinline__ void bwd_dkv_body(const CUtensorMap &tmq, const CUten
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if constexpr (KEYS == BWD_WINDOW) pdl_wait();   // D comes from the kernel before
 
     if (warp == 0) {
         // ------------------------------------------------ producer
@@ -1153,6 +1158,7 @@ template <int D>
 __global__ void __launch_bounds__(256) bwd_sink_join(const BwdArgs a) {
     constexpr int PER = D / 32, AHEAD = 8;
     const int lane = threadIdx.x & 31;
+    pdl_wait();
     int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int r = (int)(w % a.sinks);
     w /= a.sinks;
@@ -1207,6 +1213,7 @@ template <int D, bool O_BF16>
 __global__ void __launch_bounds__(256) bwd_window_dot(const uint16_t *dout, const void *o, float *dvec, int64_t rows,
                                                       int H, int64_t S) {
     constexpr int LANES = D / 8, PER_WARP = 32 / LANES, R = 4;
+    pdl_launch_dependents();
     const int lane = threadIdx.x & 31, sub = lane % LANES;
     const int64_t r0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * PER_WARP * R + lane / LANES;
     uint4 dv[R], ov[R][O_BF16 ? 1 : 2];

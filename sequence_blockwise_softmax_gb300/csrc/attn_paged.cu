@@ -11,6 +11,7 @@
 
 #include "attn_fwd_kernel.cuh"
 #include "paged_launch.h"
+#include "ra_launch.h"
 #include "ra_tensor_map.h"
 
 namespace ra {
@@ -49,6 +50,7 @@ template <int D>
 __global__ void __launch_bounds__(256) paged_join_kernel(const JoinArgs a) {
     const PagedSeqs &q = a.seqs;
     constexpr int LANES = D / 4, AHEAD = 8;
+    pdl_wait();
     const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LANES;
     const int col = threadIdx.x % LANES * 4;
     if (row >= (int64_t)q.T * q.H) return;
@@ -336,8 +338,8 @@ ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, co
     if (st != RA_OK || p.splits == 1) return st;
     JoinArgs j{args.seqs, args.part_o, args.part_lse, o, lse, o_bf16 ? 1 : 0};
     const int64_t per_block = 256 / (D / 4), blocks = (a.T * a.H + per_block - 1) / per_block;
-    paged_join_kernel<D><<<(unsigned)blocks, 256, 0, stream>>>(j);
-    return launch_error();
+    const cudaError_t e = launch_dependent(paged_join_kernel<D>, (unsigned)blocks, 256, 0, stream, j);
+    return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
 }
 
 // ------------------------------------------------------------------ append

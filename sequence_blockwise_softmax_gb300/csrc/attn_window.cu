@@ -7,6 +7,7 @@
 
 #include "attn_bwd_kernels.cuh"
 #include "attn_fwd_kernel.cuh"
+#include "ra_launch.h"
 #include "ra_tensor_map.h"
 
 namespace ra {
@@ -168,9 +169,12 @@ ra_status launch_bwd(const Window &w, const void *q, const void *k, const void *
         return set_error(RA_ERR_UNSUPPORTED, "too many rows for one launch");
     dot<<<(unsigned)((rows + per_block - 1) / per_block), 256, 0, stream>>>(
         static_cast<const uint16_t *>(dout), o, reinterpret_cast<float *>(workspace + space.dvec), rows, a.H, w.L);
-    kern<<<(unsigned)(n_far + n_kv + n_q), 384, smem, stream>>>(mq, mk, mv, mdo, a);
-    if (joins > 0) bwd_sink_join<D><<<(unsigned)((joins + 7) / 8), 256, 0, stream>>>(a);
-    return launch_error();
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess)
+        e = launch_dependent(kern, (unsigned)(n_far + n_kv + n_q), 384, smem, stream, mq, mk, mv, mdo, a);
+    if (e == cudaSuccess && joins > 0)
+        e = launch_dependent(bwd_sink_join<D>, (unsigned)((joins + 7) / 8), 256, 0, stream, a);
+    return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
 }
 
 }  // namespace

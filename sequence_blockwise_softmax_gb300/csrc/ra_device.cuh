@@ -318,6 +318,14 @@ __device__ __forceinline__ void regs_grow() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Programmatic dependent launch: a kernel launched with launch_dependent()
+// (ra_launch.h) may start while the kernel before it in the stream still runs,
+// once every block of that one has called or exited; pdl_wait() returns when it
+// has finished and its writes are visible.  Every block of such a kernel
+// waits, also one with nothing to do.
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // --------------------------------------------------------------- math
 // Two fp32 lanes in one 64-bit register, for the paired f32x2 instructions.
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {

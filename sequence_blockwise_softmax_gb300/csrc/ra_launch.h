@@ -1,0 +1,25 @@
+// ra_launch.h -- launching a kernel that may start before its predecessor ends.
+#pragma once
+#include <cuda_runtime.h>
+
+namespace ra {
+
+// Launch `kern` so that its blocks may start while the stream's previous kernel
+// still runs (see pdl_wait in ra_device.cuh).
+template <class... P, class... A>
+inline cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                                    const A &...args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
+}  // namespace ra
