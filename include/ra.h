@@ -408,7 +408,8 @@ RA_API size_t ra_window_attn_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H
  * get; it only guides how the keys are split (any value gives the same results
  * up to the rounding of the join).  scale <= 0: 1 / sqrt(d).
  * workspace: ra_paged_attn_workspace_bytes() bytes, zero-filled before its
- * first use; calls that may overlap on the GPU need one each.
+ * first use; calls that may overlap on the GPU need one each.  Calls of this
+ * and of other entry points may take turns with one workspace.
  */
 RA_API ra_status ra_paged_attn_fwd(const void *q, const void *k_pages, const void *v_pages,
                                    const int32_t *block_table, const int32_t *seq_lens,

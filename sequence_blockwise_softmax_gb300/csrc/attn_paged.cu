@@ -20,10 +20,8 @@ namespace {
 constexpr size_t kHeader = RA_WORKSPACE_MIN_BYTES;
 constexpr int kSms = 152;               // GB300; only the choice of a split depends on it
 constexpr size_t kPartBytes = (64u << 20) - (16u << 10);   // most bytes of a call's parts
-// The few-row kernel's counters, in a place of their own: they are zero
-// between calls, whatever form the calls take.
-constexpr size_t kCounters = kHeader, kCounterBytes = 4096;
-static_assert(kPagedTokensCtas * 4 <= kCounterBytes, "one counter per CTA");
+constexpr size_t kCounters = kHeader, kCounterBytes = 4096;   // the few-row kernel's
+static_assert(kPagedTokensCtas * 8 <= kCounterBytes, "one counter per CTA");
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -128,7 +126,13 @@ struct Plan {
     size_t part_o, part_lse, total;
 };
 
-Plan plan(const Paged &a) {
+Plan plan(Paged a) {
+    // hints of any size: nothing below leaves 64 bits
+    const int64_t cap = (int64_t)1 << 29;
+    if (a.max_new > a.T) a.max_new = a.T;
+    if (a.max_len > cap) a.max_len = cap;
+    if (a.window > cap) a.window = cap;
+    if (a.sinks > cap) a.sinks = cap;
     Plan p{};
     const int64_t group = a.H / a.H_kv;
     const int64_t active0 = a.n_seqs < a.T ? a.n_seqs : a.T;
@@ -306,7 +310,7 @@ ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, co
         t.ctas = p.ctas;
         t.scale_log2 = scale_log2;
         t.status = reinterpret_cast<unsigned *>(workspace);
-        t.counters = reinterpret_cast<int *>(workspace + kCounters);
+        t.counters = reinterpret_cast<unsigned long long *>(workspace + kCounters);
         t.part_o = reinterpret_cast<float *>(workspace + p.part_o);
         t.part_ml = reinterpret_cast<float *>(workspace + p.part_lse);
         return launch_paged_tokens(t, stream);
@@ -333,6 +337,7 @@ ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, co
     args.part_o = reinterpret_cast<float *>(workspace + p.part_o);
     args.part_lse = reinterpret_cast<float *>(workspace + p.part_lse);
     const bool f32 = p.splits > 1 || !o_bf16;
+    if (p.splits > 1 && a.T * a.H > (int64_t)1 << 31) return set_error(RA_ERR_UNSUPPORTED, "too many rows for one launch");
     const ra_status st = f32 ? launch_chunks<D, true>(a, p, args, q, k, v, stream)
                              : launch_chunks<D, false>(a, p, args, q, k, v, stream);
     if (st != RA_OK || p.splits == 1) return st;
@@ -343,57 +348,69 @@ ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, co
 }
 
 // ------------------------------------------------------------------ append
-// Row i of sequence s's n new rows goes to position seq_lens[s] - n + i.  One
-// thread per 16 bytes of a token's keys and of its values; a token's bytes are
-// one run on both sides.  Bound by HBM: 4 * H_kv * d * 2 bytes per token.
+// Row i of sequence s's n new rows goes to position seq_lens[s] - n + i.  A
+// token's bytes are one run on both sides; a block copies up to kAppendTokens
+// tokens, each thread four 16-byte pieces of keys and of values at a time.
+// Bound by HBM: 4 * H_kv * d * 2 bytes per token.
 struct AppendArgs {
     PagedSeqs seqs;
     const uint4 *k_new, *v_new;
     uint4 *k_pages, *v_pages;
-    int64_t new_stride, page_stride;   // in 16-byte chunks
-    int chunks;                        // per token
+    int64_t new_stride, page_stride;   // in 16-byte pieces
+    int pieces, tokens;                // pieces of a token, tokens of a block
     unsigned *status;
 };
 
-constexpr int kAppendThreads = 256, kAppendPer = 4;   // tokens a block copies at a time
+constexpr int kAppendThreads = 256, kAppendTokens = 32;
 
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendArgs a) {
     const PagedSeqs &q = a.seqs;
-    __shared__ int64_t dst_of[kAppendPer];
-    for (int64_t t0 = (int64_t)blockIdx.x * kAppendPer; t0 < q.T; t0 += (int64_t)gridDim.x * kAppendPer) {
-        if (threadIdx.x < kAppendPer) {
-            const int64_t t = t0 + threadIdx.x;
-            int64_t dst = -1;
-            if (t < q.T) {
-                int lo = 0, hi = q.n_seqs;
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (paged_bound(q, mid) <= t) lo = mid;
-                    else hi = mid;
-                }
-                const int c0 = paged_bound(q, lo), c1 = paged_bound(q, lo + 1);
-                if (t >= c0 && t < c1) {
-                    const int64_t pos = (int64_t)q.seq_lens[lo] - (c1 - t);
-                    int id = -1;
-                    if (pos >= 0 && pos / q.page < q.max_pages) id = q.table[(size_t)lo * q.max_pages + pos / q.page];
-                    if (id >= 0 && id < q.n_pages)
-                        dst = (int64_t)id * a.page_stride + (pos & (q.page - 1)) * a.chunks;
-                    else
-                        atomicOr(a.status, RA_DEV_PAGE_BIT);
-                }
-            }
-            dst_of[threadIdx.x] = dst;
+    __shared__ int64_t dst_of[kAppendTokens];
+    const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
+    const int n_tok = (int)min((int64_t)a.tokens, q.T - t0);
+    if ((int)threadIdx.x < n_tok) {
+        const int64_t t = t0 + threadIdx.x;
+        int64_t dst = -1;
+        int lo = 0, hi = q.n_seqs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (paged_bound(q, mid) <= t) lo = mid;
+            else hi = mid;
         }
-        __syncthreads();
-        for (int e = threadIdx.x; e < kAppendPer * a.chunks; e += kAppendThreads) {
-            const int i = e / a.chunks, c = e - i * a.chunks;
+        const int c0 = paged_bound(q, lo), c1 = paged_bound(q, lo + 1);
+        if (t >= c0 && t < c1) {
+            const int64_t pos = (int64_t)q.seq_lens[lo] - (c1 - t);
+            int id = -1;
+            if (pos >= 0 && pos / q.page < q.max_pages) id = q.table[(size_t)lo * q.max_pages + pos / q.page];
+            if (id >= 0 && id < q.n_pages) dst = (int64_t)id * a.page_stride + (pos & (q.page - 1)) * a.pieces;
+            else atomicOr(a.status, RA_DEV_PAGE_BIT);
+        }
+        dst_of[threadIdx.x] = dst;
+    }
+    __syncthreads();
+    constexpr int U = 4;
+    const int total = n_tok * a.pieces;
+    for (int e0 = threadIdx.x; e0 < total; e0 += U * kAppendThreads) {
+        uint4 k[U], v[U];
+        int64_t dst[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int e = e0 + j * kAppendThreads;
+            dst[j] = -1;
+            if (e >= total) continue;
+            const int i = e / a.pieces, c = e - i * a.pieces;
             if (dst_of[i] < 0) continue;
+            dst[j] = dst_of[i] + c;
             const int64_t src = (t0 + i) * a.new_stride + c;
-            const uint4 kv = a.k_new[src], vv = a.v_new[src];
-            a.k_pages[dst_of[i] + c] = kv;
-            a.v_pages[dst_of[i] + c] = vv;
+            k[j] = __ldcs(a.k_new + src);
+            v[j] = __ldcs(a.v_new + src);
         }
-        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (dst[j] >= 0) {
+                a.k_pages[dst[j]] = k[j];
+                a.v_pages[dst[j]] = v[j];
+            }
     }
 }
 
@@ -487,10 +504,13 @@ ra_status ra_paged_append(const void *k_new, const void *v_new, void *k_pages, v
     a.v_pages = static_cast<uint4 *>(v_pages);
     a.new_stride = new_stride / 8;
     a.page_stride = page_stride / 8;
-    a.chunks = (int)(H_kv * d / 8);
+    a.pieces = (int)(H_kv * d / 8);
     a.status = static_cast<unsigned *>(workspace);
-    int64_t blocks = (T + kAppendPer - 1) / kAppendPer;
-    if (blocks > kSms * 8) blocks = kSms * 8;
+    // about two rounds of the unrolled copy to a block, fewer tokens where that leaves SMs idle
+    int64_t per = 2 * 4 * kAppendThreads / a.pieces;
+    if (per > T / (2 * kSms)) per = T / (2 * kSms);
+    a.tokens = (int)(per < 1 ? 1 : per > kAppendTokens ? kAppendTokens : per);
+    const int64_t blocks = (T + a.tokens - 1) / a.tokens;
     paged_append_kernel<<<(unsigned)blocks, kAppendThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
     return launch_error();
 }

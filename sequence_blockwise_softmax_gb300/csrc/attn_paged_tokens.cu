@@ -21,17 +21,19 @@
 // at 6.8 TB/s an SM sees a chunk (8 KB at d = 128) every 0.18 us and needs 48
 // such products for it, a few per cent of the pipe, so the tensor pipe is not
 // what bounds this; 128-row tcgen05 tiles would spend their time on padding.
-// P enters its product as the sum of two bf16 values (about 16 bits), which
+// P enters its product as the sum of two bf16 values (ra_warp_mma.cuh), which
 // costs a second product and leaves the output's own rounding as the only one.
 //
 // Measured on a GB300 (64 sequences of 200-16000 keys, 32 / 8 heads, d = 128):
 // see the design doc's table of the operators.
+#include <atomic>
 #include <cmath>
 #include <type_traits>
 
 #include "paged_launch.h"
 #include "ra_device.cuh"
 #include "ra_paged.cuh"
+#include "ra_warp_mma.cuh"
 
 namespace ra {
 namespace {
@@ -50,7 +52,8 @@ struct TokensArgs {
     int o_bf16, whole_pairs;
     float scale_log2;
     unsigned *status;
-    int *counters;                  // one per CTA, zero between calls
+    unsigned call;                  // the call's number, another one for every call of the process
+    unsigned long long *counters;   // one per CTA: a call's number, then the pieces counted in it
     float *part_o, *part_ml;        // [2 * CTAs, 16 * MT, d], [2 * CTAs, 16 * MT, 2]
 };
 
@@ -64,33 +67,37 @@ struct TokensSmem {
     static constexpr int kRow = D + 8;                            // floats per row of the warps' O at the end
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
-                 : "memory");
+// A pair's pieces are counted in a word that also holds the call's number, so
+// that whatever other calls left in the workspace counts as nothing; the block
+// that counts the last piece sets the word back to the number and no pieces,
+// where a replay of the same call begins.
+__device__ __forceinline__ unsigned long long swap_word(unsigned long long *word, unsigned long long old,
+                                                        unsigned long long now) {
+    unsigned long long seen;
+    asm volatile("atom.cas.acq_rel.gpu.global.b64 %0, [%1], %2, %3;" : "=l"(seen) : "l"(word), "l"(old), "l"(now) : "memory");
+    return seen;
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// A block starts its own word (that of the pair whose first piece it may have)
+// as early as it can, so that later counts find the call's number there.
+__device__ __forceinline__ void start_word(unsigned long long *word, unsigned call) {
+    const unsigned long long old = *reinterpret_cast<volatile unsigned long long *>(word);
+    if ((unsigned)(old >> 32) != call) swap_word(word, old, (unsigned long long)call << 32);
 }
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// How many pieces were counted in this word before this one: one add where the
+// word has the call's number.  Where it has not, the add fell on what will be
+// replaced; whoever replaces it counts itself, the others add again.
+__device__ __forceinline__ int count_piece(unsigned long long *word, unsigned call) {
+    while (true) {
+        unsigned long long old;
+        asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], 1;" : "=l"(old) : "l"(word) : "memory");
+        if ((unsigned)(old >> 32) == call) return (int)(unsigned)old;
+        unsigned long long seen = *reinterpret_cast<volatile unsigned long long *>(word);
+        while ((unsigned)(seen >> 32) != call) {
+            old = seen;
+            seen = swap_word(word, old, ((unsigned long long)call << 32) + 1);
+            if (seen == old) return 0;
+        }
+    }
 }
 
 template <int D, int MT>
@@ -189,6 +196,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
 
     const uint32_t ring = smem_u32(smem) + warp * L::kWarp;
     const int g = lane >> 2, t4 = lane & 3;
+    bool word_started = false;
 
     // ---- one head's keys (or this run's part of them) after another
     while (true) {
@@ -199,18 +207,6 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
         // chunks inside [all_lo, all_hi) or [0, all_shi) are seen whole by every row
         const RowKeys first = paged_row(sq, cl.p0), last = paged_row(sq, cl.p0 + cl.n - 1);
         const int all_lo = last.lo, all_hi = first.hi, all_shi = first.shi > first.slo ? first.shi : 0;
-
-        float acc[MT][D / 8][4];
-        float m[MT][2], l[MT][2];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[mt][n][e] = 0.f;
-            m[mt][0] = m[mt][1] = -INFINITY;
-            l[mt][0] = l[mt][1] = 0.f;
-        }
 
         auto key_of = [&](int c) { return paged_chunk_key(cl, c); };
         const int *row_table = sq.table + (size_t)seq * sq.max_pages;
@@ -252,9 +248,12 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
             next_id = page_of(c + (s + 1) * kWarps);
             load(c + s * kWarps, s, id);
         }
+        if (!word_started && threadIdx.x == 32 * (kWarps - 1)) start_word(a.counters + cta, a.call);
+        word_started = true;
         // Q fragments, straight from global memory; rows past the unit's are zero
-        uint32_t qf[MT][KS][4];
-        RowKeys keys[MT][2];
+        WarpRows<D, MT> rw;
+        rw.clear();
+        int row_pos[MT][2];          // the rows' positions
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -262,12 +261,12 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
                 const int r = mt * 16 + h * 8 + g;
                 const bool live = r < rows;
                 const int tok = live ? r / sq.group : 0, head = live ? r - tok * sq.group : 0;
-                keys[mt][h] = paged_row(sq, cl.p0 + (live ? tok : cl.n - 1));
+                row_pos[mt][h] = cl.p0 + (live ? tok : cl.n - 1);
                 const uint16_t *src = a.q + (size_t)(cl.t0 + tok) * a.q_stride + (size_t)(hk * sq.group + head) * D + 2 * t4;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    qf[mt][ks][h] = live ? *reinterpret_cast<const uint32_t *>(src + ks * 16) : 0u;
-                    qf[mt][ks][2 + h] = live ? *reinterpret_cast<const uint32_t *>(src + ks * 16 + 8) : 0u;
+                    rw.q[mt][ks][h] = live ? *reinterpret_cast<const uint32_t *>(src + ks * 16) : 0u;
+                    rw.q[mt][ks][2 + h] = live ? *reinterpret_cast<const uint32_t *>(src + ks * 16 + 8) : 0u;
                 }
             }
         int stage = 0;
@@ -281,101 +280,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
             }
             const uint32_t sk = ring + stage * L::kStage, sv = sk + L::kHalf;
             const int k0 = key_of(c);
-            // S: 16 rows x 16 keys per row tile
-            float sc[MT][2][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.f;
-            {
-                // matrices: keys 0-7 / 8-15 by d 0-7 / 8-15 of the k-step
-                const int kk = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
-                const uint32_t row = sk + kk * (D * 2);
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    uint32_t b[4];
-                    ldmatrix4(b, row + (((ks * 2 + half) ^ (kk & 7)) << 4));
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        mma16816(sc[mt][0], qf[mt][ks], b[0], b[1]);
-                        mma16816(sc[mt][1], qf[mt][ks], b[2], b[3]);
-                    }
-                }
-            }
             const bool whole = (k0 >= all_lo && k0 + kChunk <= all_hi) || k0 + kChunk <= all_shi;
-            bool raise = false;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = sc[mt][n][e] * a.scale_log2;
-                        if (!whole) {
-                            const RowKeys &rk = keys[mt][e >> 1];
-                            const int key = k0 + n * 8 + 2 * t4 + (e & 1);
-                            if (!((key >= rk.lo && key < rk.hi) || (key >= rk.slo && key < rk.shi))) x = -INFINITY;
-                        }
-                        sc[mt][n][e] = x;
-                        raise = raise || x > m[mt][e >> 1] + 8.f;
-                    }
-            // The reference m of a row moves only when a score passes it by
-            // 2^8 (at the row's first key, then rarely): exponentials stay
-            // below 2^8 and their sums far inside 32 bits.
-            if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float x = fmaxf(fmaxf(sc[mt][0][2 * h], sc[mt][0][2 * h + 1]),
-                                        fmaxf(sc[mt][1][2 * h], sc[mt][1][2 * h + 1]));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                        const float m_new = fmaxf(m[mt][h], x);
-                        const float f = m[mt][h] > -INFINITY ? ex2(m[mt][h] - m_new) : 0.f;
-                        m[mt][h] = m_new;
-                        l[mt][h] *= f;
-#pragma unroll
-                        for (int n = 0; n < D / 8; ++n) {
-                            acc[mt][n][2 * h] *= f;
-                            acc[mt][n][2 * h + 1] *= f;
-                        }
-                    }
-            }
-            uint32_t hi[MT][4], lo[MT][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float ref = m[mt][h] > -INFINITY ? m[mt][h] : 0.f;
-                        const float p0 = ex2(sc[mt][n][2 * h] - ref), p1 = ex2(sc[mt][n][2 * h + 1] - ref);
-                        l[mt][h] += p0 + p1;
-                        const uint32_t top = pack_bf16x2(p0, p1);
-                        hi[mt][2 * n + h] = top;
-                        lo[mt][2 * n + h] = pack_bf16x2(p0 - __uint_as_float(top << 16),
-                                                        p1 - __uint_as_float(top & 0xffff0000u));
-                    }
-            {
-                // matrices: keys 0-7 / 8-15 by d 0-7 / 8-15 of a pair of column tiles
-                const int kk = (lane & 7) + (((lane >> 3) & 1) << 3), half = lane >> 4;
-                const uint32_t row = sv + kk * (D * 2);
-#pragma unroll
-                for (int n = 0; n < D / 16; ++n) {
-                    uint32_t b[4];
-                    ldmatrix4_trans(b, row + (((n * 2 + half) ^ (kk & 7)) << 4));
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        mma16816(acc[mt][2 * n], hi[mt], b[0], b[1]);
-                        mma16816(acc[mt][2 * n + 1], hi[mt], b[2], b[3]);
-                        mma16816(acc[mt][2 * n], lo[mt], b[0], b[1]);
-                        mma16816(acc[mt][2 * n + 1], lo[mt], b[2], b[3]);
-                    }
-                }
-            }
+            rw.chunk(sk, sv, a.scale_log2, whole, lane, [&](int mt, int h) {
+                const RowKeys rk = paged_row(sq, row_pos[mt][h]);
+                return seen_bits(rk.lo, rk.hi, rk.slo, rk.shi, k0);
+            });
             __syncwarp();
             stage = stage + 1 == NS ? 0 : stage + 1;
         }
@@ -385,11 +294,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 1);
-                l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 2);
+                rw.l[mt][h] += __shfl_xor_sync(0xffffffffu, rw.l[mt][h], 1);
+                rw.l[mt][h] += __shfl_xor_sync(0xffffffffu, rw.l[mt][h], 2);
                 if (t4 == 0) {
-                    s_m[warp][mt * 16 + h * 8 + g] = m[mt][h];
-                    s_l[warp][mt * 16 + h * 8 + g] = l[mt][h];
+                    s_m[warp][mt * 16 + h * 8 + g] = rw.m[mt][h];
+                    s_l[warp][mt * 16 + h * 8 + g] = rw.l[mt][h];
                 }
             }
         __syncthreads();     // every warp is past its ring too
@@ -400,11 +309,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
             for (int h = 0; h < 2; ++h) {
                 const int r = mt * 16 + h * 8 + g;
                 const float top = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
-                const float f = m[mt][h] > -INFINITY ? ex2(m[mt][h] - top) : 0.f;
+                const float f = rw.m[mt][h] > -INFINITY ? ex2(rw.m[mt][h] - top) : 0.f;
                 float *dst = warp_o + ((size_t)warp * 16 * MT + r) * L::kRow + 2 * t4;
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n)
-                    *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(acc[mt][n][2 * h] * f, acc[mt][n][2 * h + 1] * f);
+                    *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(rw.acc[mt][n][2 * h] * f, rw.acc[mt][n][2 * h + 1] * f);
             }
         __syncthreads();
         const bool begins = c_at == 0, ends = c_end == cl.count;
@@ -508,10 +417,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
             // count, the acquire the other pieces' rows after it
             __syncthreads();
             if (threadIdx.x == 0) {
-                int n;
-                asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(n) : "l"(a.counters + first_cta) : "memory");
-                s_last = n == last_cta - first_cta;
-                if (s_last) a.counters[first_cta] = 0;
+                s_last = count_piece(a.counters + first_cta, a.call) == last_cta - first_cta;
+                if (s_last) a.counters[first_cta] = (unsigned long long)a.call << 32;
             }
             __syncthreads();
             if (s_last) {
@@ -578,6 +485,8 @@ ra_status launch_paged_tokens(const TokensLaunch &t, cudaStream_t stream) {
     a.whole_pairs = t.whole_pairs;
     a.scale_log2 = t.scale_log2;
     a.status = t.status;
+    static std::atomic<unsigned> calls{0};
+    a.call = (calls.fetch_add(1, std::memory_order_relaxed) + 1u) * 2654435769u;   // spread over 32 bits
     a.counters = t.counters;
     a.part_o = t.part_o;
     a.part_ml = t.part_ml;

@@ -9,6 +9,7 @@
 #include "attn_fwd_kernel.cuh"
 #include "ra_launch.h"
 #include "ra_tensor_map.h"
+#include "window_few.h"
 
 namespace ra {
 namespace {
@@ -16,6 +17,15 @@ namespace {
 constexpr size_t kHeader = RA_WORKSPACE_MIN_BYTES;
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// The few-key form runs where a block of 64 rows holds at most so many keys
+// and there is enough of it to fill the GPU.  40000 tokens, 16 / 8 heads, four
+// sinks, few-key against tensor-core form in us: d = 64, window 16: 90 / 167,
+// 64: 126 / 166, 128: 230 / 165; d = 128, window 16: 152 / 201, 64: 342 / 200.
+// 512 tokens, 8 heads, window 16: 10.7 / 10.3 and 12.7 / 12.0.
+bool few_keys(int64_t B, int64_t L, int64_t H, int d, int window, int sinks) {
+    return 16 * window_few_chunks((int)L, window, sinks) <= (d == 64 ? 224 : 176) && B * H * ((L + 255) / 256) >= 64;
+}
 
 struct Window {
     int64_t B, L, H, H_kv;
@@ -201,6 +211,23 @@ ra_status ra_window_attn_fwd(const void *q, const void *k, const void *v, void *
         return set_error(RA_ERR_INVALID_ARG, "workspace smaller than RA_WORKSPACE_MIN_BYTES");
     unsigned *status = static_cast<unsigned *>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (few_keys(B, L, H, d, w.window, w.sinks)) {
+        WindowFew f{};
+        f.q = static_cast<const uint16_t *>(q);
+        f.k = static_cast<const uint16_t *>(k);
+        f.v = static_cast<const uint16_t *>(v);
+        f.o = o;
+        f.lse = lse;
+        f.cu = w.cu;
+        f.n_seqs = w.n_seqs;
+        f.S = (int)L;
+        f.H = (int)H;
+        f.Hkv = (int)H_kv;
+        f.window = w.window;
+        f.sinks = w.sinks;
+        f.scale_log2 = softmax_scale(w) * 1.4426950408889634f;
+        return launch_window_few(f, d, (flags & RA_FLAG_O_BF16) != 0, B, s);
+    }
     if (flags & RA_FLAG_O_BF16)
         return d == 128 ? launch_fwd<128, false>(w, q, k, v, o, lse, status, s)
                         : launch_fwd<64, false>(w, q, k, v, o, lse, status, s);

@@ -1,0 +1,176 @@
+// attn_window_few.cu -- the windowed forward where a row sees few keys.
+//
+// A CTA takes 64 tokens of one key/value head, copies the keys and values that
+// they see -- at most 64 + window + sinks tokens -- to shared memory once, and
+// its four warps take 16 rows of one query head after another through them, 16
+// keys at a time (ra_warp_mma.cuh): a row block meets window / 16 + 2 chunks and
+// the one or more that hold the sinks, instead of whole 128-key tiles.  There
+// is no pipeline inside a CTA; two or more CTAs on an SM cover one another's
+// loads.  The tensor-core form (attn_fwd_kernel.cuh) costs about 7 us a CTA of
+// 256 rows beside its tiles, which at these sizes is most of its time; where
+// the two cross is written at few_keys (attn_window.cu).
+#include <cmath>
+
+#include "ra_warp_mma.cuh"
+#include "ra_window.cuh"
+#include "window_few.h"
+
+namespace ra {
+namespace {
+
+constexpr int kWarps = 4, kRows = 16 * kWarps, kChunk = 16;
+
+// The chunks of a block of rows, as range_walk has tiles: n_sink from key s0 on,
+// then from m0 on (both multiples of 16).
+struct FewChunks {
+    int s0, n_sink, m0, count;
+    __device__ int key(int c) const { return c < n_sink ? s0 + c * kChunk : m0 + (c - n_sink) * kChunk; }
+};
+__device__ __forceinline__ FewChunks few_chunks(const RowKeys &first, int last_hi) {
+    FewChunks c;
+    c.m0 = first.lo & ~(kChunk - 1);
+    c.s0 = first.slo & ~(kChunk - 1);
+    const int s1 = min(first.shi, c.m0);
+    c.n_sink = first.shi > first.slo && s1 > c.s0 ? (s1 - c.s0 + kChunk - 1) / kChunk : 0;
+    c.count = c.n_sink + (last_hi - c.m0 + kChunk - 1) / kChunk;
+    return c;
+}
+
+template <int D, bool O_BF16>
+__global__ void __launch_bounds__(32 * kWarps) window_few_kernel(const WindowFew a) {
+    constexpr int KS = D / 16, CPR = D / 8;
+    constexpr uint32_t kHalf = kChunk * D * 2;       // a chunk's keys
+    constexpr int kOut = D * 2 + 16;                 // bytes of a staged bf16 row
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const int S = a.S, group = a.H / a.Hkv;
+    const int blk = blockIdx.x % a.blocks, rest = blockIdx.x / a.blocks;
+    const int hk = rest % a.Hkv, b = rest / a.Hkv;
+    const int r0 = blk * kRows, r_end = min(S, r0 + kRows);
+    const FewChunks all = few_chunks(window_row(a.cu, a.n_seqs, S, r0, a.window, a.sinks), r_end);
+    // a call's own bound on its chunks; only boundaries that do not increase could pass it
+    const int n_chunks = min(all.count, a.max_chunks);
+    const uint32_t keys = smem_u32(smem), values = keys + a.max_chunks * kHalf;
+    {
+        // the tokens' rows of head hk: 16-byte pieces, a token's pieces to neighbouring threads
+        const size_t head = ((size_t)b * S * a.Hkv + hk) * D;
+        for (int e = threadIdx.x; e < n_chunks * kChunk * CPR; e += 32 * kWarps) {
+            const int row = e / CPR, pc = e % CPR;
+            const int key = all.key(row / kChunk) + row % kChunk;
+            const bool in = key < S;
+            const size_t at = in ? head + (size_t)key * a.Hkv * D + pc * 8 : 0;
+            const uint32_t to = row * (D * 2) + ((pc ^ (row & 7)) << 4);
+            cp_async16(keys + to, a.k + at, in);
+            cp_async16(values + to, a.v + at, in);
+        }
+        cp_async_commit();
+    }
+    // this warp's 16 rows and their chunks
+    const int w0 = r0 + warp * 16, w_end = min(S, w0 + 16);
+    const bool any = w0 < S;
+    RowKeys rk[2];
+    FewChunks mine{};
+    RowKeys first{};
+    if (any) {
+        first = window_row(a.cu, a.n_seqs, S, w0, a.window, a.sinks);
+        mine = few_chunks(first, w_end);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) rk[h] = window_row(a.cu, a.n_seqs, S, min(w0 + 8 * h + g, S - 1), a.window, a.sinks);
+    }
+    // keys that every row of the warp sees: [all_lo, first.hi)
+    const int all_lo = (int)__reduce_max_sync(0xffffffffu, (unsigned)max(any ? rk[0].lo : 0, any ? rk[1].lo : 0));
+    uint8_t *stage = smem + 2 * a.max_chunks * kHalf + warp * 16 * kOut;
+    for (int head = 0; head < group; ++head) {
+        const int hq = hk * group + head;
+        WarpRows<D, 1> rw;
+        rw.clear();
+        if (any) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = w0 + 8 * h + g;
+                const uint16_t *src = a.q + (((size_t)b * S + min(r, S - 1)) * a.H + hq) * D + 2 * t4;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    rw.q[0][ks][h] = *reinterpret_cast<const uint32_t *>(src + ks * 16);
+                    rw.q[0][ks][2 + h] = *reinterpret_cast<const uint32_t *>(src + ks * 16 + 8);
+                }
+            }
+        }
+        if (head == 0) {
+            cp_async_wait<0>();
+            __syncthreads();
+        }
+        if (!any) continue;
+        for (int c = 0; c < mine.count; ++c) {
+            const int k0 = mine.key(c);
+            // its place in shared memory: among the main keys, or the sinks before them
+            const int at = k0 >= all.m0 ? all.n_sink + (k0 - all.m0) / kChunk : (k0 - all.s0) / kChunk;
+            if ((unsigned)at >= (unsigned)n_chunks) continue;
+            const bool whole = k0 >= all_lo && k0 + kChunk <= first.hi;
+            rw.chunk(keys + at * kHalf, values + at * kHalf, a.scale_log2, whole, lane,
+                     [&](int, int h) { return seen_bits(rk[h].lo, rk[h].hi, rk[h].slo, rk[h].shi, k0); });
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float l = rw.l[0][h];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const int r = w0 + 8 * h + g;
+            if (t4 == 0 && r < S)
+                a.lse[((size_t)b * a.H + hq) * S + r] = l > 0.f ? (rw.m[0][h] + lg2(l)) * 0.6931471805599453f : -INFINITY;
+            if constexpr (O_BF16) {
+                uint32_t *row = reinterpret_cast<uint32_t *>(stage + (8 * h + g) * kOut) + t4;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+                    row[n * 4] = pack_bf16x2(rw.acc[0][n][2 * h] * inv, rw.acc[0][n][2 * h + 1] * inv);
+            } else if (r < S) {
+                float *row = static_cast<float *>(a.o) + (((size_t)b * S + r) * a.H + hq) * D + 2 * t4;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+                    *reinterpret_cast<float2 *>(row + n * 8) = make_float2(rw.acc[0][n][2 * h] * inv, rw.acc[0][n][2 * h + 1] * inv);
+            }
+        }
+        if constexpr (O_BF16) {
+            __syncwarp();
+#pragma unroll
+            for (int e = lane; e < 16 * CPR; e += 32) {
+                const int r = e / CPR, pc = e % CPR;
+                if (w0 + r < S)
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o) + (((size_t)b * S + w0 + r) * a.H + hq) * D + pc * 8) =
+                        *reinterpret_cast<const uint4 *>(stage + r * kOut + pc * 16);
+            }
+            __syncwarp();
+        }
+    }
+}
+
+}  // namespace
+
+int window_few_chunks(int S, int window, int sinks) {
+    // the rows' keys, a chunk's rounding at each end, the sinks and theirs
+    const int64_t main = (kRows + (int64_t)window + sinks + kChunk - 1) / kChunk + 2, most = (S + kChunk - 1) / kChunk;
+    const int64_t sink = sinks > 0 ? (sinks + kChunk - 1) / kChunk + 1 : 0;
+    return (int)(main + sink < most ? main + sink : most);
+}
+
+size_t window_few_smem(int chunks, int d) {
+    return (size_t)chunks * 2 * kChunk * d * 2 + kWarps * 16 * (d * 2 + 16);
+}
+
+ra_status launch_window_few(WindowFew a, int d, bool o_bf16, int64_t B, cudaStream_t stream) {
+    a.blocks = (a.S + kRows - 1) / kRows;
+    a.max_chunks = window_few_chunks(a.S, a.window, a.sinks);
+    const size_t smem = window_few_smem(a.max_chunks, d);
+    auto kern = d == 128 ? (o_bf16 ? window_few_kernel<128, true> : window_few_kernel<128, false>)
+                         : (o_bf16 ? window_few_kernel<64, true> : window_few_kernel<64, false>);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
+    const int64_t grid = (int64_t)a.blocks * a.Hkv * B;
+    if (grid > 0x7fffffffLL) return set_error(RA_ERR_UNSUPPORTED, "too many query tiles for one launch");
+    kern<<<(unsigned)grid, 32 * kWarps, smem, stream>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
+}
+
+}  // namespace ra

@@ -20,7 +20,7 @@ struct TokensLaunch {
     int d, ctas;
     float scale_log2;
     unsigned *status;
-    int *counters;              // kPagedTokensCtas, zero between calls
+    unsigned long long *counters;   // kPagedTokensCtas
     float *part_o, *part_ml;    // [2 * ctas, rows up to 16 or 32, d], [.., 2]
 };
 

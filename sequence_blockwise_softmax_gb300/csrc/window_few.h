@@ -1,0 +1,25 @@
+// window_few.h -- the launch of the windowed forward's few-key form, shared
+// between its kernel (attn_window_few.cu) and the entry point (attn_window.cu).
+#pragma once
+#include "ra_internal.h"
+
+namespace ra {
+
+struct WindowFew {
+    const uint16_t *q, *k, *v;
+    void *o;
+    float *lse;
+    const int *cu;
+    int n_seqs;
+    int S, H, Hkv, window, sinks;
+    float scale_log2;
+    int blocks, max_chunks;     // set by the launch
+};
+
+// 16-key chunks a CTA may hold at these sizes, and its shared memory.
+int window_few_chunks(int S, int window, int sinks);
+size_t window_few_smem(int chunks, int d);
+
+ra_status launch_window_few(WindowFew a, int d, bool o_bf16, int64_t B, cudaStream_t stream);
+
+}  // namespace ra

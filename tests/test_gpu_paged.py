@@ -363,3 +363,49 @@ def test_more_units_than_multiprocessors(ralib, gpu, new_max):
     q = randn_bf16((sum(new), 32, 128), 5).cuda()
     o, lse, _ = attend(ralib, c, q, cu_of(new), new, torch.bfloat16)
     assert_paged(c, q, o, lse, new, 0, 0)
+
+
+@pytest.mark.parametrize("n,longest", [(300, 60), (300, 2500), (40, 900)])
+def test_many_sequences(ralib, gpu, n, longest):
+    """More sequences than a block has threads, some without new tokens; short ones, a CTA each."""
+    r = random.Random(n + longest)
+    new = [r.randint(0, 1) for _ in range(n)]
+    lens = [x + r.randint(0, longest) for x in new]
+    c = Cache(lens, 16, 8, 64, 73)
+    c.fill_all()
+    q = randn_bf16((sum(new), 16, 64), 5).cuda()
+    o, lse, _ = attend(ralib, c, q, cu_of(new), new, torch.bfloat16)
+    assert_paged(c, q, o, lse, new, 0, 0)
+
+
+def test_workspace_left_by_other_calls(ralib, gpu):
+    """A workspace that other calls have written to, its header apart, serves the split forms."""
+    c = Cache([9000, 5000], 64, 2, 128, 79)
+    c.fill_all()
+    ws = ralib.new_workspace(64 << 20)
+    for n in (1, 40, 1):
+        ws[256:] = torch.randint(0, 256, (ws.numel() - 256,), dtype=torch.uint8, device="cuda")
+        q = randn_bf16((2 * n, 8, 128), 4 + n).cuda()
+        for _ in range(3):
+            o, lse, _ = attend(ralib, c, q, cu_of([n, n]), [n, n], torch.bfloat16, ws=ws)
+            assert_paged(c, q, o, lse, [n, n], 0, 0)
+
+
+def test_two_streams_two_workspaces(ralib, gpu):
+    """The same call on two streams at once, a workspace each, many times over."""
+    c = Cache([20000, 300, 7000], 64, 2, 128, 83)
+    c.fill_all()
+    new = [1, 1, 1]
+    q = randn_bf16((3, 8, 128), 4).cuda()
+    want, want_lse, _ = attend(ralib, c, q, cu_of(new), new, torch.bfloat16)
+    cu = cu_of(new)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [(torch.empty_like(want), torch.empty_like(want_lse), ralib.new_workspace(16 << 20)) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (o, lse, ws) in zip(streams, outs):
+            ralib.ra_paged_attn_fwd(q, c.k, c.v, c.table, c.seq_lens, cu, o, lse, 1, max(c.lens), workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for o, lse, _ in outs:
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)

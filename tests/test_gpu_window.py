@@ -24,6 +24,12 @@ CASES = [
     (1, 2300, 2, 1, 128, 60, 5, None),
     (1, 2600, 2, 2, 64, 77, 131, [0, 30, 2048, 2049, 2060, 2600]),
     (1, 800, 2, 2, 128, 40, 6, [0, 300, 500]),
+    # enough row blocks for the form with few keys (the first two pack sequences)
+    (1, 2100, 16, 4, 128, 17, 3, [0, 1, 40, 41, 300, 1000, 2049, 2100]),
+    (1, 2090, 8, 8, 64, 30, 33, [0, 70, 1024, 2000]),
+    (2, 2050, 8, 2, 64, 60, 4, None),
+    (1, 4099, 4, 2, 128, 1, 0, None),
+    (1, 2049, 12, 4, 128, 2, 65, None),
 ]
 
 

@@ -144,6 +144,9 @@ def test_workspace(ralib):
                                             (4096, 300, 64, 8, 128, 2048, 1 << 20, 0), (64, 64, 16, 2, 64, 1, 1 << 17, 4096),
                                             (1, 1, 128, 1, 64, 1, 1 << 20, 0)):
         assert 256 <= f(T, n, H, Hkv, d, new, length, W, 4) <= 64 << 20
+    big = (1 << 63) - 1
+    assert f(100, 4, 8, 2, 128, big, 300) == f(100, 4, 8, 2, 128, 100, 300)
+    assert 256 <= f(100, 4, 8, 2, 128, big, big, big, big) <= 64 << 20
 
 
 def test_binding_refuses_host_tensors(ralib):
