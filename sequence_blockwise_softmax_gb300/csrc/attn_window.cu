@@ -18,13 +18,18 @@ constexpr size_t kHeader = RA_WORKSPACE_MIN_BYTES;
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// The few-key form runs where a block of 64 rows holds at most so many keys
-// and there is enough of it to fill the GPU.  40000 tokens, 16 / 8 heads, four
-// sinks, few-key against tensor-core form in us: d = 64, window 16: 90 / 167,
-// 64: 126 / 166, 128: 230 / 165; d = 128, window 16: 152 / 201, 64: 342 / 200.
-// 512 tokens, 8 heads, window 16: 10.7 / 10.3 and 12.7 / 12.0.
+// The few-key form runs where 16 rows meet few 16-key chunks.  Few-key against
+// tensor-core form in us, four sinks:
+//   512 tokens, 8 / 2 heads (one wave of CTAs), d = 64: window 16: 4.1 / 10.3,
+//   128: 6.4 / 10.0, 200: 8.0 / 10.1, 300: 10.0 / 9.8; d = 128: 4.8 / 12.0,
+//   8.2 / 11.9, 10.3 / 11.9, 13.2 / 11.5.
+//   40000 tokens, 16 / 8 heads, d = 64: 80 / 167, 157 / 165, 257 / 185; d = 128:
+//   window 16: 142 / 201, 64: 201 / 200, 128: 424 / 200.
 bool few_keys(int64_t B, int64_t L, int64_t H, int d, int window, int sinks) {
-    return 16 * window_few_chunks((int)L, window, sinks) <= (d == 64 ? 224 : 176) && B * H * ((L + 255) / 256) >= 64;
+    const int64_t row_chunks = ((int64_t)window + 30) / 16 + ((int64_t)sinks + 15) / 16;
+    const bool one_wave = B * H * ((L + 63) / 64) <= 304;
+    return row_chunks <= (one_wave ? 16 : d == 64 ? 11 : 5) &&
+           window_few_smem(window_few_chunks((int)L, window, sinks), d) <= (size_t)227 << 10;
 }
 
 struct Window {

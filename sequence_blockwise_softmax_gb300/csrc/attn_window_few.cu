@@ -37,14 +37,18 @@ __device__ __forceinline__ FewChunks few_chunks(const RowKeys &first, int last_h
 }
 
 template <int D, bool O_BF16>
-__global__ void __launch_bounds__(32 * kWarps) window_few_kernel(const WindowFew a) {
+__global__ void __launch_bounds__(32 * kWarps, D == 64 ? 3 : 2) window_few_kernel(const WindowFew a) {
     constexpr int KS = D / 16, CPR = D / 8;
     constexpr uint32_t kHalf = kChunk * D * 2;       // a chunk's keys
     constexpr int kOut = D * 2 + 16;                 // bytes of a staged bf16 row
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int S = a.S, group = a.H / a.Hkv;
-    const int blk = blockIdx.x % a.blocks, rest = blockIdx.x / a.blocks;
+    // blockIdx.x = ((b * H_kv + hk) * parts of the group + part) * blocks + block
+    const int blk = blockIdx.x % a.blocks;
+    int rest = blockIdx.x / a.blocks;
+    const int head0 = rest % a.group_parts * a.heads, head1 = min(group, head0 + a.heads);
+    rest /= a.group_parts;
     const int hk = rest % a.Hkv, b = rest / a.Hkv;
     const int r0 = blk * kRows, r_end = min(S, r0 + kRows);
     const FewChunks all = few_chunks(window_row(a.cu, a.n_seqs, S, r0, a.window, a.sinks), r_end);
@@ -80,23 +84,24 @@ __global__ void __launch_bounds__(32 * kWarps) window_few_kernel(const WindowFew
     // keys that every row of the warp sees: [all_lo, first.hi)
     const int all_lo = (int)__reduce_max_sync(0xffffffffu, (unsigned)max(any ? rk[0].lo : 0, any ? rk[1].lo : 0));
     uint8_t *stage = smem + 2 * a.max_chunks * kHalf + warp * 16 * kOut;
-    for (int head = 0; head < group; ++head) {
-        const int hq = hk * group + head;
-        WarpRows<D, 1> rw;
-        rw.clear();
-        if (any) {
+    auto load_q = [&](uint32_t (&q)[KS][4], int hq) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = w0 + 8 * h + g;
-                const uint16_t *src = a.q + (((size_t)b * S + min(r, S - 1)) * a.H + hq) * D + 2 * t4;
+        for (int h = 0; h < 2; ++h) {
+            const int r = w0 + 8 * h + g;
+            const uint16_t *src = a.q + (((size_t)b * S + min(r, S - 1)) * a.H + hq) * D + 2 * t4;
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    rw.q[0][ks][h] = *reinterpret_cast<const uint32_t *>(src + ks * 16);
-                    rw.q[0][ks][2 + h] = *reinterpret_cast<const uint32_t *>(src + ks * 16 + 8);
-                }
+            for (int ks = 0; ks < KS; ++ks) {
+                q[ks][h] = *reinterpret_cast<const uint32_t *>(src + ks * 16);
+                q[ks][2 + h] = *reinterpret_cast<const uint32_t *>(src + ks * 16 + 8);
             }
         }
-        if (head == 0) {
+    };
+    WarpRows<D, 1> rw;
+    if (any) load_q(rw.q[0], hk * group + head0);
+    for (int head = head0; head < head1; ++head) {
+        const int hq = hk * group + head;
+        rw.clear();
+        if (head == head0) {
             cp_async_wait<0>();
             __syncthreads();
         }
@@ -110,6 +115,7 @@ __global__ void __launch_bounds__(32 * kWarps) window_few_kernel(const WindowFew
             rw.chunk(keys + at * kHalf, values + at * kHalf, a.scale_log2, whole, lane,
                      [&](int, int h) { return seen_bits(rk[h].lo, rk[h].hi, rk[h].slo, rk[h].shi, k0); });
         }
+        if (head + 1 < head1) load_q(rw.q[0], hq + 1);     // on its way while the rows are written
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float l = rw.l[0][h];
@@ -148,10 +154,14 @@ __global__ void __launch_bounds__(32 * kWarps) window_few_kernel(const WindowFew
 }  // namespace
 
 int window_few_chunks(int S, int window, int sinks) {
-    // the rows' keys, a chunk's rounding at each end, the sinks and theirs
-    const int64_t main = (kRows + (int64_t)window + sinks + kChunk - 1) / kChunk + 2, most = (S + kChunk - 1) / kChunk;
-    const int64_t sink = sinks > 0 ? (sinks + kChunk - 1) / kChunk + 1 : 0;
-    return (int)(main + sink < most ? main + sink : most);
+    // The main keys end at the rows' end, a multiple of 16 (or of the tokens),
+    // and begin window - 1 before the first row, earlier by up to `sinks` where
+    // the sinks touch the window; else the sinks lie apart, anywhere.
+    auto chunks = [](int64_t keys) { return (keys + kChunk - 1) / kChunk; };
+    const int64_t main = chunks(kRows + (int64_t)window - 1), touching = chunks(kRows + (int64_t)window - 1 + sinks);
+    const int64_t apart = main + (sinks > 0 ? chunks(sinks + kChunk - 1) : 0);
+    const int64_t most = chunks(S), need = touching > apart ? touching : apart;
+    return (int)(need < most ? need : most);
 }
 
 size_t window_few_smem(int chunks, int d) {
@@ -166,7 +176,14 @@ ra_status launch_window_few(WindowFew a, int d, bool o_bf16, int64_t B, cudaStre
                          : (o_bf16 ? window_few_kernel<64, true> : window_few_kernel<64, false>);
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
-    const int64_t grid = (int64_t)a.blocks * a.Hkv * B;
+    // a CTA takes the heads of a group one after another; where there are too
+    // few CTAs for that, each takes fewer and the keys are copied again
+    const int group = a.H / a.Hkv;
+    const int64_t whole = (int64_t)a.blocks * a.Hkv * B;
+    const int64_t parts = whole >= 304 ? 1 : (304 + whole - 1) / whole;
+    a.heads = (int)(parts >= group ? 1 : (group + parts - 1) / parts);
+    a.group_parts = (group + a.heads - 1) / a.heads;
+    const int64_t grid = whole * a.group_parts;
     if (grid > 0x7fffffffLL) return set_error(RA_ERR_UNSUPPORTED, "too many query tiles for one launch");
     kern<<<(unsigned)grid, 32 * kWarps, smem, stream>>>(a);
     const cudaError_t e = cudaGetLastError();

@@ -13,7 +13,7 @@ struct WindowFew {
     int n_seqs;
     int S, H, Hkv, window, sinks;
     float scale_log2;
-    int blocks, max_chunks;     // set by the launch
+    int blocks, max_chunks, heads, group_parts;     // set by the launch
 };
 
 // 16-key chunks a CTA may hold at these sizes, and its shared memory.

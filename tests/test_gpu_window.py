@@ -24,12 +24,17 @@ CASES = [
     (1, 2300, 2, 1, 128, 60, 5, None),
     (1, 2600, 2, 2, 64, 77, 131, [0, 30, 2048, 2049, 2060, 2600]),
     (1, 800, 2, 2, 128, 40, 6, [0, 300, 500]),
-    # enough row blocks for the form with few keys (the first two pack sequences)
+    # the form with few keys at one wave of blocks above, at several here (the first two pack sequences)
     (1, 2100, 16, 4, 128, 17, 3, [0, 1, 40, 41, 300, 1000, 2049, 2100]),
     (1, 2090, 8, 8, 64, 30, 33, [0, 70, 1024, 2000]),
     (2, 2050, 8, 2, 64, 60, 4, None),
     (1, 4099, 4, 2, 128, 1, 0, None),
     (1, 2049, 12, 4, 128, 2, 65, None),
+    # and the tensor-core form on short and ragged inputs
+    (1, 300, 2, 1, 128, 260, 3, [0, 290, 300]),
+    (2, 257, 2, 2, 64, 257, 0, None),
+    (1, 1025, 8, 1, 128, 300, 200, [0, 5, 700, 1025]),
+    (1, 3000, 8, 8, 128, 129, 4, None),
 ]
 
 
