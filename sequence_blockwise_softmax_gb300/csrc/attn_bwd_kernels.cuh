@@ -340,6 +340,32 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &tmq, const CUtens
     else
         walk0 = window_unit_walk(args.cu_seqlens, args.n_seqs, S, row0, row_end, args.window, args.sinks);
 
+    // the tile loads, by one thread
+    auto load_q = [&]() {
+        mbar_arrive_expect_tx(BAR(B_QFULL), 2 * L::kTile);
+        int c1, c2, c3;
+        tile_coords(args.seq_order, args.layout, S, N, qi, b, row0, c1, c2, c3);
+        for (int c = 0; c < HALVES; ++c) {
+            tma_load_4d(s_base + L::kQ + c * L::kBox, &tmq, BAR(B_QFULL), h * D + 64 * c, c1, c2, c3);
+            tma_load_4d(s_base + L::kDO + c * L::kBox, &tmdo, BAR(B_QFULL), h * D + 64 * c, c1, c2, c3);
+        }
+    };
+    auto load_k = [&](int t, int j, int tile) {
+        const int sk = t % NK;
+        int k1, k2, k3;
+        tile_coords(args.seq_order, args.layout, S, N, j, b, tile * 128, k1, k2, k3);
+        mbar_arrive_expect_tx(BAR(B_KFULL + sk), L::kTile);
+        for (int c = 0; c < HALVES; ++c)
+            tma_load_4d(s_base + L::kK + sk * L::kTile + c * L::kBox, &tmk, BAR(B_KFULL + sk), hk * D + 64 * c, k1, k2, k3);
+    };
+    auto load_v = [&](int t, int j, int tile) {
+        const int sv = t % NV;
+        int k1, k2, k3;
+        tile_coords(args.seq_order, args.layout, S, N, j, b, tile * 128, k1, k2, k3);
+        mbar_arrive_expect_tx(BAR(B_VFULL + sv), L::kTile);
+        for (int c = 0; c < HALVES; ++c)
+            tma_load_4d(s_base + L::kV + sv * L::kTile + c * L::kBox, &tmv, BAR(B_VFULL + sv), hk * D + 64 * c, k1, k2, k3);
+    };
     if (threadIdx.x == 0) {
         mbar_init(BAR(B_QFULL), 1);
         for (int s = 0; s < NK; ++s) {
@@ -362,6 +388,17 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &tmq, const CUtens
         mbar_init(BAR(B_FINAL), 3);   // the three MMA issuers
         *abort_flag = 0;
         fence_mbar_init();
+        if constexpr (KEYS == BWD_WINDOW) {
+            // Q, dO, K(0) and V(0) are on their way before tensor memory is
+            // allocated and the roles start
+            load_q();
+            if (walk0.valid()) {
+                Walk w0 = walk0;
+                w0.start_step();
+                load_k(0, 0, w0.tile);
+                load_v(0, 0, w0.tile);
+            }
+        }
     }
     if (warp == 2) {
         tmem_alloc(smem_u32(tmem_slot), 512);
@@ -377,38 +414,18 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &tmq, const CUtens
         // ------------------------------------------------ producer
         int t = 0, k_issued = 0, v_issued = 0;
         bool ok = true;
-        if (lane == 0) {
-            mbar_arrive_expect_tx(BAR(B_QFULL), 2 * L::kTile);
-            int c1, c2, c3;
-            tile_coords(args.seq_order, args.layout, S, N, qi, b, row0, c1, c2, c3);
-            for (int c = 0; c < HALVES; ++c) {
-                tma_load_4d(s_base + L::kQ + c * L::kBox, &tmq, BAR(B_QFULL), h * D + 64 * c, c1, c2, c3);
-                tma_load_4d(s_base + L::kDO + c * L::kBox, &tmdo, BAR(B_QFULL), h * D + 64 * c, c1, c2, c3);
-            }
-        }
+        constexpr bool EARLY = KEYS == BWD_WINDOW;   // the first loads went out in the setup
+        if (!EARLY && lane == 0) load_q();
         __syncwarp();
         Walk w = walk0;
         w.start_step();
         for (; w.valid(); w.next(), ++t) {
-            const int sk = t % NK, sv = t % NV;
-            int k1, k2, k3;
-            tile_coords(args.seq_order, args.layout, S, N, w.j, b, w.tile * 128, k1, k2, k3);
-            if (t >= NK && !(ok = warp_wait(BAR(B_KEMPTY + sk), ((t / NK) - 1) & 1, abort_flag))) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(BAR(B_KFULL + sk), L::kTile);
-                for (int c = 0; c < HALVES; ++c)
-                    tma_load_4d(s_base + L::kK + sk * L::kTile + c * L::kBox, &tmk, BAR(B_KFULL + sk),
-                                hk * D + 64 * c, k1, k2, k3);
-            }
+            if (t >= NK && !(ok = warp_wait(BAR(B_KEMPTY + t % NK), ((t / NK) - 1) & 1, abort_flag))) break;
+            if (lane == 0 && !(EARLY && t == 0)) load_k(t, w.j, w.tile);
             __syncwarp();
             k_issued = t + 1;
-            if (t >= NV && !(ok = warp_wait(BAR(B_VEMPTY + sv), ((t / NV) - 1) & 1, abort_flag))) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(BAR(B_VFULL + sv), L::kTile);
-                for (int c = 0; c < HALVES; ++c)
-                    tma_load_4d(s_base + L::kV + sv * L::kTile + c * L::kBox, &tmv, BAR(B_VFULL + sv),
-                                hk * D + 64 * c, k1, k2, k3);
-            }
+            if (t >= NV && !(ok = warp_wait(BAR(B_VEMPTY + t % NV), ((t / NV) - 1) & 1, abort_flag))) break;
+            if (lane == 0 && !(EARLY && t == 0)) load_v(t, w.j, w.tile);
             __syncwarp();
             v_issued = t + 1;
         }
@@ -745,6 +762,26 @@ __device__ __forceinline__ void bwd_dkv_body(const CUtensorMap &tmq, const CUten
         }
     }
 
+    // the tile loads, by one thread
+    auto load_kv = [&]() {
+        mbar_arrive_expect_tx(BAR(B_KVFULL), 2 * L::kTile);
+        int c1, c2, c3;
+        tile_coords(args.seq_order, args.layout, S, N, kj, b, c0, c1, c2, c3);
+        for (int c = 0; c < HALVES; ++c) {
+            tma_load_4d(s_base + L::kK + c * L::kBox, &tmk, BAR(B_KVFULL), hk * D + 64 * c, c1, c2, c3);
+            tma_load_4d(s_base + L::kV + c * L::kBox, &tmv, BAR(B_KVFULL), hk * D + 64 * c, c1, c2, c3);
+        }
+    };
+    auto load_qdo = [&](int t, int i, int head, int row) {
+        const int st = t % NS;
+        int c1, c2, c3;
+        tile_coords(args.seq_order, args.layout, S, N, i, b, row, c1, c2, c3);
+        mbar_arrive_expect_tx(BAR(B_QFULL + st), 2 * L::kTile);
+        for (int c = 0; c < HALVES; ++c) {
+            tma_load_4d(s_base + L::kQ + st * L::kTile + c * L::kBox, &tmq, BAR(B_QFULL + st), head * D + 64 * c, c1, c2, c3);
+            tma_load_4d(s_base + L::kDO + st * L::kTile + c * L::kBox, &tmdo, BAR(B_QFULL + st), head * D + 64 * c, c1, c2, c3);
+        }
+    };
     if (threadIdx.x == 0) {
         mbar_init(BAR(B_KVFULL), 1);
         for (int s = 0; s < NS; ++s) {
@@ -763,6 +800,12 @@ __device__ __forceinline__ void bwd_dkv_body(const CUtensorMap &tmq, const CUten
         mbar_init(BAR(B_FINAL), 2);   // both MMA issuers
         *abort_flag = 0;
         fence_mbar_init();
+        if constexpr (KEYS == BWD_WINDOW) {
+            load_kv();
+            QWalk w0 = walk0;
+            w0.start();
+            if (w0.valid()) load_qdo(0, w0.i, hk * group + w0.head, w0.tile * 128);
+        }
     }
     if (warp == 2) {
         tmem_alloc(smem_u32(tmem_slot), 512);
@@ -778,15 +821,8 @@ __device__ __forceinline__ void bwd_dkv_body(const CUtensorMap &tmq, const CUten
         // ------------------------------------------------ producer
         bool ok = true;
         int t = 0, issued = 0;
-        if (lane == 0) {
-            mbar_arrive_expect_tx(BAR(B_KVFULL), 2 * L::kTile);
-            int c1, c2, c3;
-            tile_coords(args.seq_order, args.layout, S, N, kj, b, c0, c1, c2, c3);
-            for (int c = 0; c < HALVES; ++c) {
-                tma_load_4d(s_base + L::kK + c * L::kBox, &tmk, BAR(B_KVFULL), hk * D + 64 * c, c1, c2, c3);
-                tma_load_4d(s_base + L::kV + c * L::kBox, &tmv, BAR(B_KVFULL), hk * D + 64 * c, c1, c2, c3);
-            }
-        }
+        constexpr bool EARLY = KEYS == BWD_WINDOW;   // the first loads went out in the setup
+        if (!EARLY && lane == 0) load_kv();
         __syncwarp();
         QWalk w = walk0;
         w.start();
@@ -805,18 +841,8 @@ __device__ __forceinline__ void bwd_dkv_body(const CUtensorMap &tmq, const CUten
                 nl[e] = lv > -INFINITY ? lv * -1.4426950408889634f : 0.f;
                 dd[e] = row < S ? args.dvec[base + row] : 0.f;
             }
-            int c1, c2, c3;
-            tile_coords(args.seq_order, args.layout, S, N, w.i, b, y, c1, c2, c3);
             if (t >= NS && !(ok = warp_wait(BAR(B_QEMPTY + st), ((t / NS) - 1) & 1, abort_flag))) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(BAR(B_QFULL + st), 2 * L::kTile);
-                for (int c = 0; c < HALVES; ++c) {
-                    tma_load_4d(s_base + L::kQ + st * L::kTile + c * L::kBox, &tmq, BAR(B_QFULL + st),
-                                h * D + 64 * c, c1, c2, c3);
-                    tma_load_4d(s_base + L::kDO + st * L::kTile + c * L::kBox, &tmdo, BAR(B_QFULL + st),
-                                h * D + 64 * c, c1, c2, c3);
-                }
-            }
+            if (lane == 0 && !(EARLY && t == 0)) load_qdo(t, w.i, h, y);
             float *vec = reinterpret_cast<float *>(smem + L::kVec + st * 1024);
             *reinterpret_cast<float4 *>(vec + lane * 4) = make_float4(nl[0], nl[1], nl[2], nl[3]);
             *reinterpret_cast<float4 *>(vec + 128 + lane * 4) = make_float4(dd[0], dd[1], dd[2], dd[3]);
