@@ -123,8 +123,17 @@ struct Plan {
     int64_t units;
     bool tokens, whole_pairs;   // the few-row form, with this many CTAs
     int ctas;
+    bool few;                   // the few-key form: units of its own, the keys it expects
+    int64_t few_units, few_keys;
     size_t part_o, part_lse, total;
 };
+
+// The few-key form runs where a block of 64 rows sees few keys.  Chunks of 33 to
+// L new tokens over L keys, few-key against tensor-core form in us: 40 sequences,
+// 8 / 8 heads, d = 64: L = 40: 7.2 / 17.5, 100: 13.7 / 17.8, 160: 18.7 / 22.7,
+// 250: 33 / 23; 32 / 8 heads: 14 / 20, 25 / 25, 41 / 37; d = 128, 8 / 8 heads:
+// 12 / 21, 19 / 21, 43 / 27; 8 sequences, 16 / 8 heads: 6.0 / 7.8, 10.1 / 8.6.
+bool few_keys(int64_t keys, int d) { return keys <= (d == 64 ? 128 : 64); }
 
 Plan plan(Paged a) {
     // hints of any size: nothing below leaves 64 bits
@@ -148,6 +157,17 @@ Plan plan(Paged a) {
         p.part_lse = p.part_o + round256(rows * a.d * 4);
         p.total = p.part_lse + round256(rows * 8);
         return p;
+    }
+    if (group <= kPagedFewRows) {
+        const int unit = (int)(kPagedFewRows / group);
+        p.few_units = paged_units(a.T, a.n_seqs, unit);
+        p.few_keys = a.max_len;
+        if (a.window > 0 && a.window + unit + a.sinks < p.few_keys) p.few_keys = a.window + unit + a.sinks;
+        p.few = few_keys(p.few_keys, a.d);
+        if (p.few) {
+            p.total = p.part_o;
+            return p;
+        }
     }
     p.tile_tokens = (int)(128 / group);
     const int unit = 2 * p.tile_tokens;
@@ -314,6 +334,25 @@ ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, co
         t.part_o = reinterpret_cast<float *>(workspace + p.part_o);
         t.part_ml = reinterpret_cast<float *>(workspace + p.part_lse);
         return launch_paged_tokens(t, stream);
+    }
+    if (p.few) {
+        PagedFewLaunch t{};
+        t.seqs = sequences(a, table, seq_lens, cu_q);
+        t.seqs.unit_tokens = kPagedFewRows / t.seqs.group;
+        t.q = q;
+        t.k = k;
+        t.v = v;
+        t.q_stride = a.q_stride;
+        t.page_stride = a.page_stride;
+        t.o = o;
+        t.lse = lse;
+        t.o_bf16 = o_bf16;
+        t.d = D;
+        t.units = (int)p.few_units;
+        t.keys = p.few_keys;
+        t.scale_log2 = scale_log2;
+        t.status = reinterpret_cast<unsigned *>(workspace);
+        return launch_paged_few(t, stream);
     }
     AttnArgs args{};
     args.o = o;

@@ -1,6 +1,6 @@
-// paged_launch.h -- the launch of paged attention's few-row form, shared
-// between its kernel (attn_paged_tokens.cu) and the entry point
-// (attn_paged.cu).
+// paged_launch.h -- the launches of paged attention's few-row form
+// (attn_paged_tokens.cu) and few-key form (attn_paged_few.cu), shared with the
+// entry point (attn_paged.cu).
 #pragma once
 #include "ra_internal.h"
 #include "ra_paged.cuh"
@@ -33,5 +33,23 @@ bool paged_tokens_whole(int64_t pairs, int64_t keys);
 int paged_tokens_ctas(int64_t pairs, int64_t keys);
 
 ra_status launch_paged_tokens(const TokensLaunch &t, cudaStream_t stream);
+
+constexpr int kPagedFewRows = 64;           // rows of a CTA
+constexpr int kPagedFewRoom = 24;           // most 16-key chunks a CTA holds at a time
+
+struct PagedFewLaunch {
+    PagedSeqs seqs;                         // unit_tokens = kPagedFewRows / group
+    const void *q, *k, *v;
+    int64_t q_stride, page_stride;
+    void *o;
+    float *lse;
+    bool o_bf16;
+    int d, units;
+    int64_t keys;                           // a row block's keys, as the call expects them
+    float scale_log2;
+    unsigned *status;
+};
+
+ra_status launch_paged_few(const PagedFewLaunch &t, cudaStream_t stream);
 
 }  // namespace ra

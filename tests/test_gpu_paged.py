@@ -115,6 +115,12 @@ CASES = [
     ([5, 6], [1500, 40], 66, 2, 128, 16, 0, 0),
     ([2], [900], 128, 1, 64, 64, 0, 0),
     ([33], [12000], 8, 1, 128, 16, 0, 0),
+    # few keys: short prompts, short windows
+    ([40, 3, 64, 0, 1], [40, 60, 64, 9, 1], 8, 8, 128, 16, 0, 0),
+    ([90, 1, 128], [90, 128, 128], 6, 2, 64, 32, 0, 0),
+    ([100, 40], [3000, 900], 20, 4, 64, 16, 20, 4),
+    ([70, 33], [1500, 33], 3, 1, 128, 64, 7, 17),
+    ([35, 41], [50, 41], 64, 1, 64, 128, 0, 0),
 ]
 
 
@@ -129,7 +135,7 @@ def test_paged_matches_definition(ralib, gpu, new, lens, H, Hkv, d, page, window
 
 
 @pytest.mark.parametrize("max_len", [1, 1 << 20])
-@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("n", [1, 9, 40])
 def test_any_guess_of_the_length(ralib, gpu, n, max_len):
     """max_len only guides the split: far too short or too long, the results hold."""
     new, lens = [n, n], [6000, 77]
