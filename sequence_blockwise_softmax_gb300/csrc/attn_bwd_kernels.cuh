@@ -1239,6 +1239,9 @@ template <int D, bool O_BF16>
 __global__ void __launch_bounds__(256) bwd_window_dot(const uint16_t *dout, const void *o, float *dvec, int64_t rows,
                                                       int H, int64_t S) {
     constexpr int LANES = D / 8, PER_WARP = 32 / LANES, R = 4;
+    // in this order: the next kernel reads q, k, v and dO before it waits for D,
+    // so it may only start once what came before this kernel has finished
+    pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, sub = lane % LANES;
     const int64_t r0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * PER_WARP * R + lane / LANES;

@@ -255,6 +255,7 @@ __global__ void __launch_bounds__(384, 1)
     using KT = KvTile<D, KEYS == KEYS_PAGED && D == 128>;
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
+    if constexpr (KEYS != KEYS_RING) pdl_wait();   // launched with launch_dependent()
     uint8_t *smem = smem_raw;
     const uint32_t s_base = smem_u32(smem);
     if ((s_base & 1023u) != 0u) {

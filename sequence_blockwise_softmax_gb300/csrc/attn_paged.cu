@@ -26,8 +26,7 @@ static_assert(kPagedTokensCtas * 8 <= kCounterBytes, "one counter per CTA");
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-ra_status launch_error() {
-    const cudaError_t e = cudaGetLastError();
+ra_status launched(cudaError_t e) {
     return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
 }
 
@@ -303,8 +302,7 @@ ra_status launch_chunks(const Paged &a, const Plan &p, const AttnArgs &args, con
         return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
     const int64_t grid = p.units * a.H_kv * p.splits;
     if (grid > 0x7fffffffLL) return set_error(RA_ERR_UNSUPPORTED, "too many query tiles for one launch");
-    kern<<<(unsigned)grid, 384, smem, stream>>>(mq, mk, mv, mq, args);
-    return launch_error();
+    return launched(launch_dependent(kern, (unsigned)grid, 384, smem, stream, mq, mk, mv, mq, args));
 }
 
 template <int D>
@@ -382,8 +380,7 @@ ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, co
     if (st != RA_OK || p.splits == 1) return st;
     JoinArgs j{args.seqs, args.part_o, args.part_lse, o, lse, o_bf16 ? 1 : 0};
     const int64_t per_block = 256 / (D / 4), blocks = (a.T * a.H + per_block - 1) / per_block;
-    const cudaError_t e = launch_dependent(paged_join_kernel<D>, (unsigned)blocks, 256, 0, stream, j);
-    return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
+    return launched(launch_dependent(paged_join_kernel<D>, (unsigned)blocks, 256, 0, stream, j));
 }
 
 // ------------------------------------------------------------------ append
@@ -405,6 +402,7 @@ constexpr int kAppendThreads = 256, kAppendTokens = 32;
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendArgs a) {
     const PagedSeqs &q = a.seqs;
     __shared__ int64_t dst_of[kAppendTokens];
+    pdl_wait();
     const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
     const int n_tok = (int)min((int64_t)a.tokens, q.T - t0);
     if ((int)threadIdx.x < n_tok) {
@@ -550,8 +548,8 @@ ra_status ra_paged_append(const void *k_new, const void *v_new, void *k_pages, v
     if (per > T / (2 * kSms)) per = T / (2 * kSms);
     a.tokens = (int)(per < 1 ? 1 : per > kAppendTokens ? kAppendTokens : per);
     const int64_t blocks = (T + a.tokens - 1) / a.tokens;
-    paged_append_kernel<<<(unsigned)blocks, kAppendThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return launch_error();
+    return launched(launch_dependent(paged_append_kernel, (unsigned)blocks, kAppendThreads, 0,
+                                     static_cast<cudaStream_t>(stream), a));
 }
 
 }  // extern "C"

@@ -11,6 +11,7 @@
 #include <cmath>
 
 #include "paged_launch.h"
+#include "ra_launch.h"
 #include "ra_paged.cuh"
 #include "ra_warp_mma.cuh"
 
@@ -50,6 +51,7 @@ __global__ void __launch_bounds__(32 * kWarps, D == 64 ? 3 : 2) paged_few_kernel
     __shared__ int ids[kMostChunks];
     const PagedSeqs &sq = a.seqs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    pdl_wait();
     // blockIdx.x = hk * units + unit
     const int unit = blockIdx.x % a.n_units, hk = blockIdx.x / a.n_units;
     const int s = paged_find_seq(sq, unit);
@@ -201,8 +203,7 @@ ra_status launch_paged_few(const PagedFewLaunch &t, cudaStream_t stream) {
         return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
     const int64_t grid = (int64_t)t.units * t.seqs.Hkv;
     if (grid > 0x7fffffffLL) return set_error(RA_ERR_UNSUPPORTED, "too many query tiles for one launch");
-    kern<<<(unsigned)grid, 32 * kWarps, smem, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_dependent(kern, (unsigned)grid, 32 * kWarps, smem, stream, a);
     return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
 }
 

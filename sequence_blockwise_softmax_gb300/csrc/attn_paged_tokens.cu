@@ -31,6 +31,7 @@
 #include <type_traits>
 
 #include "paged_launch.h"
+#include "ra_launch.h"
 #include "ra_device.cuh"
 #include "ra_paged.cuh"
 #include "ra_warp_mma.cuh"
@@ -113,6 +114,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
     const PagedSeqs &sq = a.seqs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
+    pdl_wait();
 
     // ---- how the work is cut, from the lengths the call finds
     // An inclusive scan of x over the block (its total added to `base`).
@@ -452,8 +454,7 @@ ra_status launch(const TokensLaunch &t, const TokensArgs &args, cudaStream_t str
     static_assert(kWarps * 16 * MT * TokensSmem<D>::kRow * 4 <= TokensSmem<D>::kBytes, "the warps' rows fit in the rings");
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
-    kern<<<(unsigned)t.ctas, 32 * kWarps, smem, stream>>>(args);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_dependent(kern, (unsigned)t.ctas, 32 * kWarps, smem, stream, args);
     return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
 }
 

@@ -72,8 +72,7 @@ ra_status check(Window &w, int64_t window, int64_t sinks, const int *cu_seqlens,
 
 float softmax_scale(const Window &w) { return w.scale > 0.f ? w.scale : 1.0f / std::sqrt((float)w.d); }
 
-ra_status launch_error() {
-    const cudaError_t e = cudaGetLastError();
+ra_status launched(cudaError_t e) {
     return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
 }
 
@@ -110,8 +109,7 @@ ra_status launch_fwd(const Window &w, const void *q, const void *k, const void *
     const int smem = (int)AttnSmem<D>::kBytes;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
-    kern<<<(unsigned)(w.B * w.H * a.n_units_seq), 384, smem, stream>>>(mq, mk, mv, mo, a);
-    return launch_error();
+    return launched(launch_dependent(kern, (unsigned)(w.B * w.H * a.n_units_seq), 384, smem, stream, mq, mk, mv, mo, a));
 }
 
 // Workspace of the backward: the status word, D, the sinks' partial gradients.
@@ -182,14 +180,14 @@ ra_status launch_bwd(const Window &w, const void *q, const void *k, const void *
         return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
     if ((rows + per_block - 1) / per_block > 0x7fffffffLL)
         return set_error(RA_ERR_UNSUPPORTED, "too many rows for one launch");
-    dot<<<(unsigned)((rows + per_block - 1) / per_block), 256, 0, stream>>>(
-        static_cast<const uint16_t *>(dout), o, reinterpret_cast<float *>(workspace + space.dvec), rows, a.H, w.L);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_dependent(dot, (unsigned)((rows + per_block - 1) / per_block), 256, 0, stream,
+                                     static_cast<const uint16_t *>(dout), o,
+                                     reinterpret_cast<float *>(workspace + space.dvec), rows, a.H, w.L);
     if (e == cudaSuccess)
         e = launch_dependent(kern, (unsigned)(n_far + n_kv + n_q), 384, smem, stream, mq, mk, mv, mdo, a);
     if (e == cudaSuccess && joins > 0)
         e = launch_dependent(bwd_sink_join<D>, (unsigned)((joins + 7) / 8), 256, 0, stream, a);
-    return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
+    return launched(e);
 }
 
 }  // namespace

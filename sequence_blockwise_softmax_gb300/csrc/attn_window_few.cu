@@ -11,6 +11,7 @@
 // the two cross is written at few_keys (attn_window.cu).
 #include <cmath>
 
+#include "ra_launch.h"
 #include "ra_warp_mma.cuh"
 #include "ra_window.cuh"
 #include "window_few.h"
@@ -44,6 +45,7 @@ __global__ void __launch_bounds__(32 * kWarps, D == 64 ? 3 : 2) window_few_kerne
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int S = a.S, group = a.H / a.Hkv;
+    pdl_wait();
     // blockIdx.x = ((b * H_kv + hk) * parts of the group + part) * blocks + block
     const int blk = blockIdx.x % a.blocks;
     int rest = blockIdx.x / a.blocks;
@@ -185,8 +187,7 @@ ra_status launch_window_few(WindowFew a, int d, bool o_bf16, int64_t B, cudaStre
     a.group_parts = (group + a.heads - 1) / a.heads;
     const int64_t grid = whole * a.group_parts;
     if (grid > 0x7fffffffLL) return set_error(RA_ERR_UNSUPPORTED, "too many query tiles for one launch");
-    kern<<<(unsigned)grid, 32 * kWarps, smem, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_dependent(kern, (unsigned)grid, 32 * kWarps, smem, stream, a);
     return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
 }
 

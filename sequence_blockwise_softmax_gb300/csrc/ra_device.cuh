@@ -320,9 +320,11 @@ __device__ __forceinline__ void regs_grow() {
 
 // Programmatic dependent launch: a kernel launched with launch_dependent()
 // (ra_launch.h) may start while the kernel before it in the stream still runs,
-// once every block of that one has called or exited; pdl_wait() returns when it
-// has finished and its writes are visible.  Every block of such a kernel
-// waits, also one with nothing to do.
+// once every block of that one has called pdl_launch_dependents() or exited;
+// pdl_wait() returns when it has finished and its writes are visible.  Every
+// block of such a kernel waits before it touches memory, also one with nothing
+// to do.  Without an early call before it this hides the launch itself: a
+// decode step of 7.7 us took 10.2 without, a cache append 2.7 and 4.1.
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
