@@ -173,18 +173,28 @@ Plan plan(Paged a) {
     p.units = paged_units(a.T, a.n_seqs, unit);
     const int64_t rows = (a.max_new < unit ? a.max_new : unit) * group;
     const size_t part = (size_t)p.units * a.H_kv * rows * (a.d + 1) * 4;     // one part of every unit
-    // The time of s parts: waves of CTAs, about 7 us and 1.3 us per key tile
-    // each, and the join's launch.
+    // The time of s parts, in us: a CTA costs about 8 and 1.35 a key tile (1.0 at
+    // d = 64).  While one wave holds them all it is the longest CTA's; past that
+    // the SMs' even share and, since longer units go first, about half a CTA more.
+    // max_len bounds the lengths: several sequences are taken to have half of it
+    // on average.  The join reads the parts at about 3 TB/s.
+    //   512 tokens over 32768 keys, 32 / 8 heads, d = 128, s = 1, 2, 3, 4, 7:
+    //   357, 199, 260, 210, 202; 8 ragged sequences of up to 700 tokens over 9000
+    //   keys, 16 / 4 heads, d = 64, s = 1, 2, 3: 104, 120, 123.
     const int64_t full = (a.T + unit - 1) / unit;
     const int64_t ctas = (full > active0 ? full : active0) * a.H_kv;
     int64_t keys = a.max_len;
     if (a.window > 0 && a.window + a.max_new + a.sinks < keys) keys = a.window + (a.max_new < unit ? a.max_new : unit) + a.sinks;
     const int64_t tiles = (keys + 127) / 128 + 1;
+    const double tile = a.d == 128 ? 1.35 : 1.0, fixed = 8.0;
+    const double mean = active0 > 1 && !(a.window > 0) ? 0.55 * (double)tiles : (double)tiles;
     p.splits = 1;
     double best = 0;
     for (int s = 1; s <= 64 && (s == 1 || (tiles / s >= kSplitTiles && part * s <= kPartBytes)); ++s) {
-        const double t = (double)((ctas * s + kSms - 1) / kSms) * (7.0 + 1.3 * (double)((tiles + s - 1) / s)) +
-                         (s > 1 ? 4.0 : 0.0);
+        const double longest = fixed + tile * (double)((tiles + s - 1) / s);
+        const double share = (double)ctas * (s * fixed + mean * tile) / kSms;
+        const double join = s > 1 ? 4.0 + (double)(a.T * a.H) * s * a.d * 4 / 3e6 : 0.0;
+        const double t = (ctas * s <= kSms || longest > share + 0.5 * longest ? longest : share + 0.5 * longest) + join;
         if (s == 1 || t < best) {
             best = t;
             p.splits = s;
