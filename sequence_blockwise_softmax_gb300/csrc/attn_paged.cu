@@ -27,7 +27,9 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 ra_status launched(cudaError_t e) {
-    return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
+    if (e == cudaSuccess) return RA_OK;
+    cudaGetLastError();      // reported here, not to the next caller
+    return set_error(RA_ERR_CUDA, cudaGetErrorString(e));
 }
 
 // ------------------------------------------------------------------ join

@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
 
     const uint32_t ring = smem_u32(smem) + warp * L::kWarp;
     const int g = lane >> 2, t4 = lane & 3;
-    bool word_started = false;
+    bool word_started = a.whole_pairs;      // no pair is cut, no word is used (and there may be more CTAs than words)
 
     // ---- one head's keys (or this run's part of them) after another
     while (true) {

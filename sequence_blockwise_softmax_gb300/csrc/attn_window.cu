@@ -73,7 +73,9 @@ ra_status check(Window &w, int64_t window, int64_t sinks, const int *cu_seqlens,
 float softmax_scale(const Window &w) { return w.scale > 0.f ? w.scale : 1.0f / std::sqrt((float)w.d); }
 
 ra_status launched(cudaError_t e) {
-    return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
+    if (e == cudaSuccess) return RA_OK;
+    cudaGetLastError();      // reported here, not to the next caller
+    return set_error(RA_ERR_CUDA, cudaGetErrorString(e));
 }
 
 template <int D, bool F32>
@@ -123,9 +125,16 @@ BwdSpace bwd_space(int64_t B, int64_t L, int64_t H, int64_t H_kv, int d, int64_t
     // no query lies past a window of L tokens: no far part
     s.units = sinks > 0 && window < L ? sink_units(L, n_seqs, sink_chunk(window)) : 0;
     s.dvec = kHeader;
-    s.part = s.dvec + round256((size_t)B * L * H * 4);
-    const size_t slots = s.units > 0 ? s.units + n_seqs + 1 : 0;
-    s.total = s.part + round256(2 * (size_t)B * H_kv * slots * sinks * d * 4);
+    const size_t slots = s.units > 0 ? s.units + (size_t)n_seqs + 1 : 0;
+    // (sizes that no GPU holds would leave 64 bits)
+    const unsigned __int128 rows = (unsigned __int128)B * L * H * 4,
+                            part = (unsigned __int128)2 * B * H_kv * slots * sinks * d * 4;
+    if (rows + part > ((unsigned __int128)1 << 46)) {
+        s.part = s.total = 0;
+        return s;
+    }
+    s.part = s.dvec + round256((size_t)rows);
+    s.total = s.part + round256((size_t)part);
     return s;
 }
 
@@ -261,6 +270,7 @@ ra_status ra_window_attn_bwd(const void *q, const void *k, const void *v, const 
         if (!aligned16(p)) return set_error(RA_ERR_ALIGNMENT, "every tensor pointer must be 16-byte aligned");
     }
     const BwdSpace space = bwd_space(B, L, H, H_kv, d, window, sinks, n_seqs);
+    if (space.total == 0) return set_error(RA_ERR_UNSUPPORTED, "sizes beyond the supported range");
     if (workspace_bytes < space.total)
         return set_error(RA_ERR_INVALID_ARG, "workspace smaller than ra_window_attn_bwd_workspace_bytes()");
     auto launch = d == 128 ? launch_bwd<128> : launch_bwd<64>;

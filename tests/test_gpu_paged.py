@@ -397,6 +397,30 @@ def test_workspace_left_by_other_calls(ralib, gpu):
             assert_paged(c, q, o, lse, [n, n], 0, 0)
 
 
+@pytest.mark.parametrize("new,longest,H,Hkv,d", [
+    ([1] * 300, 900, 16, 8, 64),            # a CTA for each pair, more of them than counters
+    ([1] * 70, 3000, 16, 8, 64),            # equal runs of all pairs
+    ([1, 1], 9000, 8, 1, 128),              # pieces of one pair
+    ([4, 8], 3000, 8, 2, 128),              # two row tiles
+    ([40], 20000, 8, 2, 128),               # tiles, split and joined
+    ([40, 2, 300], 700, 8, 2, 64),
+    ([40, 2, 60], 100, 8, 2, 64),           # few keys
+])
+def test_workspace_is_not_left(ralib, gpu, new, longest, H, Hkv, d):
+    """Nothing is written past the bytes a call asks for."""
+    r = random.Random(longest)
+    lens = [longest] + [max(x, r.randint(1, longest)) for x in new[1:]]
+    c = Cache(lens, 16, Hkv, d, 91)
+    c.fill_all()
+    q = randn_bf16((sum(new), H, d), 4).cuda()
+    need = ralib.ra_paged_attn_workspace_bytes(sum(new), len(new), H, Hkv, d, max(new), longest)
+    room = torch.zeros(need + (1 << 20), dtype=torch.uint8, device="cuda")
+    room[need:] = 0xA5
+    o, lse, _ = attend(ralib, c, q, cu_of(new), new, torch.bfloat16, ws=room[:need])
+    assert bool((room[need:] == 0xA5).all())
+    assert_paged(c, q, o, lse, new, 0, 0)
+
+
 def test_two_streams_two_workspaces(ralib, gpu):
     """The same call on two streams at once, a workspace each, many times over."""
     c = Cache([20000, 300, 7000], 64, 2, 128, 83)

@@ -163,6 +163,25 @@ def test_gradients_repeat_and_replay(ralib, gpu):
     ralib.ra_check_status(ws)
 
 
+@pytest.mark.parametrize("L,sinks,cu", [(700, 5, None), (3000, 131, [0, 10, 1500, 2900]), (600, 0, None)])
+def test_workspace_is_not_left(ralib, gpu, L, sinks, cu):
+    """The backward writes nothing past the bytes it asks for."""
+    H, Hkv, d, window = 4, 2, 64, 50
+    q, k, v, do = inputs(1, L, H, Hkv, d, 17)
+    cu_dev, _ = boundaries(cu, L)
+    o, lse = run_fwd(ralib, q, k, v, window, sinks, cu_dev, torch.bfloat16)
+    want = run_bwd(ralib, q, k, v, o, do, lse, window, sinks, cu_dev, torch.bfloat16)
+    need = ralib.ra_window_attn_bwd_workspace_bytes(1, L, H, Hkv, d, window, sinks, 0 if cu is None else len(cu) - 1)
+    room = torch.zeros(need + (1 << 20), dtype=torch.uint8, device="cuda")
+    room[need:] = 0xA5
+    grads = [torch.empty_like(x) for x in (q, k, v)]
+    ralib.ra_window_attn_bwd(q, k, v, o, do, lse, *grads, 1, L, H, Hkv, d, window, sinks, cu_seqlens=cu_dev,
+                             workspace=room[:need])
+    assert bool((room[need:] == 0xA5).all())
+    for x, y in zip(grads, want):
+        assert torch.equal(x, y)
+
+
 def test_side_stream(ralib, gpu):
     B, L, H, d = 1, 1000, 2, 128
     q, k, v, _ = inputs(B, L, H, H, d, 3)

@@ -125,6 +125,8 @@ def test_backward_workspace(ralib):
     # chunks of 512 queries, one more for each sequence, and each sequence's own part
     assert f(1, 5000, 4, 2, 64, 100, 8) == 256 + r(80000) + 2 * 2 * (10 + 1) * 8 * 64 * 4
     assert f(1, 5000, 4, 2, 64, 100, 8, n_seqs=5) == 256 + r(80000) + 2 * 2 * (15 + 6) * 8 * 64 * 4
+    assert f(1, 1 << 29, 1 << 9, 1 << 9, 128, 1, 1 << 29) == 0      # would leave 64 bits
+    assert f(1, 128, 1 << 20, 1 << 20, 128, 1, 128, n_seqs=(1 << 31) - 1) == 0
     assert f(1, 5000, 4, 2, 96, 100, 8) == 0 and f(1, 5000, 4, 2, 64, 0, 8) == 0
 
 
