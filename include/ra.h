@@ -357,8 +357,9 @@ RA_API ra_status ra_window_attn_fwd(const void *q, const void *k, const void *v,
  * written.  Deterministic (no atomics).  The sinks' gradient from the queries
  * past their windows is taken in chunks of queries and added in their order.
  * workspace: ra_window_attn_bwd_workspace_bytes() bytes (the status word, D and
- * the sinks' partial gradients), zero-filled before its first use; calls that
- * may overlap on the GPU need one each.
+ * the sinks' partial gradients, about 32 MiB unless there are many sequences),
+ * zero-filled before its first use; calls that may overlap on the GPU need one
+ * each.
  */
 RA_API ra_status ra_window_attn_bwd(const void *q, const void *k, const void *v, const void *o,
                                     const void *dout, const float *lse, void *dq, void *dk, void *dv,

@@ -118,12 +118,16 @@ ra_status launch_fwd(const Window &w, const void *q, const void *k, const void *
 struct BwdSpace {
     size_t dvec, part, total;
     int64_t units;
+    int chunk;          // queries of a unit
 };
 BwdSpace bwd_space(int64_t B, int64_t L, int64_t H, int64_t H_kv, int d, int64_t window, int64_t sinks, int n_seqs) {
     BwdSpace s;
     if (sinks > L) sinks = L;
     // no query lies past a window of L tokens: no far part
-    s.units = sinks > 0 && window < L ? sink_units(L, n_seqs, sink_chunk(window)) : 0;
+    // (a slot past 2^46 bytes is refused below)
+    const double slot = 8.0 * (double)B * (double)H_kv * (double)sinks * d;
+    s.chunk = sink_chunk(window, L, n_seqs, slot < 0x1p46 ? (int64_t)slot : (int64_t)1 << 46);
+    s.units = sinks > 0 && window < L ? sink_units(L, n_seqs, s.chunk) : 0;
     s.dvec = kHeader;
     const size_t slots = s.units > 0 ? s.units + (size_t)n_seqs + 1 : 0;
     // (sizes that no GPU holds would leave 64 bits)
@@ -173,7 +177,7 @@ ra_status launch_bwd(const Window &w, const void *q, const void *k, const void *
     a.grad_bf16 = grad_bf16 ? 1 : 0;
     a.sink_units = (int)space.units;
     a.sink_part = reinterpret_cast<float *>(workspace + space.part);
-    a.sink_chunk = sink_chunk(w.window);
+    a.sink_chunk = space.chunk;
     const int64_t n_far = w.B * w.H_kv * ((w.sinks + 127) / 128) * space.units;
     const int64_t n_kv = w.B * w.H_kv * a.n_tiles_seq, n_q = w.B * w.H * a.n_tiles_seq;
     const int64_t joins = space.units > 0 ? w.B * w.H_kv * (w.n_seqs + 1) * w.sinks : 0;   // warps

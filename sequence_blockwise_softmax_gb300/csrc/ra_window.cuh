@@ -144,9 +144,14 @@ RA_HD int window_col_end(int t, int end, int window) {
 // [start, end) are start / chunk .. (end - 1) / chunk, one more than
 // the next sequence's start is on at most, which the "+ s" has room for.
 // A chunk is about as long as a key block's own queries (the window), so that
-// the two kinds of block take alike; from 512 to 2048 rows.
-RA_HD int sink_chunk(int64_t window) {
-    return window <= 512 ? 512 : window >= 2048 ? 2048 : (int)((window + 127) / 128 * 128);
+// the two kinds of block take alike, from 512 rows (shorter ones cost more CTAs
+// than they even out: 3000 tokens, window 100, 36 us with 256 against 32) to
+// 2048; longer where the partial gradients (slot_bytes for each unit and each sequence) would pass 32
+// MiB.
+RA_HD int sink_chunk(int64_t window, int64_t S, int64_t n_seqs, int64_t slot_bytes) {
+    int64_t c = window <= 512 ? 512 : window >= 2048 ? 2048 : (window + 127) / 128 * 128;
+    while (c < S && (S / c + 2 * n_seqs + 2) > ((int64_t)32 << 20) / (slot_bytes > 0 ? slot_bytes : 1)) c *= 2;
+    return (int)c;
 }
 
 struct SinkUnit {

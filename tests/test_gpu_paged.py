@@ -421,6 +421,27 @@ def test_workspace_is_not_left(ralib, gpu, new, longest, H, Hkv, d):
     assert_paged(c, q, o, lse, new, 0, 0)
 
 
+@pytest.mark.parametrize("n,length,window", [(1, 3000, 0), (40, 3000, 0), (40, 50, 0), (9, 3000, 20)])
+def test_pool_past_32_bits(ralib, gpu, n, length, window):
+    """Pages whose offsets pass 2^32 elements and 2^33 bytes, in each form; appended and read."""
+    Hkv, d, page, H = 8, 128, 256, 16
+    n_pages = (1 << 32) // (page * Hkv * d) + 40
+    c = Cache([length], page, Hkv, d, 5)
+    pool = torch.empty((n_pages, 2, page, Hkv, d), dtype=torch.bfloat16, device="cuda")
+    held = -(-length // page)
+    high = torch.randperm(30)[:held] + n_pages - 35
+    c.n_pages, c.k, c.v = n_pages, pool[:, 0], pool[:, 1]
+    c.table = torch.full((1, held + 1), -1, dtype=torch.int32, device="cuda")
+    c.table[0, :held] = high.to(torch.int32).cuda()
+    pool[n_pages - 40:] = NAN
+    c.fill(0, 0, length - n)
+    ws = ralib.new_workspace(64 << 20)
+    ralib.ra_paged_append(c.ks[0][length - n:], c.vs[0][length - n:], c.k, c.v, c.table, c.seq_lens, cu_of([n]), workspace=ws)
+    q = randn_bf16((n, H, d), 3).cuda()
+    o, lse, _ = attend(ralib, c, q, cu_of([n]), [n], torch.bfloat16, window, 4 if window else 0, ws=ws)
+    assert_paged(c, q, o, lse, [n], window, 4 if window else 0)
+
+
 def test_two_streams_two_workspaces(ralib, gpu):
     """The same call on two streams at once, a workspace each, many times over."""
     c = Cache([20000, 300, 7000], 64, 2, 128, 83)

@@ -50,9 +50,10 @@ def test_every_pair_once(probe, S, window, sinks, cu):
         cnt = np.zeros((S, S), dtype=np.int32)
         probe.ra_test_window_rows(S, window, sinks, ptr, n, rows, ctypes.c_void_p(cnt.ctypes.data))
         assert np.array_equal(cnt, ok.astype(np.int32)), rows
-    cnt = np.zeros((S, S), dtype=np.int32)
-    assert probe.ra_test_window_cols(S, window, sinks, ptr, n, ctypes.c_void_p(cnt.ctypes.data)) == 0
-    assert np.array_equal(cnt, ok.astype(np.int32))
+    for slot_bytes in (0, 4 << 20):         # the second makes the sinks' chunks longer
+        cnt = np.zeros((S, S), dtype=np.int32)
+        assert probe.ra_test_window_cols(S, window, sinks, ptr, n, slot_bytes, ctypes.c_void_p(cnt.ctypes.data)) == 0
+        assert np.array_equal(cnt, ok.astype(np.int32))
 
 
 def test_reference_gradients_are_differences():
@@ -125,6 +126,9 @@ def test_backward_workspace(ralib):
     # chunks of 512 queries, one more for each sequence, and each sequence's own part
     assert f(1, 5000, 4, 2, 64, 100, 8) == 256 + r(80000) + 2 * 2 * (10 + 1) * 8 * 64 * 4
     assert f(1, 5000, 4, 2, 64, 100, 8, n_seqs=5) == 256 + r(80000) + 2 * 2 * (15 + 6) * 8 * 64 * 4
+    assert f(1, 5000, 4, 2, 64, 1000, 8) == 256 + r(80000) + 2 * 2 * (5 + 1) * 8 * 64 * 4
+    # many sinks and heads: longer chunks keep the partial gradients near 32 MiB
+    assert f(2, 32768, 8, 8, 128, 1, 129) - 256 - 4 * 2 * 32768 * 8 <= 33 << 20
     assert f(1, 1 << 29, 1 << 9, 1 << 9, 128, 1, 1 << 29) == 0      # would leave 64 bits
     assert f(1, 128, 1 << 20, 1 << 20, 128, 1, 128, n_seqs=(1 << 31) - 1) == 0
     assert f(1, 5000, 4, 2, 96, 100, 8) == 0 and f(1, 5000, 4, 2, 64, 0, 8) == 0

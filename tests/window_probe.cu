@@ -24,8 +24,8 @@ void ra_test_window_rows(int S, int window, int sinks, const int *cu, int n_seqs
 // in 128-query tiles of its block's walk, and each sink against the units past
 // its window; a unit's partial counts only if the key's sum reads it.
 // Returns 1 if a unit number leaves [0, sink_units).
-int ra_test_window_cols(int S, int window, int sinks, const int *cu, int n_seqs, int *cnt) {
-    const int chunk = ra::sink_chunk(window);
+int ra_test_window_cols(int S, int window, int sinks, const int *cu, int n_seqs, int slot_bytes, int *cnt) {
+    const int chunk = ra::sink_chunk(window, S, cu ? n_seqs : 0, slot_bytes);
     const int64_t units = ra::sink_units(S, cu ? n_seqs : 0, chunk);
     for (int c0 = 0; c0 < S; c0 += 128) {
         const int c_end = c0 + 128 < S ? c0 + 128 : S;
