@@ -6,7 +6,11 @@
 // KEYS_PAGED): units of up to 256 rows (the query heads of one key/value head
 // by consecutive new tokens), key tiles of 128 gathered page by page with TMA.
 // Where there are few units, each unit's key tiles are cut into parts that run
-// as CTAs of their own and are joined by their LSE.
+// as CTAs of their own and are joined by their LSE.  Bound by the tensor cores'
+// pace (about 1.35 us for 128 keys by 256 rows at d = 128) and a CTA's fixed 8
+// us: 512 tokens over 32768 keys, 32 / 8 heads, 217 us in pages of 16 and 200 in
+// pages of 128 (1255 and 1360 TFLOP/s); two prompts of 2048 tokens over 8192: 329
+// us (1460 TFLOP/s).  Few rows and few keys have forms of their own.
 #include <cmath>
 
 #include "attn_fwd_kernel.cuh"
@@ -399,7 +403,8 @@ ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, co
 // Row i of sequence s's n new rows goes to position seq_lens[s] - n + i.  A
 // token's bytes are one run on both sides; a block copies up to kAppendTokens
 // tokens, each thread four 16-byte pieces of keys and of values at a time.
-// Bound by HBM: 4 * H_kv * d * 2 bytes per token.
+// Bound by HBM: 4 * H_kv * d * 2 bytes per token; 20589 tokens of 8 heads, d =
+// 128: 29 us, 5.8 TB/s; 64 tokens 2.7 us, the launch.
 struct AppendArgs {
     PagedSeqs seqs;
     const uint4 *k_new, *v_new;

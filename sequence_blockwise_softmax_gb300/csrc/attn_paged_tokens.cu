@@ -24,8 +24,14 @@
 // P enters its product as the sum of two bf16 values (ra_warp_mma.cuh), which
 // costs a second product and leaves the output's own rounding as the only one.
 //
-// Measured on a GB300 (64 sequences of 200-16000 keys, 32 / 8 heads, d = 128):
-// see the design doc's table of the operators.
+// The mathematics: S = q K^T, P = 2^(S scale log2 e - m), l = sum P, O = P V / l,
+// LSE = (m + log2 l) ln 2, with m moved rarely; pieces with (m_i, l_i, O_i) add to
+// m = max m_i, l = sum l_i 2^(m_i - m), O = sum O_i 2^(m_i - m).
+//
+// Measured on a GB300, 32 / 8 heads, d = 128: 64 sequences of 200-16000 keys 355
+// us (6.75 TB/s; the bytes alone take 353 at the copy rate), 8 of 3000-4000 keys
+// 24 us, one of 1000 keys 7.7 us, which is a chain of latencies: lengths, table,
+// keys, the warps' rows, the join.
 #include <atomic>
 #include <cmath>
 #include <type_traits>
