@@ -49,7 +49,8 @@ METRIC_BWD = "causal ring-attention bwd TFLOP/s (bf16, 1×GB300; algorithmic 8·
 DEFAULT_WORKLOAD = "striped_B1_H8_L131072_d128_N16"
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "attn_fwd_striped_128k_traffic.txt")
 KERNEL_SOURCES = [os.path.join(ROOT, "sequence_blockwise_softmax_gb300", "csrc", f)
-                  for f in ("attn_sm103.cu", "attn_fwd_kernel.cuh", "ra_device.cuh", "ra_positions.cuh", "ra_internal.h")]
+                  for f in ("attn_sm103.cu", "attn_fwd_kernel.cuh", "kv_tile.cuh", "ra_device.cuh", "ra_positions.cuh",
+                            "ra_internal.h")]
 
 
 def algorithmic_flops(B, L, H, d, causal):

@@ -337,10 +337,12 @@ RA_API size_t ra_ring_attn_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, 
  * no window); sinks >= 0 (0: none); scale <= 0: 1 / sqrt(d).
  * cu_seqlens / n_seqs: packed sequences, n_seqs + 1 int32 boundaries on the
  * device from 0 up (B = 1), or NULL / 0 for B sequences of L tokens.  Tokens
- * past the last boundary form one more sequence.  Boundaries that do not
+ * from the last boundary on belong to no sequence: they may hold anything, and
+ * their rows of o and lse are left as they were.  Boundaries that do not
  * increase give wrong masks, never an access out of range.
- * Every element of q, k and v must be finite: tiles are multiplied whole, and
- * an infinity or NaN in V reaches the rows of the same tile that mask it.
+ * Every element of the sequences' q, k and v must be finite: tiles are
+ * multiplied whole, and an infinity or NaN in V reaches the rows of the same
+ * tile that mask it.
  * workspace: RA_WORKSPACE_MIN_BYTES bytes, zero-filled before its first use.
  */
 RA_API ra_status ra_window_attn_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
@@ -353,8 +355,8 @@ RA_API ra_status ra_window_attn_fwd(const void *q, const void *k, const void *v,
  * ra_window_attn_bwd -- gradients of ra_window_attn_fwd (the formulas of
  * ra_ring_attn_bwd under the windowed mask).  o: the forward's output, fp32, or
  * bf16 with RA_FLAG_O_BF16; dout: bf16 like q; lse: from the forward.  dq like
- * q, dk and dv like k: fp32, or bf16 with RA_FLAG_GRAD_BF16; every element is
- * written.  Deterministic (no atomics).  The sinks' gradient from the queries
+ * q, dk and dv like k: fp32, or bf16 with RA_FLAG_GRAD_BF16; every row of a
+ * sequence is written, the others are left as they were.  Deterministic (no atomics).  The sinks' gradient from the queries
  * past their windows is taken in chunks of queries and added in their order.
  * workspace: ra_window_attn_bwd_workspace_bytes() bytes (the status word, D and
  * the sinks' partial gradients, about 32 MiB unless there are many sequences),

@@ -47,6 +47,7 @@
 #pragma once
 #include <type_traits>
 
+#include "kv_tile.cuh"
 #include "ra_device.cuh"
 #include "ra_internal.h"
 #include "ra_positions.cuh"
@@ -323,12 +324,18 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &tmq, const CUtens
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    const int S = args.S, H = args.H, N = args.N;
+    const int H = args.H, N = args.N;
+    // BWD_WINDOW: the tokens in sequences; rows behind them are left alone
+    const int S = KEYS == BWD_WINDOW ? packed_tokens(args.cu_seqlens, args.n_seqs, args.S) : args.S;
     // causal work grows with the query position: heaviest tiles first
     const UnitId unit = decode_unit(block, args.bh_chunk_q, args.B, H, N, args.n_tiles_seq, args.layout);
     const int b = unit.b, h = unit.h, qi = unit.qi, qt = unit.qt;
     const int zq = qi * args.B + b;
     const int row0 = qt * 128;
+    if (KEYS == BWD_WINDOW && row0 >= S) {
+        pdl_wait();
+        return;
+    }
     const int row_end = min(S, row0 + 128);
     const int hk = h / (H / args.Hkv);
     const int64_t total = (int64_t)N * S;
@@ -460,6 +467,9 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &tmq, const CUtens
             tc_commit_elect(BAR(B_DPFULL));
             tc_commit_elect(BAR(B_VEMPTY + u % NV));
         };
+        // keys behind the last sequence may hold anything: they are read as zeros
+        // (K by dQ's product too, which follows dS and so this warp's S)
+        const bool ragged = KEYS == BWD_WINDOW && S < args.S;
         bool ok = warp_wait(BAR(B_QFULL), 0, abort_flag);
         Walk w = walk0;
         w.start_step();
@@ -469,6 +479,7 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &tmq, const CUtens
             for (; ok && w.valid(); w.next(), ++t) {
                 if (!(ok = warp_wait(BAR(B_VFULL + t % NV), (t / NV) & 1, abort_flag))) break;
                 if (t > 0 && !(ok = warp_wait(BAR(B_DPFREE), (t - 1) & 1, abort_flag))) break;
+                if (ragged) zero_rows<D, KvTile<D, false>>(s_base + L::kV + t % NV * L::kTile, S - w.tile * 128, lane);
                 tc_fence_after();
                 issue_dp(t);
                 __syncwarp();
@@ -481,6 +492,7 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &tmq, const CUtens
                 if (!(ok = warp_wait(BAR(B_KFULL + t % NK), (t / NK) & 1, abort_flag))) break;
                 if (t > 1 && !(ok = warp_wait(BAR(B_DQDONE + ((t - 2) & 1)), ((t - 2) >> 1) & 1, abort_flag)))
                     break;
+                if (ragged) zero_rows<D, KvTile<D, false>>(s_base + L::kK + t % NK * L::kTile, S - w.tile * 128, lane);
                 tc_fence_after();
                 issue_s(t);
                 __syncwarp();
@@ -528,7 +540,7 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &tmq, const CUtens
             row_key_bounds(args.cu_seqlens, args.n_seqs, total, my_pos, args.causal, lo_pos, hi_pos);
         else
             rk = window_row(args.cu_seqlens, args.n_seqs, S, a_c, args.window, args.sinks);
-        const size_t vi = ((size_t)zq * H + h) * S + a_c;
+        const size_t vi = ((size_t)zq * H + h) * args.S + a_c;
         const float lse_v = args.lse[vi];
         const float lse2 = lse_v > -INFINITY ? lse_v * 1.4426950408889634f : 0.f;   // no key: P = 0 anyway
         const float dval = args.dvec[vi];
@@ -620,7 +632,7 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &tmq, const CUtens
             // Each half writes half of the d columns.
             if (ok) {
                 const size_t at = ((args.seq_order ? (size_t)b * total + (size_t)my_pos
-                                                   : (size_t)zq * S + a_c) * H + h) * D;
+                                                   : (size_t)zq * args.S + a_c) * H + h) * D;
                 float *dst = args.dq + at;
 #pragma unroll
                 for (int q = hh * (D / 64); q < (hh + 1) * (D / 64); ++q) {
@@ -711,7 +723,8 @@ __device__ __forceinline__ void bwd_dkv_body(const CUtensorMap &tmq, const CUten
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    const int S = args.S, H = args.H, N = args.N, Hkv = args.Hkv;
+    const int H = args.H, N = args.N, Hkv = args.Hkv;
+    const int S = KEYS == BWD_WINDOW ? packed_tokens(args.cu_seqlens, args.n_seqs, args.S) : args.S;
     const int group = H / Hkv;
     // causal work shrinks with the key position: earliest keys first
     UnitId unit;
@@ -741,6 +754,10 @@ __device__ __forceinline__ void bwd_dkv_body(const CUtensorMap &tmq, const CUten
                                 args.n_tiles_seq, args.layout);
         c0 = unit.qt * 128;
         c_end = min(S, c0 + 128);
+        if (KEYS == BWD_WINDOW && c0 >= S) {
+            pdl_wait();
+            return;
+        }
     }
     const int b = unit.b, hk = unit.h, kj = unit.qi;
     const int zk = kj * args.B + b;
@@ -832,7 +849,7 @@ __device__ __forceinline__ void bwd_dkv_body(const CUtensorMap &tmq, const CUten
             const int y = w.tile * 128;
             // -lse*log2(e) and D of the 128 query rows (0 past the shard's end),
             // read before the stage wait so their latency overlaps it
-            const size_t base = ((size_t)(w.i * args.B + b) * H + h) * S;
+            const size_t base = ((size_t)(w.i * args.B + b) * H + h) * args.S;
             float nl[4], dd[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -881,6 +898,14 @@ __device__ __forceinline__ void bwd_dkv_body(const CUtensorMap &tmq, const CUten
             tc_commit_elect(BAR(B_DPFULL));
         };
         const uint64_t dp_k = sdesc_sw128(s_base + L::kP, 16, 1024);   // P^T as a K-major operand
+        // queries behind the last sequence may hold anything: Q and dO are read as
+        // zeros there (by the gradient products too, which follow P^T and dS^T)
+        auto zero_tail = [&](int st, int tile) {
+            if (KEYS == BWD_WINDOW && S < args.S) {
+                zero_rows<D, KvTile<D, false>>(s_base + L::kQ + st * L::kTile, S - tile * 128, lane);
+                zero_rows<D, KvTile<D, false>>(s_base + L::kDO + st * L::kTile, S - tile * 128, lane);
+            }
+        };
         bool ok = warp_wait(BAR(B_KVFULL), 0, abort_flag);
         QWalk w = walk0;
         w.start();
@@ -889,6 +914,7 @@ __device__ __forceinline__ void bwd_dkv_body(const CUtensorMap &tmq, const CUten
             if (ok && w.valid()) {
                 ok = warp_wait(BAR(B_QFULL), 0, abort_flag);
                 if (ok) {
+                    zero_tail(0, w.tile);
                     tc_fence_after();
                     issue_sT(0);
                     issue_dpT(0);
@@ -901,6 +927,7 @@ __device__ __forceinline__ void bwd_dkv_body(const CUtensorMap &tmq, const CUten
                 const int u = t + 1;
                 if (!(ok = warp_wait(BAR(B_SFREE), t & 1, abort_flag))) break;
                 if (!(ok = warp_wait(BAR(B_QFULL + u % NS), (u / NS) & 1, abort_flag))) break;
+                zero_tail(u % NS, w.tile);
                 tc_fence_after();
                 issue_sT(u);
                 __syncwarp();
@@ -1101,7 +1128,7 @@ __device__ __forceinline__ void bwd_dkv_body(const CUtensorMap &tmq, const CUten
             // Each half writes half of the d columns.
             if (ok) {
                 size_t row = ((args.seq_order ? (size_t)b * total + (size_t)kpos
-                                              : (size_t)zk * S + kk_c) * Hkv + hk) * D;
+                                              : (size_t)zk * args.S + kk_c) * Hkv + hk) * D;
                 float *out_dv = args.dv, *out_dk = args.dk;
                 float dk_mul = args.scale;
                 bool bf16 = KEYS == BWD_WINDOW && args.grad_bf16;
@@ -1194,8 +1221,9 @@ __global__ void __launch_bounds__(256) bwd_sink_join(const BwdArgs a) {
     w /= a.n_seqs + 1;
     const int hk = (int)(w % a.Hkv), b = (int)(w / a.Hkv);
     if (b >= a.B) return;
-    const int start = a.cu_seqlens ? seq_bound(a.cu_seqlens, a.n_seqs, a.S, s) : 0;
-    const int end = a.cu_seqlens ? seq_bound(a.cu_seqlens, a.n_seqs, a.S, s + 1) : a.S;
+    const int S = packed_tokens(a.cu_seqlens, a.n_seqs, a.S);
+    const int start = a.cu_seqlens ? seq_bound(a.cu_seqlens, a.n_seqs, S, s) : 0;
+    const int end = a.cu_seqlens ? seq_bound(a.cu_seqlens, a.n_seqs, S, s + 1) : S;
     const int key = start + r, past = key + a.window;
     if (past >= end) return;
     const int u0 = s + past / a.sink_chunk, u1 = s + (end - 1) / a.sink_chunk + 1;

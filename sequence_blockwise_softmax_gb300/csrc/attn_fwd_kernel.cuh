@@ -53,6 +53,7 @@
 #pragma once
 #include <type_traits>
 
+#include "kv_tile.cuh"
 #include "ra_device.cuh"
 #include "ra_internal.h"
 #include "ra_paged.cuh"
@@ -144,20 +145,6 @@ struct AttnSmem {
     static constexpr uint32_t kBytesSkip = kTab + kMaxSteps * 6 * 4;
 };
 
-// How a K or V tile lies in its slot: eight rows of 128 bytes (64 columns) are
-// 1024 bytes; kGroup is the distance from one such group of rows to the next,
-// kHalf from columns 0-63 to 64-127.  A 2-D box per half gives all groups of a
-// half in a row.  Paged tiles at d = 128 interleave the halves, so that one box
-// brings a page's rows whole: half the copies of a tile of small pages (32 of
-// 2 KB at 16 tokens a page otherwise, whose issue held the tile back by 0.5 us).
-template <int D, bool INTERLEAVED>
-struct KvTile {
-    static constexpr uint32_t kGroup = INTERLEAVED ? 2048 : 1024;
-    static constexpr uint32_t kHalf = INTERLEAVED ? 1024 : 128 * 128;
-    static constexpr uint32_t kH = kHalf >> 4;            // descriptor units
-    static constexpr uint32_t kStep = 2 * kGroup >> 4;    // 16 rows
-};
-
 // The key tiles of a unit's walk as the tile-skipping variant sees them: the
 // walk visits tiles [lo, hi) of each step's shard in step order, and Q tile g
 // needs only tiles [glo_g, ghi_g) of them.  With no table (more steps than it
@@ -206,24 +193,6 @@ struct StepCursor {
 // it.  For scores of ordinary size (|s * scale| up to about 20) the
 // reference never moves at all.
 constexpr float kSumLo = 0x1p-32f, kSumHi = 0x1p32f;
-
-// Zero rows [from, 128) of a V tile in shared memory (nothing for from >= 128),
-// by one warp before it issues the products that read them: what lies behind a
-// sequence's last token was never written and may hold NaN, which P = 0 would
-// not remove.
-template <int D, class Tile>
-__device__ __forceinline__ void zero_rows(uint32_t tile, int from, int lane) {
-    if (from >= 128) return;
-    for (int e = max(from, 0) * 8 + lane; e < 128 * 8; e += 32)
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             tile + c * Tile::kHalf + (e >> 6) * Tile::kGroup + (e & 63) * 16),
-                         "r"(0)
-                         : "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-}
 
 // SKIP: each Q tile of a unit skips the key tiles none of its own rows sees
 // (packed sequences in the striped layout, where a unit's 256 rows span many
@@ -277,7 +246,9 @@ __global__ void __launch_bounds__(384, 1)
 
     // ---- unit decode: heavy units first, in L2-sized chunks of (batch, head)
     // pairs (decode_unit)
-    const int S = args.S, H = args.H, N = args.N;
+    const int H = args.H, N = args.N;
+    // KEYS_WINDOW: the tokens in sequences; rows behind them are left alone
+    const int S = KEYS == KEYS_WINDOW ? packed_tokens(args.cu_seqlens, args.n_seqs, args.S) : args.S;
     UnitId unit{};
     PagedUnit pu{};
     int part = 0;             // KEYS_PAGED: which part of the unit's keys
@@ -304,7 +275,14 @@ __global__ void __launch_bounds__(384, 1)
     const int q_rank = ring ? qi : args.q_rank_fixed;
     const int zq = (ring ? qi * args.B : 0) + b;
     const int row0 = qt * 256;
+    if (KEYS == KEYS_WINDOW && row0 >= S) return;
     const int row_end = min(S, row0 + 256);
+    // first row of a key tile that is to be read as zeros (KEYS_PAGED: behind the
+    // sequence; KEYS_WINDOW: behind the last one; past args.S the copy gives zeros)
+    auto zeros_from = [&](int tile) -> int {
+        if (KEYS == KEYS_PAGED) return pu.len - tile * 128;
+        return KEYS == KEYS_WINDOW && S < args.S ? S - tile * 128 : 128;
+    };
 
     Walk walk0;
     if constexpr (KEYS == KEYS_RING)
@@ -635,8 +613,8 @@ __global__ void __launch_bounds__(384, 1)
                 __syncwarp();
             }
             if (!(ok = v_wait(vi % NSL))) break;
-            if constexpr (KEYS == KEYS_PAGED)
-                zero_rows<D, KT>(s_base + L::kRing + (vi % NSL) * L::kTile, pu.len - v_tile * 128, lane);
+            if constexpr (KEYS != KEYS_RING)
+                zero_rows<D, KT>(s_base + L::kRing + (vi % NSL) * L::kTile, zeros_from(v_tile), lane);
             if (need(0, v_tile)) {
                 if (!(ok = warp_wait(BAR(B_PFULL + 0), n_p0 & 1, abort_flag))) break;
                 tc_fence_after();
@@ -857,8 +835,8 @@ __global__ void __launch_bounds__(384, 1)
                 const bool has_next = t + 1 < T;
                 const int vi = has_next ? 2 * t + 2 : 2 * t + 1; // load index of V(t)
                 if (!(ok = v_wait(vi % NSL))) break;
-                if constexpr (KEYS == KEYS_PAGED)
-                    zero_rows<D, KT>(s_base + L::kRing + (vi % NSL) * L::kTile, pu.len - wv.tile * 128, lane);
+                if constexpr (KEYS != KEYS_RING)
+                    zero_rows<D, KT>(s_base + L::kRing + (vi % NSL) * L::kTile, zeros_from(wv.tile), lane);
                 if (!EDGES || seen0.has(w_tile(wv))) {
                     if (!(ok = warp_wait(BAR(B_PFULL + 0), (EDGES ? n0 : t) & 1, abort_flag))) break;
                     tc_fence_after();
@@ -1003,7 +981,7 @@ __global__ void __launch_bounds__(384, 1)
         // KEYS_PAGED: row r is token r / group of the Q tile; rows past the
         // tile's tokens or the unit's take the last token's keys, so that no
         // tile is masked for their sake, and are not stored
-        bool live = true;           // the row is stored
+        bool live = KEYS != KEYS_WINDOW || a < S;           // the row is stored
         bool warp_live = true;      // some row of the warp is
         int my_tok = 0;
         if constexpr (KEYS == KEYS_PAGED) {
@@ -1289,13 +1267,17 @@ __global__ void __launch_bounds__(384, 1)
                 }
             }
         }
-        if constexpr (KEYS == KEYS_PAGED) {
+        // KEYS_WINDOW: a Q tile that ends behind the last sequence goes out row by row
+        const bool ragged = KEYS == KEYS_WINDOW && S < args.S && row0 + 128 * g + 128 > S;
+        if (KEYS == KEYS_PAGED || ragged) {
             // each warp copies its own rows out: final rows of [T, H, d], or
             // this part's rows (fp32) for the join
             const float lse = l > 0.f ? (m_ref + lg2(l)) * 0.6931471805599453f : -INFINITY;
             const int head = h * args.seqs.group + r % args.seqs.group;
             long long at = -1;       // the row's first element
-            if (ok && live && (g == 0 || two_tiles)) {
+            if (KEYS == KEYS_WINDOW) {
+                if (ok && live) at = (long long)((((size_t)b * args.S + a) * H + h) * D);
+            } else if (ok && live && (g == 0 || two_tiles)) {
                 const size_t part_row = (((size_t)unit_no * args.seqs.Hkv + h) * args.seqs.num_splits + part) *
                                             paged_unit_rows(args.seqs) +
                                         my_tok * args.seqs.group + r % args.seqs.group;
@@ -1318,7 +1300,7 @@ __global__ void __launch_bounds__(384, 1)
             uint8_t *out = split ? reinterpret_cast<uint8_t *>(args.part_o) : static_cast<uint8_t *>(args.o);
             const int esz = OUT_F32 && !round ? 4 : 2;
             const int cpr = D * esz / 16;            // 16-byte chunks per row
-            if (warp_live && *abort_flag == 0) {
+            if ((KEYS == KEYS_WINDOW || warp_live) && *abort_flag == 0) {
 #pragma unroll 4
                 for (int e = lane; e < 32 * cpr; e += 32) {
                     const int row = e / cpr, ch = e % cpr;
@@ -1339,7 +1321,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         if constexpr (KEYS != KEYS_PAGED) named_barrier_sync(1 + g, 128);
-        if (KEYS != KEYS_PAGED && wq == 0 && lane == 0 && *abort_flag == 0) {
+        if (KEYS != KEYS_PAGED && !ragged && wq == 0 && lane == 0 && *abort_flag == 0) {
             // rows past the shard's end fall outside the tensor and are not written
             int c1, c2, c3;
             tile_coords(args.seq_order, args.layout, args.S, args.N, ring ? qi : 0, b, row0 + 128 * g, c1, c2, c3);
@@ -1351,7 +1333,7 @@ __global__ void __launch_bounds__(384, 1)
         if (KEYS != KEYS_PAGED && ok && a < S) {
             // shard stacks: [N or 1, B, H, S]; sequence order: [B, H, L] at the row's position
             const size_t at = args.seq_order ? ((size_t)b * H + h) * ((size_t)N * S) + (size_t)my_pos
-                                             : ((size_t)zq * H + h) * S + a;
+                                             : ((size_t)zq * H + h) * args.S + a;
             args.lse[at] = l > 0.f ? (m_ref + lg2(l)) * 0.6931471805599453f : -INFINITY;
         }
     }

@@ -47,8 +47,9 @@ __global__ void __launch_bounds__(32 * kWarps, D == 64 ? 3 : 2) window_few_kerne
     constexpr int kOut = D * 2 + 16;                 // bytes of a staged bf16 row
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    const int S = a.S, group = a.H / a.Hkv;
+    const int group = a.H / a.Hkv;
     pdl_wait();
+    const int S = packed_tokens(a.cu, a.n_seqs, a.S);     // rows behind them are left alone
     // blockIdx.x = ((b * H_kv + hk) * parts of the group + part) * blocks + block
     const int blk = blockIdx.x % a.blocks;
     int rest = blockIdx.x / a.blocks;
@@ -56,13 +57,14 @@ __global__ void __launch_bounds__(32 * kWarps, D == 64 ? 3 : 2) window_few_kerne
     rest /= a.group_parts;
     const int hk = rest % a.Hkv, b = rest / a.Hkv;
     const int r0 = blk * kRows, r_end = min(S, r0 + kRows);
+    if (r0 >= S) return;
     const FewChunks all = few_chunks(window_row(a.cu, a.n_seqs, S, r0, a.window, a.sinks), r_end);
     // a call's own bound on its chunks; only boundaries that do not increase could pass it
     const int n_chunks = min(all.count, a.max_chunks);
     const uint32_t keys = smem_u32(smem), values = keys + a.max_chunks * kHalf;
     {
         // the tokens' rows of head hk: 16-byte pieces, a token's pieces to neighbouring threads
-        const size_t head = ((size_t)b * S * a.Hkv + hk) * D;
+        const size_t head = ((size_t)b * a.S * a.Hkv + hk) * D;
         for (int e = threadIdx.x; e < n_chunks * kChunk * CPR; e += 32 * kWarps) {
             const int row = e / CPR, pc = e % CPR;
             const int key = all.key(row / kChunk) + row % kChunk;
@@ -93,7 +95,7 @@ __global__ void __launch_bounds__(32 * kWarps, D == 64 ? 3 : 2) window_few_kerne
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = w0 + 8 * h + g;
-            const uint16_t *src = a.q + (((size_t)b * S + min(r, S - 1)) * a.H + hq) * D + 2 * t4;
+            const uint16_t *src = a.q + (((size_t)b * a.S + min(r, S - 1)) * a.H + hq) * D + 2 * t4;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 q[ks][h] = *reinterpret_cast<const uint32_t *>(src + ks * 16);
@@ -129,14 +131,14 @@ __global__ void __launch_bounds__(32 * kWarps, D == 64 ? 3 : 2) window_few_kerne
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const int r = w0 + 8 * h + g;
             if (t4 == 0 && r < S)
-                a.lse[((size_t)b * a.H + hq) * S + r] = l > 0.f ? (rw.m[0][h] + lg2(l)) * 0.6931471805599453f : -INFINITY;
+                a.lse[((size_t)b * a.H + hq) * a.S + r] = l > 0.f ? (rw.m[0][h] + lg2(l)) * 0.6931471805599453f : -INFINITY;
             if constexpr (O_BF16) {
                 uint32_t *row = reinterpret_cast<uint32_t *>(stage + (8 * h + g) * kOut) + t4;
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n)
                     row[n * 4] = pack_bf16x2(rw.acc[0][n][2 * h] * inv, rw.acc[0][n][2 * h + 1] * inv);
             } else if (r < S) {
-                float *row = static_cast<float *>(a.o) + (((size_t)b * S + r) * a.H + hq) * D + 2 * t4;
+                float *row = static_cast<float *>(a.o) + (((size_t)b * a.S + r) * a.H + hq) * D + 2 * t4;
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n)
                     *reinterpret_cast<float2 *>(row + n * 8) = make_float2(rw.acc[0][n][2 * h] * inv, rw.acc[0][n][2 * h + 1] * inv);
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(32 * kWarps, D == 64 ? 3 : 2) window_few_kerne
             for (int e = lane; e < 16 * CPR; e += 32) {
                 const int r = e / CPR, pc = e % CPR;
                 if (w0 + r < S)
-                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o) + (((size_t)b * S + w0 + r) * a.H + hq) * D + pc * 8) =
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o) + (((size_t)b * a.S + w0 + r) * a.H + hq) * D + pc * 8) =
                         *reinterpret_cast<const uint4 *>(stage + r * kOut + pc * 16);
             }
             __syncwarp();

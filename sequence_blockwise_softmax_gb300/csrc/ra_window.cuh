@@ -15,9 +15,14 @@
 
 namespace ra {
 
-// Boundary i of the packed sequences, i in [0, n_seqs + 1]: the tokens past
-// the last boundary are one more sequence.  Every read stays inside the
-// n_seqs + 1 boundaries and every value inside [0, S], whatever they hold.
+// The tokens that belong to sequences: up to the last boundary, or all L.  Rows
+// behind them are neither read into a result nor written.
+RA_HD int packed_tokens(const int *cu, int n_seqs, int L) { return cu ? (int)clamp64(cu[n_seqs], 0, L) : L; }
+
+// Boundary i of the packed sequences over S tokens, i in [0, n_seqs + 1] (what
+// lies past the last boundary, if anything, is one more sequence).  Every read
+// stays inside the n_seqs + 1 boundaries and every value inside [0, S],
+// whatever they hold.
 RA_HD int seq_bound(const int *cu, int n_seqs, int S, int i) {
     return i > n_seqs ? S : (int)clamp64(cu[i], 0, S);
 }

@@ -24,6 +24,12 @@ CASES = [
     (1, 2300, 2, 1, 128, 60, 5, None),
     (1, 2600, 2, 2, 64, 77, 131, [0, 30, 2048, 2049, 2060, 2600]),
     (1, 800, 2, 2, 128, 40, 6, [0, 300, 500]),
+    # tokens behind the last sequence, in each form
+    (1, 800, 4, 2, 64, 500, 6, [0, 300, 641]),
+    (1, 1200, 4, 2, 128, 300, 140, [0, 5, 1025]),
+    (1, 1500, 2, 1, 128, 260, 0, [0, 1024]),
+    (1, 400, 2, 2, 64, 5, 3, [0, 0]),
+    (1, 900, 2, 2, 64, 700, 3, [0, 0, 1]),
     # the form with few keys at one wave of blocks above, at several here (the first two pack sequences)
     (1, 2100, 16, 4, 128, 17, 3, [0, 1, 40, 41, 300, 1000, 2049, 2100]),
     (1, 2090, 8, 8, 64, 30, 33, [0, 70, 1024, 2000]),
@@ -38,15 +44,16 @@ CASES = [
 ]
 
 
-def inputs(B, L, H, Hkv, d, seed):
-    return [randn_bf16((B, L, h, d), seed + i).cuda() for i, h in enumerate((H, Hkv, Hkv, H))]
+def inputs(B, L, H, Hkv, d, seed, tokens=None):
+    """q, k, v, dO; what lies behind the first `tokens` tokens is NaN."""
+    xs = [randn_bf16((B, L, h, d), seed + i).cuda() for i, h in enumerate((H, Hkv, Hkv, H))]
+    for x in xs:
+        x[:, L if tokens is None else tokens:] = float("nan")
+    return xs
 
 
-def boundaries(cu, L):
-    """The device boundaries of a call and the reference's, which closes the last sequence."""
-    if cu is None:
-        return None, None
-    return torch.tensor(cu, dtype=torch.int32, device="cuda"), cu if cu[-1] == L else cu + [L]
+def boundaries(cu):
+    return None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
 
 
 def run_fwd(ra, q, k, v, window, sinks, cu, o_dtype, scale=0.0):
@@ -82,21 +89,24 @@ def reference(q, k, v, window, sinks, cu, scale):
 @pytest.mark.parametrize("B,L,H,Hkv,d,window,sinks,cu", CASES)
 @pytest.mark.parametrize("o_dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
 def test_window_matches_definition(ralib, gpu, B, L, H, Hkv, d, window, sinks, cu, o_dtype):
-    q, k, v, do = inputs(B, L, H, Hkv, d, 7 * L + window)
-    cu_dev, cu_ref = boundaries(cu, L)
+    n = L if cu is None else cu[-1]           # tokens in sequences; the others' rows stay as they were
+    q, k, v, do = inputs(B, L, H, Hkv, d, 7 * L + window, n)
+    cu_dev = boundaries(cu)
     scale = d ** -0.5
     o, lse = run_fwd(ralib, q, k, v, window, sinks, cu_dev, o_dtype)
-    ok, qd, kd, vd, (o_ref, lse_ref, p) = reference(q, k, v, window, sinks, cu_ref, scale)
+    assert bool(torch.isnan(o[:, n:]).all()) and bool(torch.isnan(lse[:, :, n:]).all())
+    ok, qd, kd, vd, (o_ref, lse_ref, p) = reference(*(x[:, :n] for x in (q, k, v)), window, sinks, cu, scale)
     what = "window %d sinks %d" % (window, sinks)
-    ref.assert_within(o, o_ref, ref.forward_tolerance(p, vd, o_ref, o_dtype == torch.bfloat16), what + " O")
-    ref.assert_within(lse, lse_ref, torch.full_like(lse_ref, ref.EPS), what + " LSE")
+    ref.assert_within(o[:, :n], o_ref, ref.forward_tolerance(p, vd, o_ref, o_dtype == torch.bfloat16), what + " O")
+    ref.assert_within(lse[:, :, :n], lse_ref, torch.full_like(lse_ref, ref.EPS), what + " LSE")
     del p
-    grads, tols = ref.backward(qd, kd, vd, o.double(), do.double(), lse.double(), ok, scale, Hkv)
+    grads, tols = ref.backward(qd, kd, vd, o[:, :n].double(), do[:, :n].double(), lse[:, :, :n].double(), ok, scale, Hkv)
     for g_dtype in (torch.float32, torch.bfloat16):
         out = run_bwd(ralib, q, k, v, o, do, lse, window, sinks, cu_dev, g_dtype)
         for name, x, g, t in zip(("dq", "dk", "dv"), out, grads, tols):
             end = ref.U * 1.01 * g.abs() if g_dtype == torch.bfloat16 else 0.0
-            ref.assert_within(x, g, t + end + 1e-5, what + " " + name)
+            ref.assert_within(x[:, :n], g, t + end + 1e-5, what + " " + name)
+            assert bool(torch.isnan(x[:, n:]).all()), what + " " + name + " behind the sequences"
 
 
 def test_scores_far_from_zero(ralib, gpu):
@@ -168,7 +178,7 @@ def test_workspace_is_not_left(ralib, gpu, L, sinks, cu):
     """The backward writes nothing past the bytes it asks for."""
     H, Hkv, d, window = 4, 2, 64, 50
     q, k, v, do = inputs(1, L, H, Hkv, d, 17)
-    cu_dev, _ = boundaries(cu, L)
+    cu_dev = boundaries(cu)
     o, lse = run_fwd(ralib, q, k, v, window, sinks, cu_dev, torch.bfloat16)
     want = run_bwd(ralib, q, k, v, o, do, lse, window, sinks, cu_dev, torch.bfloat16)
     need = ralib.ra_window_attn_bwd_workspace_bytes(1, L, H, Hkv, d, window, sinks, 0 if cu is None else len(cu) - 1)
@@ -178,8 +188,9 @@ def test_workspace_is_not_left(ralib, gpu, L, sinks, cu):
     ralib.ra_window_attn_bwd(q, k, v, o, do, lse, *grads, 1, L, H, Hkv, d, window, sinks, cu_seqlens=cu_dev,
                              workspace=room[:need])
     assert bool((room[need:] == 0xA5).all())
+    n = L if cu is None else cu[-1]
     for x, y in zip(grads, want):
-        assert torch.equal(x, y)
+        assert torch.equal(x[:, :n], y[:, :n])
 
 
 def test_side_stream(ralib, gpu):
