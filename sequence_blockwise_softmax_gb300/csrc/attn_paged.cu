@@ -30,12 +30,6 @@ static_assert(kPagedTokensCtas * 8 <= kCounterBytes, "one counter per CTA");
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-ra_status launched(cudaError_t e) {
-    if (e == cudaSuccess) return RA_OK;
-    cudaGetLastError();      // reported here, not to the next caller
-    return set_error(RA_ERR_CUDA, cudaGetErrorString(e));
-}
-
 // ------------------------------------------------------------------ join
 // O = sum_i w_i O_i, w_i = exp(LSE_i - LSE), over a row's parts in order, so
 // that the result does not depend on timing; rows of one part were written by

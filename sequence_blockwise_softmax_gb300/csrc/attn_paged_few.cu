@@ -205,8 +205,7 @@ ra_status launch_paged_few(const PagedFewLaunch &t, cudaStream_t stream) {
         return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
     const int64_t grid = (int64_t)t.units * t.seqs.Hkv;
     if (grid > 0x7fffffffLL) return set_error(RA_ERR_UNSUPPORTED, "too many query tiles for one launch");
-    const cudaError_t e = launch_dependent(kern, (unsigned)grid, 32 * kWarps, smem, stream, a);
-    return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
+    return launched(launch_dependent(kern, (unsigned)grid, 32 * kWarps, smem, stream, a));
 }
 
 }  // namespace ra

@@ -460,8 +460,7 @@ ra_status launch(const TokensLaunch &t, const TokensArgs &args, cudaStream_t str
     static_assert(kWarps * 16 * MT * TokensSmem<D>::kRow * 4 <= TokensSmem<D>::kBytes, "the warps' rows fit in the rings");
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
-    const cudaError_t e = launch_dependent(kern, (unsigned)t.ctas, 32 * kWarps, smem, stream, args);
-    return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
+    return launched(launch_dependent(kern, (unsigned)t.ctas, 32 * kWarps, smem, stream, args));
 }
 
 }  // namespace

@@ -81,12 +81,6 @@ ra_status check(Window &w, int64_t window, int64_t sinks, const int *cu_seqlens,
 
 float softmax_scale(const Window &w) { return w.scale > 0.f ? w.scale : 1.0f / std::sqrt((float)w.d); }
 
-ra_status launched(cudaError_t e) {
-    if (e == cudaSuccess) return RA_OK;
-    cudaGetLastError();      // reported here, not to the next caller
-    return set_error(RA_ERR_CUDA, cudaGetErrorString(e));
-}
-
 template <int D, bool F32>
 ra_status launch_fwd(const Window &w, const void *q, const void *k, const void *v, void *o, float *lse,
                      unsigned *status, cudaStream_t stream) {

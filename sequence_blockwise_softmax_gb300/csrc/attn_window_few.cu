@@ -192,8 +192,7 @@ ra_status launch_window_few(WindowFew a, int d, bool o_bf16, int64_t B, cudaStre
     a.group_parts = (group + a.heads - 1) / a.heads;
     const int64_t grid = whole * a.group_parts;
     if (grid > 0x7fffffffLL) return set_error(RA_ERR_UNSUPPORTED, "too many query tiles for one launch");
-    const cudaError_t e = launch_dependent(kern, (unsigned)grid, 32 * kWarps, smem, stream, a);
-    return e == cudaSuccess ? RA_OK : set_error(RA_ERR_CUDA, cudaGetErrorString(e));
+    return launched(launch_dependent(kern, (unsigned)grid, 32 * kWarps, smem, stream, a));
 }
 
 }  // namespace ra

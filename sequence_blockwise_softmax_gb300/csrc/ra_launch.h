@@ -2,6 +2,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include "ra_internal.h"
+
 namespace ra {
 
 // Launch `kern` so that its blocks may start while the stream's previous kernel
@@ -20,6 +22,13 @@ inline cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned 
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
+// A call's status from that of its launches.
+inline ra_status launched(cudaError_t e) {
+    if (e == cudaSuccess) return RA_OK;
+    cudaGetLastError();      // reported here, not to the next caller
+    return set_error(RA_ERR_CUDA, cudaGetErrorString(e));
 }
 
 }  // namespace ra
