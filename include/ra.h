@@ -404,7 +404,8 @@ RA_API size_t ra_window_attn_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H
  * q: bf16 [T, H, d] with q_stride elements from token to token (at least H * d,
  * a multiple of 8); o: fp32 [T, H, d], or bf16 with RA_FLAG_O_BF16; lse: fp32
  * [H, T], natural log, or NULL.  d in {64, 128}; H_kv divides H, at most 128
- * query heads to one key/value head.  A token at a negative position gets
+ * query heads to one key/value head; min(n_seqs, T) * H_kv * max_pages *
+ * page_size at most 2^43.  A token at a negative position gets
  * O = 0 and LSE = -inf.  What lies in a page behind a sequence's last token may
  * be anything, NaN included; what a sequence's tokens hold must be finite.
  * max_new: no sequence has more new tokens.  max_len: how long the sequences

@@ -504,6 +504,10 @@ ra_status ra_paged_attn_fwd(const void *q, const void *k_pages, const void *v_pa
         if (!aligned(p, 4)) return set_error(RA_ERR_ALIGNMENT, "block_table, seq_lens and cu_q must be 4-byte aligned");
     }
     if (!aligned(lse, 4)) return set_error(RA_ERR_ALIGNMENT, "lse must be 4-byte aligned");
+    // a CTA of the few-row form counts its 16-key chunks in 31 bits
+    const int64_t active = n_seqs < T ? n_seqs : T;
+    if ((double)(active * H_kv) * (double)(max_pages * page_size) > 0x1p43)
+        return set_error(RA_ERR_UNSUPPORTED, "sequences * H_kv * max_pages * page_size beyond the supported range (2^43)");
     if (workspace_bytes < plan(a).total)
         return set_error(RA_ERR_INVALID_ARG, "workspace smaller than ra_paged_attn_workspace_bytes()");
     auto launch = d == 128 ? launch_paged<128> : launch_paged<64>;

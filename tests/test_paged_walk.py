@@ -111,7 +111,7 @@ def _fwd(lib, **kw):
     (dict(max_pages=1 << 27), 3), (dict(W=-1), 1), (dict(sinks=-1), 1), (dict(scale=float("nan")), 1), (dict(flags=4), 1),
     (dict(q=0), 1), (dict(k=FAKE + 8), 4), (dict(table=0), 1), (dict(table=FAKE + 2), 4), (dict(lse=FAKE + 2), 4),
     (dict(o=0), 1), (dict(ws=0), 1), (dict(wsb=255), 1), (dict(n_pages=0), 2), (dict(new=-1), 2), (dict(len=-1), 2),
-    (dict(T=(1 << 24) + 1), 3),
+    (dict(T=(1 << 24) + 1), 3), (dict(T=1 << 15, n=1 << 15, page=1 << 16, pstride=1 << 24, max_pages=1 << 13, new=1), 3),
 ])
 def test_forward_refuses(ralib, kw, status):
     assert _fwd(ralib.lib(), **kw) == status
