@@ -59,8 +59,8 @@ struct TokensArgs {
     int o_bf16, whole_pairs;
     float scale_log2;
     unsigned *status;
-    unsigned call;                  // the call's number, another one for every call of the process
-    unsigned long long *counters;   // one per CTA: a call's number, then the pieces counted in it
+    unsigned long long call;        // the call's tag, another one for every call of the process
+    unsigned long long *counters;   // one per CTA: a call's tag, then the pieces counted in it
     float *part_o, *part_ml;        // [2 * CTAs, 16 * MT, d], [2 * CTAs, 16 * MT, 2]
 };
 
@@ -74,10 +74,16 @@ struct TokensSmem {
     static constexpr int kRow = D + 8;                            // floats per row of the warps' O at the end
 };
 
-// A pair's pieces are counted in a word that also holds the call's number, so
-// that whatever other calls left in the workspace counts as nothing; the block
-// that counts the last piece sets the word back to the number and no pieces,
-// where a replay of the same call begins.
+// A pair's pieces are counted in the low bits of a word whose others are the
+// call's tag, so that whatever other calls left in the workspace counts as
+// nothing; the block that counts the last piece sets the word back to the tag
+// and no pieces, where a replay of the same call begins.  A tag's upper half
+// is, as fp32, a signalling NaN, which no arithmetic leaves behind: floats that
+// other entry points keep in a workspace are never taken for a call's count.
+constexpr unsigned long long kCountMask = 1023, kTag = 0xffaull << 52;
+static_assert(kPagedTokensCtas <= (int)kCountMask, "a word counts as many pieces");
+__host__ __device__ constexpr unsigned long long call_tag(unsigned long long n) { return kTag | ((n << 10) & ~(0xfffull << 52)); }
+
 __device__ __forceinline__ unsigned long long swap_word(unsigned long long *word, unsigned long long old,
                                                         unsigned long long now) {
     unsigned long long seen;
@@ -85,23 +91,23 @@ __device__ __forceinline__ unsigned long long swap_word(unsigned long long *word
     return seen;
 }
 // A block starts its own word (that of the pair whose first piece it may have)
-// as early as it can, so that later counts find the call's number there.
-__device__ __forceinline__ void start_word(unsigned long long *word, unsigned call) {
+// as early as it can, so that later counts find the call's tag there.
+__device__ __forceinline__ void start_word(unsigned long long *word, unsigned long long call) {
     const unsigned long long old = *reinterpret_cast<volatile unsigned long long *>(word);
-    if ((unsigned)(old >> 32) != call) swap_word(word, old, (unsigned long long)call << 32);
+    if ((old & ~kCountMask) != call) swap_word(word, old, call);
 }
 // How many pieces were counted in this word before this one: one add where the
-// word has the call's number.  Where it has not, the add fell on what will be
+// word has the call's tag.  Where it has not, the add fell on what will be
 // replaced; whoever replaces it counts itself, the others add again.
-__device__ __forceinline__ int count_piece(unsigned long long *word, unsigned call) {
+__device__ __forceinline__ int count_piece(unsigned long long *word, unsigned long long call) {
     while (true) {
         unsigned long long old;
         asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], 1;" : "=l"(old) : "l"(word) : "memory");
-        if ((unsigned)(old >> 32) == call) return (int)(unsigned)old;
+        if ((old & ~kCountMask) == call) return (int)(old & kCountMask);
         unsigned long long seen = *reinterpret_cast<volatile unsigned long long *>(word);
-        while ((unsigned)(seen >> 32) != call) {
+        while ((seen & ~kCountMask) != call) {
             old = seen;
-            seen = swap_word(word, old, ((unsigned long long)call << 32) + 1);
+            seen = swap_word(word, old, call + 1);
             if (seen == old) return 0;
         }
     }
@@ -426,7 +432,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
             __syncthreads();
             if (threadIdx.x == 0) {
                 s_last = count_piece(a.counters + first_cta, a.call) == last_cta - first_cta;
-                if (s_last) a.counters[first_cta] = (unsigned long long)a.call << 32;
+                if (s_last) a.counters[first_cta] = a.call;
             }
             __syncthreads();
             if (s_last) {
@@ -491,8 +497,8 @@ ra_status launch_paged_tokens(const TokensLaunch &t, cudaStream_t stream) {
     a.whole_pairs = t.whole_pairs;
     a.scale_log2 = t.scale_log2;
     a.status = t.status;
-    static std::atomic<unsigned> calls{0};
-    a.call = (calls.fetch_add(1, std::memory_order_relaxed) + 1u) * 2654435769u;   // spread over 32 bits
+    static std::atomic<unsigned long long> calls{0};
+    a.call = call_tag(calls.fetch_add(1, std::memory_order_relaxed));
     a.counters = t.counters;
     a.part_o = t.part_o;
     a.part_ml = t.part_ml;

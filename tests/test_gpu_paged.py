@@ -397,6 +397,24 @@ def test_workspace_left_by_other_calls(ralib, gpu):
             assert_paged(c, q, o, lse, [n, n], 0, 0)
 
 
+def test_counters_are_never_floats(ralib, gpu):
+    """The words a split call counts in are signalling NaNs in their upper half,
+    so that no float that arithmetic left in a workspace can pass for one, and
+    an own one for each call."""
+    c = Cache([9000, 5000], 64, 2, 128, 80)
+    c.fill_all()
+    q = randn_bf16((2, 8, 128), 6).cuda()
+    tags = []
+    for _ in range(2):
+        ws = ralib.new_workspace(64 << 20)
+        o, lse, _ = attend(ralib, c, q, cu_of([1, 1]), [1, 1], torch.bfloat16, ws=ws)
+        assert_paged(c, q, o, lse, [1, 1], 0, 0)
+        words = {w & (1 << 64) - 1 for w in ws[256:256 + 4096].view(torch.int64).tolist()} - {0}
+        assert len(words) == 1
+        tags += words
+    assert tags[0] != tags[1] and all(w >> 52 == 0xffa and w & 1023 == 0 for w in tags)
+
+
 @pytest.mark.parametrize("new,longest,H,Hkv,d", [
     ([1] * 300, 900, 16, 8, 64),            # a CTA for each pair, more of them than counters
     ([1] * 70, 3000, 16, 8, 64),            # equal runs of all pairs
