@@ -1128,16 +1128,19 @@ __global__ void __launch_bounds__(384, 1)
                     const float *s = reinterpret_cast<const float *>(&sr[0][0]);
                     float mA = s[0], mB = s[1];
 #pragma unroll
-                    for (int c = 2; c < 128; c += 4) {
+                    for (int c = 2; c < 126; c += 4) {
                         mA = max3(mA, s[c], s[c + 1]);
                         mB = max3(mB, s[c + 2], s[c + 3]);
                     }
+                    mA = max3(mA, s[126], s[127]);
                     float m_new = m_ref;
                     if (bad) {
                         const float cand = fmaxf(fmaxf(mA, mB) * sl2, l > 0.f ? m_ref + lg2(l) : -INFINITY);
                         if (cand != -INFINITY) m_new = cand;
                     }
-                    const float alpha = ex2(m_ref - m_new);
+                    // a row that has summed nothing yet has nothing to rescale (and
+                    // its factor may pass 2^128, where 0 would become NaN)
+                    const float alpha = l > 0.f ? ex2(m_ref - m_new) : 1.f;
                     l *= alpha;
                     lr *= alpha;
                     m_ref = m_new;
