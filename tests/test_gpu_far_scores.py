@@ -1,5 +1,5 @@
-"""Rows all of whose scores lie far below zero, past the exponents of 32 bits (2^-128): the first
-keys a row sees must not be scaled by what its empty sum was.
+"""Rows all of whose scores lie far below zero, past the exponents of 32 bits (2^-128), or far
+above and below it: the first keys a row sees must not be scaled by what its empty sum was.
 
 Keys lie near one direction u per head (k = s (u + 0.1 n)) and queries near -u, so that every
 score is about -s^2 |u|^2 scale = -200.  A score's 32-bit sum of d products is then off by at most
@@ -75,3 +75,38 @@ def test_ring(ralib, gpu, layout, causal, d):
     for flags in (0, 1):
         o, lse = run_ring(ralib, q, k, v, N, layout, causal, flags=flags)
         assert_attention_close(o, o_ref, lse, lse_ref, layout)
+
+
+@pytest.mark.parametrize("d,window,sinks", [(64, 20, 4), (128, 20, 4), (64, 400, 200), (128, 400, 200), (128, 900, 0)])
+def test_window_both_signs(ralib, gpu, far, d, window, sinks):
+    """Scores of +200 and -200 in runs of keys: a row's reference moves up and, past the sinks, stays."""
+    B, L, H, Hkv = 1, 900, 4, 2
+    q, k = near((B, L, H, d), -1, 1).cuda(), near((B, L, Hkv, d), 1, 2).cuda()
+    for a, b in ((0, 3), (130, 170), (420, 650)):
+        k[:, a:b] = -k[:, a:b]
+    v, do = (torch.randn((B, L, h, d), generator=torch.Generator().manual_seed(h)).bfloat16().cuda() for h in (Hkv, H))
+    o, lse = run_fwd(ralib, q, k, v, window, sinks, None, torch.float32)
+    scale = d ** -0.5
+    ok, qd, kd, vd, (o_ref, lse_ref, p) = reference(q, k, v, window, sinks, None, scale)
+    assert lse_ref.max() > 120
+    ref.assert_within(o, o_ref, ref.forward_tolerance(p, vd, o_ref, False), "O")
+    ref.assert_within(lse, lse_ref, torch.full_like(lse_ref, ref.EPS), "LSE")
+    grads, tols = ref.backward(qd, kd, vd, o.double(), do.double(), lse.double(), ok, scale, Hkv)
+    for x, g, t in zip(run_bwd(ralib, q, k, v, o, do, lse, window, sinks, None, torch.float32), grads, tols):
+        ref.assert_within(x, g, t + 1e-5, "gradient")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,lens", [([1, 2], [600, 5000]), ([40, 33], [40, 60]), ([300, 50], [900, 4000]),
+                                      ([100], [12000])])
+def test_paged_both_signs(ralib, gpu, far, d, new, lens):
+    H, Hkv = 4, 2
+    c = Cache(lens, 32, Hkv, d, 3)
+    c.ks = [near((n, Hkv, d), 1, 10 + s).cuda() for s, n in enumerate(lens)]
+    for x in c.ks:
+        x[17:33] = -x[17:33]
+        x[len(x) // 2:len(x) // 2 + 5] = -x[len(x) // 2:len(x) // 2 + 5]
+    c.fill_all()
+    q = near((sum(new), H, d), -1, 4).cuda()
+    o, lse, _ = attend(ralib, c, q, cu_of(new), new, torch.float32)
+    assert_paged(c, q, o, lse, new, 0, 0)
