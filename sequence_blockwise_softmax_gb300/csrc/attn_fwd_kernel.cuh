@@ -82,6 +82,7 @@ struct AttnArgs {
     int bh_chunk;       // (batch, head) pairs whose units are interleaved heavy-first
     int seq_order;      // q/k/v/o in sequence order [B, L, H, d], LSE [B, H, L] (ring mode)
     int window, sinks;  // windowed keys (KEYS_WINDOW)
+    int whole_units;    // and its units of 256 rows; the others run in halves
     // KEYS_PAGED: the sequences and pages; the parts' rows when the keys are
     // split, [units, H_kv, num_splits, rows of a unit, d], and their LSE
     PagedSeqs seqs;
@@ -268,15 +269,18 @@ __global__ void __launch_bounds__(384, 1)
             atomicOr(args.status, RA_DEV_PAGE_BIT);
         if (pu.n <= 0) return;
     } else {
-        unit = decode_unit(blockIdx.x, args.bh_chunk, args.B, H, args.num_q_ranks, args.n_units_seq, args.layout);
+        unit = decode_unit(KEYS == KEYS_WINDOW ? window_rows(blockIdx.x, args.whole_units).unit : (int)blockIdx.x,
+                           args.bh_chunk, args.B, H, args.num_q_ranks, args.n_units_seq, args.layout);
     }
     const int b = unit.b, h = unit.h, qi = unit.qi, qt = unit.qt;
     const bool ring = args.q_rank_fixed < 0;
     const int q_rank = ring ? qi : args.q_rank_fixed;
     const int zq = (ring ? qi * args.B : 0) + b;
-    const int row0 = qt * 256;
+    // (a half unit's other Q tile sees no key and is not stored)
+    const WindowRows wr = KEYS == KEYS_WINDOW ? window_rows(blockIdx.x, args.whole_units) : WindowRows{0, -1};
+    const int row0 = wr.first(qt * 256);
     if (KEYS == KEYS_WINDOW && row0 >= S) return;
-    const int row_end = min(S, row0 + 256);
+    const int row_end = min(S, row0 + wr.rows());
     // first row of a key tile that is to be read as zeros (KEYS_PAGED: behind the
     // sequence; KEYS_WINDOW: behind the last one; past args.S the copy gives zeros)
     auto zeros_from = [&](int tile) -> int {
@@ -981,7 +985,7 @@ __global__ void __launch_bounds__(384, 1)
         // KEYS_PAGED: row r is token r / group of the Q tile; rows past the
         // tile's tokens or the unit's take the last token's keys, so that no
         // tile is masked for their sake, and are not stored
-        bool live = KEYS != KEYS_WINDOW || a < S;           // the row is stored
+        bool live = KEYS != KEYS_WINDOW || a < row_end;     // the row is stored
         bool warp_live = true;      // some row of the warp is
         int my_tok = 0;
         if constexpr (KEYS == KEYS_PAGED) {
@@ -1324,7 +1328,8 @@ __global__ void __launch_bounds__(384, 1)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         if constexpr (KEYS != KEYS_PAGED) named_barrier_sync(1 + g, 128);
-        if (KEYS != KEYS_PAGED && !ragged && wq == 0 && lane == 0 && *abort_flag == 0) {
+        if (KEYS != KEYS_PAGED && !ragged && !(KEYS == KEYS_WINDOW && row0 + 128 * g >= row_end) && wq == 0 &&
+            lane == 0 && *abort_flag == 0) {
             // rows past the shard's end fall outside the tensor and are not written
             int c1, c2, c3;
             tile_coords(args.seq_order, args.layout, args.S, args.N, ring ? qi : 0, b, row0 + 128 * g, c1, c2, c3);
@@ -1333,7 +1338,7 @@ __global__ void __launch_bounds__(384, 1)
             tma_store_commit();
             tma_store_wait_read();
         }
-        if (KEYS != KEYS_PAGED && ok && a < S) {
+        if (KEYS != KEYS_PAGED && ok && (KEYS == KEYS_WINDOW ? live : a < S)) {
             // shard stacks: [N or 1, B, H, S]; sequence order: [B, H, L] at the row's position
             const size_t at = args.seq_order ? ((size_t)b * H + h) * ((size_t)N * S) + (size_t)my_pos
                                              : ((size_t)zq * H + h) * args.S + a;

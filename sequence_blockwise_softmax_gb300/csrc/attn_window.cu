@@ -24,21 +24,24 @@ namespace ra {
 namespace {
 
 constexpr size_t kHeader = RA_WORKSPACE_MIN_BYTES;
+constexpr int kSms = 152;     // GB300; only choices of a form depend on it
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // The few-key form runs where 16 rows meet few 16-key chunks.  Few-key against
 // tensor-core form in us, four sinks:
-//   512 tokens, 8 / 2 heads (one wave of CTAs), d = 64: window 16: 4.1 / 10.3,
-//   128: 6.4 / 10.0, 200: 8.0 / 10.1, 300: 10.0 / 9.8; d = 128: 4.8 / 12.0,
-//   8.2 / 11.9, 10.3 / 11.9, 13.2 / 11.5.
+//   512 tokens, 8 / 2 heads (one wave of CTAs), d = 64: window 16: 3.7 / 7.8,
+//   128: 6.0 / 7.8, 200: 7.8 / 8.6, 300: 9.7 / 8.3; d = 128: 4.6 / 9.4,
+//   7.8 / 9.2, 10.1 / 10.5, 12.7 / 10.0.
+//   2000 tokens, 8 / 8 heads, d = 128: 6.0 / 10.7 and, where an SM holds one
+//   CTA, not two, 14.8 / 10.5.
 //   40000 tokens, 16 / 8 heads, d = 64: 80 / 167, 157 / 165, 257 / 185; d = 128:
 //   window 16: 142 / 201, 64: 201 / 200, 128: 424 / 200.
 bool few_keys(int64_t B, int64_t L, int64_t H, int d, int window, int sinks) {
     const int64_t row_chunks = ((int64_t)window + 30) / 16 + ((int64_t)sinks + 15) / 16;
-    const bool one_wave = B * H * ((L + 63) / 64) <= 304;
-    return row_chunks <= (one_wave ? 16 : d == 64 ? 11 : 5) &&
-           window_few_smem(window_few_chunks((int)L, window, sinks), d) <= (size_t)227 << 10;
+    const size_t smem = window_few_smem(window_few_chunks((int)L, window, sinks), d), most = (size_t)227 << 10;
+    const bool one_wave = B * H * ((L + 63) / 64) <= (2 * (smem + 1024) <= most + 1024 ? 2 * kSms : kSms);
+    return row_chunks <= (one_wave ? 16 : d == 64 ? 11 : 5) && smem <= most;
 }
 
 struct Window {
@@ -114,7 +117,9 @@ ra_status launch_fwd(const Window &w, const void *q, const void *k, const void *
     const int smem = (int)AttnSmem<D>::kBytes;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
-    return launched(launch_dependent(kern, (unsigned)(w.B * w.H * a.n_units_seq), 384, smem, stream, mq, mk, mv, mo, a));
+    const int64_t units = w.B * w.H * a.n_units_seq;
+    a.whole_units = (int)window_whole_units(units, kSms);
+    return launched(launch_dependent(kern, (unsigned)(2 * units - a.whole_units), 384, smem, stream, mq, mk, mv, mo, a));
 }
 
 // Workspace of the backward: the status word, D, the sinks' partial gradients.

@@ -115,6 +115,25 @@ RA_HD RowKeys window_row(const int *cu, int n_seqs, int S, int p, int window, in
     return window_row_keys(start, p, window, sinks);
 }
 
+// Block number `block` of the forward: whole units of 256 rows, then the rest
+// in halves of 128 rows.
+struct WindowRows {
+    int unit, half;     // half < 0: the whole unit
+    RA_HD int first(int row0) const { return half > 0 ? row0 + 128 : row0; }    // row0: the unit's
+    RA_HD int rows() const { return half < 0 ? 256 : 128; }
+};
+RA_HD WindowRows window_rows(int block, int whole) {
+    const int rest = block - whole;
+    return rest < 0 ? WindowRows{block, -1} : WindowRows{whole + rest / 2, rest & 1};
+}
+// The whole units of a call's `units` on `sms` SMs: none where an SM for each
+// half is there.  A half takes about two thirds of a unit's time: 1024 tokens, 8
+// heads, window 600: 15.7 us against 18.6 at d = 128, 12.5 against 16.1 at d =
+// 64; 2048 tokens, window 1024: 20.0 against 22.9.  (Halves for the last wave of
+// a longer call cost more than they even out, since its units are the lightest:
+// 3000 tokens, 16 heads, window 1024: 33.9 against 29.2; 8192: 78 against 80.)
+RA_HD int64_t window_whole_units(int64_t units, int sms) { return 2 * units <= sms ? 0 : units; }
+
 RA_HD RangeWalk window_unit_walk(const int *cu, int n_seqs, int S, int row0, int row_end, int window, int sinks) {
     return range_walk(window_row(cu, n_seqs, S, row0, window, sinks), row_end);
 }

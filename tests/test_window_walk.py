@@ -56,6 +56,13 @@ def test_every_pair_once(probe, S, window, sinks, cu):
         assert np.array_equal(cnt, ok.astype(np.int32))
 
 
+@pytest.mark.parametrize("units,blocks", [(1, 2), (75, 150), (76, 152), (77, 77), (152, 152), (153, 153), (4096, 4096)])
+def test_units_and_halves(probe, units, blocks):
+    cnt = np.zeros(units * 256, dtype=np.int32)
+    assert probe.ra_test_window_units(units, 152, ctypes.c_void_p(cnt.ctypes.data)) == blocks
+    assert (cnt == 1).all()
+
+
 def test_reference_gradients_are_differences():
     """The formula the kernels are held to, against central differences of the 64-bit forward."""
     g = torch.Generator().manual_seed(3)

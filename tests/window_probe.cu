@@ -20,6 +20,18 @@ void ra_test_window_rows(int S, int window, int sinks, const int *cu, int n_seqs
     }
 }
 
+// cnt[u * 256 + r]: how often the forward's blocks have row r of unit u.
+// Returns the number of blocks of a launch, or -1 if one leaves the units.
+int ra_test_window_units(int units, int sms, int *cnt) {
+    const int whole = (int)ra::window_whole_units(units, sms), blocks = 2 * units - whole;
+    for (int i = 0; i < blocks; ++i) {
+        const ra::WindowRows w = ra::window_rows(i, whole);
+        if (w.unit < 0 || w.unit >= units) return -1;
+        for (int r = 0; r < w.rows(); ++r) ++cnt[w.unit * 256 + w.first(0) + r];
+    }
+    return blocks;
+}
+
 // The same for the dK / dV pass: each key against the queries of its window,
 // in 128-query tiles of its block's walk, and each sink against the units past
 // its window; a unit's partial counts only if the key's sum reads it.
