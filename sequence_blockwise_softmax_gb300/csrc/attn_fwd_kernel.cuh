@@ -256,13 +256,13 @@ __global__ void __launch_bounds__(384, 1)
     bool split = false;       // ... and whether there is more than one
     int unit_no = 0;
     if constexpr (KEYS == KEYS_PAGED) {
-        // blockIdx.x = (hk * num_splits + part) * n_units + unit, a sequence's
-        // last (longest) unit first; the CTAs of one head and part stand
-        // together and share its keys in L2
+        // blockIdx.x = (part * H_kv + hk) * n_units + unit, a sequence's last
+        // (longest) unit first and shorter last parts at the end; the CTAs of
+        // one head and part stand together and share its keys in L2
         unit_no = args.n_units - 1 - blockIdx.x % args.n_units;
         const int rest = blockIdx.x / args.n_units;
-        part = rest % args.seqs.num_splits;
-        unit.h = rest / args.seqs.num_splits;    // the key/value head
+        unit.h = rest % args.seqs.Hkv;    // the key/value head
+        part = rest / args.seqs.Hkv;
         const int sq = paged_find_seq_warp(args.seqs, unit_no, lane);
         pu = paged_unit(args.seqs, sq, unit_no - paged_first_unit(args.seqs, sq));
         if (part == 0 && unit.h == 0 && threadIdx.x == 0 && pu.first == 0 && paged_bad_counts(args.seqs, sq))

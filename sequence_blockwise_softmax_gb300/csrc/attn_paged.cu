@@ -8,8 +8,8 @@
 // Where there are few units, each unit's key tiles are cut into parts that run
 // as CTAs of their own and are joined by their LSE.  Bound by the tensor cores'
 // pace (about 1.35 us for 128 keys by 256 rows at d = 128) and a CTA's fixed 8
-// us: 512 tokens over 32768 keys, 32 / 8 heads, 217 us in pages of 16 and 200 in
-// pages of 128 (1255 and 1360 TFLOP/s); two prompts of 2048 tokens over 8192: 329
+// us: 512 tokens over 32768 keys, 32 / 8 heads, 197 us in pages of 16 and 184 in
+// pages of 128 (1385 and 1480 TFLOP/s); two prompts of 2048 tokens over 8192: 329
 // us (1460 TFLOP/s).  Few rows and few keys have forms of their own.
 #include <cmath>
 
@@ -118,7 +118,7 @@ struct Paged {
 
 // How a call is cut: tokens per unit, the most parts per unit, the parts' bytes.
 struct Plan {
-    int tile_tokens, splits;    // the tensor-core form
+    int tile_tokens, splits, tail_share;    // the tensor-core form
     int64_t units;
     bool tokens, whole_pairs;   // the few-row form, with this many CTAs
     int ctas;
@@ -198,6 +198,24 @@ Plan plan(Paged a) {
         if (s == 1 || t < best) {
             best = t;
             p.splits = s;
+        }
+    }
+    // One sequence whose parts leave SMs idle: s long parts of each unit on SMs of
+    // their own and a short last part, `rounds` of which follow one another on the
+    // others and end with the long ones.  512 tokens over 32768 keys, 32 / 8 heads,
+    // two parts against two and a short one: 219 / 197 us in pages of 16, 202 / 184
+    // in pages of 128; 256 tokens 110 / 102.  Where the estimate promises less than
+    // 5 % it does not hold: 1000 tokens over 16000 keys 171 / 183.
+    for (int s = 1; active0 == 1 && s < 64 && s * ctas < kSms && part * (s + 1) <= kPartBytes; ++s) {
+        const int64_t idle = kSms - s * ctas, rounds = (ctas + idle - 1) / idle;
+        const double tail = ((double)tiles * tile / s - fixed * (double)(rounds - 1)) / (tile * ((double)rounds + 1.0 / s));
+        const double longest = ((double)tiles - tail) / s;
+        if (tail < kSplitTiles || longest < tail) continue;
+        const double t = fixed + tile * longest + 4.0 + (double)(a.T * a.H) * (s + 1) * a.d * 4 / 3e6;
+        if (t < 0.95 * best) {
+            best = t;
+            p.splits = s + 1;
+            p.tail_share = (int)(1024.0 * tail / (double)tiles);
         }
     }
     p.part_lse = p.total = p.part_o;
@@ -377,6 +395,7 @@ ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, co
     args.seqs = sequences(a, table, seq_lens, cu_q);
     args.seqs.unit_tokens = 2 * p.tile_tokens;
     args.seqs.num_splits = p.splits;
+    args.seqs.tail_share = p.tail_share;
     args.n_units = (int)p.units;
     args.tile_tokens = p.tile_tokens;
     args.page_box = (int)(a.page < 128 ? a.page : 128);

@@ -27,6 +27,7 @@ struct PagedSeqs {
     int max_new;            // no sequence has more new tokens; rows past that are not computed
     int window, sinks;      // window 0: none
     int num_splits;         // most parts a unit's keys are cut into
+    int tail_share;         // 0, or 1024ths of the keys in the last, shorter part
 };
 
 // A unit: tokens [t0, t0 + n) of q, at positions p0 .. p0 + n - 1 of sequence
@@ -97,12 +98,17 @@ RA_HD int paged_unit_rows(const PagedSeqs &q) {
 
 // A unit's tiles are cut into at most num_splits parts of equal size, at least
 // kSplitTiles tiles each: a part costs its CTA about 7 us and the join a read
-// of its rows, a tile about 1 us.
+// of its rows, a tile about 1 us.  With tail_share (at most a part's equal
+// share) the last part has that much and the others the rest.
 constexpr int kSplitTiles = 6;
 RA_HD int paged_split_tiles(const PagedSeqs &q, int tiles) {
     int ns = tiles / kSplitTiles;
     if (ns > q.num_splits) ns = q.num_splits;
     if (ns < 1) ns = 1;
+    if (q.tail_share > 0 && ns > 1 && ns == q.num_splits) {
+        const int tail = (int)((int64_t)tiles * q.tail_share >> 10);
+        return (tiles - tail + ns - 2) / (ns - 1);
+    }
     return (tiles + ns - 1) / ns;
 }
 RA_HD int paged_split_count(const PagedSeqs &q, int tiles) {

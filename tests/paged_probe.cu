@@ -8,8 +8,8 @@ extern "C" {
 // cnt[t * cap + key], cap = max_pages * page.  loaded[s * max_pages + i]: page
 // i of sequence s is read.  Returns 0, or what went wrong.
 int ra_test_paged(const int *seq_lens, const int *cu_q, int n_seqs, int T, int max_pages, int page, int H, int Hkv,
-                  int unit_tokens, int max_new, int window, int sinks, int num_splits, int *cnt, int *loaded,
-                  int *parts_seen) {
+                  int unit_tokens, int max_new, int window, int sinks, int num_splits, int tail_share, int *cnt,
+                  int *loaded, int *parts_seen) {
     ra::PagedSeqs q{};
     q.seq_lens = seq_lens;
     q.cu_q = cu_q;
@@ -26,6 +26,7 @@ int ra_test_paged(const int *seq_lens, const int *cu_q, int n_seqs, int T, int m
     q.window = window;
     q.sinks = sinks;
     q.num_splits = num_splits;
+    q.tail_share = tail_share;
     const size_t cap = (size_t)max_pages * page;
     const int box = page < 128 ? page : 128;
     const int64_t units = ra::paged_units(T, n_seqs, unit_tokens);

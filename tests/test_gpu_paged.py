@@ -115,6 +115,8 @@ CASES = [
     ([5, 6], [1500, 40], 66, 2, 128, 16, 0, 0),
     ([2], [900], 128, 1, 64, 64, 0, 0),
     ([33], [12000], 8, 1, 128, 16, 0, 0),
+    ([40], [9000], 60, 60, 64, 64, 0, 0),      # long parts and a short one
+    ([200], [7000], 60, 30, 128, 16, 0, 0),
     # few keys: short prompts, short windows
     ([40, 3, 64, 0, 1], [40, 60, 64, 9, 1], 8, 8, 128, 16, 0, 0),
     ([90, 1, 128], [90, 128, 128], 6, 2, 64, 32, 0, 0),

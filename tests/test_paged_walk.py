@@ -40,8 +40,8 @@ CASES = [
 
 
 @pytest.mark.parametrize("new,lens,page,max_pages,group,unit,window,sinks,splits", CASES)
-@pytest.mark.parametrize("tail", [0, 5])
-def test_every_pair_once(probe, new, lens, page, max_pages, group, unit, window, sinks, splits, tail):
+@pytest.mark.parametrize("tail,share", [(0, 0), (5, 0), (0, 1), (0, 0.4)])
+def test_every_pair_once(probe, new, lens, page, max_pages, group, unit, window, sinks, splits, tail, share):
     n, T = len(new), sum(new) + tail
     cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
     sl = np.asarray(lens, dtype=np.int32)
@@ -51,7 +51,7 @@ def test_every_pair_once(probe, new, lens, page, max_pages, group, unit, window,
     seen = ctypes.c_int(0)
     p = lambda a: ctypes.c_void_p(a.ctypes.data)
     assert probe.ra_test_paged(p(sl), p(cu), n, T, max_pages, page, group, 1, unit, max(new), window, sinks, splits,
-                               p(cnt), p(loaded), ctypes.byref(seen)) == 0
+                               int(share * 1024 / splits), p(cnt), p(loaded), ctypes.byref(seen)) == 0
     want = np.zeros_like(cnt)
     key = np.arange(cap)
     for s in range(n):
@@ -86,7 +86,8 @@ def test_bad_boundaries_stay_inside(probe):
         seen = ctypes.c_int(0)
         p = lambda a: ctypes.c_void_p(a.ctypes.data)
         assert probe.ra_test_paged(p(sl), p(cu), n, T, max_pages, page, 4, 1, 64, int(rng.randint(1, 300)),
-                                   int(rng.randint(0, 200)), int(rng.randint(0, 200)), 4, p(cnt), p(loaded),
+                                   int(rng.randint(0, 200)), int(rng.randint(0, 200)), 4, int(rng.randint(0, 257)),
+                                   p(cnt), p(loaded),
                                    ctypes.byref(seen)) == 0
         assert probe.ra_test_paged_chunks(p(sl), p(cu), n, T, max_pages, page, int(rng.randint(1, 300)), 50, 20, p(cnt)) == 0
 
