@@ -120,8 +120,8 @@ struct Paged {
 struct Plan {
     int tile_tokens, splits, tail_share;    // the tensor-core form
     int64_t units;
-    bool tokens, whole_pairs;   // the few-row form, with this many CTAs
-    int ctas;
+    bool tokens, whole_pairs;   // the few-row form, with this many CTAs, in clusters or not
+    int ctas, cluster;
     bool few;                   // the few-key form: units of its own, the keys it expects
     int64_t few_units, few_keys;
     size_t part_o, part_lse, total;
@@ -152,7 +152,8 @@ Plan plan(Paged a) {
         if (a.window > 0 && a.window + a.max_new + a.sinks < seen) seen = a.window + a.max_new + a.sinks;
         p.ctas = paged_tokens_ctas(active0 * a.H_kv, seen);
         p.whole_pairs = paged_tokens_whole(active0 * a.H_kv, seen);
-        const size_t rows = p.whole_pairs ? 0 : (size_t)2 * p.ctas * (a.max_new * group <= 16 ? 16 : 32);
+        p.cluster = paged_tokens_cluster(active0 * a.H_kv, seen);
+        const size_t rows = p.whole_pairs || p.cluster ? 0 : (size_t)2 * p.ctas * (a.max_new * group <= 16 ? 16 : 32);
         p.part_lse = p.part_o + round256(rows * a.d * 4);
         p.total = p.part_lse + round256(rows * 8);
         return p;
@@ -353,6 +354,7 @@ ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, co
         t.o_bf16 = o_bf16;
         t.d = D;
         t.whole_pairs = p.whole_pairs;
+        t.cluster = p.cluster;
         t.ctas = p.ctas;
         t.scale_log2 = scale_log2;
         t.status = reinterpret_cast<unsigned *>(workspace);

@@ -13,7 +13,10 @@
 // not a whole pair leaves O (unnormalised, fp32), the reference and the sum of
 // exponentials in the workspace, and the CTA that counts the last piece of a
 // pair adds them in the order of their keys, so the result does not depend on
-// which one it is.
+// which one it is.  Up to 152 pairs that are not too long take no such way through
+// memory: each pair gets a cluster of 2 to 16 CTAs, which join their equal pieces
+// through shared memory (paged_tokens_cluster): one sequence of 1000 keys 7.4 -> 5.9
+// us, 8 of 500-1000 10.3 -> 8.6.
 //
 // Inside a run the four warps take the chunks in turn and share nothing until
 // the end of a head: each has its own ring of cp.async stages (96 KB per CTA in
@@ -30,7 +33,7 @@
 //
 // Measured on a GB300, 32 / 8 heads, d = 128: 64 sequences of 200-16000 keys 355
 // us (6.75 TB/s; the bytes alone take 353 at the copy rate), 8 of 3000-4000 keys
-// 24 us, one of 1000 keys 7.7 us, which is a chain of latencies: lengths, table,
+// 23 us, one of 1000 keys 5.9 us, which is a chain of latencies: lengths, table,
 // keys, the warps' rows, the join.
 #include <atomic>
 #include <cmath>
@@ -113,7 +116,30 @@ __device__ __forceinline__ int count_piece(unsigned long long *word, unsigned lo
     }
 }
 
-template <int D, int MT>
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(addr) : "memory");
+    return x;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+    float2 x;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(addr) : "memory");
+    return x;
+}
+// `addr` in the shared memory of the cluster's CTA number `rank`
+__device__ __forceinline__ uint32_t in_cluster(uint32_t addr, int rank) {
+    uint32_t x;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(x) : "r"(addr), "r"(rank));
+    return x;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// CLUSTER > 0: each pair's keys are cut into CLUSTER equal pieces (some maybe
+// empty), which the CTAs of a cluster take and join through shared memory.
+template <int D, int MT, int CLUSTER>
 __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const TokensArgs a) {
     using L = TokensSmem<D>;
     constexpr int NS = L::kStages, KS = D / 16, CPR = D / 8;   // k-steps, 16-byte pieces per row
@@ -123,6 +149,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
     __shared__ PagedChunks s_list;
     __shared__ int s_seq, s_last;
     __shared__ float s_m[kWarps][16 * MT], s_l[kWarps][16 * MT];
+    __shared__ float2 s_ml[16 * MT];           // CLUSTER: of the CTA's rows
     const PagedSeqs &sq = a.seqs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
@@ -154,7 +181,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
     PagedChunks mine = list_of(threadIdx.x);
     // total chunks, and (sequence, head) pairs with new tokens in the high half
     long long total = 0;
-    for (int i = 0; i < blocks; ++i) {
+    for (int i = 0; CLUSTER == 0 && i < blocks; ++i) {
         const PagedChunks l = i == 0 ? mine : list_of(i * blockDim.x + threadIdx.x);
         scan(l.count + (l.count > 0 ? 1ll << 40 : 0ll), total);
     }
@@ -162,8 +189,10 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
     total = (total & ((1ll << 40) - 1)) * sq.Hkv;
     const int grid = gridDim.x;
     // Few pairs: each is cut into pieces of its own, at most one to a CTA.
-    // Many: equal runs of the flat list, whose ends fall anywhere.
-    const bool flat = !a.whole_pairs && pairs * 2 > grid;
+    // Many: equal runs of the flat list, whose ends fall anywhere.  Between half
+    // as many pairs as CTAs and a third, by the length of a run: 128 pairs of
+    // 14400-16000 keys 152 us in runs and 180 in pieces, of 16-4000 41 and 28.
+    const bool flat = CLUSTER == 0 && !a.whole_pairs && (pairs * 2 > grid || (pairs * 3 > grid && total > 96ll * grid));
     const long long room = flat ? grid : max(grid - pairs, 1ll);
     const long long per64 = total < 0x7fffffff ? (long long)(((unsigned)total + (unsigned)room - 1) / (unsigned)room)
                                                : (total + room - 1) / room;
@@ -182,7 +211,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
         long long base = 0;
         for (int i = 0; i < blocks; ++i) {
             if (i > 0) mine = list_of(i * blockDim.x + threadIdx.x);
-            const long long n = (long long)(flat ? mine.count : (mine.count + per - 1) / per) * sq.Hkv;
+            const int pieces = CLUSTER ? (mine.count > 0 ? CLUSTER : 0) : (mine.count + per - 1) / per;
+            const long long n = (long long)(flat ? mine.count : pieces) * sq.Hkv;
             const long long inc = scan(n, base);
             if (n > 0 && inc - n <= at && at < inc) {
                 s_seq = i * blockDim.x + threadIdx.x;
@@ -200,17 +230,18 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
     long long pos = at;
     const long long end = at + per < total ? at + per : total;    // of a flat run
     {
-        const unsigned each = flat ? cl.count : (cl.count + per - 1) / per;
+        if constexpr (CLUSTER > 0) per = (cl.count + CLUSTER - 1) / CLUSTER;
+        const unsigned each = flat ? cl.count : CLUSTER ? CLUSTER : (cl.count + per - 1) / per;
         hk = s_at < 0x7fffffff ? (int)((unsigned)s_at / each) : (int)(s_at / each);
         const int in = (int)(s_at - (long long)hk * each);
-        c_at = flat ? in : in * per;
+        c_at = flat ? in : min(in * per, cl.count);
         first_cta = cta - in;             // of a pair in pieces
         last_cta = first_cta + (int)each - 1;
     }
 
     const uint32_t ring = smem_u32(smem) + warp * L::kWarp;
     const int g = lane >> 2, t4 = lane & 3;
-    bool word_started = a.whole_pairs;      // no pair is cut, no word is used (and there may be more CTAs than words)
+    bool word_started = CLUSTER > 0 || a.whole_pairs;      // no pair is cut, no word is used (and there may be more CTAs than words)
 
     // ---- one head's keys (or this run's part of them) after another
     while (true) {
@@ -416,7 +447,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
             }
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) lsum += s_m[w][r] > -INFINITY ? s_l[w][r] * ex2(s_m[w][r] - top) : 0.f;
-            if (begins && ends) {
+            if constexpr (CLUSTER > 0) {
+                // over the first warp's rows, which this thread alone has read here
+                *reinterpret_cast<float4 *>(warp_o + (size_t)r * L::kRow + col) = make_float4(x[0], x[1], x[2], x[3]);
+                if (col == 0) s_ml[r] = make_float2(top, lsum);
+            } else if (begins && ends) {
                 store(r, col, x, lsum > 0.f ? 1.f / lsum : 0.f);
                 if (col == 0) store_lse(r, top, lsum);
             } else {
@@ -424,6 +459,36 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
                 if (col == 0)
                     *reinterpret_cast<float2 *>(a.part_ml + (slot * 16 * MT + r) * 2) = make_float2(top, lsum);
             }
+        }
+        if constexpr (CLUSTER > 0) {
+            cluster_sync();
+            const int rank = cta % CLUSTER;
+            for (int e = rank * 32 * kWarps + threadIdx.x; e < rows * (D / 4); e += CLUSTER * 32 * kWarps) {
+                const int r = e / (D / 4), col = (e % (D / 4)) * 4;
+                float2 ml[CLUSTER];
+                float4 f[CLUSTER];
+#pragma unroll
+                for (int p = 0; p < CLUSTER; ++p) {
+                    ml[p] = ld_cluster2(in_cluster(smem_u32(s_ml + r), p));
+                    f[p] = ld_cluster4(in_cluster(smem_u32(warp_o + (size_t)r * L::kRow + col), p));
+                }
+                float x[4] = {}, top = -INFINITY, lsum = 0.f;
+#pragma unroll
+                for (int p = 0; p < CLUSTER; ++p) top = fmaxf(top, ml[p].x);
+#pragma unroll
+                for (int p = 0; p < CLUSTER; ++p) {
+                    const float now = ml[p].x > -INFINITY ? ex2(ml[p].x - top) : 0.f;
+                    x[0] += f[p].x * now;
+                    x[1] += f[p].y * now;
+                    x[2] += f[p].z * now;
+                    x[3] += f[p].w * now;
+                    lsum += ml[p].y * now;
+                }
+                store(r, col, x, lsum > 0.f ? 1.f / lsum : 0.f);
+                if (col == 0) store_lse(r, top, lsum);
+            }
+            cluster_sync();      // the others have read this CTA's rows
+            return;
         }
         if (!(begins && ends)) {
             // the head's last piece to arrive joins them, in order: the
@@ -459,13 +524,18 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
     }
 }
 
-template <int D, int MT>
+template <int D, int MT, int CLUSTER>
 ra_status launch(const TokensLaunch &t, const TokensArgs &args, cudaStream_t stream) {
-    auto kern = paged_tokens_kernel<D, MT>;
+    auto kern = paged_tokens_kernel<D, MT, CLUSTER>;
     const int smem = (int)TokensSmem<D>::kBytes;
     static_assert(kWarps * 16 * MT * TokensSmem<D>::kRow * 4 <= TokensSmem<D>::kBytes, "the warps' rows fit in the rings");
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
+    if constexpr (CLUSTER > 8)
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(NonPortableClusterSizeAllowed) failed");
+    if constexpr (CLUSTER > 0)
+        return launched(launch_dependent_clusters(kern, CLUSTER, (unsigned)t.ctas, 32 * kWarps, smem, stream, args));
     return launched(launch_dependent(kern, (unsigned)t.ctas, 32 * kWarps, smem, stream, args));
 }
 
@@ -475,7 +545,27 @@ bool paged_tokens_whole(int64_t pairs, int64_t keys) {
     return 2 * pairs > kPagedTokensCtas && keys <= kWholeKeys && pairs < (int64_t)1 << 30;
 }
 
+// One sequence's 8 pairs, 32 / 8 heads, d = 128, in us as clusters of 2, 4, 8, 16
+// and as pieces joined through the workspace: 100 keys 4.9, 4.9, 5.0, 6.2, 5.6; 700:
+// 8.5, 6.4, 5.9, 6.6, 7.5; 2000: clusters of 8 and 16 7.4, 7.4, pieces 8.4; 4000: 10.3,
+// 9.5, 10.8; 8000: 15.7, 13.0, 12.7.  8 sequences, 64 pairs, of 500-1000 keys: clusters
+// of 2 and 4 10.1, 8.6, pieces 10.3; of 16-2000: 14.8, 11.5, 11.4; of 16-4000: 24.4,
+// 17.7, 15.0.  19 sequences, 152 pairs, of 900-1000 keys: clusters of 2 12.4, pieces
+// 20.9.  More CTAs than the GPU holds at once cost a second wave: 37 pairs of 1000
+// keys as clusters of 8 11.6, 36 pairs 7.4.
+int paged_tokens_cluster(int64_t pairs, int64_t keys) {
+    // as many CTAs as have keys enough each
+    int c = keys <= 128 ? 2 : keys <= (pairs <= 8 ? 256 : 768) ? 4 : keys <= (pairs <= 4 ? 512 : 2560) ? 8 : 16;
+    // and as the GPU holds for all pairs
+    while (c > 1 && pairs > (c == 16 ? 8 : c == 8 ? 36 : c == 4 ? 74 : 152)) c /= 2;
+    // long sequences want all SMs, and even runs where their lengths differ
+    const bool full = 10 * pairs * c >= 9 * kPagedTokensCtas;
+    // (about 512 keys a CTA: a window of 4096 has sinks and new tokens beside it)
+    return c > 1 && keys <= (int64_t)c * (full ? 1024 : 576) ? c : 0;
+}
+
 int paged_tokens_ctas(int64_t pairs, int64_t keys) {
+    if (const int cluster = paged_tokens_cluster(pairs, keys)) return (int)(pairs * cluster);
     if (paged_tokens_whole(pairs, keys)) return (int)pairs;
     const int64_t chunks = pairs * ((keys + kChunk - 1) / kChunk + 1);
     int64_t n = (chunks + kMinRun - 1) / kMinRun;
@@ -503,8 +593,16 @@ ra_status launch_paged_tokens(const TokensLaunch &t, cudaStream_t stream) {
     a.part_o = t.part_o;
     a.part_ml = t.part_ml;
     const int rows = t.seqs.max_new * t.seqs.group;
-    if (t.d == 128) return rows <= 16 ? launch<128, 1>(t, a, stream) : launch<128, 2>(t, a, stream);
-    return rows <= 16 ? launch<64, 1>(t, a, stream) : launch<64, 2>(t, a, stream);
+    auto go = [&](auto cluster) {
+        constexpr int C = decltype(cluster)::value;
+        if (t.d == 128) return rows <= 16 ? launch<128, 1, C>(t, a, stream) : launch<128, 2, C>(t, a, stream);
+        return rows <= 16 ? launch<64, 1, C>(t, a, stream) : launch<64, 2, C>(t, a, stream);
+    };
+    if (t.cluster == 16) return go(std::integral_constant<int, 16>());
+    if (t.cluster == 8) return go(std::integral_constant<int, 8>());
+    if (t.cluster == 4) return go(std::integral_constant<int, 4>());
+    if (t.cluster == 2) return go(std::integral_constant<int, 2>());
+    return go(std::integral_constant<int, 0>());
 }
 
 }  // namespace ra

@@ -17,7 +17,7 @@ struct TokensLaunch {
     void *o;
     float *lse;
     bool o_bf16, whole_pairs;
-    int d, ctas;
+    int d, ctas, cluster;
     float scale_log2;
     unsigned *status;
     unsigned long long *counters;   // kPagedTokensCtas
@@ -27,6 +27,9 @@ struct TokensLaunch {
 // Whether every (sequence, key/value head) pair gets one CTA and is never cut:
 // there are enough of them and they are short.
 bool paged_tokens_whole(int64_t pairs, int64_t keys);
+
+// The size of the cluster of CTAs that each pair gets, or 0.
+int paged_tokens_cluster(int64_t pairs, int64_t keys);
 
 // CTAs for `pairs` (sequence, key/value head) pairs of up to `keys` keys: the
 // grid, not the split, which the kernel takes from the lengths it finds.

@@ -399,6 +399,39 @@ def test_workspace_left_by_other_calls(ralib, gpu):
             assert_paged(c, q, o, lse, [n, n], 0, 0)
 
 
+@pytest.mark.parametrize("new,lens,H,Hkv,d,window,sinks", [
+    # clusters of 2, 4, 8 and 16: few keys, single tokens and several, no new tokens, windows
+    ([1, 1], [1, 100], 8, 8, 128, 0, 0),
+    ([1, 0, 2] * 20, [5, 0, 128] * 20, 8, 2, 64, 0, 0),
+    ([1] * 70, [16 * i + 1 for i in range(44, 9, -1)] * 2, 4, 1, 128, 0, 0),
+    ([1, 3], [200, 250], 16, 2, 128, 0, 0),
+    ([2, 1, 0, 1], [700, 2000, 3, 1], 32, 8, 64, 0, 0),
+    ([1] * 12, [90 * i + 300 for i in range(12)], 16, 2, 128, 300, 4),
+    ([4, 8], [3000, 17], 8, 2, 128, 0, 0),
+    ([1], [8192], 32, 8, 128, 0, 0),
+    ([2], [8000], 16, 1, 64, 0, 0),
+    ([1, 2], [6000, 9000], 16, 2, 64, 4000, 130),
+    ([16], [5000], 2, 2, 128, 0, 0),
+    # pieces of two row tiles, and runs of a third as many pairs as CTAs
+    ([4, 8], [9500, 12000], 8, 2, 128, 0, 0),
+    ([1] * 16, [7000 + 16 * i for i in range(16)], 16, 8, 64, 0, 0),
+])
+@pytest.mark.parametrize("o_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_clusters(ralib, gpu, new, lens, H, Hkv, d, window, sinks, o_dtype):
+    c = Cache(lens, 32, Hkv, d, sum(lens))
+    c.fill_all()
+    T = sum(new) + 3                # rows behind the last sequence are left alone
+    q = randn_bf16((T, H, d), 31).cuda()
+    ws = ralib.new_workspace(ralib.ra_paged_attn_workspace_bytes(T, len(new), H, Hkv, d, max(new), max(lens), window, sinks))
+    first = None
+    for _ in range(3):
+        o, lse, _ = attend(ralib, c, q, cu_of(new), new, o_dtype, window, sinks, ws=ws)
+        assert_paged(c, q, o, lse, new, window, sinks)
+        assert bool(torch.isnan(o[sum(new):]).all()) and bool(torch.isnan(lse[:, sum(new):]).all())
+        assert first is None or torch.equal(first, o[:sum(new)])
+        first = o[:sum(new)]
+
+
 def test_counters_are_never_floats(ralib, gpu):
     """The words a split call counts in are signalling NaNs in their upper half,
     so that no float that arithmetic left in a workspace can pass for one, and
