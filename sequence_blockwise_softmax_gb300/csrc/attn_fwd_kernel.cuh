@@ -112,6 +112,26 @@ __device__ __forceinline__ int paged_find_seq_warp(const PagedSeqs &q, int u, in
     return lo;
 }
 
+// The at-th unit of a call with up to 32 sequences, the longest sequence's last
+// unit first (its number in its sequence, or -1 past the last one); the whole
+// warp gets the same answer.  Long units that start last leave SMs idle.
+__device__ __forceinline__ int paged_sorted_unit(const PagedSeqs &q, int n_units, int at, int lane, int &seq) {
+    int len = -1, units = 0;
+    if (lane < q.n_seqs) {
+        len = paged_len(q, lane);
+        units = max((lane + 1 < q.n_seqs ? paged_first_unit(q, lane + 1) : n_units) - paged_first_unit(q, lane), 0);
+    }
+    int before = 0;       // units of longer sequences
+    for (int j = 0; j < q.n_seqs; ++j) {
+        const int other = __shfl_sync(0xffffffffu, len, j), n = __shfl_sync(0xffffffffu, units, j);
+        if (other > len || (other == len && j < lane)) before += n;
+    }
+    const int local = units - 1 - (at - before);
+    const unsigned mine = __ballot_sync(0xffffffffu, local >= 0 && local < units);
+    seq = mine ? __ffs(mine) - 1 : 0;
+    return mine ? __shfl_sync(0xffffffffu, local, seq) : -1;
+}
+
 __device__ __forceinline__ void record_timeout(unsigned *status, volatile int *abort) {
     *abort = 1;
     atomicOr(status, RA_DEV_TIMEOUT_BIT);
@@ -256,15 +276,28 @@ __global__ void __launch_bounds__(384, 1)
     bool split = false;       // ... and whether there is more than one
     int unit_no = 0;
     if constexpr (KEYS == KEYS_PAGED) {
-        // blockIdx.x = (part * H_kv + hk) * n_units + unit, a sequence's last
-        // (longest) unit first and shorter last parts at the end; the CTAs of
-        // one head and part stand together and share its keys in L2
-        unit_no = args.n_units - 1 - blockIdx.x % args.n_units;
-        const int rest = blockIdx.x / args.n_units;
-        unit.h = rest % args.seqs.Hkv;    // the key/value head
-        part = rest / args.seqs.Hkv;
-        const int sq = paged_find_seq_warp(args.seqs, unit_no, lane);
-        pu = paged_unit(args.seqs, sq, unit_no - paged_first_unit(args.seqs, sq));
+        // Shorter last parts at the end.  Several sequences: blockIdx.x = (part *
+        // n_units + at) * H_kv + hk, longer sequences and their last (longest)
+        // units first.  One, or too many to sort here: (part * H_kv + hk) *
+        // n_units + at, so that the CTAs of one head and part stand together and
+        // share its keys in L2.
+        int sq, local;
+        if (args.seqs.n_seqs > 1 && args.seqs.n_seqs <= 32) {
+            unit.h = blockIdx.x % args.seqs.Hkv;      // the key/value head
+            const int rest = blockIdx.x / args.seqs.Hkv;
+            part = rest / args.n_units;
+            local = paged_sorted_unit(args.seqs, args.n_units, rest % args.n_units, lane, sq);
+            if (local < 0) return;
+            unit_no = paged_first_unit(args.seqs, sq) + local;
+        } else {
+            const int rest = blockIdx.x / args.n_units;
+            unit.h = rest % args.seqs.Hkv;
+            part = rest / args.seqs.Hkv;
+            unit_no = args.n_units - 1 - blockIdx.x % args.n_units;
+            sq = paged_find_seq_warp(args.seqs, unit_no, lane);
+            local = unit_no - paged_first_unit(args.seqs, sq);
+        }
+        pu = paged_unit(args.seqs, sq, local);
         if (part == 0 && unit.h == 0 && threadIdx.x == 0 && pu.first == 0 && paged_bad_counts(args.seqs, sq))
             atomicOr(args.status, RA_DEV_PAGE_BIT);
         if (pu.n <= 0) return;

@@ -8,9 +8,9 @@
 // Where there are few units, each unit's key tiles are cut into parts that run
 // as CTAs of their own and are joined by their LSE.  Bound by the tensor cores'
 // pace (about 1.35 us for 128 keys by 256 rows at d = 128) and a CTA's fixed 8
-// us: 512 tokens over 32768 keys, 32 / 8 heads, 197 us in pages of 16 and 184 in
-// pages of 128 (1385 and 1480 TFLOP/s); two prompts of 2048 tokens over 8192: 329
-// us (1460 TFLOP/s).  Few rows and few keys have forms of their own.
+// us: 512 tokens over 32768 keys, 32 / 8 heads, 193 us in pages of 16 and 175 in
+// pages of 128 (1415 and 1560 TFLOP/s); two prompts of 2048 tokens over 8192: 313
+// us (1535 TFLOP/s).  Few rows and few keys have forms of their own.
 #include <cmath>
 
 #include "attn_fwd_kernel.cuh"
@@ -176,12 +176,14 @@ Plan plan(Paged a) {
     const size_t part = (size_t)p.units * a.H_kv * rows * (a.d + 1) * 4;     // one part of every unit
     // The time of s parts, in us: a CTA costs about 8 and 1.35 a key tile (1.0 at
     // d = 64).  While one wave holds them all it is the longest CTA's; past that
-    // the SMs' even share and, since longer units go first, about half a CTA more.
-    // max_len bounds the lengths: several sequences are taken to have half of it
-    // on average.  The join reads the parts at about 3 TB/s.
+    // the SMs' even share and a part of a CTA more, a smaller one where longer
+    // sequences go first.  max_len bounds the lengths: several sequences are taken
+    // to have half of it on average.  The parts are written and read at about 3 TB/s.
     //   512 tokens over 32768 keys, 32 / 8 heads, d = 128, s = 1, 2, 3, 4, 7:
     //   357, 199, 260, 210, 202; 8 ragged sequences of up to 700 tokens over 9000
-    //   keys, 16 / 4 heads, d = 64, s = 1, 2, 3: 104, 120, 123.
+    //   keys, 16 / 4 heads, d = 64, s = 1, 2, 3: 83, 116, 124 (s = 1 in the order of
+    //   the sequences: 105); 4 of 300-500 over up to 16000, 32 / 8 heads, d = 128: 168,
+    //   206, 222; 16 of 50-100 over up to 8000, 8 / 2 heads: 80, 55, 44, and 4: 50.
     const int64_t full = (a.T + unit - 1) / unit;
     const int64_t ctas = (full > active0 ? full : active0) * a.H_kv;
     int64_t keys = a.max_len;
@@ -189,13 +191,14 @@ Plan plan(Paged a) {
     const int64_t tiles = (keys + 127) / 128 + 1;
     const double tile = a.d == 128 ? 1.35 : 1.0, fixed = 8.0;
     const double mean = active0 > 1 && !(a.window > 0) ? 0.55 * (double)tiles : (double)tiles;
+    const double late = a.n_seqs > 1 && a.n_seqs <= 32 ? 0.2 : 0.5;
+    auto join = [&](int s) { return s > 1 ? 4.0 + (double)(a.T * a.H) * s * a.d * 8 / 3e6 : 0.0; };
     p.splits = 1;
     double best = 0;
     for (int s = 1; s <= 64 && (s == 1 || (tiles / s >= kSplitTiles && part * s <= kPartBytes)); ++s) {
         const double longest = fixed + tile * (double)((tiles + s - 1) / s);
         const double share = (double)ctas * (s * fixed + mean * tile) / kSms;
-        const double join = s > 1 ? 4.0 + (double)(a.T * a.H) * s * a.d * 4 / 3e6 : 0.0;
-        const double t = (ctas * s <= kSms || longest > share + 0.5 * longest ? longest : share + 0.5 * longest) + join;
+        const double t = (ctas * s <= kSms || longest > share + late * longest ? longest : share + late * longest) + join(s);
         if (s == 1 || t < best) {
             best = t;
             p.splits = s;
@@ -212,7 +215,7 @@ Plan plan(Paged a) {
         const double tail = ((double)tiles * tile / s - fixed * (double)(rounds - 1)) / (tile * ((double)rounds + 1.0 / s));
         const double longest = ((double)tiles - tail) / s;
         if (tail < kSplitTiles || longest < tail) continue;
-        const double t = fixed + tile * longest + 4.0 + (double)(a.T * a.H) * (s + 1) * a.d * 4 / 3e6;
+        const double t = fixed + tile * longest + join(s + 1);
         if (t < 0.95 * best) {
             best = t;
             p.splits = s + 1;

@@ -388,7 +388,7 @@ def test_many_sequences(ralib, gpu, n, longest):
 
 def test_workspace_left_by_other_calls(ralib, gpu):
     """A workspace that other calls have written to, its header apart, serves the split forms."""
-    c = Cache([9000, 5000], 64, 2, 128, 79)
+    c = Cache([20000, 5000], 64, 2, 128, 79)
     c.fill_all()
     ws = ralib.new_workspace(64 << 20)
     for n in (1, 40, 1):
@@ -436,7 +436,7 @@ def test_counters_are_never_floats(ralib, gpu):
     """The words a split call counts in are signalling NaNs in their upper half,
     so that no float that arithmetic left in a workspace can pass for one, and
     an own one for each call."""
-    c = Cache([9000, 5000], 64, 2, 128, 80)
+    c = Cache([20000, 5000], 64, 2, 128, 80)
     c.fill_all()
     q = randn_bf16((2, 8, 128), 6).cuda()
     tags = []
@@ -453,7 +453,8 @@ def test_counters_are_never_floats(ralib, gpu):
 @pytest.mark.parametrize("new,longest,H,Hkv,d", [
     ([1] * 300, 900, 16, 8, 64),            # a CTA for each pair, more of them than counters
     ([1] * 70, 3000, 16, 8, 64),            # equal runs of all pairs
-    ([1, 1], 9000, 8, 1, 128),              # pieces of one pair
+    ([1, 1], 9000, 8, 1, 128),              # a cluster for each pair
+    ([1, 1], 20000, 8, 1, 128),             # pieces of one pair
     ([4, 8], 3000, 8, 2, 128),              # two row tiles
     ([40], 20000, 8, 2, 128),               # tiles, split and joined
     ([40, 2, 300], 700, 8, 2, 64),
