@@ -30,6 +30,8 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 // The few-key form runs where 16 rows meet few 16-key chunks.  Few-key against
 // tensor-core form in us, four sinks:
+//   Its warps sharing 16 rows, 512 tokens, 2 heads, d = 64: window 128: 4.1 / 7.6,
+//   400: 6.0 / 8.0; d = 128, 300: 7.2 / 9.9; 8 heads, d = 64, 300: 6.6 / 8.2.  Else
 //   512 tokens, 8 / 2 heads (one wave of CTAs), d = 64: window 16: 3.7 / 7.8,
 //   128: 6.0 / 7.8, 200: 7.8 / 8.6, 300: 9.7 / 8.3; d = 128: 4.6 / 9.4,
 //   7.8 / 9.2, 10.1 / 10.5, 12.7 / 10.0.
@@ -39,7 +41,8 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 //   window 16: 142 / 201, 64: 201 / 200, 128: 424 / 200.
 bool few_keys(int64_t B, int64_t L, int64_t H, int d, int window, int sinks) {
     const int64_t row_chunks = ((int64_t)window + 30) / 16 + ((int64_t)sinks + 15) / 16;
-    const size_t smem = window_few_smem(window_few_chunks((int)L, window, sinks), d), most = (size_t)227 << 10;
+    if (window_few_split(B, L, H, d, window, sinks)) return true;
+    const size_t smem = window_few_smem(window_few_chunks((int)L, window, sinks, false), d, false), most = (size_t)227 << 10;
     const bool one_wave = B * H * ((L + 63) / 64) <= (2 * (smem + 1024) <= most + 1024 ? 2 * kSms : kSms);
     return row_chunks <= (one_wave ? 16 : d == 64 ? 11 : 5) && smem <= most;
 }

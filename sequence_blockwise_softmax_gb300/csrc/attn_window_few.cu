@@ -6,13 +6,17 @@
 // keys at a time (ra_warp_mma.cuh): a row block meets window / 16 + 2 chunks and
 // the one or more that hold the sinks, instead of whole 128-key tiles.  There
 // is no pipeline inside a CTA; two or more CTAs on an SM cover one another's
-// loads.  The tensor-core form (attn_fwd_kernel.cuh) costs about 7 us a CTA of
+// loads.  Where there are few rows a CTA takes 16 of one head, and its warps
+// share their keys and join: the chain of a warp's chunks, 0.2 us each, is a
+// quarter as long.  512 tokens, 2 heads, d = 64: window 128: 6.0 -> 4.1 us, 400: 8.0
+// (tensor-core form) -> 6.0.  The tensor-core form (attn_fwd_kernel.cuh) costs about 7 us a CTA of
 // 256 rows beside its tiles, which at these sizes is most of its time; where
 // the two cross is written at few_keys (attn_window.cu).  With many tokens it is
 // bound by the CTAs an SM holds (two at d = 128, three at d = 64, by registers and
 // shared memory) and each one's latencies: 40000 tokens, 16 / 8 heads, window 16:
 // 80 us at d = 64 and 142 at d = 128, where the bytes take 36 and 72.
 #include <cmath>
+#include <type_traits>
 
 #include "ra_launch.h"
 #include "ra_warp_mma.cuh"
@@ -22,7 +26,9 @@
 namespace ra {
 namespace {
 
-constexpr int kWarps = 4, kRows = 16 * kWarps, kChunk = 16;
+constexpr int kWarps = 4, kChunk = 16;
+// rows of a CTA: 16 a warp, or 16 whose keys the warps share
+constexpr int few_rows(bool split) { return split ? 16 : 16 * kWarps; }
 
 // The chunks of a block of rows, as range_walk has tiles: n_sink from key s0 on,
 // then from m0 on (both multiples of 16).
@@ -40,9 +46,11 @@ __device__ __forceinline__ FewChunks few_chunks(const RowKeys &first, int last_h
     return c;
 }
 
-template <int D, bool O_BF16>
+// SPLIT: the warps take the chunks of the CTA's 16 rows in turn and join at the end.
+template <int D, bool O_BF16, bool SPLIT>
 __global__ void __launch_bounds__(32 * kWarps, D == 64 ? 3 : 2) window_few_kernel(const WindowFew a) {
-    constexpr int KS = D / 16, CPR = D / 8;
+    constexpr int KS = D / 16, CPR = D / 8, kRows = few_rows(SPLIT), kJoin = D + 8;   // kJoin: floats per row of the join
+    __shared__ float s_m[kWarps][16], s_l[kWarps][16];
     constexpr uint32_t kHalf = kChunk * D * 2;       // a chunk's keys
     constexpr int kOut = D * 2 + 16;                 // bytes of a staged bf16 row
     extern __shared__ __align__(128) uint8_t smem[];
@@ -77,7 +85,7 @@ __global__ void __launch_bounds__(32 * kWarps, D == 64 ? 3 : 2) window_few_kerne
         cp_async_commit();
     }
     // this warp's 16 rows and their chunks
-    const int w0 = r0 + warp * 16, w_end = min(S, w0 + 16);
+    const int w0 = SPLIT ? r0 : r0 + warp * 16, w_end = min(S, w0 + 16);
     const bool any = w0 < S;
     RowKeys rk[2];
     FewChunks mine{};
@@ -113,7 +121,7 @@ __global__ void __launch_bounds__(32 * kWarps, D == 64 ? 3 : 2) window_few_kerne
             __syncthreads();
         }
         if (!any) continue;
-        for (int c = 0; c < mine.count; ++c) {
+        for (int c = SPLIT ? warp : 0; c < mine.count; c += SPLIT ? kWarps : 1) {
             const int k0 = mine.key(c);
             // its place in shared memory: among the main keys, or the sinks before them
             const int at = k0 >= all.m0 ? all.n_sink + (k0 - all.m0) / kChunk : (k0 - all.s0) / kChunk;
@@ -123,6 +131,56 @@ __global__ void __launch_bounds__(32 * kWarps, D == 64 ? 3 : 2) window_few_kerne
                      [&](int, int h) { return seen_bits(rk[h].lo, rk[h].hi, rk[h].slo, rk[h].shi, k0); });
         }
         if (head + 1 < head1) load_q(rw.q[0], hq + 1);     // on its way while the rows are written
+        if constexpr (SPLIT) {
+            // (any holds for every warp or for none: the rows are the CTA's)
+            float *rows = reinterpret_cast<float *>(smem + 2 * a.max_chunks * kHalf);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                rw.l[0][h] += __shfl_xor_sync(0xffffffffu, rw.l[0][h], 1);
+                rw.l[0][h] += __shfl_xor_sync(0xffffffffu, rw.l[0][h], 2);
+                if (t4 == 0) {
+                    s_m[warp][8 * h + g] = rw.m[0][h];
+                    s_l[warp][8 * h + g] = rw.l[0][h];
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = 8 * h + g;
+                const float top = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+                const float f = rw.m[0][h] > -INFINITY ? ex2(rw.m[0][h] - top) : 0.f;
+                float *dst = rows + ((size_t)warp * 16 + r) * kJoin + 2 * t4;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+                    *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(rw.acc[0][n][2 * h] * f, rw.acc[0][n][2 * h + 1] * f);
+            }
+            __syncthreads();
+            for (int e = threadIdx.x; e < 16 * (D / 4); e += 32 * kWarps) {
+                const int r = e / (D / 4), col = (e % (D / 4)) * 4;
+                if (w0 + r >= S) break;
+                float x[4] = {}, top = -INFINITY, l = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float4 f = *reinterpret_cast<const float4 *>(rows + ((size_t)w * 16 + r) * kJoin + col);
+                    x[0] += f.x, x[1] += f.y, x[2] += f.z, x[3] += f.w;
+                    top = fmaxf(top, s_m[w][r]);
+                }
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) l += s_m[w][r] > -INFINITY ? s_l[w][r] * ex2(s_m[w][r] - top) : 0.f;
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const size_t at = (((size_t)b * a.S + w0 + r) * a.H + hq) * D + col;
+                if constexpr (O_BF16)
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + at) =
+                        make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+                else
+                    *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + at) =
+                        make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+                if (col == 0)
+                    a.lse[((size_t)b * a.H + hq) * a.S + w0 + r] = l > 0.f ? (top + lg2(l)) * 0.6931471805599453f : -INFINITY;
+            }
+            __syncthreads();     // before the next head's rows
+            continue;
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float l = rw.l[0][h];
@@ -160,7 +218,15 @@ __global__ void __launch_bounds__(32 * kWarps, D == 64 ? 3 : 2) window_few_kerne
 
 }  // namespace
 
-int window_few_chunks(int S, int window, int sinks) {
+bool window_few_split(int64_t B, int64_t S, int64_t H, int d, int window, int sinks) {
+    const int chunks = window_few_chunks((int)S, window, sinks, true);
+    const size_t smem = window_few_smem(chunks, d, true), most = (size_t)227 << 10;
+    const int per_sm = d == 64 && 2 * (smem + 1024) <= most + 1024 ? 2 : 1;
+    return chunks > 2 && smem <= most && B * H * ((S + 15) / 16) <= 152 * per_sm;
+}
+
+int window_few_chunks(int S, int window, int sinks, bool split) {
+    const int kRows = few_rows(split);
     // The main keys end at the rows' end, a multiple of 16 (or of the tokens),
     // and begin window - 1 before the first row, earlier by up to `sinks` where
     // the sinks touch the window; else the sinks lie apart, anywhere.
@@ -171,16 +237,21 @@ int window_few_chunks(int S, int window, int sinks) {
     return (int)(need < most ? need : most);
 }
 
-size_t window_few_smem(int chunks, int d) {
-    return (size_t)chunks * 2 * kChunk * d * 2 + kWarps * 16 * (d * 2 + 16);
+size_t window_few_smem(int chunks, int d, bool split) {
+    return (size_t)chunks * 2 * kChunk * d * 2 + kWarps * 16 * (split ? (d + 8) * 4 : d * 2 + 16);
 }
 
 ra_status launch_window_few(WindowFew a, int d, bool o_bf16, int64_t B, cudaStream_t stream) {
-    a.blocks = (a.S + kRows - 1) / kRows;
-    a.max_chunks = window_few_chunks(a.S, a.window, a.sinks);
-    const size_t smem = window_few_smem(a.max_chunks, d);
-    auto kern = d == 128 ? (o_bf16 ? window_few_kernel<128, true> : window_few_kernel<128, false>)
-                         : (o_bf16 ? window_few_kernel<64, true> : window_few_kernel<64, false>);
+    const bool split = window_few_split(B, a.S, a.H, d, a.window, a.sinks);
+    a.blocks = (a.S + few_rows(split) - 1) / few_rows(split);
+    a.max_chunks = window_few_chunks(a.S, a.window, a.sinks, split);
+    const size_t smem = window_few_smem(a.max_chunks, d, split);
+    auto pick = [&](auto s) {
+        constexpr bool SPLIT = decltype(s)::value;
+        return d == 128 ? (o_bf16 ? window_few_kernel<128, true, SPLIT> : window_few_kernel<128, false, SPLIT>)
+                        : (o_bf16 ? window_few_kernel<64, true, SPLIT> : window_few_kernel<64, false, SPLIT>);
+    };
+    auto kern = split ? pick(std::true_type()) : pick(std::false_type());
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
     // a CTA takes the heads of a group one after another; where there are too

@@ -17,8 +17,12 @@ struct WindowFew {
 };
 
 // 16-key chunks a CTA may hold at these sizes, and its shared memory.
-int window_few_chunks(int S, int window, int sinks);
-size_t window_few_smem(int chunks, int d);
+int window_few_chunks(int S, int window, int sinks, bool split);
+size_t window_few_smem(int chunks, int d, bool split);
+
+// Whether a CTA's warps share 16 rows: the call's CTAs run at once and have more
+// than two chunks.
+bool window_few_split(int64_t B, int64_t S, int64_t H, int d, int window, int sinks);
 
 ra_status launch_window_few(WindowFew a, int d, bool o_bf16, int64_t B, cudaStream_t stream);
 
