@@ -8,13 +8,15 @@
 // is no pipeline inside a CTA; two or more CTAs on an SM cover one another's
 // loads.  Where there are few rows a CTA takes 16 of one head, and its warps
 // share their keys and join: the chain of a warp's chunks, 0.2 us each, is a
-// quarter as long.  512 tokens, 2 heads, d = 64: window 128: 6.0 -> 4.1 us, 400: 8.0
-// (tensor-core form) -> 6.0.  The tensor-core form (attn_fwd_kernel.cuh) costs about 7 us a CTA of
-// 256 rows beside its tiles, which at these sizes is most of its time; where
-// the two cross is written at few_keys (attn_window.cu).  With many tokens it is
-// bound by the CTAs an SM holds (two at d = 128, three at d = 64, by registers and
-// shared memory) and each one's latencies: 40000 tokens, 16 / 8 heads, window 16:
-// 80 us at d = 64 and 142 at d = 128, where the bytes take 36 and 72.
+// quarter as long.  512 tokens, 2 heads, d = 64: window 128: 6.0 -> 4.1 us, 400:
+// 8.0 (tensor-core form) -> 6.0.
+//
+// The tensor-core form (attn_fwd_kernel.cuh) costs about 7 us a CTA of 256 rows
+// beside its tiles, which at these sizes is most of its time; where the two cross
+// is written at few_keys (attn_window.cu).  With many tokens this form is bound by
+// the CTAs an SM holds (two at d = 128, three at d = 64, by registers and shared
+// memory) and each one's latencies: 40000 tokens, 16 / 8 heads, window 16: 80 us
+// at d = 64 and 142 at d = 128, where the bytes take 36 and 72.
 #include <cmath>
 #include <type_traits>
 
