@@ -198,10 +198,12 @@ ra_status launch_paged_few(const PagedFewLaunch &t, cudaStream_t stream) {
     const int64_t want = (t.keys + kChunk - 1) / kChunk + 2;
     a.room = (int)(want < kPagedFewRoom ? want : kPagedFewRoom);
     static_assert(kPagedFewRoom <= kMostChunks, "a thread and a place for each chunk's page");
-    const size_t smem = (size_t)a.room * 2 * kChunk * t.d * 2 + kWarps * 16 * (t.d * 2 + 16);
+    auto smem_of = [&](int room) { return (size_t)room * 2 * kChunk * t.d * 2 + kWarps * 16 * (t.d * 2 + 16); };
+    const size_t smem = smem_of(a.room), most = smem_of(kPagedFewRoom);
     auto kern = t.d == 128 ? (t.o_bf16 ? paged_few_kernel<128, true> : paged_few_kernel<128, false>)
                            : (t.o_bf16 ? paged_few_kernel<64, true> : paged_few_kernel<64, false>);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    // the limit is the form's largest, not this call's: host threads share it
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess)
         return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
     const int64_t grid = (int64_t)t.units * t.seqs.Hkv;
     if (grid > 0x7fffffffLL) return set_error(RA_ERR_UNSUPPORTED, "too many query tiles for one launch");

@@ -44,7 +44,7 @@ bool few_keys(int64_t B, int64_t L, int64_t H, int d, int window, int sinks) {
     if (window_few_split(B, L, H, d, window, sinks)) return true;
     const size_t smem = window_few_smem(window_few_chunks((int)L, window, sinks, false), d, false), most = (size_t)227 << 10;
     const bool one_wave = B * H * ((L + 63) / 64) <= (2 * (smem + 1024) <= most + 1024 ? 2 * kSms : kSms);
-    return row_chunks <= (one_wave ? 16 : d == 64 ? 11 : 5) && smem <= most;
+    return row_chunks <= (one_wave ? 16 : d == 64 ? 11 : 5) && smem <= kWindowFewSmem;
 }
 
 struct Window {

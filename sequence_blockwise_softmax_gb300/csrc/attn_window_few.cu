@@ -224,7 +224,7 @@ bool window_few_split(int64_t B, int64_t S, int64_t H, int d, int window, int si
     const int chunks = window_few_chunks((int)S, window, sinks, true);
     const size_t smem = window_few_smem(chunks, d, true), most = (size_t)227 << 10;
     const int per_sm = d == 64 && 2 * (smem + 1024) <= most + 1024 ? 2 : 1;
-    return chunks > 2 && smem <= most && B * H * ((S + 15) / 16) <= 152 * per_sm;
+    return chunks > 2 && smem <= kWindowFewSmem && B * H * ((S + 15) / 16) <= 152 * per_sm;
 }
 
 int window_few_chunks(int S, int window, int sinks, bool split) {
@@ -254,7 +254,7 @@ ra_status launch_window_few(WindowFew a, int d, bool o_bf16, int64_t B, cudaStre
                         : (o_bf16 ? window_few_kernel<64, true, SPLIT> : window_few_kernel<64, false, SPLIT>);
     };
     auto kern = split ? pick(std::true_type()) : pick(std::false_type());
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWindowFewSmem) != cudaSuccess)
         return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
     // a CTA takes the heads of a group one after another; where there are too
     // few CTAs for that, each takes fewer and the keys are copied again

@@ -16,6 +16,11 @@ struct WindowFew {
     int blocks, max_chunks, heads, group_parts;     // set by the launch
 };
 
+// The most dynamic shared memory of a CTA: 227 KB, less 1 KB for the kernel's static
+// part.  The limit set on the kernel is this one whatever a call needs, since host
+// threads share it: one lowered by another thread's call would refuse the launch.
+constexpr size_t kWindowFewSmem = (size_t)226 << 10;
+
 // 16-key chunks a CTA may hold at these sizes, and its shared memory.
 int window_few_chunks(int S, int window, int sinks, bool split);
 size_t window_few_smem(int chunks, int d, bool split);
