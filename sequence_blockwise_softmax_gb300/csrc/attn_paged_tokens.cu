@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
     using L = TokensSmem<D>;
     constexpr int NS = L::kStages, KS = D / 16, CPR = D / 8;   // k-steps, 16-byte pieces per row
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_sum[kWarps];
+    __shared__ unsigned long long s_sum[kWarps];
     __shared__ long long s_at;                 // the first chunk (or piece) inside its sequence
     __shared__ PagedChunks s_list;
     __shared__ int s_seq, s_last;
@@ -157,11 +157,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
 
     // ---- how the work is cut, from the lengths the call finds
     // An inclusive scan of x over the block (its total added to `base`).
-    auto scan = [&](long long x, long long &base) -> long long {
-        long long inc = x;
+    auto scan = [&](unsigned long long x, unsigned long long &base) -> unsigned long long {
+        unsigned long long inc = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+            const unsigned long long up = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += up;
         }
         __syncthreads();
@@ -179,14 +179,14 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
     const PagedChunks none{};
     auto list_of = [&](int s) { return s < sq.n_seqs ? paged_chunks(sq, s) : none; };
     PagedChunks mine = list_of(threadIdx.x);
-    // total chunks, and (sequence, head) pairs with new tokens in the high half
-    long long total = 0;
+    unsigned long long sum = 0;
     for (int i = 0; CLUSTER == 0 && i < blocks; ++i) {
         const PagedChunks l = i == 0 ? mine : list_of(i * blockDim.x + threadIdx.x);
-        scan(l.count + (l.count > 0 ? 1ll << 40 : 0ll), total);
+        scan(paged_tally(l.count), sum);
     }
-    const long long pairs = (total >> 40) * sq.Hkv;
-    total = (total & ((1ll << 40) - 1)) * sq.Hkv;
+    // (sequence, head) pairs with new tokens, and their chunks
+    const long long pairs = paged_tally_seqs(sum) * sq.Hkv;
+    const long long total = paged_tally_chunks(sum) * sq.Hkv;
     const int grid = gridDim.x;
     // Few pairs: each is cut into pieces of its own, at most one to a CTA.
     // Many: equal runs of the flat list, whose ends fall anywhere.  Between half
@@ -208,20 +208,20 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
     // where this CTA begins: chunk (or piece) number `at` of the list
     const long long at = flat ? (long long)cta * per : cta;
     {
-        long long base = 0;
+        unsigned long long base = 0;
         for (int i = 0; i < blocks; ++i) {
             if (i > 0) mine = list_of(i * blockDim.x + threadIdx.x);
             const int pieces = CLUSTER ? (mine.count > 0 ? CLUSTER : 0) : (mine.count + per - 1) / per;
             const long long n = (long long)(flat ? mine.count : pieces) * sq.Hkv;
-            const long long inc = scan(n, base);
+            const long long inc = (long long)scan(n, base);
             if (n > 0 && inc - n <= at && at < inc) {
                 s_seq = i * blockDim.x + threadIdx.x;
                 s_list = mine;
                 s_at = at - (inc - n);
             }
-            if (base > at) break;
+            if ((long long)base > at) break;
         }
-        if (at >= base) return;
+        if (at >= (long long)base) return;
     }
     __syncthreads();
     int seq = s_seq;

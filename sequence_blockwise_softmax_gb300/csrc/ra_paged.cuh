@@ -154,6 +154,18 @@ RA_HD PagedChunks paged_chunks(const PagedSeqs &q, int s) {
     return c;
 }
 
+// One sequence's share of a sum over all of them, which counts the sequences
+// with chunks above bit 39 and their chunks but one below.  Up to 2^24 sequences
+// of 2^39 chunks in all (a call's limits) stay inside its 64 bits.
+constexpr int kPagedTallyBits = 39;
+RA_HD uint64_t paged_tally(int chunks) {
+    return chunks > 0 ? ((uint64_t)1 << kPagedTallyBits) + (uint64_t)(chunks - 1) : 0;
+}
+RA_HD int64_t paged_tally_seqs(uint64_t sum) { return (int64_t)(sum >> kPagedTallyBits); }
+RA_HD int64_t paged_tally_chunks(uint64_t sum) {
+    return (int64_t)(sum & (((uint64_t)1 << kPagedTallyBits) - 1)) + paged_tally_seqs(sum);
+}
+
 // The first key of chunk number c.
 RA_HD int paged_chunk_key(const PagedChunks &l, int c) {
     return (c < l.n_sink ? c : l.m0 + (c - l.n_sink)) * kPagedChunk;
