@@ -150,8 +150,8 @@ Plan plan(Paged a) {
         p.tokens = true;
         int64_t seen = a.max_len;
         if (a.window > 0 && a.window + a.max_new + a.sinks < seen) seen = a.window + a.max_new + a.sinks;
-        p.ctas = paged_tokens_ctas(active0 * a.H_kv, seen);
-        p.whole_pairs = paged_tokens_whole(active0 * a.H_kv, seen);
+        p.ctas = paged_tokens_ctas(active0 * a.H_kv, seen, a.n_seqs);
+        p.whole_pairs = paged_tokens_whole(active0 * a.H_kv, seen, a.n_seqs);
         p.cluster = paged_tokens_cluster(active0 * a.H_kv, seen);
         const size_t rows = p.whole_pairs || p.cluster ? 0 : (size_t)2 * p.ctas * (a.max_new * group <= 16 ? 16 : 32);
         p.part_lse = p.part_o + round256(rows * a.d * 4);

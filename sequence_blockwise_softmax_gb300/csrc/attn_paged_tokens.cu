@@ -51,6 +51,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kChunk = kPagedChunk;
 constexpr int kWholeKeys = 1024;    // many pairs of at most so many keys: one CTA each, no pieces
+constexpr int kWholeSeqs = 512;     // of at most so many sequences
 constexpr int kMinRun = 4;          // chunks of a piece at least: one per warp
 
 struct TokensArgs {
@@ -541,8 +542,12 @@ ra_status launch(const TokensLaunch &t, const TokensArgs &args, cudaStream_t str
 
 }  // namespace
 
-bool paged_tokens_whole(int64_t pairs, int64_t keys) {
-    return 2 * pairs > kPagedTokensCtas && keys <= kWholeKeys && pairs < (int64_t)1 << 30;
+// Each CTA reads all sequences' lengths, so a CTA to a pair costs the square of
+// their number.  In us as pairs and as runs of all pairs, of 1-300 keys: 32 / 8
+// heads, d = 128: 160 sequences 33 and 50, 320: 67 and 82, 640: 145 and 114, 5120:
+// 4330 and 770; 8 / 2 heads, d = 64: 12 and 20, 19 and 25, 36 and 34, 970 and 190.
+bool paged_tokens_whole(int64_t pairs, int64_t keys, int64_t n_seqs) {
+    return 2 * pairs > kPagedTokensCtas && keys <= kWholeKeys && n_seqs <= kWholeSeqs;
 }
 
 // One sequence's 8 pairs, 32 / 8 heads, d = 128, in us as clusters of 2, 4, 8, 16
@@ -564,9 +569,9 @@ int paged_tokens_cluster(int64_t pairs, int64_t keys) {
     return c > 1 && keys <= (int64_t)c * (full ? 1024 : 576) ? c : 0;
 }
 
-int paged_tokens_ctas(int64_t pairs, int64_t keys) {
+int paged_tokens_ctas(int64_t pairs, int64_t keys, int64_t n_seqs) {
     if (const int cluster = paged_tokens_cluster(pairs, keys)) return (int)(pairs * cluster);
-    if (paged_tokens_whole(pairs, keys)) return (int)pairs;
+    if (paged_tokens_whole(pairs, keys, n_seqs)) return (int)pairs;
     const int64_t chunks = pairs * ((keys + kChunk - 1) / kChunk + 1);
     int64_t n = (chunks + kMinRun - 1) / kMinRun;
     if (n < 2 * pairs) n = 2 * pairs;      // so that few pairs are cut on their own

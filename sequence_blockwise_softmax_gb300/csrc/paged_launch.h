@@ -25,15 +25,16 @@ struct TokensLaunch {
 };
 
 // Whether every (sequence, key/value head) pair gets one CTA and is never cut:
-// there are enough of them and they are short.
-bool paged_tokens_whole(int64_t pairs, int64_t keys);
+// there are enough of them and they are short, and few enough sequences for each
+// CTA to look at all of them.
+bool paged_tokens_whole(int64_t pairs, int64_t keys, int64_t n_seqs);
 
 // The size of the cluster of CTAs that each pair gets, or 0.
 int paged_tokens_cluster(int64_t pairs, int64_t keys);
 
 // CTAs for `pairs` (sequence, key/value head) pairs of up to `keys` keys: the
 // grid, not the split, which the kernel takes from the lengths it finds.
-int paged_tokens_ctas(int64_t pairs, int64_t keys);
+int paged_tokens_ctas(int64_t pairs, int64_t keys, int64_t n_seqs);
 
 ra_status launch_paged_tokens(const TokensLaunch &t, cudaStream_t stream);
 
