@@ -3,8 +3,10 @@
 Each CUDA translation unit is compiled in parallel, then linked into
 ``sequence_blockwise_softmax_gb300/_lib/libra_gb300.so`` with the CUDA runtime
 linked statically.  Beside it g++ builds ``_lib/ra_torch.so``, the marshalling
-of torch tensors for the calls whose host time counts.  Rebuilds only when a
-source or header is newer than the libraries.
+of torch tensors for the calls whose host time counts.  Each is rebuilt only when
+a source or header is newer.  The library needs nvcc alone: where the binding
+cannot be built, the library is there all the same, for callers from C, and then
+the failure is raised.
 """
 import concurrent.futures
 import glob
@@ -41,20 +43,32 @@ def _deps():
         [os.path.join(ROOT, "include", "ra.h")]
 
 
-def up_to_date():
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = os.path.getmtime(LIB)
-    header = os.path.join(ROOT, "include", "ra.h")
-    return all(os.path.getmtime(p) <= t for p in _deps()) and \
-        all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in (BINDING_SOURCE, header))
+def _newer(path, deps):
+    """Whether `path` exists and no dependency is newer."""
+    return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps)
+
+
+def library_up_to_date():
+    return _newer(LIB, _deps())
+
+
+def binding_up_to_date():
+    return _newer(BINDING, (BINDING_SOURCE, os.path.join(ROOT, "include", "ra.h")))
+
+
+class BindingError(RuntimeError):
+    """The torch binding could not be built; the library was."""
 
 
 def build_binding():
     """Compile the torch binding against the installed torch's headers and libraries."""
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError as e:
+        raise BindingError("the torch binding needs torch: %s" % e)
+    os.makedirs(OUT_DIR, exist_ok=True)
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     tmp = BINDING + ".%d.tmp" % os.getpid()
@@ -65,16 +79,17 @@ def build_binding():
            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"), BINDING_SOURCE, "-o", tmp,
            "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise BindingError("g++ did not run for %s: %s" % (BINDING_SOURCE, e))
     if r.returncode != 0:
-        raise RuntimeError("g++ failed for %s:\n%s%s" % (BINDING_SOURCE, r.stdout, r.stderr))
+        raise BindingError("g++ failed for %s:\n%s%s" % (BINDING_SOURCE, r.stdout, r.stderr))
     os.replace(tmp, BINDING)
     return BINDING
 
 
-def build(force=False, verbose=False, extra_flags=()):
-    if not force and up_to_date():
-        return LIB
+def build_library(verbose=False, extra_flags=()):
     os.makedirs(OUT_DIR, exist_ok=True)
     obj_dir = os.path.join(OUT_DIR, "obj")
     os.makedirs(obj_dir, exist_ok=True)
@@ -91,10 +106,8 @@ def build(force=False, verbose=False, extra_flags=()):
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(9, len(sources()) + 1)) as ex:
-        binding = ex.submit(build_binding)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(sources()))) as ex:
         objs = list(ex.map(compile_one, sources()))
-        binding.result()
     tmp = LIB + ".%d.tmp" % os.getpid()
     cmd = [exe, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -104,7 +117,22 @@ def build(force=False, verbose=False, extra_flags=()):
     return LIB
 
 
+def build(force=False, verbose=False, extra_flags=()):
+    """The library and the binding side by side; BindingError once the library is there."""
+    with concurrent.futures.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = None if not force and binding_up_to_date() else ex.submit(build_binding)
+        if force or not library_up_to_date():
+            build_library(verbose, extra_flags)
+        if binding is not None:
+            binding.result()
+    return LIB
+
+
 if __name__ == "__main__":
     v = "-v" in sys.argv
     flags = ["-Xptxas", "-v"] if v else []
-    print(build(force=True, verbose=v, extra_flags=flags))
+    try:
+        print(build(force=True, verbose=v, extra_flags=flags))
+    except BindingError as e:
+        print(LIB)
+        sys.exit("the library is built, the torch binding is not: %s" % e)

@@ -1,0 +1,69 @@
+"""What the build makes where a part of the toolchain is missing, with a stand-in for nvcc."""
+import importlib.util
+import os
+import stat
+import sys
+
+import pytest
+
+from conftest import ROOT
+
+BUILD = os.path.join(ROOT, "sequence_blockwise_softmax_gb300", "build.py")
+
+
+def script(path, text):
+    path.write_text("#!/bin/sh\n" + text)
+    path.chmod(path.stat().st_mode | stat.S_IXUSR)
+    return str(path)
+
+
+@pytest.fixture
+def build(tmp_path, monkeypatch):
+    """build.py writing to a folder of its own; its nvcc creates whatever -o names and logs that."""
+    spec = importlib.util.spec_from_file_location("build_under_test", BUILD)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    for name in ("OUT_DIR", "LIB", "BINDING"):
+        if hasattr(module, name):
+            monkeypatch.setattr(module, name, str(tmp_path / "_lib" / os.path.basename(getattr(module, name))))
+    monkeypatch.setattr(module, "OUT_DIR", str(tmp_path / "_lib"))
+    module.log = tmp_path / "nvcc.log"
+    module.log.write_text("")
+    monkeypatch.setenv("NVCC", script(tmp_path / "nvcc", """
+while [ $# -gt 1 ]; do
+  if [ "$1" = -o ]; then : > "$2"; echo "$2" >> "%s"; fi
+  shift
+done
+""" % module.log))
+    return module
+
+
+def without_gxx(tmp_path, monkeypatch):
+    bin_dir = tmp_path / "bin"
+    bin_dir.mkdir()
+    script(bin_dir / "g++", "echo no such header >&2; exit 1\n")
+    monkeypatch.setenv("PATH", str(bin_dir) + os.pathsep + os.environ["PATH"])
+
+
+def test_the_library_does_not_need_the_binding(build, tmp_path, monkeypatch):
+    """A C caller's machine: no compiler or headers for the torch binding.  The library is there all
+    the same, and the failure is reported."""
+    without_gxx(tmp_path, monkeypatch)
+    with pytest.raises(RuntimeError, match="no such header"):
+        build.build()
+    assert os.path.exists(build.LIB)
+
+
+def test_the_library_does_not_need_torch(build, monkeypatch):
+    monkeypatch.setitem(sys.modules, "torch", None)         # import torch raises ImportError
+    with pytest.raises(RuntimeError, match="torch"):
+        build.build()
+    assert os.path.exists(build.LIB)
+
+
+def test_a_missing_binding_does_not_rebuild_the_library(build, tmp_path, monkeypatch):
+    without_gxx(tmp_path, monkeypatch)
+    for _ in range(2):
+        with pytest.raises(RuntimeError):
+            build.build()
+    assert sum("libra_gb300.so" in x for x in build.log.read_text().split()) == 1
