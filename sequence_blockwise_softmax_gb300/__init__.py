@@ -4,7 +4,7 @@ Argument marshalling only: every function here checks that it was given CUDA
 tensors, takes their device pointers and the current CUDA stream, and calls
 the C entry point of the same name declared in ``include/ra.h`` -- the windowed
 and paged attention calls, whose host time counts, through the compiled
-``ra_torch.so`` (``csrc/torch_binding.cpp``).  All work
+binding ``ra_torch`` (``csrc/torch_binding.cpp``).  All work
 runs in the library's kernels; there is no fallback of any kind -- if the
 library is missing, the first call raises.
 
@@ -107,12 +107,14 @@ _native = None
 
 
 def native():
-    """The compiled tensor marshalling (ra_torch.so), bound to the loaded library; raise if it is missing."""
+    """The compiled tensor marshalling (ra_torch), bound to the loaded library; raise if it is not there
+    for the torch that runs."""
     global _native
     if _native is None:
-        path = _build.BINDING
+        path = _build.binding_path()
         if not os.path.exists(path):
-            raise RuntimeError("ra_torch.so is not built (%s); run __graft_entry__.build()" % path)
+            raise RuntimeError("the binding for torch %s is not built (%s); run __graft_entry__.build()" %
+                               (torch.__version__, path))
         spec = importlib.util.spec_from_file_location("ra_torch", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

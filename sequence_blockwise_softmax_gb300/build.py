@@ -2,15 +2,18 @@
 
 Each CUDA translation unit is compiled in parallel, then linked into
 ``sequence_blockwise_softmax_gb300/_lib/libra_gb300.so`` with the CUDA runtime
-linked statically.  Beside it g++ builds ``_lib/ra_torch.so``, the marshalling
-of torch tensors for the calls whose host time counts.  Each is rebuilt only when
-a source or header is newer.  The library needs nvcc alone: where the binding
+linked statically.  Beside it g++ builds ``_lib/ra_torch.<python>-<torch>.so``, the
+marshalling of torch tensors for the calls whose host time counts; it holds the
+layout of the installed torch's tensors, so its name says which torch that is and
+another one builds its own.  Each is rebuilt only when a source or header is
+newer.  The library needs nvcc alone: where the binding
 cannot be built, the library is there all the same, for callers from C, and then
 the failure is raised.
 """
 import concurrent.futures
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -20,7 +23,6 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libra_gb300.so")
-BINDING = os.path.join(OUT_DIR, "ra_torch.so")
 BINDING_SOURCE = os.path.join(CSRC, "torch_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr",
@@ -52,26 +54,38 @@ def library_up_to_date():
     return _newer(LIB, _deps())
 
 
-def binding_up_to_date():
-    return _newer(BINDING, (BINDING_SOURCE, os.path.join(ROOT, "include", "ra.h")))
-
-
 class BindingError(RuntimeError):
     """The torch binding could not be built; the library was."""
+
+
+def binding_path():
+    """Where the binding for this Python and the installed torch lies."""
+    try:
+        import torch
+    except ImportError as e:
+        raise BindingError("the torch binding needs torch: %s" % e)
+    tag = "%s-torch%s-%s" % (sys.implementation.cache_tag, torch.__version__, (torch.version.git_version or "")[:12])
+    return os.path.join(OUT_DIR, "ra_torch.%s.so" % re.sub(r"[^\w.-]", "_", tag))
+
+
+def binding_up_to_date():
+    try:
+        path = binding_path()
+    except BindingError:
+        return False
+    return _newer(path, (BINDING_SOURCE, os.path.join(ROOT, "include", "ra.h")))
 
 
 def build_binding():
     """Compile the torch binding against the installed torch's headers and libraries."""
     import sysconfig
 
-    try:
-        import torch
-    except ImportError as e:
-        raise BindingError("the torch binding needs torch: %s" % e)
+    path = binding_path()
+    import torch
     os.makedirs(OUT_DIR, exist_ok=True)
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    tmp = BINDING + ".%d.tmp" % os.getpid()
+    tmp = path + ".%d.tmp" % os.getpid()
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
            "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
@@ -85,8 +99,8 @@ def build_binding():
         raise BindingError("g++ did not run for %s: %s" % (BINDING_SOURCE, e))
     if r.returncode != 0:
         raise BindingError("g++ failed for %s:\n%s%s" % (BINDING_SOURCE, r.stdout, r.stderr))
-    os.replace(tmp, BINDING)
-    return BINDING
+    os.replace(tmp, path)
+    return path
 
 
 def build_library(verbose=False, extra_flags=()):

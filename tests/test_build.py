@@ -5,6 +5,7 @@ import stat
 import sys
 
 import pytest
+import torch
 
 from conftest import ROOT
 
@@ -23,7 +24,7 @@ def build(tmp_path, monkeypatch):
     spec = importlib.util.spec_from_file_location("build_under_test", BUILD)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
-    for name in ("OUT_DIR", "LIB", "BINDING"):
+    for name in ("LIB", "BINDING"):
         if hasattr(module, name):
             monkeypatch.setattr(module, name, str(tmp_path / "_lib" / os.path.basename(getattr(module, name))))
     monkeypatch.setattr(module, "OUT_DIR", str(tmp_path / "_lib"))
@@ -67,3 +68,32 @@ def test_a_missing_binding_does_not_rebuild_the_library(build, tmp_path, monkeyp
         with pytest.raises(RuntimeError):
             build.build()
     assert sum("libra_gb300.so" in x for x in build.log.read_text().split()) == 1
+
+
+def test_the_binding_belongs_to_one_torch(build, tmp_path, monkeypatch):
+    """It holds the layout of torch's tensors: another torch gets its own, and does not load this one."""
+    bin_dir = tmp_path / "bin"
+    bin_dir.mkdir()
+    log = tmp_path / "g++.log"
+    script(bin_dir / "g++", """
+echo run >> "%s"
+while [ $# -gt 1 ]; do
+  if [ "$1" = -o ]; then : > "$2"; fi
+  shift
+done
+""" % log)
+    monkeypatch.setenv("PATH", str(bin_dir) + os.pathsep + os.environ["PATH"])
+    for _ in range(2):
+        build.build()
+    assert log.read_text().split() == ["run"]
+    monkeypatch.setattr(torch, "__version__", "2.0.0+other")
+    build.build()
+    assert log.read_text().split() == ["run", "run"]
+
+
+def test_the_package_does_not_load_another_torchs_binding(ralib, monkeypatch):
+    ralib.native()
+    monkeypatch.setattr(ralib, "_native", None)
+    monkeypatch.setattr(torch, "__version__", "2.0.0+other")
+    with pytest.raises(RuntimeError, match="not built"):
+        ralib.native()
