@@ -135,7 +135,8 @@ struct Plan {
 bool few_keys(int64_t keys, int d) { return keys <= (d == 64 ? 128 : 64); }
 
 Plan plan(Paged a) {
-    // hints of any size: nothing below leaves 64 bits
+    // hints of any size: with the sizes that the checks admit nothing below leaves
+    // 64 bits (pairs reach 2^40, keys 2^30, a part's bytes 2^58, of which 64 are tried)
     const int64_t cap = (int64_t)1 << 29;
     if (a.max_new > a.T) a.max_new = a.T;
     if (a.max_len > cap) a.max_len = cap;

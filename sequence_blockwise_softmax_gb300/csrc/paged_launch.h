@@ -1,6 +1,6 @@
 // paged_launch.h -- the launches of paged attention's few-row form
 // (attn_paged_tokens.cu) and few-key form (attn_paged_few.cu), shared with the
-// entry point (attn_paged.cu).
+// entry point (attn_paged.cu), and the few-row form's rules on how a call is cut.
 #pragma once
 #include "ra_internal.h"
 #include "ra_paged.cuh"
@@ -9,6 +9,9 @@ namespace ra {
 
 constexpr int kPagedTokensRows = 32;        // most rows (new tokens x query heads) per key/value head
 constexpr int kPagedTokensCtas = 2 * 152;   // two resident CTAs on each SM of a GB300
+constexpr int kPagedMinRun = 4;             // chunks of a piece at least: one per warp
+constexpr int kPagedWholeKeys = 1024;       // many pairs of at most so many keys: one CTA each, no pieces
+constexpr int kPagedWholeSeqs = 512;        // of at most so many sequences
 
 struct TokensLaunch {
     PagedSeqs seqs;
@@ -26,15 +29,47 @@ struct TokensLaunch {
 
 // Whether every (sequence, key/value head) pair gets one CTA and is never cut:
 // there are enough of them and they are short, and few enough sequences for each
-// CTA to look at all of them.
-bool paged_tokens_whole(int64_t pairs, int64_t keys, int64_t n_seqs);
+// CTA to look at all of them: it reads their lengths, so a CTA to a pair costs the
+// square of their number.  In us as pairs and as runs of all pairs, of 1-300 keys:
+// 32 / 8 heads, d = 128: 160 sequences 33 and 50, 320: 67 and 82, 640: 145 and 114,
+// 5120: 4330 and 770; 8 / 2 heads, d = 64: 12 and 20, 19 and 25, 36 and 34, 970 and
+// 190.
+inline bool paged_tokens_whole(int64_t pairs, int64_t keys, int64_t n_seqs) {
+    return 2 * pairs > kPagedTokensCtas && keys <= kPagedWholeKeys && n_seqs <= kPagedWholeSeqs;
+}
 
 // The size of the cluster of CTAs that each pair gets, or 0.
-int paged_tokens_cluster(int64_t pairs, int64_t keys);
+// One sequence's 8 pairs, 32 / 8 heads, d = 128, in us as clusters of 2, 4, 8, 16
+// and as pieces joined through the workspace: 100 keys 4.9, 4.9, 5.0, 6.2, 5.6; 700:
+// 8.5, 6.4, 5.9, 6.6, 7.5; 2000: clusters of 8 and 16 7.4, 7.4, pieces 8.4; 4000: 10.3,
+// 9.5, 10.8; 8000: 15.7, 13.0, 12.7.  8 sequences, 64 pairs, of 500-1000 keys: clusters
+// of 2 and 4 10.1, 8.6, pieces 10.3; of 16-2000: 14.8, 11.5, 11.4; of 16-4000: 24.4,
+// 17.7, 15.0.  19 sequences, 152 pairs, of 900-1000 keys: clusters of 2 12.4, pieces
+// 20.9.  More CTAs than the GPU holds at once cost a second wave: 37 pairs of 1000
+// keys as clusters of 8 11.6, 36 pairs 7.4.
+inline int paged_tokens_cluster(int64_t pairs, int64_t keys) {
+    // as many CTAs as have keys enough each
+    int c = keys <= 128 ? 2 : keys <= (pairs <= 8 ? 256 : 768) ? 4 : keys <= (pairs <= 4 ? 512 : 2560) ? 8 : 16;
+    // and as the GPU holds for all pairs
+    while (c > 1 && pairs > (c == 16 ? 8 : c == 8 ? 36 : c == 4 ? 74 : 152)) c /= 2;
+    // long sequences want all SMs, and even runs where their lengths differ
+    const bool full = 10 * pairs * c >= 9 * kPagedTokensCtas;
+    // (about 512 keys a CTA: a window of 4096 has sinks and new tokens beside it)
+    return c > 1 && keys <= (int64_t)c * (full ? 1024 : 576) ? c : 0;
+}
 
 // CTAs for `pairs` (sequence, key/value head) pairs of up to `keys` keys: the
 // grid, not the split, which the kernel takes from the lengths it finds.
-int paged_tokens_ctas(int64_t pairs, int64_t keys, int64_t n_seqs);
+inline int paged_tokens_ctas(int64_t pairs, int64_t keys, int64_t n_seqs) {
+    if (const int cluster = paged_tokens_cluster(pairs, keys)) return (int)(pairs * cluster);
+    if (paged_tokens_whole(pairs, keys, n_seqs)) return (int)pairs;
+    // two CTAs to a pair at least, so that few pairs are cut on their own
+    if (2 * pairs >= kPagedTokensCtas) return kPagedTokensCtas;
+    const int64_t chunks = pairs * ((keys + kPagedChunk - 1) / kPagedChunk + 1);
+    int64_t n = (chunks + kPagedMinRun - 1) / kPagedMinRun;
+    if (n < 2 * pairs) n = 2 * pairs;
+    return (int)(n < 1 ? 1 : n > kPagedTokensCtas ? kPagedTokensCtas : n);
+}
 
 ra_status launch_paged_tokens(const TokensLaunch &t, cudaStream_t stream);
 
