@@ -231,6 +231,8 @@ Plan plan(Paged a) {
     return p;
 }
 
+constexpr int64_t kMostStride = (int64_t)1 << 39;     // elements; a tensor map's strides stay below 2^40 bytes
+
 ra_status check_heads(int64_t H, int64_t H_kv, int d) {
     if (d != 64 && d != 128) return set_error(RA_ERR_UNSUPPORTED, "head dimension d must be 64 or 128");
     if (H_kv < 1 || H_kv > H || H % H_kv)
@@ -247,11 +249,11 @@ ra_status check_cache(int64_t T, int64_t n_seqs, int64_t H_kv, int d, int64_t n_
         return set_error(RA_ERR_UNSUPPORTED, "page_size must be a power of two, at least 16 and at most 65536");
     if (T > (int64_t)1 << 24 || n_seqs > (int64_t)1 << 24 || n_pages > (int64_t)1 << 30)
         return set_error(RA_ERR_UNSUPPORTED, "tokens, sequences or pages beyond the supported range");
-    if (max_pages * page > (int64_t)1 << 29)
+    if (max_pages > ((int64_t)1 << 29) / page)
         return set_error(RA_ERR_UNSUPPORTED, "max_pages * page_size beyond the supported range (2^29 tokens)");
     if (page_stride < page * H_kv * d) return set_error(RA_ERR_SHAPE, "page_stride is smaller than a page: pages would overlap");
     if (page_stride % 8) return set_error(RA_ERR_ALIGNMENT, "page_stride must be a multiple of 8 elements (16 bytes)");
-    if (page_stride * 2 >= ((int64_t)1 << 40)) return set_error(RA_ERR_UNSUPPORTED, "page_stride beyond the supported range");
+    if (page_stride >= kMostStride) return set_error(RA_ERR_UNSUPPORTED, "page_stride beyond the supported range");
     return RA_OK;
 }
 
@@ -262,7 +264,7 @@ ra_status check(const Paged &a) {
     if (std::isnan(a.scale) || std::isinf(a.scale)) return set_error(RA_ERR_INVALID_ARG, "scale must be finite");
     if (a.q_stride < a.H * a.d) return set_error(RA_ERR_SHAPE, "q_stride is smaller than H * d: tokens would overlap");
     if (a.q_stride % 8) return set_error(RA_ERR_ALIGNMENT, "q_stride must be a multiple of 8 elements (16 bytes)");
-    if (a.q_stride * 2 >= ((int64_t)1 << 40)) return set_error(RA_ERR_UNSUPPORTED, "q_stride beyond the supported range");
+    if (a.q_stride >= kMostStride) return set_error(RA_ERR_UNSUPPORTED, "q_stride beyond the supported range");
     if (a.max_new < 0 || a.max_len < 0) return set_error(RA_ERR_SHAPE, "max_new and max_len must be non-negative");
     if (a.window < 0) return set_error(RA_ERR_INVALID_ARG, "window must not be negative (0: none)");
     if (a.sinks < 0) return set_error(RA_ERR_INVALID_ARG, "sinks must not be negative");
@@ -551,7 +553,7 @@ ra_status ra_paged_append(const void *k_new, const void *v_new, void *k_pages, v
     if ((st = check_cache(T, n_seqs, H_kv, d, n_pages, page_size, page_stride, max_pages)) != RA_OK) return st;
     if (new_stride < H_kv * d) return set_error(RA_ERR_SHAPE, "new_stride is smaller than H_kv * d: tokens would overlap");
     if (new_stride % 8) return set_error(RA_ERR_ALIGNMENT, "new_stride must be a multiple of 8 elements (16 bytes)");
-    if (new_stride * 2 >= ((int64_t)1 << 40)) return set_error(RA_ERR_UNSUPPORTED, "new_stride beyond the supported range");
+    if (new_stride >= kMostStride) return set_error(RA_ERR_UNSUPPORTED, "new_stride beyond the supported range");
     if (T == 0 || n_seqs == 0) return RA_OK;
     if (n_pages == 0 || max_pages == 0) return set_error(RA_ERR_SHAPE, "new tokens need pages to lie in");
     const void *ptrs[] = {k_new, v_new, k_pages, v_pages, workspace};
