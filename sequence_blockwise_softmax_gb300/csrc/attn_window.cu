@@ -25,6 +25,7 @@ namespace {
 
 constexpr size_t kHeader = RA_WORKSPACE_MIN_BYTES;
 constexpr int kSms = 152;     // GB300; only choices of a form depend on it
+constexpr int kMostSeqs = 1 << 29;   // two of them and the sinks' units stay inside 32 bits
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -74,6 +75,7 @@ ra_status check(Window &w, int64_t window, int64_t sinks, const int *cu_seqlens,
     if (cu_seqlens) {
         if (w.B != 1) return set_error(RA_ERR_SHAPE, "packed sequences need B = 1");
         if (n_seqs < 1) return set_error(RA_ERR_SHAPE, "n_seqs must be at least 1");
+        if (n_seqs > kMostSeqs) return set_error(RA_ERR_UNSUPPORTED, "n_seqs beyond the supported range (2^29)");
         if (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u)
             return set_error(RA_ERR_ALIGNMENT, "cu_seqlens must be 4-byte aligned");
         w.n_seqs = n_seqs;
@@ -265,7 +267,7 @@ ra_status ra_window_attn_fwd(const void *q, const void *k, const void *v, void *
 size_t ra_window_attn_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t H_kv, int d, int64_t window,
                                           int64_t sinks, int n_seqs) {
     if (B < 0 || L < 0 || H < 0 || H_kv < 0 || window < 1 || sinks < 0 || n_seqs < 0 || (d != 64 && d != 128)) return 0;
-    if (B > (int64_t)1 << 20 || L > (int64_t)1 << 29 || H > (int64_t)1 << 20 || H_kv > H) return 0;
+    if (B > (int64_t)1 << 20 || L > (int64_t)1 << 29 || H > (int64_t)1 << 20 || H_kv > H || n_seqs > ra::kMostSeqs) return 0;
     return ra::bwd_space(B, L, H, H_kv, d, window, sinks, n_seqs).total;
 }
 
