@@ -356,12 +356,16 @@ RA_API ra_status ra_window_attn_fwd(const void *q, const void *k, const void *v,
  * ra_ring_attn_bwd under the windowed mask).  o: the forward's output, fp32, or
  * bf16 with RA_FLAG_O_BF16; dout: bf16 like q; lse: from the forward.  dq like
  * q, dk and dv like k: fp32, or bf16 with RA_FLAG_GRAD_BF16; every row of a
- * sequence is written, the others are left as they were.  Deterministic (no atomics).  The sinks' gradient from the queries
- * past their windows is taken in chunks of queries and added in their order.
- * workspace: ra_window_attn_bwd_workspace_bytes() bytes (the status word, D and
- * the sinks' partial gradients, about 32 MiB unless there are many sequences),
- * zero-filled before its first use; calls that may overlap on the GPU need one
- * each.
+ * sequence is written, the others are left as they were.  Deterministic (no
+ * atomics).  The sinks' gradient from the queries past their windows is taken in
+ * chunks of queries and added in their order.
+ * workspace: ra_window_attn_bwd_workspace_bytes() bytes, zero-filled before its
+ * first use; calls that may overlap on the GPU need one each.  They are the
+ * status word, D (4 * B * L * H) and the sinks' partial gradients: at most 32 MiB,
+ * or (2 * n_seqs + 3) * 8 * B * H_kv * sinks * d where that is more.  Where it is
+ * more the chunks are as long as the whole input, which costs time: a sequence's
+ * queries past the sinks' windows are then one block for each 128 sinks of a
+ * key/value head, as from 31 sequences on with 64 sinks, H_kv = 8 and d = 128.
  */
 RA_API ra_status ra_window_attn_bwd(const void *q, const void *k, const void *v, const void *o,
                                     const void *dout, const float *lse, void *dq, void *dk, void *dv,

@@ -170,8 +170,10 @@ RA_HD int window_col_end(int t, int end, int window) {
 // A chunk is about as long as a key block's own queries (the window), so that
 // the two kinds of block take alike, from 512 rows (shorter ones cost more CTAs
 // than they even out: 3000 tokens, window 100, 36 us with 256 against 32) to
-// 2048; longer where the partial gradients (slot_bytes for each unit and each sequence) would pass 32
-// MiB.
+// 2048; longer where the partial gradients (slot_bytes for each unit and each
+// sequence) would pass 32 MiB.  Where the two slots of each sequence pass that by
+// themselves no length keeps inside it, and one chunk holds all S rows: the far
+// queries of a sequence are then one block, in (2 n_seqs + 3) slots at most.
 RA_HD int sink_chunk(int64_t window, int64_t S, int64_t n_seqs, int64_t slot_bytes) {
     int64_t c = window <= 512 ? 512 : window >= 2048 ? 2048 : (window + 127) / 128 * 128;
     while (c < S && (S / c + 2 * n_seqs + 2) > ((int64_t)32 << 20) / (slot_bytes > 0 ? slot_bytes : 1)) c *= 2;
