@@ -8,9 +8,10 @@
 // Where there are few units, each unit's key tiles are cut into parts that run
 // as CTAs of their own and are joined by their LSE.  Bound by the tensor cores'
 // pace (about 1.35 us for 128 keys by 256 rows at d = 128) and a CTA's fixed 8
-// us: 512 tokens over 32768 keys, 32 / 8 heads, 193 us in pages of 16 and 175 in
-// pages of 128 (1415 and 1560 TFLOP/s); two prompts of 2048 tokens over 8192: 313
-// us (1535 TFLOP/s).  Few rows and few keys have forms of their own.
+// us: 512 tokens over 32768 keys, 32 / 8 heads, 202 us in pages of 16 and 190 in
+// pages of 128 (1350 and 1440 TFLOP/s); two prompts of 2048 tokens over 8192: 335
+// us (1440 TFLOP/s), each call on other inputs (the same again: 190 us in pages of
+// 16).  Few rows and few keys have forms of their own.
 #include <cmath>
 
 #include "attn_fwd_kernel.cuh"

@@ -9,7 +9,7 @@
 // short sequence to 256 rows; where the two cross is written at few_keys
 // (attn_paged.cu).  Bound by the latency of one pass: table, keys, at most eight
 // dependent chunks, rows out.  40 prompts of 33-40 tokens, 8 / 8 heads, d = 64:
-// 7.2 us against 17.5.
+// 6.6 us against 17.5.
 #include <cmath>
 
 #include "paged_launch.h"

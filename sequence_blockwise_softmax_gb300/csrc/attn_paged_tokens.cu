@@ -31,9 +31,9 @@
 // LSE = (m + log2 l) ln 2, with m moved rarely; pieces with (m_i, l_i, O_i) add to
 // m = max m_i, l = sum l_i 2^(m_i - m), O = sum O_i 2^(m_i - m).
 //
-// Measured on a GB300, 32 / 8 heads, d = 128: 64 sequences of 200-16000 keys 355
-// us (6.75 TB/s; the bytes alone take 353 at the copy rate), 8 of 3000-4000 keys
-// 23 us, one of 1000 keys 5.9 us, which is a chain of latencies: lengths, table,
+// Measured on a GB300, 32 / 8 heads, d = 128: 64 sequences of 200-16000 keys 362
+// us (6.6 TB/s; the bytes alone take 353 at the copy rate), 8 of 3000-4000 keys
+// 25 us, one of 1000 keys 6.1 us, which is a chain of latencies: lengths, table,
 // keys, the warps' rows, the join.
 #include <atomic>
 #include <cmath>

@@ -6,12 +6,14 @@
 //
 // Forward: bound by a unit's fixed 7 us (set-up, first loads, epilogue) beside
 // about 1.3 us a tile, the tensor cores' own pace inside the loop: 128K tokens, 8
-// heads, d = 128, window 1024: 570 us (1020 TFLOP/s over the visible pairs), 8192
-// tokens, 16 heads: 80 us; window 4096 over 32K tokens: 350 us (1470 TFLOP/s).
+// heads, d = 128, window 1024: 592 us (980 TFLOP/s over the visible pairs), 8192
+// tokens, 16 heads: 80 us, 67 at d = 64; window 4096 over 32K tokens, 8 heads: 376
+// us (1370 TFLOP/s).
 // Backward: 7 products for the 5 that the formulas need (both passes rebuild S
-// and dP): 32K tokens, 8 heads, d = 128, window 2048, 128 sinks: 785 us (1250
-// TFLOP/s executed); 8191 packed tokens, 16 / 4 heads, d = 64, window 500: 125 us,
-// where the CTAs are short.
+// and dP): 32K tokens, 8 heads, d = 128, window 2048, 128 sinks: 838 us (1180
+// TFLOP/s executed); 8191 packed tokens, 16 / 4 heads, d = 64, window 500: 128 us,
+// where the CTAs are short.  These are calls one after another on other inputs each
+// time; on the same inputs again, part of them in L2, 569, 804 and 127 us.
 #include <cmath>
 
 #include "attn_bwd_kernels.cuh"

@@ -46,7 +46,11 @@ inline bool paged_tokens_whole(int64_t pairs, int64_t keys, int64_t n_seqs) {
 // of 2 and 4 10.1, 8.6, pieces 10.3; of 16-2000: 14.8, 11.5, 11.4; of 16-4000: 24.4,
 // 17.7, 15.0.  19 sequences, 152 pairs, of 900-1000 keys: clusters of 2 12.4, pieces
 // 20.9.  More CTAs than the GPU holds at once cost a second wave: 37 pairs of 1000
-// keys as clusters of 8 11.6, 36 pairs 7.4.
+// keys as clusters of 8 11.6, 36 pairs 7.4.  At the limit of 576 keys a CTA, with 480,
+// 512, 544 and 576, clusters against pieces: 32 pairs, d = 64, clusters of 8: 10.5 / 12.1,
+// 10.5 / 12.2, 11.3 / 12.4, 11.3 / 12.8; d = 128: 12.6 / 14.2 to 13.6 / 15.3; 64 pairs, of 4:
+// 12.5 / 14.8 to 13.6 / 16.0; 16 pairs, d = 64, of 8: 10.1 / 10.0 to 10.8 / 10.6; 8 pairs, of
+// 16: 13.4 / 12.4 to 14.3 / 13.0.
 inline int paged_tokens_cluster(int64_t pairs, int64_t keys) {
     // as many CTAs as have keys enough each
     int c = keys <= 128 ? 2 : keys <= (pairs <= 8 ? 256 : 768) ? 4 : keys <= (pairs <= 4 ? 512 : 2560) ? 8 : 16;

@@ -97,8 +97,8 @@ RA_HD int paged_unit_rows(const PagedSeqs &q) {
 }
 
 // A unit's tiles are cut into at most num_splits parts of equal size, at least
-// kSplitTiles tiles each: a part costs its CTA about 7 us and the join a read
-// of its rows, a tile about 1 us.  With tail_share (at most a part's equal
+// kSplitTiles tiles each: a part costs its CTA about 8 us and the join a read
+// of its rows, a tile 1.35 us (1.0 at d = 64).  With tail_share (at most a part's equal
 // share) the last part has that much and the others the rest.
 constexpr int kSplitTiles = 6;
 RA_HD int paged_split_tiles(const PagedSeqs &q, int tiles) {
