@@ -336,7 +336,8 @@ RA_API size_t ra_ring_attn_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, 
  * RA_FLAG_O_BF16; lse: fp32 [B, H, L].  d in {64, 128}; window >= 1 (L or more:
  * no window); sinks >= 0 (0: none); scale <= 0: 1 / sqrt(d).
  * cu_seqlens / n_seqs: packed sequences, n_seqs + 1 int32 boundaries on the
- * device from 0 up (B = 1), or NULL / 0 for B sequences of L tokens.  Tokens
+ * device from 0 up (B = 1, n_seqs at most 2^29), or NULL / 0 for B sequences of
+ * L tokens (at most 2^29).  Tokens
  * from the last boundary on belong to no sequence: they may hold anything, and
  * their rows of o and lse are left as they were.  Boundaries that do not
  * increase give wrong masks, never an access out of range.
@@ -408,8 +409,9 @@ RA_API size_t ra_window_attn_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H
  * q: bf16 [T, H, d] with q_stride elements from token to token (at least H * d,
  * a multiple of 8); o: fp32 [T, H, d], or bf16 with RA_FLAG_O_BF16; lse: fp32
  * [H, T], natural log, or NULL.  d in {64, 128}; H_kv divides H, at most 128
- * query heads to one key/value head; min(n_seqs, T) * H_kv * max_pages *
- * page_size at most 2^43.  A token at a negative position gets
+ * query heads to one key/value head; T and n_seqs at most 2^24, max_pages *
+ * page_size at most 2^29, and min(n_seqs, T) * H_kv * max_pages * page_size at
+ * most 2^43.  A token at a negative position gets
  * O = 0 and LSE = -inf.  What lies in a page behind a sequence's last token may
  * be anything, NaN included; what a sequence's tokens hold must be finite.
  * max_new: no sequence has more new tokens.  max_len: how long the sequences

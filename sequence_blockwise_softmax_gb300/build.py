@@ -142,11 +142,16 @@ def build(force=False, verbose=False, extra_flags=()):
     return LIB
 
 
-if __name__ == "__main__":
-    v = "-v" in sys.argv
-    flags = ["-Xptxas", "-v"] if v else []
+def main(argv):
+    """For callers from C: the library's path; a binding that cannot be built is only reported."""
+    v = "-v" in argv
     try:
-        print(build(force=True, verbose=v, extra_flags=flags))
+        build(force=True, verbose=v, extra_flags=["-Xptxas", "-v"] if v else [])
     except BindingError as e:
-        print(LIB)
-        sys.exit("the library is built, the torch binding is not: %s" % e)
+        print("the library is built, the torch binding is not: %s" % e, file=sys.stderr)
+    print(LIB)
+    return 0
+
+
+if __name__ == "__main__":
+    sys.exit(main(sys.argv[1:]))

@@ -55,6 +55,14 @@ def test_the_library_does_not_need_the_binding(build, tmp_path, monkeypatch):
     assert os.path.exists(build.LIB)
 
 
+def test_the_command_line_builds_the_library(build, tmp_path, monkeypatch, capsys):
+    without_gxx(tmp_path, monkeypatch)
+    assert build.main([]) == 0
+    out, err = capsys.readouterr()
+    assert out.split() == [build.LIB] and os.path.exists(build.LIB)
+    assert "no such header" in err
+
+
 def test_the_library_does_not_need_torch(build, monkeypatch):
     monkeypatch.setitem(sys.modules, "torch", None)         # import torch raises ImportError
     with pytest.raises(RuntimeError, match="torch"):
