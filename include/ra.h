@@ -102,6 +102,8 @@ typedef enum {
 /* ra_window_attn_bwd: dq, dk and dv are bf16 (rounded once, to nearest even,
  * from the fp32 accumulators) instead of fp32. */
 #define RA_FLAG_GRAD_BF16 8u
+/* ra_paged_append_rotary: neighbouring columns 2 m and 2 m + 1 turn together. */
+#define RA_FLAG_ROTARY_PAIRS 16u
 /* Test hook for the timeout path: the first CTA of the fused sweep (or of
  * the first step of ra_ring_attn_fwd_stepwise_noalloc) never loads one key tile, so the waits that depend on it run out after about two
  * seconds; the kernel records RA_ERR_TIMEOUT in the status word, releases what
@@ -451,12 +453,98 @@ RA_API ra_status ra_paged_append(const void *k_new, const void *v_new, void *k_p
                                  size_t workspace_bytes, void *stream);
 
 /*
+ * Trees of new tokens (drafts of several continuations, checked in one pass).
+ * parents: int32 [T] beside cu: row i of a sequence's n new rows follows its row
+ * parents[cu[s] + i], one of 0 .. i - 1, or with -1 the c = seq_lens[s] - n tokens
+ * that the cache held before.  A row lies at place c + i of the cache and stands
+ * at position c + depth, its depth the number of its ancestors (several rows may
+ * stand at one position).  At most 1024 new rows to a sequence.  parents may
+ * change between replays of a captured call.  What it may not hold counts as -1,
+ * and ra_check_status() returns RA_ERR_INVALID_ARG.
+ */
+
+/*
+ * ra_paged_tree_attn_fwd -- ra_paged_attn_fwd for trees: a row sees the c tokens
+ * before the new ones, its ancestors and itself; with window > 0 those of them
+ * whose position is above its own minus window or below sinks.  The rest as
+ * there: the cache holds the new rows' keys and values already, at places c + i.
+ * max_new is at most 1024 (else RA_ERR_UNSUPPORTED).  A row whose place is
+ * negative (more new rows than the sequence is long) sees what of its ancestors
+ * lies in the cache; one that sees nothing gets O = 0 and LSE = -inf.
+ * workspace: ra_paged_tree_attn_workspace_bytes() bytes, under the terms of
+ * ra_paged_attn_fwd's.
+ */
+RA_API ra_status ra_paged_tree_attn_fwd(const void *q, const void *k_pages, const void *v_pages,
+                                        const int32_t *block_table, const int32_t *seq_lens,
+                                        const int32_t *cu_q, const int32_t *parents, void *o, float *lse,
+                                        int64_t T, int64_t n_seqs, int64_t H, int64_t H_kv, int d,
+                                        int64_t n_pages, int64_t page_size, int64_t page_stride,
+                                        int64_t max_pages, int64_t q_stride, int64_t max_new,
+                                        int64_t max_len, int64_t window, int64_t sinks, float scale,
+                                        unsigned flags, void *workspace, size_t workspace_bytes,
+                                        void *stream);
+
+/* Workspace bytes ra_paged_tree_attn_fwd needs (0 on bad arguments); at most 64 MiB. */
+RA_API size_t ra_paged_tree_attn_workspace_bytes(int64_t T, int64_t n_seqs, int64_t H, int64_t H_kv, int d,
+                                                 int64_t max_new, int64_t max_len, int64_t window,
+                                                 int64_t sinks);
+
+/*
+ * ra_paged_append_rotary -- ra_paged_append with the position rotation applied on
+ * the way, to the keys and to the call's queries.  At position p the pair (x, y)
+ * number m of each head's first `rot` columns becomes
+ *   (x cos(p f) - y sin(p f), x sin(p f) + y cos(p f)),  f = inv_freq[m],
+ * the pair being columns m and m + rot / 2, or 2 m and 2 m + 1 with
+ * RA_FLAG_ROTARY_PAIRS; the other columns, and the values, are copied.  The angle
+ * is taken modulo one turn exactly enough for any position (off by 1e-7 of a
+ * radian at most for f <= 1), the rotation computed in fp32 and rounded once.
+ * p is the token's place, seq_lens[s] - n + i, or with parents (else NULL) its
+ * position in a tree.
+ * q: bf16 [T, H, d] with q_stride elements from token to token, q_out: bf16 [T, H,
+ * d] with q_out_stride, or q itself; rows of no sequence are left as they were.  H
+ * = 0: no queries (q, q_out may be NULL).  inv_freq: fp32 [rot / 2] on the device,
+ * finite; rot: a multiple of 16, at most d.  flags: 0 or RA_FLAG_ROTARY_PAIRS.
+ * The rest as ra_paged_append.
+ */
+RA_API ra_status ra_paged_append_rotary(const void *q, const void *k_new, const void *v_new, void *q_out,
+                                        void *k_pages, void *v_pages, const int32_t *block_table,
+                                        const int32_t *seq_lens, const int32_t *cu_new,
+                                        const int32_t *parents, const float *inv_freq, int64_t T,
+                                        int64_t n_seqs, int64_t H, int64_t H_kv, int d, int rot,
+                                        int64_t n_pages, int64_t page_size, int64_t page_stride,
+                                        int64_t max_pages, int64_t q_stride, int64_t q_out_stride,
+                                        int64_t new_stride, unsigned flags, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+
+/*
+ * ra_paged_keep_path -- keep of each sequence's tree of new rows the path from a
+ * root to row last[s] (-1: nothing) in the cache: the path's j-th row moves to
+ * place c + j in every layer, where its position (and its rotation) has it.
+ * new_lens: int32 [n_seqs], receives c + the path's length; the places from there
+ * on hold anything.  path: int32 [T] or NULL, receives the rows of q that stay,
+ * cu[s] + the j-th row's number at cu[s] + j, and -1 behind them.  Layer l's pages
+ * begin l * layer_stride elements behind k_pages and v_pages (one pool after
+ * another, or side by side within page_stride; any value for n_layers = 1), and all
+ * layers have one block table.  Pages with new rows belong to one sequence each.
+ * A last[s] outside -1 .. n - 1, or a page outside the pool, moves nothing (of that
+ * row), and ra_check_status() returns RA_ERR_INVALID_ARG.  new_lens must not
+ * overlap seq_lens.  workspace: RA_WORKSPACE_MIN_BYTES bytes, zero-filled before
+ * its first use.
+ */
+RA_API ra_status ra_paged_keep_path(void *k_pages, void *v_pages, const int32_t *block_table,
+                                    const int32_t *seq_lens, const int32_t *cu_new, const int32_t *parents,
+                                    const int32_t *last, int32_t *new_lens, int32_t *path, int64_t T,
+                                    int64_t n_seqs, int64_t n_layers, int64_t H_kv, int d, int64_t n_pages,
+                                    int64_t page_size, int64_t page_stride, int64_t layer_stride,
+                                    int64_t max_pages, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * ra_check_status -- synchronise `stream`, read the status word at the start
  * of `workspace`, clear it, and return RA_ERR_TIMEOUT if a kernel recorded a
  * timeout since the last check, RA_ERR_ALIGNMENT if a kernel found its
  * dynamic shared memory base not 1024-byte aligned (it then computed
- * nothing), RA_ERR_INVALID_ARG if a paged call met a page outside the pool or
- * counts outside its bounds, RA_OK otherwise.
+ * nothing), RA_ERR_INVALID_ARG if a paged call met a page outside the pool,
+ * counts outside its bounds or a tree that is none, RA_OK otherwise.
  */
 RA_API ra_status ra_check_status(void *workspace, void *stream);
 

@@ -27,6 +27,7 @@ RA_FLAG_STEPWISE = 1
 RA_FLAG_O_BF16 = 2
 RA_FLAG_SEQ_ORDER = 4
 RA_FLAG_GRAD_BF16 = 8
+RA_FLAG_ROTARY_PAIRS = 16
 RA_FLAG_INJECT_STALL = 0x80000000
 RA_WORKSPACE_MIN_BYTES = 256
 LAYOUTS = {"contiguous": RA_CONTIGUOUS, "striped": RA_STRIPED, "zigzag": RA_ZIGZAG}
@@ -66,6 +67,13 @@ SIGNATURES = {
     "ra_paged_attn_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I, _I64, _I64, _I64, _I64]),
     "ra_paged_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I64, _I64, _I64, _I64, _I64, _P, _SZ,
                              _P]),
+    "ra_paged_tree_attn_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _I64, _I64, _I64,
+                                    _I64, _I64, _I64, _I64, _I64, _I64, _F, _U, _P, _SZ, _P]),
+    "ra_paged_tree_attn_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I, _I64, _I64, _I64, _I64]),
+    "ra_paged_append_rotary": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _I64,
+                                    _I64, _I64, _I64, _I64, _I64, _I64, _U, _P, _SZ, _P]),
+    "ra_paged_keep_path": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _I64, _I64, _I64, _I64,
+                                _I64, _P, _SZ, _P]),
     "ra_check_status": (_I, [_P, _P]),
     "ra_last_error": (ctypes.c_char_p, []),
     "ra_version": (ctypes.c_char_p, []),
@@ -119,7 +127,8 @@ def native():
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         module.bind(*[ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
-                      for name in ("ra_window_attn_fwd", "ra_window_attn_bwd", "ra_paged_attn_fwd", "ra_paged_append")])
+                      for name in ("ra_window_attn_fwd", "ra_window_attn_bwd", "ra_paged_attn_fwd", "ra_paged_append",
+                                  "ra_paged_tree_attn_fwd", "ra_paged_append_rotary", "ra_paged_keep_path")])
         _native = module
     return _native
 
@@ -349,6 +358,37 @@ def ra_paged_append(k_new, v_new, k_pages, v_pages, block_table, seq_lens, cu_ne
     """Copy new keys and values [T, H_kv, d] (tokens may be strided) to their places in the cache."""
     _check((_native or native()).append(k_new, v_new, k_pages, v_pages, block_table, seq_lens, cu_new, workspace,
                                         _raw_stream(stream)))
+
+
+def ra_paged_tree_attn_workspace_bytes(T, n_seqs, H, H_kv, d, max_new, max_len, window=0, sinks=0):
+    return int(lib().ra_paged_tree_attn_workspace_bytes(T, n_seqs, H, H_kv, d, max_new, max_len, window, sinks))
+
+
+def ra_paged_tree_attn_fwd(q, k_pages, v_pages, block_table, seq_lens, cu_q, parents, o, lse, max_new, max_len, window=0,
+                           sinks=0, scale=0.0, workspace=None, stream=None):
+    """ra_paged_attn_fwd for trees of new tokens: each sees the tokens before the new ones, its ancestors
+    and itself.  ``parents``: int32 [T], the number of a row's parent among its sequence's rows, or -1."""
+    _check((_native or native()).tree_fwd(q, k_pages, v_pages, block_table, seq_lens, cu_q, parents, o, lse, max_new,
+                                          max_len, window, sinks, scale, workspace, _raw_stream(stream)))
+
+
+def ra_paged_append_rotary(q, k_new, v_new, q_out, k_pages, v_pages, block_table, seq_lens, cu_new, inv_freq, parents=None,
+                           pairs=False, workspace=None, stream=None):
+    """ra_paged_append with the keys, and the queries q [T, H, d] into q_out (or q itself), rotated by their
+    positions; q and q_out may be None.  ``inv_freq``: fp32, an angle per position for each pair of the
+    first 2 * len(inv_freq) columns; ``parents``: the new tokens are trees (see ra_paged_tree_attn_fwd);
+    ``pairs``: neighbouring columns turn together, else those half of the rotated columns apart."""
+    _check((_native or native()).append_rotary(q, k_new, v_new, q_out, k_pages, v_pages, block_table, seq_lens, cu_new,
+                                               inv_freq, parents, pairs, workspace, _raw_stream(stream)))
+
+
+def ra_paged_keep_path(k_pages, v_pages, block_table, seq_lens, cu_new, parents, last, new_lens, path=None, workspace=None,
+                       stream=None):
+    """Keep the path to row ``last`` (int32 [n_seqs], -1: nothing) of each sequence's tree in the cache, one pool
+    [n_pages, page, H_kv, d] or the layers' [layers, n_pages, page, H_kv, d]; writes the sequences' lengths
+    then to ``new_lens`` and the rows that stay to ``path`` (int32 [T] or None)."""
+    _check((_native or native()).keep_path(k_pages, v_pages, block_table, seq_lens, cu_new, parents, last, new_lens, path,
+                                           workspace, _raw_stream(stream)))
 
 
 def ra_check_status(workspace, stream=None):

@@ -485,7 +485,7 @@ ra_status ra_check_status(void *workspace, void *stream) {
         if (word & ra::RA_DEV_SMEM_ALIGN_BIT)
             return fail(RA_ERR_ALIGNMENT, "a kernel found its dynamic shared memory base not 1024-byte aligned");
         if (word & ra::RA_DEV_PAGE_BIT)
-            return fail(RA_ERR_INVALID_ARG, "a paged call met a page outside the pool, or lengths outside its bounds");
+            return fail(RA_ERR_INVALID_ARG, "a paged call met a page outside the pool, lengths outside its bounds or a tree that is none");
     }
     return RA_OK;
 }

@@ -15,6 +15,7 @@
 #include <cmath>
 
 #include "attn_fwd_kernel.cuh"
+#include "paged_checks.h"
 #include "paged_launch.h"
 #include "ra_launch.h"
 #include "ra_tensor_map.h"
@@ -29,7 +30,6 @@ constexpr size_t kCounters = kHeader, kCounterBytes = 4096;   // the few-row ker
 static_assert(kPagedTokensCtas * 8 <= kCounterBytes, "one counter per CTA");
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
-bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // ------------------------------------------------------------------ join
 // O = sum_i w_i O_i, w_i = exp(LSE_i - LSE), over a row's parts in order, so
@@ -115,6 +115,8 @@ struct Paged {
     int64_t T, n_seqs, H, H_kv, n_pages, page, page_stride, max_pages, q_stride, max_new, max_len, window, sinks;
     int d;
     float scale;
+    const int *parents = nullptr;       // trees of new tokens
+    bool tree = false;
 };
 
 // How a call is cut: tokens per unit, the most parts per unit, the parts' bytes.
@@ -160,7 +162,7 @@ Plan plan(Paged a) {
         p.total = p.part_lse + round256(rows * 8);
         return p;
     }
-    if (group <= kPagedFewRows) {
+    if (group <= kPagedFewRows && !a.tree) {
         const int unit = (int)(kPagedFewRows / group);
         p.few_units = paged_units(a.T, a.n_seqs, unit);
         p.few_keys = a.max_len;
@@ -232,32 +234,6 @@ Plan plan(Paged a) {
     return p;
 }
 
-constexpr int64_t kMostStride = (int64_t)1 << 39;     // elements; a tensor map's strides stay below 2^40 bytes
-
-ra_status check_heads(int64_t H, int64_t H_kv, int d) {
-    if (d != 64 && d != 128) return set_error(RA_ERR_UNSUPPORTED, "head dimension d must be 64 or 128");
-    if (H_kv < 1 || H_kv > H || H % H_kv)
-        return set_error(RA_ERR_SHAPE, "the key/value head count must divide the query head count");
-    if (H / H_kv > 128) return set_error(RA_ERR_UNSUPPORTED, "at most 128 query heads per key/value head");
-    if (H > (int64_t)1 << 16) return set_error(RA_ERR_UNSUPPORTED, "H beyond the supported range");
-    return RA_OK;
-}
-
-ra_status check_cache(int64_t T, int64_t n_seqs, int64_t H_kv, int d, int64_t n_pages, int64_t page,
-                      int64_t page_stride, int64_t max_pages) {
-    if (T < 0 || n_seqs < 0 || n_pages < 0 || max_pages < 0) return set_error(RA_ERR_SHAPE, "sizes must be non-negative");
-    if (page < 16 || page > 65536 || (page & (page - 1)))
-        return set_error(RA_ERR_UNSUPPORTED, "page_size must be a power of two, at least 16 and at most 65536");
-    if (T > (int64_t)1 << 24 || n_seqs > (int64_t)1 << 24 || n_pages > (int64_t)1 << 30)
-        return set_error(RA_ERR_UNSUPPORTED, "tokens, sequences or pages beyond the supported range");
-    if (max_pages > ((int64_t)1 << 29) / page)
-        return set_error(RA_ERR_UNSUPPORTED, "max_pages * page_size beyond the supported range (2^29 tokens)");
-    if (page_stride < page * H_kv * d) return set_error(RA_ERR_SHAPE, "page_stride is smaller than a page: pages would overlap");
-    if (page_stride % 8) return set_error(RA_ERR_ALIGNMENT, "page_stride must be a multiple of 8 elements (16 bytes)");
-    if (page_stride >= kMostStride) return set_error(RA_ERR_UNSUPPORTED, "page_stride beyond the supported range");
-    return RA_OK;
-}
-
 ra_status check(const Paged &a) {
     ra_status st = check_heads(a.H, a.H_kv, a.d);
     if (st != RA_OK) return st;
@@ -323,6 +299,7 @@ PagedSeqs sequences(const Paged &a, const int *table, const int *seq_lens, const
     const int64_t cap = (int64_t)1 << 29;      // at least as long as any cache
     s.window = (int)(a.window < cap ? a.window : cap);
     s.sinks = (int)(a.sinks < cap ? a.sinks : cap);
+    s.parents = a.parents;
     return s;
 }
 
@@ -332,8 +309,8 @@ ra_status launch_chunks(const Paged &a, const Plan &p, const AttnArgs &args, con
     CUtensorMap mq, mk, mv;
     if (!query_map(&mq, q, a, p.tile_tokens) || !page_map(&mk, k, a, args.page_box) || !page_map(&mv, v, a, args.page_box))
         return set_error(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the q and page maps");
-    auto kern = attn_fwd_kernel<D, F32, false, KEYS_PAGED>;
-    const int smem = (int)AttnSmem<D>::kBytes;
+    int smem = (int)AttnSmem<D>::kBytes;
+    const AttnKernel kern = a.tree ? tree_chunk_kernel(D, F32, &smem) : attn_fwd_kernel<D, F32, false, KEYS_PAGED>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
     const int64_t grid = p.units * a.H_kv * p.splits;
@@ -495,8 +472,8 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
 
 extern "C" {
 
-size_t ra_paged_attn_workspace_bytes(int64_t T, int64_t n_seqs, int64_t H, int64_t H_kv, int d, int64_t max_new,
-                                     int64_t max_len, int64_t window, int64_t sinks) {
+static size_t workspace_bytes(int64_t T, int64_t n_seqs, int64_t H, int64_t H_kv, int d, int64_t max_new,
+                              int64_t max_len, int64_t window, int64_t sinks, bool tree) {
     if (T < 0 || n_seqs < 0 || max_new < 0 || max_len < 0 || window < 0 || sinks < 0 || H_kv < 1 || H < H_kv ||
         H % H_kv || H / H_kv > 128 || H > (int64_t)1 << 16 || (d != 64 && d != 128) || T > (int64_t)1 << 24 ||
         n_seqs > (int64_t)1 << 24)
@@ -504,23 +481,32 @@ size_t ra_paged_attn_workspace_bytes(int64_t T, int64_t n_seqs, int64_t H, int64
     ra::Paged a{};
     a.T = T, a.n_seqs = n_seqs, a.H = H, a.H_kv = H_kv, a.d = d, a.max_new = max_new, a.max_len = max_len;
     a.window = window, a.sinks = sinks;
+    a.tree = tree;
     return ra::plan(a).total;
 }
 
-ra_status ra_paged_attn_fwd(const void *q, const void *k_pages, const void *v_pages, const int32_t *block_table,
-                            const int32_t *seq_lens, const int32_t *cu_q, void *o, float *lse, int64_t T,
-                            int64_t n_seqs, int64_t H, int64_t H_kv, int d, int64_t n_pages, int64_t page_size,
-                            int64_t page_stride, int64_t max_pages, int64_t q_stride, int64_t max_new,
-                            int64_t max_len, int64_t window, int64_t sinks, float scale, unsigned flags,
-                            void *workspace, size_t workspace_bytes, void *stream) {
+size_t ra_paged_attn_workspace_bytes(int64_t T, int64_t n_seqs, int64_t H, int64_t H_kv, int d, int64_t max_new,
+                                     int64_t max_len, int64_t window, int64_t sinks) {
+    return workspace_bytes(T, n_seqs, H, H_kv, d, max_new, max_len, window, sinks, false);
+}
+
+size_t ra_paged_tree_attn_workspace_bytes(int64_t T, int64_t n_seqs, int64_t H, int64_t H_kv, int d, int64_t max_new,
+                                          int64_t max_len, int64_t window, int64_t sinks) {
+    if (max_new > ra::kTreeMost) return 0;
+    return workspace_bytes(T, n_seqs, H, H_kv, d, max_new, max_len, window, sinks, true);
+}
+
+static ra_status attend(const ra::Paged &a, const void *q, const void *k_pages, const void *v_pages, const int32_t *block_table,
+                        const int32_t *seq_lens, const int32_t *cu_q, void *o, float *lse, unsigned flags,
+                        void *workspace, size_t workspace_bytes, void *stream) {
     using namespace ra;
     if (flags & ~RA_FLAG_O_BF16) return set_error(RA_ERR_INVALID_ARG, "unknown flag bits");
-    Paged a{T, n_seqs, H, H_kv, n_pages, page_size, page_stride, max_pages, q_stride, max_new, max_len, window, sinks,
-            d, scale};
     const ra_status st = check(a);
     if (st != RA_OK) return st;
-    if (T == 0 || n_seqs == 0 || max_new == 0) return RA_OK;
-    if (n_pages == 0 || max_pages == 0) return set_error(RA_ERR_SHAPE, "new tokens need pages to lie in");
+    if (a.tree && a.max_new > kTreeMost)
+        return set_error(RA_ERR_UNSUPPORTED, "a tree of more than 1024 new tokens");
+    if (a.T == 0 || a.n_seqs == 0 || a.max_new == 0) return RA_OK;
+    if (a.n_pages == 0 || a.max_pages == 0) return set_error(RA_ERR_SHAPE, "new tokens need pages to lie in");
     const void *ptrs[] = {q, k_pages, v_pages, o, workspace};
     for (const void *p : ptrs) {
         if (!p) return set_error(RA_ERR_INVALID_ARG, "null pointer argument");
@@ -532,15 +518,40 @@ ra_status ra_paged_attn_fwd(const void *q, const void *k_pages, const void *v_pa
         if (!aligned(p, 4)) return set_error(RA_ERR_ALIGNMENT, "block_table, seq_lens and cu_q must be 4-byte aligned");
     }
     if (!aligned(lse, 4)) return set_error(RA_ERR_ALIGNMENT, "lse must be 4-byte aligned");
+    if (a.tree && !a.parents) return set_error(RA_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned(a.parents, 4)) return set_error(RA_ERR_ALIGNMENT, "parents must be 4-byte aligned");
     // a CTA of the few-row form counts its 16-key chunks in 31 bits
-    const int64_t active = n_seqs < T ? n_seqs : T;
-    if ((double)(active * H_kv) * (double)(max_pages * page_size) > 0x1p43)
+    const int64_t active = a.n_seqs < a.T ? a.n_seqs : a.T;
+    if ((double)(active * a.H_kv) * (double)(a.max_pages * a.page) > 0x1p43)
         return set_error(RA_ERR_UNSUPPORTED, "sequences * H_kv * max_pages * page_size beyond the supported range (2^43)");
     if (workspace_bytes < plan(a).total)
-        return set_error(RA_ERR_INVALID_ARG, "workspace smaller than ra_paged_attn_workspace_bytes()");
-    auto launch = d == 128 ? launch_paged<128> : launch_paged<64>;
+        return set_error(RA_ERR_INVALID_ARG, a.tree ? "workspace smaller than ra_paged_tree_attn_workspace_bytes()"
+                                                    : "workspace smaller than ra_paged_attn_workspace_bytes()");
+    auto launch = a.d == 128 ? launch_paged<128> : launch_paged<64>;
     return launch(a, block_table, seq_lens, cu_q, q, k_pages, v_pages, o, lse, (flags & RA_FLAG_O_BF16) != 0,
                   static_cast<uint8_t *>(workspace), static_cast<cudaStream_t>(stream));
+}
+
+ra_status ra_paged_attn_fwd(const void *q, const void *k_pages, const void *v_pages, const int32_t *block_table,
+                            const int32_t *seq_lens, const int32_t *cu_q, void *o, float *lse, int64_t T,
+                            int64_t n_seqs, int64_t H, int64_t H_kv, int d, int64_t n_pages, int64_t page_size,
+                            int64_t page_stride, int64_t max_pages, int64_t q_stride, int64_t max_new,
+                            int64_t max_len, int64_t window, int64_t sinks, float scale, unsigned flags,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+    const ra::Paged a{T, n_seqs, H, H_kv, n_pages, page_size, page_stride, max_pages, q_stride, max_new, max_len, window,
+                      sinks, d, scale};
+    return attend(a, q, k_pages, v_pages, block_table, seq_lens, cu_q, o, lse, flags, workspace, workspace_bytes, stream);
+}
+
+ra_status ra_paged_tree_attn_fwd(const void *q, const void *k_pages, const void *v_pages, const int32_t *block_table,
+                                 const int32_t *seq_lens, const int32_t *cu_q, const int32_t *parents, void *o,
+                                 float *lse, int64_t T, int64_t n_seqs, int64_t H, int64_t H_kv, int d, int64_t n_pages,
+                                 int64_t page_size, int64_t page_stride, int64_t max_pages, int64_t q_stride,
+                                 int64_t max_new, int64_t max_len, int64_t window, int64_t sinks, float scale,
+                                 unsigned flags, void *workspace, size_t workspace_bytes, void *stream) {
+    const ra::Paged a{T, n_seqs, H, H_kv, n_pages, page_size, page_stride, max_pages, q_stride, max_new, max_len, window,
+                      sinks, d, scale, parents, true};
+    return attend(a, q, k_pages, v_pages, block_table, seq_lens, cu_q, o, lse, flags, workspace, workspace_bytes, stream);
 }
 
 ra_status ra_paged_append(const void *k_new, const void *v_new, void *k_pages, void *v_pages,

@@ -28,6 +28,7 @@ struct PagedSeqs {
     int window, sinks;      // window 0: none
     int num_splits;         // most parts a unit's keys are cut into
     int tail_share;         // 0, or 1024ths of the keys in the last, shorter part
+    const int *parents;     // [T], trees of new tokens (see tree_parent), or null: one token after another
 };
 
 // A unit: tokens [t0, t0 + n) of q, at positions p0 .. p0 + n - 1 of sequence
@@ -79,8 +80,14 @@ RA_HD PagedUnit paged_unit(const PagedSeqs &q, int s, int local) {
 // The keys of the token at position p (a negative position sees none).
 RA_HD RowKeys paged_row(const PagedSeqs &q, int p) { return window_row_keys(0, p, q.window, q.sinks); }
 
+// The keys that bound a unit's: its first row's, or with trees, whose rows all
+// stand at the first new token's position or behind it, those of a row there.
+RA_HD RowKeys paged_first_row(const PagedSeqs &q, const PagedUnit &u) {
+    return paged_row(q, q.parents ? u.p0 - u.first : u.p0);
+}
+
 RA_HD RangeWalk paged_walk(const PagedSeqs &q, const PagedUnit &u) {
-    return range_walk(paged_row(q, u.p0), u.p0 + u.n);
+    return range_walk(paged_first_row(q, u), u.p0 + u.n);
 }
 
 // Whether sequence s breaks the call's bounds: more new tokens than max_new or
@@ -169,6 +176,102 @@ RA_HD int64_t paged_tally_chunks(uint64_t sum) {
 // The first key of chunk number c.
 RA_HD int paged_chunk_key(const PagedChunks &l, int c) {
     return (c < l.n_sink ? c : l.m0 + (c - l.n_sink)) * kPagedChunk;
+}
+
+// Trees of new tokens.  Row i of a sequence follows row parents[cu[s] + i] < i
+// of the same sequence, or with -1 the c = seq_lens[s] - n tokens before the
+// new ones.  It lies at place c + i of the cache and stands at position c +
+// depth, its depth the number of its ancestors; it sees the c tokens, its
+// ancestors and itself, of which a window leaves those less than `window`
+// positions away and the sinks.  A chain of ancestors has falling numbers and
+// positions, so what a window leaves of it are its first `window` nodes from
+// the row up, and as many at the other end as stand before the sinks' end.
+constexpr int kTreeMost = 1024;     // new tokens of a sequence
+
+// Row i's parent; what is none of -1 .. i - 1 counts as -1 and is `bad`.
+RA_HD int tree_parent(const int *parents, int t0, int i, bool &bad) {
+    const int p = parents[t0 + i];
+    if (p >= -1 && p < i) return p;
+    bad = true;
+    return -1;
+}
+
+// What the row at position p sees of the c tokens before the new ones.
+RA_HD RowKeys tree_row(const PagedSeqs &q, int p, int c) {
+    RowKeys r = paged_row(q, p);
+    if (r.hi > c) r.hi = c;
+    if (r.shi > c) r.shi = c;
+    return r;
+}
+
+// What a window leaves of a chain given as the bits of its nodes, of at most
+// 32: the `window` highest, and the lowest `near` (nodes before the sinks' end).
+RA_HD uint32_t tree_window(uint32_t chain, int window, int near) {
+    int n = 0;
+    for (uint32_t x = chain; x; x &= x - 1) ++n;
+    uint32_t keep = 0;
+    for (int i = 0; i < n - window; ++i) {
+        const uint32_t low = chain & (0u - chain);
+        chain ^= low;
+        if (i < near) keep |= low;
+    }
+    return chain | keep;
+}
+
+// A row's chain walked up as its unit's key tiles go down.
+struct TreeChain {
+    int at, steps;      // the node next in turn (-1: none left), its distance from the row
+    int window, far;    // nodes of a distance below `window` or above `far` are seen
+
+    // row `node` with `depth` ancestors; window 0: none (depth is then not used)
+    RA_HD void start(int node, int depth, int c, int win, int sinks) {
+        at = node;
+        steps = 0;
+        window = win > 0 ? win : 0x7fffffff;
+        far = win > 0 ? c + depth - sinks : 0x7fffffff;
+    }
+    // the seen nodes of [base, base + 128), bit i & 31 of word i >> 5 for node base + i
+    template <class Parent>
+    RA_HD void tile(const Parent *parents, int base, uint32_t (&word)[4]) {
+        word[0] = word[1] = word[2] = word[3] = 0;
+        while (at >= 0 && at >= base) {
+            const int i = at - base;
+            if (i < 128 && (steps < window || steps > far)) {
+                const uint32_t bit = 1u << (i & 31);
+                word[0] |= i < 32 ? bit : 0u;
+                word[1] |= i >= 32 && i < 64 ? bit : 0u;
+                word[2] |= i >= 64 && i < 96 ? bit : 0u;
+                word[3] |= i >= 96 ? bit : 0u;
+            }
+            at = parents[at];
+            ++steps;
+        }
+    }
+};
+
+// The key tiles of a unit of tree rows: the main ones from the last down, then
+// the sinks'.
+struct TreeWalk {
+    int i, end, n_main, last, s0;
+    int tile, j;
+
+    RA_HD_STEP void seek() { tile = i < n_main ? last - i : s0 + (i - n_main); }
+    RA_HD_STEP void start_step() { seek(); }
+    RA_HD_STEP bool valid() const { return i < end; }
+    RA_HD_STEP void next() {
+        ++i;
+        seek();
+    }
+};
+RA_HD TreeWalk tree_walk(const RangeWalk &r) {
+    TreeWalk w;
+    w.i = r.i;
+    w.end = r.end;
+    w.n_main = r.end - r.n_sink;
+    w.last = r.m0 + w.n_main - 1;
+    w.s0 = r.s0;
+    w.tile = w.j = 0;
+    return w;
 }
 
 }  // namespace ra

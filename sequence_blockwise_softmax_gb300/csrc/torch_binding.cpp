@@ -134,6 +134,9 @@ decltype(&ra_window_attn_fwd) window_fwd_fn;
 decltype(&ra_window_attn_bwd) window_bwd_fn;
 decltype(&ra_paged_attn_fwd) paged_fwd_fn;
 decltype(&ra_paged_append) append_fn;
+decltype(&ra_paged_tree_attn_fwd) tree_fwd_fn;
+decltype(&ra_paged_append_rotary) append_rotary_fn;
+decltype(&ra_paged_keep_path) keep_path_fn;
 
 template <class F>
 PyObject *guarded(Py_ssize_t got, Py_ssize_t want, F f) {
@@ -198,8 +201,12 @@ struct Pool {
     int64_t n_pages, page, Hkv, d, stride;
 };
 bool gapless(const at::Tensor &t) { return t.is_contiguous() || (t.size(0) > 0 && t.select(0, 0).is_contiguous()); }
-Pool pool(PyObject *ko, PyObject *vo) {
-    const at::Tensor &k = tensor(ko, "k_pages"), &v = tensor(vo, "v_pages");
+// ... and of the layers [layers, n_pages, page, H_kv, d] with one layer stride, or of one pool.
+struct Layers {
+    Pool pool;
+    int64_t n, stride;
+};
+Pool pool_of(const at::Tensor &k, const at::Tensor &v) {
     if (k.dim() != 4 || v.sizes() != k.sizes())
         refuse(PyExc_ValueError, "k_pages and v_pages must have one shape, [n_pages, page, H_kv, d]");
     Pool p{k.data_ptr(), v.data_ptr(), k.size(0), k.size(1), k.size(2), k.size(3), 0};
@@ -207,6 +214,14 @@ Pool pool(PyObject *ko, PyObject *vo) {
     if (!gapless(k) || !gapless(v) || (p.n_pages > 1 && v.stride(0) != p.stride))
         refuse(PyExc_ValueError, "k_pages and v_pages: a page must be contiguous, and both pools have one page stride");
     return p;
+}
+Pool pool(PyObject *ko, PyObject *vo) { return pool_of(tensor(ko, "k_pages"), tensor(vo, "v_pages")); }
+Layers layers(PyObject *ko, PyObject *vo) {
+    const at::Tensor &k = tensor(ko, "k_pages"), &v = tensor(vo, "v_pages");
+    if (k.dim() != 5) return {pool_of(k, v), 1, 0};
+    if (v.sizes() != k.sizes() || k.size(0) < 1 || (k.size(0) > 1 && v.stride(0) != k.stride(0)))
+        refuse(PyExc_ValueError, "k_pages and v_pages must have one shape and layer stride, and a layer at least");
+    return {pool_of(k.select(0, 0), v.select(0, 0)), k.size(0), k.size(0) > 1 ? k.stride(0) : 0};
 }
 
 int pool_device(PyObject *first, const char *name, PyObject *ko, PyObject *vo) {
@@ -277,13 +292,104 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// The addresses of ra_window_attn_fwd, ra_window_attn_bwd, ra_paged_attn_fwd, ra_paged_append
+const int32_t *vector(PyObject *o, const char *name, int dev, int64_t n) {
+    return static_cast<const int32_t *>(contiguous(o, name, kI32, dev, {n}));
+}
+
+// q, k_pages, v_pages, block_table, seq_lens, cu_q, parents, o, lse, max_new, max_len, window, sinks, scale, workspace,
+// stream
+PyObject *tree_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 16, [&] {
+        const at::Tensor &q = tensor(a[0], "q");
+        const Pool p = pool(a[1], a[2]);
+        const int dev = pool_device(a[0], "q", a[1], a[2]);
+        if (q.dim() != 3) refuse(PyExc_ValueError, "q must be [T, H, d]");
+        const int64_t T = q.size(0), H = q.size(1);
+        const int64_t q_stride = token_stride(q, "q", H, p.d, dev);
+        const Sequences s = sequences(a[3], a[4], a[5], "cu_q", dev);
+        const int32_t *parents = vector(a[6], "parents", dev, T);
+        void *o = contiguous(a[7], "o", kBF16 | kF32, dev, {T, H, p.d});
+        void *lse = a[8] == Py_None ? nullptr : contiguous(a[8], "lse", kF32, dev, {H, T});
+        const Workspace ws = workspace(a[14], dev);
+        if (p.d != (int)p.d) refuse(PyExc_ValueError, "d does not fit in 32 bits");
+        return tree_fwd_fn(q.data_ptr(), p.k, p.v, s.table, s.lens, s.cu, parents, o, static_cast<float *>(lse), T, s.n, H,
+                           p.Hkv, (int)p.d, p.n_pages, p.page, p.stride, s.max_pages, q_stride, integer(a[9]),
+                           integer(a[10]), integer(a[11]), integer(a[12]), real(a[13]),
+                           type_of(tensor(a[7], "o")) == kBF16 ? RA_FLAG_O_BF16 : 0, ws.ptr, ws.bytes, stream_of(a[15]));
+    });
+}
+
+// q, k_new, v_new, q_out, k_pages, v_pages, block_table, seq_lens, cu_new, inv_freq, parents, pairs, workspace, stream
+PyObject *append_rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 14, [&] {
+        const at::Tensor &k = tensor(a[1], "k_new"), &v = tensor(a[2], "v_new");
+        const Pool p = pool(a[4], a[5]);
+        const int dev = pool_device(a[1], "k_new", a[4], a[5]);
+        const int64_t T = k.dim() > 0 ? k.size(0) : 0, stride = token_stride(k, "k_new", p.Hkv, p.d, dev);
+        if (v.sizes() != k.sizes() || token_stride(v, "v_new", p.Hkv, p.d, dev) != stride)
+            refuse(PyExc_ValueError, "k_new and v_new must have one shape and token stride");
+        int64_t H = 0, q_stride = 0, out_stride = 0;
+        void *q = nullptr, *q_out = nullptr;
+        if ((a[0] == Py_None) != (a[3] == Py_None)) refuse(PyExc_ValueError, "q and q_out are given both or neither");
+        if (a[0] != Py_None) {
+            const at::Tensor &x = tensor(a[0], "q"), &y = tensor(a[3], "q_out");
+            if (x.dim() != 3 || x.size(0) != T || y.sizes() != x.sizes())
+                refuse(PyExc_ValueError, "q and q_out must be [T, H, d] with k_new's T");
+            H = x.size(1);
+            q_stride = token_stride(x, "q", H, p.d, dev);
+            out_stride = token_stride(y, "q_out", H, p.d, dev);
+            q = x.data_ptr();
+            q_out = y.data_ptr();
+        }
+        const Sequences s = sequences(a[6], a[7], a[8], "cu_new", dev);
+        const at::Tensor &f = tensor(a[9], "inv_freq");
+        if (f.dim() != 1) refuse(PyExc_ValueError, "inv_freq must be a vector");
+        const void *freq = contiguous(a[9], "inv_freq", kF32, dev, {f.size(0)});
+        const int32_t *parents = a[10] == Py_None ? nullptr : vector(a[10], "parents", dev, T);
+        const int pairs = PyObject_IsTrue(a[11]);
+        if (pairs < 0) throw Refused();
+        const Workspace ws = workspace(a[12], dev);
+        if (p.d != (int)p.d || f.size(0) > p.d) refuse(PyExc_ValueError, "d or inv_freq is too large");
+        return append_rotary_fn(q, k.data_ptr(), v.data_ptr(), q_out, p.k, p.v, s.table, s.lens, s.cu, parents,
+                                static_cast<const float *>(freq), T, s.n, H, p.Hkv, (int)p.d, (int)(2 * f.size(0)),
+                                p.n_pages, p.page, p.stride, s.max_pages, q_stride, out_stride, stride,
+                                pairs ? RA_FLAG_ROTARY_PAIRS : 0, ws.ptr, ws.bytes, stream_of(a[13]));
+    });
+}
+
+// k_pages, v_pages, block_table, seq_lens, cu_new, parents, last, new_lens, path, workspace, stream
+PyObject *keep_path(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 11, [&] {
+        const Layers l = layers(a[0], a[1]);
+        const Pool &p = l.pool;
+        const int dev = pool_device(a[0], "k_pages", a[0], a[1]);
+        const Sequences s = sequences(a[2], a[3], a[4], "cu_new", dev);
+        const at::Tensor &t = tensor(a[5], "parents");
+        if (t.dim() != 1) refuse(PyExc_ValueError, "parents must be a vector");
+        const int64_t T = t.size(0);
+        const int32_t *parents = vector(a[5], "parents", dev, T);
+        const int32_t *last = vector(a[6], "last", dev, s.n);
+        const int32_t *lens = vector(a[7], "new_lens", dev, s.n);
+        const int32_t *path = a[8] == Py_None ? nullptr : vector(a[8], "path", dev, T);
+        const Workspace ws = workspace(a[9], dev);
+        if (p.d != (int)p.d) refuse(PyExc_ValueError, "d does not fit in 32 bits");
+        return keep_path_fn(p.k, p.v, s.table, s.lens, s.cu, parents, last, const_cast<int32_t *>(lens),
+                            const_cast<int32_t *>(path), T, s.n, l.n, p.Hkv, (int)p.d, p.n_pages, p.page, p.stride,
+                            l.stride, s.max_pages, ws.ptr, ws.bytes, stream_of(a[10]));
+    });
+}
+
+// The addresses of ra_window_attn_fwd, ra_window_attn_bwd, ra_paged_attn_fwd, ra_paged_append,
+// ra_paged_tree_attn_fwd, ra_paged_append_rotary, ra_paged_keep_path
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 4, [&] {
+    return guarded(n, 7, [&] {
         window_fwd_fn = reinterpret_cast<decltype(window_fwd_fn)>((uintptr_t)integer(a[0]));
         window_bwd_fn = reinterpret_cast<decltype(window_bwd_fn)>((uintptr_t)integer(a[1]));
         paged_fwd_fn = reinterpret_cast<decltype(paged_fwd_fn)>((uintptr_t)integer(a[2]));
         append_fn = reinterpret_cast<decltype(append_fn)>((uintptr_t)integer(a[3]));
+        tree_fwd_fn = reinterpret_cast<decltype(tree_fwd_fn)>((uintptr_t)integer(a[4]));
+        append_rotary_fn = reinterpret_cast<decltype(append_rotary_fn)>((uintptr_t)integer(a[5]));
+        keep_path_fn = reinterpret_cast<decltype(keep_path_fn)>((uintptr_t)integer(a[6]));
         return 0;
     });
 }
@@ -296,6 +402,9 @@ PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                          {"window_bwd", fast(window_bwd), METH_FASTCALL, nullptr},
                          {"paged_fwd", fast(paged_fwd), METH_FASTCALL, nullptr},
                          {"append", fast(append), METH_FASTCALL, nullptr},
+                         {"tree_fwd", fast(tree_fwd), METH_FASTCALL, nullptr},
+                         {"append_rotary", fast(append_rotary), METH_FASTCALL, nullptr},
+                         {"keep_path", fast(keep_path), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "ra_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
