@@ -96,10 +96,7 @@ struct AttnArgs {
 // tokens over a paged cache (ra_paged.cuh): a unit's rows are the group of
 // query heads of up to 2 * tile_tokens tokens, its key tiles are gathered from
 // the block table's pages, and its tiles may be split over several CTAs.
-// KEYS_TREE: the same with a tree of new tokens (ra_paged.cuh): the tiles are
-// taken from the last down, so that each row walks its ancestors once, from
-// itself up, and makes of those that lie in a tile the bits of their columns.
-enum KeySet { KEYS_RING = 0, KEYS_WINDOW = 1, KEYS_PAGED = 2, KEYS_TREE = 3 };
+enum KeySet { KEYS_RING = 0, KEYS_WINDOW = 1, KEYS_PAGED = 2 };
 
 // The sequence of unit u, searched by a whole warp: 32 probes at a time.
 __device__ __forceinline__ int paged_find_seq_warp(const PagedSeqs &q, int u, int lane) {
@@ -135,10 +132,6 @@ __device__ __forceinline__ int paged_sorted_unit(const PagedSeqs &q, int n_units
     return mine ? __shfl_sync(0xffffffffu, local, seq) : -1;
 }
 
-using AttnKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, AttnArgs);
-// The tensor-core form for trees (attn_paged_tree.cu) and its shared memory.
-AttnKernel tree_chunk_kernel(int d, bool f32, int *smem);
-
 __device__ __forceinline__ void record_timeout(unsigned *status, volatile int *abort) {
     *abort = 1;
     atomicOr(status, RA_DEV_TIMEOUT_BIT);
@@ -171,8 +164,6 @@ struct AttnSmem {
     // dynamic base, which is what leaves room for P
     static constexpr uint32_t kBytes = kMisc + 16;
     static constexpr uint32_t kBytesSkip = kTab + kMaxSteps * 6 * 4;
-    // the tree form keeps its sequence's parents there, two bytes a node
-    static constexpr uint32_t kBytesTree = kTab + kTreeMost * 2;
 };
 
 // The key tiles of a unit's walk as the tile-skipping variant sees them: the
@@ -250,10 +241,8 @@ __global__ void __launch_bounds__(384, 1)
     constexpr uint32_t LOW_REGS = TWO_ISSUERS ? 72u : 64u;
     static_assert(!SKIP || TWO_ISSUERS, "tile skipping is built on the two-issuer pipeline");
     static_assert(!SKIP || KEYS == KEYS_RING, "tile skipping is a variant of the ring sweep");
-    constexpr bool TREE = KEYS == KEYS_TREE, PAGED = KEYS == KEYS_PAGED || TREE;
-    using Walk = typename std::conditional<KEYS == KEYS_RING, TileWalk,
-                                           typename std::conditional<TREE, TreeWalk, RangeWalk>::type>::type;
-    using KT = KvTile<D, PAGED && D == 128>;
+    using Walk = typename std::conditional<KEYS == KEYS_RING, TileWalk, RangeWalk>::type;
+    using KT = KvTile<D, KEYS == KEYS_PAGED && D == 128>;
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     if constexpr (KEYS != KEYS_RING) pdl_wait();   // launched with launch_dependent()
@@ -286,7 +275,7 @@ __global__ void __launch_bounds__(384, 1)
     int part = 0;             // KEYS_PAGED: which part of the unit's keys
     bool split = false;       // ... and whether there is more than one
     int unit_no = 0;
-    if constexpr (PAGED) {
+    if constexpr (KEYS == KEYS_PAGED) {
         // Shorter last parts at the end.  Several sequences: blockIdx.x = (part *
         // n_units + at) * H_kv + hk, longer sequences and their last (longest)
         // units first.  One, or too many to sort here: (part * H_kv + hk) *
@@ -328,7 +317,7 @@ __global__ void __launch_bounds__(384, 1)
     // first row of a key tile that is to be read as zeros (KEYS_PAGED: behind the
     // sequence; KEYS_WINDOW: behind the last one; past args.S the copy gives zeros)
     auto zeros_from = [&](int tile) -> int {
-        if (PAGED) return pu.len - tile * 128;
+        if (KEYS == KEYS_PAGED) return pu.len - tile * 128;
         return KEYS == KEYS_WINDOW && S < args.S ? S - tile * 128 : 128;
     };
 
@@ -339,8 +328,7 @@ __global__ void __launch_bounds__(384, 1)
     else if constexpr (KEYS == KEYS_WINDOW)
         walk0 = window_unit_walk(args.cu_seqlens, args.n_seqs, S, row0, row_end, args.window, args.sinks);
     else {
-        if constexpr (TREE) walk0 = tree_walk(paged_walk(args.seqs, pu));
-        else walk0 = paged_walk(args.seqs, pu);
+        walk0 = paged_walk(args.seqs, pu);
         if (args.seqs.num_splits > 1) {
             const int parts = paged_split_count(args.seqs, walk0.end);
             if (part >= parts) return;
@@ -352,7 +340,7 @@ __global__ void __launch_bounds__(384, 1)
     }
     // KEYS_PAGED: a unit of few tokens has no second Q tile; its products and
     // softmax are left out
-    const bool two_tiles = !PAGED || pu.n > args.tile_tokens;
+    const bool two_tiles = KEYS != KEYS_PAGED || pu.n > args.tile_tokens;
     // KEYS_WINDOW: a Q tile's products and softmax skip the key tiles that only
     // the other one's rows see (its neighbour's diagonal, its window's start):
     // one of 9 and more at a window of 1024, one of 4 at 128
@@ -401,13 +389,6 @@ __global__ void __launch_bounds__(384, 1)
             }
         }
     }
-    short *parents = reinterpret_cast<short *>(smem + L::kTab);
-    if constexpr (TREE) {
-        bool bad = false;
-        for (int i = threadIdx.x; i < pu.first + pu.n; i += 384)
-            parents[i] = (short)tree_parent(args.seqs.parents, pu.t0 - pu.first, i, bad);
-        if (bad) atomicOr(args.status, RA_DEV_PAGE_BIT);
-    }
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmq);
         tma_prefetch_desc(&tmk);
@@ -431,8 +412,8 @@ __global__ void __launch_bounds__(384, 1)
         // ================================================= TMA producer
         regs_shrink<LOW_REGS>();
         const int xh = h * D;                        // Q columns of head h
-        const int xkv = PAGED ? h * D : (h / args.kv_group) * D;   // K/V columns of its key/value head
-        if constexpr (PAGED) {
+        const int xkv = KEYS == KEYS_PAGED ? h * D : (h / args.kv_group) * D;   // K/V columns of its key/value head
+        if constexpr (KEYS == KEYS_PAGED) {
             // a box of the group's heads by tile_tokens tokens: rows in the
             // packed order; rows of later tokens of q are loaded but not used
             if (lane == 0) {
@@ -469,7 +450,7 @@ __global__ void __launch_bounds__(384, 1)
         // KEYS_PAGED: lane i's page of a key tile (its box of page_box keys), or
         // one past the last page, which reads as zeros, where the unit sees none
         // of its keys
-        const RowKeys first = PAGED ? paged_first_row(args.seqs, pu) : RowKeys{};
+        const RowKeys first = KEYS == KEYS_PAGED ? paged_row(args.seqs, pu.p0) : RowKeys{};
         auto page_of = [&](int wtile) -> int {
             int z = args.seqs.n_pages;
             const int k0 = wtile * 128 + lane * args.page_box;
@@ -490,7 +471,7 @@ __global__ void __launch_bounds__(384, 1)
             const uint32_t full = BAR((is_k ? B_KF : B_VF) + sl);
             uint32_t &loads = is_k ? k_loads : v_loads;
             loads = (loads & (1u << sl)) ? loads ^ (256u << sl) : loads | (1u << sl);
-            if constexpr (PAGED) {
+            if constexpr (KEYS == KEYS_PAGED) {
                 const uint32_t dst = s_base + L::kRing + sl * L::kTile;
                 if (lane == 0) mbar_arrive_expect_tx(full, L::kTile);
                 __syncwarp();
@@ -517,7 +498,7 @@ __global__ void __launch_bounds__(384, 1)
             ++i;
             return true;
         };
-        if constexpr (PAGED) {
+        if constexpr (KEYS == KEYS_PAGED) {
             if (wk.valid()) wk.j = page_of(wk.tile);
             // the next tile's table entries are read a tile ahead
             while (ok && wk.valid()) {
@@ -1040,22 +1021,12 @@ __global__ void __launch_bounds__(384, 1)
         bool live = KEYS != KEYS_WINDOW || a < row_end;     // the row is stored
         bool warp_live = true;      // some row of the warp is
         int my_tok = 0;
-        if constexpr (PAGED) {
+        if constexpr (KEYS == KEYS_PAGED) {
             const int tok = r / args.seqs.group;
             my_tok = g * args.tile_tokens + tok;
             live = tok < args.tile_tokens && my_tok < pu.n;
             warp_live = __any_sync(0xffffffffu, live);
-            if constexpr (!TREE) rk = paged_row(args.seqs, pu.p0 + min(my_tok, pu.n - 1));
-        }
-        TreeChain chain{};
-        const int before = pu.p0 - pu.first;      // TREE: the tokens before the new ones
-        if constexpr (TREE) {
-            const int node = pu.first + min(my_tok, pu.n - 1);
-            int depth = 0;
-            if (args.seqs.window > 0)
-                for (int p = parents[node]; p >= 0; p = parents[p]) ++depth;
-            rk = tree_row(args.seqs, before + depth, before);
-            chain.start(node, depth, before, args.seqs.window, args.seqs.sinks);
+            rk = paged_row(args.seqs, pu.p0 + min(my_tok, pu.n - 1));
         }
         Walk w = walk0;
         w.start_step();
@@ -1075,7 +1046,7 @@ __global__ void __launch_bounds__(384, 1)
             if constexpr (EDGES) {
                 if (!seen_g.has(w.tile)) continue;
             }
-            if constexpr (PAGED) {
+            if constexpr (KEYS == KEYS_PAGED) {
                 if (g == 1 && !two_tiles) break;
                 if (!warp_live) {
                     // no row here is stored: its P may be anything
@@ -1110,9 +1081,6 @@ __global__ void __launch_bounds__(384, 1)
             const int sk_lo = KEYS == KEYS_RING ? 0 : rk.slo - w.tile * 128;
             const int sk_hi = KEYS == KEYS_RING ? 0 : rk.shi - w.tile * 128;
             const bool partial = lim < 128 || lim_lo > 0;
-            uint32_t drafted[4] = {0u, 0u, 0u, 0u};      // TREE: the seen columns of new tokens
-            if constexpr (TREE)
-                if (w.tile * 128 + 128 > before) chain.tile(parents, w.tile * 128 - before, drafted);
             uint32_t sr[4][32];
             auto load_s = [&]() {
 #pragma unroll
@@ -1141,7 +1109,7 @@ __global__ void __launch_bounds__(384, 1)
                             if (32 * q >= lo_max && 32 * q + 32 <= hi_min) continue;
                             // bit c: column 32 q + c is visible
                             const uint32_t seen = (low_bits(lim - 32 * q) & ~low_bits(lim_lo - 32 * q)) |
-                                                  (low_bits(sk_hi - 32 * q) & ~low_bits(sk_lo - 32 * q)) | drafted[q];
+                                                  (low_bits(sk_hi - 32 * q) & ~low_bits(sk_lo - 32 * q));
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
                                 if (!(seen & (1u << c))) s[32 * q + c] = -INFINITY;
@@ -1191,8 +1159,7 @@ __global__ void __launch_bounds__(384, 1)
                 // a windowed row may see no column of a tile its unit visits:
                 // nothing is added and nothing has to move
                 if constexpr (KEYS != KEYS_RING)
-                    bad = bad && live && (max(lim_lo, 0) < min(lim, 128) || max(sk_lo, 0) < min(sk_hi, 128) ||
-                                          (drafted[0] | drafted[1] | drafted[2] | drafted[3]) != 0u);
+                    bad = bad && live && (max(lim_lo, 0) < min(lim, 128) || max(sk_lo, 0) < min(sk_hi, 128));
                 if (__builtin_expect(__any_sync(0xffffffffu, bad), 0)) {
                     load_s();
                     const float *s = reinterpret_cast<const float *>(&sr[0][0]);
@@ -1342,7 +1309,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         // KEYS_WINDOW: a Q tile that ends behind the last sequence goes out row by row
         const bool ragged = KEYS == KEYS_WINDOW && S < args.S && row0 + 128 * g + 128 > S;
-        if (PAGED || ragged) {
+        if (KEYS == KEYS_PAGED || ragged) {
             // each warp copies its own rows out: final rows of [T, H, d], or
             // this part's rows (fp32) for the join
             const float lse = l > 0.f ? (m_ref + lg2(l)) * 0.6931471805599453f : -INFINITY;
@@ -1393,8 +1360,8 @@ __global__ void __launch_bounds__(384, 1)
             }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        if constexpr (!PAGED) named_barrier_sync(1 + g, 128);
-        if (!PAGED && !ragged && !(KEYS == KEYS_WINDOW && row0 + 128 * g >= row_end) && wq == 0 &&
+        if constexpr (KEYS != KEYS_PAGED) named_barrier_sync(1 + g, 128);
+        if (KEYS != KEYS_PAGED && !ragged && !(KEYS == KEYS_WINDOW && row0 + 128 * g >= row_end) && wq == 0 &&
             lane == 0 && *abort_flag == 0) {
             // rows past the shard's end fall outside the tensor and are not written
             int c1, c2, c3;
@@ -1404,7 +1371,7 @@ __global__ void __launch_bounds__(384, 1)
             tma_store_commit();
             tma_store_wait_read();
         }
-        if (!PAGED && ok && (KEYS == KEYS_WINDOW ? live : a < S)) {
+        if (KEYS != KEYS_PAGED && ok && (KEYS == KEYS_WINDOW ? live : a < S)) {
             // shard stacks: [N or 1, B, H, S]; sequence order: [B, H, L] at the row's position
             const size_t at = args.seq_order ? ((size_t)b * H + h) * ((size_t)N * S) + (size_t)my_pos
                                              : ((size_t)zq * H + h) * args.S + a;

@@ -127,7 +127,8 @@ struct Plan {
     int ctas, cluster;
     bool few;                   // the few-key form: units of its own, the keys it expects
     int64_t few_units, few_keys;
-    size_t part_o, part_lse, total;
+    bool two;                   // trees: units of two Q tiles (and ctas as above)
+    size_t part_o, part_lse, cuts, total;
 };
 
 // The few-key form runs where a block of 64 rows sees few keys.  Chunks of 33 to
@@ -136,6 +137,28 @@ struct Plan {
 // 250: 33 / 23; 32 / 8 heads: 14 / 20, 25 / 25, 41 / 37; d = 128, 8 / 8 heads:
 // 12 / 21, 19 / 21, 43 / 27; 8 sequences, 16 / 8 heads: 6.0 / 7.8, 10.1 / 8.6.
 bool few_keys(int64_t keys, int d) { return keys <= (d == 64 ? 128 : 64); }
+
+// Trees: units of one Q tile or, where those fill the GPU twice, of two, in runs.
+void plan_tree(const Paged &a, Plan &p) {
+    const int64_t active = a.n_seqs < a.T ? a.n_seqs : a.T;
+    int64_t keys = a.max_len;
+    if (a.window > 0 && a.window + a.max_new + a.sinks < keys) keys = a.window + a.max_new + a.sinks;
+    const int64_t tiles = (keys + 127) / 128 + 1;
+    // no more units than this have rows
+    auto most = [&](int tokens) { return (a.T / tokens + active) * a.H_kv; };
+    // a unit of two Q tiles takes 1.85 times as long as one of one
+    const int64_t ones = (a.max_new + p.tile_tokens - 1) / p.tile_tokens;
+    p.two = (ones + 1) / 2 * 50 <= ones * 27;
+    const int64_t streams = tree_streams(a.H_kv);
+    p.units = most((p.two ? 2 : 1) * p.tile_tokens);
+    int64_t runs = (p.units * tiles / streams + kTreeMinRun - 1) / kTreeMinRun;
+    if (runs > kTreeCtas / streams) runs = kTreeCtas / streams;
+    p.ctas = (int)(runs * streams);
+    const size_t rows = (size_t)p.ctas * 2 * 256;
+    p.part_lse = p.part_o + rows * a.d * 4;
+    p.cuts = p.part_lse + rows * 16;
+    p.total = p.cuts + round256((size_t)p.ctas * 16);
+}
 
 Plan plan(Paged a) {
     // hints of any size: with the sizes that the checks admit nothing below leaves
@@ -174,6 +197,10 @@ Plan plan(Paged a) {
         }
     }
     p.tile_tokens = (int)(128 / group);
+    if (a.tree) {
+        plan_tree(a, p);
+        return p;
+    }
     const int unit = 2 * p.tile_tokens;
     p.units = paged_units(a.T, a.n_seqs, unit);
     const int64_t rows = (a.max_new < unit ? a.max_new : unit) * group;
@@ -309,8 +336,8 @@ ra_status launch_chunks(const Paged &a, const Plan &p, const AttnArgs &args, con
     CUtensorMap mq, mk, mv;
     if (!query_map(&mq, q, a, p.tile_tokens) || !page_map(&mk, k, a, args.page_box) || !page_map(&mv, v, a, args.page_box))
         return set_error(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the q and page maps");
-    int smem = (int)AttnSmem<D>::kBytes;
-    const AttnKernel kern = a.tree ? tree_chunk_kernel(D, F32, &smem) : attn_fwd_kernel<D, F32, false, KEYS_PAGED>;
+    auto kern = attn_fwd_kernel<D, F32, false, KEYS_PAGED>;
+    const int smem = (int)AttnSmem<D>::kBytes;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
     const int64_t grid = p.units * a.H_kv * p.splits;
@@ -365,6 +392,30 @@ ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, co
         t.scale_log2 = scale_log2;
         t.status = reinterpret_cast<unsigned *>(workspace);
         return launch_paged_few(t, stream);
+    }
+    if (a.tree) {
+        TreeLaunch t{};
+        t.seqs = sequences(a, table, seq_lens, cu_q);
+        t.seqs.unit_tokens = (p.two ? 2 : 1) * p.tile_tokens;
+        t.tile_tokens = p.tile_tokens;
+        t.page_box = (int)(a.page < 128 ? a.page : 128);
+        t.two = p.two;
+        t.units = p.units;
+        t.ctas = p.ctas;
+        t.streams = tree_streams(a.H_kv);
+        t.d = D;
+        t.o = o;
+        t.lse = lse;
+        t.o_bf16 = o_bf16;
+        t.scale_log2 = scale_log2;
+        t.status = reinterpret_cast<unsigned *>(workspace);
+        t.part_o = workspace + p.part_o;
+        t.part_ml = workspace + p.part_lse;
+        t.cuts = workspace + p.cuts;
+        CUtensorMap mq, mk, mv;
+        if (!query_map(&mq, q, a, p.tile_tokens) || !page_map(&mk, k, a, t.page_box) || !page_map(&mv, v, a, t.page_box))
+            return set_error(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the q and page maps");
+        return launch_tree(t, mq, mk, mv, stream);
     }
     AttnArgs args{};
     args.o = o;

@@ -5,6 +5,11 @@
 
 namespace ra {
 
+unsigned long long next_call_tag() {
+    static std::atomic<unsigned long long> calls{0};
+    return call_tag(calls.fetch_add(1, std::memory_order_relaxed));
+}
+
 ra_status launch_paged_tokens(const TokensLaunch &t, cudaStream_t stream) {
     TokensArgs a{};
     a.seqs = t.seqs;
@@ -19,8 +24,7 @@ ra_status launch_paged_tokens(const TokensLaunch &t, cudaStream_t stream) {
     a.whole_pairs = t.whole_pairs;
     a.scale_log2 = t.scale_log2;
     a.status = t.status;
-    static std::atomic<unsigned long long> calls{0};
-    a.call = call_tag(calls.fetch_add(1, std::memory_order_relaxed));
+    a.call = next_call_tag();
     a.counters = t.counters;
     a.part_o = t.part_o;
     a.part_ml = t.part_ml;

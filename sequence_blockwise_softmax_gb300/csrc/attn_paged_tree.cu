@@ -1,8 +1,8 @@
-// attn_paged_tree.cu -- the tree forms of paged attention's kernels: the few-row
-// form (attn_paged_tokens.cuh) and the tensor-core form (attn_fwd_kernel.cuh,
-// KEYS_TREE).  The entry point is in attn_paged.cu.
-#include "attn_fwd_kernel.cuh"
+// attn_paged_tree.cu -- the launches of tree attention: the few-row form
+// (attn_paged_tokens.cuh) and the tensor-core form (attn_tree.cuh).  The entry
+// point, its checks and its plan are in attn_paged.cu.
 #include "attn_paged_tokens.cuh"
+#include "attn_tree.cuh"
 
 namespace ra {
 
@@ -10,11 +10,38 @@ ra_status launch_tree_tokens(const TokensLaunch &t, const TokensArgs &a, cudaStr
     return launch_tokens<true>(t, a, stream);
 }
 
-AttnKernel tree_chunk_kernel(int d, bool f32, int *smem) {
-    *smem = (int)(d == 128 ? AttnSmem<128>::kBytesTree : AttnSmem<64>::kBytesTree);
-    static_assert(AttnSmem<128>::kBytesTree <= 232448, "what a CTA may have");
-    if (d == 128) return f32 ? attn_fwd_kernel<128, true, false, KEYS_TREE> : attn_fwd_kernel<128, false, false, KEYS_TREE>;
-    return f32 ? attn_fwd_kernel<64, true, false, KEYS_TREE> : attn_fwd_kernel<64, false, false, KEYS_TREE>;
+ra_status launch_tree(const TreeLaunch &t, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                      cudaStream_t stream) {
+    TreeArgs a{};
+    a.seqs = t.seqs;
+    a.tile_tokens = t.tile_tokens;
+    a.page_box = t.page_box;
+    a.two = t.two;
+    a.min_run = kTreeMinRun;
+    a.streams = t.streams;
+    a.heads = t.seqs.Hkv / t.streams;
+    a.scale_log2 = t.scale_log2;
+    a.status = t.status;
+    a.o = t.o;
+    a.lse = t.lse;
+    a.o_bf16 = t.o_bf16;
+    a.part_o = static_cast<float4 *>(t.part_o);
+    a.part_ml = static_cast<float4 *>(t.part_ml);
+    a.cuts = static_cast<TreeCut *>(t.cuts);
+    // few units to a stream are cut into many pieces
+    const bool many = t.units * 6 < t.ctas;
+    auto go = [&](auto kern, auto join, int smem) -> ra_status {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return set_error(RA_ERR_CUDA, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize) failed");
+        const ra_status st = launched(launch_dependent(kern, (unsigned)t.ctas, 384, smem, stream, q, k, v, a));
+        if (st != RA_OK || t.ctas == t.streams) return st;       // one run to a stream cuts no unit
+        return launched(launch_dependent(join, (unsigned)(many ? kTreeCtas : 3 * kTreeCtas), 256, 0, stream, a, t.ctas));
+    };
+    if (t.d == 128)
+        return go(paged_tree_kernel<128>, many ? paged_tree_join_kernel<128, 10> : paged_tree_join_kernel<128, 4>,
+                  (int)TreeSmem<128>::kBytes);
+    return go(paged_tree_kernel<64>, many ? paged_tree_join_kernel<64, 10> : paged_tree_join_kernel<64, 4>,
+              (int)TreeSmem<64>::kBytes);
 }
 
 }  // namespace ra

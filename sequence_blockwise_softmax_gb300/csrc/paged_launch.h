@@ -2,6 +2,8 @@
 // (attn_paged_tokens.cu) and few-key form (attn_paged_few.cu), shared with the
 // entry point (attn_paged.cu), and the few-row form's rules on how a call is cut.
 #pragma once
+#include <cuda.h>
+
 #include "ra_internal.h"
 #include "ra_paged.cuh"
 
@@ -94,5 +96,31 @@ struct PagedFewLaunch {
 };
 
 ra_status launch_paged_few(const PagedFewLaunch &t, cudaStream_t stream);
+
+// Tree attention's tensor-core form (attn_tree.cuh).
+constexpr int kTreeCtas = 152;              // one to each SM of a GB300
+constexpr int kTreeMinRun = 4;              // tiles of a run at least
+
+// The lists of tiles side by side: as many of the key/value heads as divide them, up to eight.
+inline int tree_streams(int64_t H_kv) {
+    int n = 8;
+    while (H_kv % n) --n;
+    return n;
+}
+
+struct TreeLaunch {
+    PagedSeqs seqs;                         // unit_tokens: tokens of a unit
+    int64_t units;                          // at most
+    int tile_tokens, page_box, two, ctas, streams, d;
+    void *o;
+    float *lse;
+    bool o_bf16;
+    float scale_log2;
+    unsigned *status;
+    void *part_o, *part_ml, *cuts;          // 2 * ctas pieces of [256 rows, d] fp32, 16 bytes a row, 16 a CTA
+};
+
+ra_status launch_tree(const TreeLaunch &t, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                      cudaStream_t stream);
 
 }  // namespace ra

@@ -61,10 +61,9 @@ RA_HD int paged_find_seq(const PagedSeqs &q, int u) {
     return lo;
 }
 
-// Unit number `local` of sequence s; n <= 0 if it has none.
-RA_HD PagedUnit paged_unit(const PagedSeqs &q, int s, int local) {
+// Unit number `local` of sequence s, whose rows are [c0, c1); n <= 0 if it has none.
+RA_HD PagedUnit paged_unit_of(const PagedSeqs &q, int s, int c0, int c1, int len, int local) {
     PagedUnit u;
-    const int c0 = paged_bound(q, s), c1 = paged_bound(q, s + 1);
     const int n_new = c1 - c0;
     const int n = n_new < q.max_new ? n_new : q.max_new;
     u.s = s;
@@ -72,9 +71,12 @@ RA_HD PagedUnit paged_unit(const PagedSeqs &q, int s, int local) {
     u.t0 = c0 + u.first;
     u.n = n - u.first < q.unit_tokens ? n - u.first : q.unit_tokens;
     if (local < 0) u.n = 0;     // a unit before the first sequence's rows
-    u.len = paged_len(q, s);
+    u.len = len;
     u.p0 = u.len - n_new + u.first;
     return u;
+}
+RA_HD PagedUnit paged_unit(const PagedSeqs &q, int s, int local) {
+    return paged_unit_of(q, s, paged_bound(q, s), paged_bound(q, s + 1), paged_len(q, s), local);
 }
 
 // The keys of the token at position p (a negative position sees none).
