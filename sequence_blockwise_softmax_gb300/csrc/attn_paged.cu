@@ -124,7 +124,7 @@ struct Plan {
     int tile_tokens, splits, tail_share;    // the tensor-core form
     int64_t units;
     bool tokens, whole_pairs;   // the few-row form, with this many CTAs, in clusters or not
-    int ctas, cluster;
+    int ctas, cluster, row_blocks;
     bool few;                   // the few-key form: units of its own, the keys it expects
     int64_t few_units, few_keys;
     bool two;                   // trees: units of two Q tiles (and ctas as above)
@@ -173,13 +173,23 @@ Plan plan(Paged a) {
     const int64_t active0 = a.n_seqs < a.T ? a.n_seqs : a.T;
     p.part_o = kCounters + kCounterBytes;
     // Few rows per key/value head: bound by the cache's bytes (see attn_paged_tokens.cu)
-    if (a.max_new * group <= kPagedTokensRows) {
+    int64_t seen = a.max_len;
+    if (a.window > 0 && a.window + a.max_new + a.sinks < seen) seen = a.window + a.max_new + a.sinks;
+    if (a.max_new * group <= kPagedTokensRows &&
+        !(a.tree && a.max_new * group > 16 && tree_in_runs(active0 * a.H_kv, seen, a.d))) {
         p.tokens = true;
-        int64_t seen = a.max_len;
-        if (a.window > 0 && a.window + a.max_new + a.sinks < seen) seen = a.window + a.max_new + a.sinks;
-        p.ctas = paged_tokens_ctas(active0 * a.H_kv, seen, a.n_seqs);
-        p.whole_pairs = paged_tokens_whole(active0 * a.H_kv, seen, a.n_seqs);
-        p.cluster = paged_tokens_cluster(active0 * a.H_kv, seen);
+        p.row_blocks = 1;
+        if (a.tree && a.max_new * group > 16 && group <= 16) {
+            // blocks of 16 rows while clusters for all of them stand side by side: half the
+            // products to a warp, the keys twice from L2.  8 nodes over 1000 keys, 32 / 8
+            // heads, d = 128: 10.0 us as one block, 8.0 as two.
+            const int64_t blocks = (a.max_new + 16 / group - 1) / (16 / group);
+            if (paged_tokens_cluster(active0 * blocks * a.H_kv, seen)) p.row_blocks = (int)blocks;
+        }
+        const int64_t pairs = active0 * p.row_blocks * a.H_kv;
+        p.ctas = paged_tokens_ctas(pairs, seen, a.n_seqs);
+        p.whole_pairs = p.row_blocks == 1 && paged_tokens_whole(pairs, seen, a.n_seqs);
+        p.cluster = paged_tokens_cluster(pairs, seen);
         const size_t rows = p.whole_pairs || p.cluster ? 0 : (size_t)2 * p.ctas * (a.max_new * group <= 16 ? 16 : 32);
         p.part_lse = p.part_o + round256(rows * a.d * 4);
         p.total = p.part_lse + round256(rows * 8);
@@ -354,7 +364,9 @@ ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, co
     if (p.tokens) {
         TokensLaunch t{};
         t.seqs = sequences(a, table, seq_lens, cu_q);
-        t.seqs.unit_tokens = t.seqs.max_new;        // a sequence's tokens are one unit
+        // a sequence's tokens are one unit, or blocks of 16 rows
+        t.seqs.unit_tokens = p.row_blocks > 1 ? 16 / t.seqs.group : t.seqs.max_new;
+        t.row_blocks = p.row_blocks;
         t.q = q;
         t.k = k;
         t.v = v;

@@ -22,6 +22,7 @@ ra_status launch_paged_tokens(const TokensLaunch &t, cudaStream_t stream) {
     a.lse = t.lse;
     a.o_bf16 = t.o_bf16;
     a.whole_pairs = t.whole_pairs;
+    a.row_blocks = t.row_blocks;
     a.scale_log2 = t.scale_log2;
     a.status = t.status;
     a.call = next_call_tag();

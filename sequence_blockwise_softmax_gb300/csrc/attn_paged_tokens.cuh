@@ -59,6 +59,7 @@ struct TokensArgs {
     void *o;
     float *lse;
     int o_bf16, whole_pairs;
+    int row_blocks;                 // trees: blocks of unit_tokens of a sequence's new tokens
     float scale_log2;
     unsigned *status;
     unsigned long long call;        // the call's tag, another one for every call of the process
@@ -144,9 +145,12 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
         }
         return inc;
     };
-    const int blocks = (sq.n_seqs + blockDim.x - 1) / blockDim.x;    // of sequences, one to a thread
+    // TREE: a sequence's new tokens may be several blocks, each a sequence of its own here
+    const int row_blocks = TREE ? a.row_blocks : 1, n_lists = sq.n_seqs * row_blocks;
+    const int blocks = (n_lists + blockDim.x - 1) / blockDim.x;      // of sequences, one to a thread
     const PagedChunks none{};
-    auto list_of = [&](int s) { return s < sq.n_seqs ? paged_chunks(sq, s) : none; };
+    auto chunks_of = [&](int s) { return TREE ? paged_chunks(sq, s / row_blocks, s % row_blocks) : paged_chunks(sq, s); };
+    auto list_of = [&](int s) { return s < n_lists ? chunks_of(s) : none; };
     PagedChunks mine = list_of(threadIdx.x);
     unsigned long long sum = 0;
     for (int i = 0; CLUSTER == 0 && i < blocks; ++i) {
@@ -220,12 +224,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
 
         // chunks inside [all_lo, all_hi) or [0, all_shi) are seen whole by every row
         // (no tree is deeper than a chain of all its nodes)
-        const RowKeys first = TREE ? tree_row(sq, cl.p0, cl.p0) : paged_row(sq, cl.p0);
+        const int before = cl.p0 - cl.first;     // TREE: tokens before the new ones
+        const RowKeys first = TREE ? tree_row(sq, before, before) : paged_row(sq, cl.p0);
         const RowKeys last = paged_row(sq, cl.p0 + cl.n - 1);
         const int all_lo = last.lo, all_hi = first.hi, all_shi = first.shi > first.slo ? first.shi : 0;
 
         auto key_of = [&](int c) { return paged_chunk_key(cl, c); };
-        const int *row_table = sq.table + (size_t)seq * sq.max_pages;
+        const int *row_table = sq.table + (size_t)(TREE ? seq / row_blocks : seq) * sq.max_pages;
         auto page_of = [&](int c) -> int {
             const int k0 = key_of(c);
             return c < c_end && k0 < cl.len ? row_table[k0 / sq.page] : 0;
@@ -256,6 +261,10 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
             cp_async_commit();
         };
 
+        // TREE: lane i's parent, on its way beside the first keys
+        bool no_tree = false;
+        int up = -1;
+        if constexpr (TREE) up = lane < cl.first + cl.n ? tree_parent(sq.parents, cl.t0 - cl.first, lane, no_tree) : -1;
         int c = c_at + warp;
         int next_id = page_of(c);
 #pragma unroll
@@ -266,21 +275,6 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
         }
         if (!word_started && threadIdx.x == 32 * (kWarps - 1)) start_word(a.counters + cta, a.call);
         word_started = true;
-        // TREE: lane i's node i, the node its known chain ends at, that chain's bits
-        uint32_t chain = 1u << lane;
-        if constexpr (TREE) {
-            bool bad = false;
-            int up = lane < cl.n ? tree_parent(sq.parents, cl.t0, lane, bad) : -1;
-            if (bad) atomicOr(a.status, RA_DEV_PAGE_BIT);
-            if (up >= 0) chain |= 1u << up;
-#pragma unroll
-            for (int i = 0; i < 5; ++i) {
-                const uint32_t more = __shfl_sync(0xffffffffu, chain, up < 0 ? lane : up);
-                const int next = __shfl_sync(0xffffffffu, up, up < 0 ? lane : up);
-                chain |= more;
-                if (up >= 0) up = next;
-            }
-        }
         // Q fragments, straight from global memory; rows past the unit's are zero
         WarpRows<D, MT> rw;
         rw.clear();
@@ -293,14 +287,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
                 const int r = mt * 16 + h * 8 + g;
                 const bool live = r < rows;
                 const int tok = live ? r / sq.group : 0, head = live ? r - tok * sq.group : 0;
-                const int node = live ? tok : cl.n - 1;
-                row_pos[mt][h] = cl.p0 + node;
-                if constexpr (TREE) {
-                    const uint32_t all = __shfl_sync(0xffffffffu, chain, node);
-                    const int depth = __popc(all) - 1;
-                    row_pos[mt][h] = cl.p0 + depth;
-                    row_chain[mt][h] = sq.window > 0 && depth >= sq.window ? tree_window(all, sq.window, sq.sinks - cl.p0) : all;
-                }
+                row_pos[mt][h] = cl.p0 + (live ? tok : cl.n - 1);
                 const uint16_t *src = a.q + (size_t)(cl.t0 + tok) * a.q_stride + (size_t)(hk * sq.group + head) * D + 2 * t4;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
@@ -308,6 +295,28 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
                     rw.q[mt][ks][2 + h] = live ? *reinterpret_cast<const uint32_t *>(src + ks * 16 + 8) : 0u;
                 }
             }
+        if constexpr (TREE) {
+            // lane i's chain as far as it is known, as bits, and the node that it ends at
+            uint32_t chain = 1u << lane;
+            if (no_tree) atomicOr(a.status, RA_DEV_PAGE_BIT);
+            if (up >= 0) chain |= 1u << up;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                const uint32_t more = __shfl_sync(0xffffffffu, chain, up < 0 ? lane : up);
+                const int next = __shfl_sync(0xffffffffu, up, up < 0 ? lane : up);
+                chain |= more;
+                if (up >= 0) up = next;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t all = __shfl_sync(0xffffffffu, chain, row_pos[mt][h] - before);
+                    const int depth = __popc(all) - 1;
+                    row_pos[mt][h] = before + depth;
+                    row_chain[mt][h] = sq.window > 0 && depth >= sq.window ? tree_window(all, sq.window, sq.sinks - before) : all;
+                }
+        }
         int stage = 0;
         for (; c < c_end; c += kWarps) {
             cp_async_wait<NS - 2>();
@@ -322,8 +331,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
             const bool whole = (k0 >= all_lo && k0 + kChunk <= all_hi) || k0 + kChunk <= all_shi;
             rw.chunk(sk, sv, a.scale_log2, whole, lane, [&](int mt, int h) {
                 if constexpr (TREE) {
-                    const RowKeys rk = tree_row(sq, row_pos[mt][h], cl.p0);
-                    const int from = k0 - cl.p0;       // column 0's node
+                    const RowKeys rk = tree_row(sq, row_pos[mt][h], before);
+                    const int from = k0 - before;       // column 0's node
                     const uint32_t nodes = from <= -32 || from >= 32 ? 0u : from < 0 ? row_chain[mt][h] << -from : row_chain[mt][h] >> from;
                     return seen_bits(rk.lo, rk.hi, rk.slo, rk.shi, k0) | nodes;
                 } else {
@@ -519,7 +528,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_tokens_kernel(const Toke
         c_at = 0;
         if (++hk == sq.Hkv) {
             hk = 0;
-            do cl = paged_chunks(sq, ++seq);
+            do cl = chunks_of(++seq);
             while (cl.count == 0);
         }
     }
@@ -542,7 +551,7 @@ ra_status launch(const TokensLaunch &t, const TokensArgs &args, cudaStream_t str
 
 template <bool TREE>
 ra_status launch_tokens(const TokensLaunch &t, const TokensArgs &a, cudaStream_t stream) {
-    const int rows = t.seqs.max_new * t.seqs.group;
+    const int rows = (t.seqs.max_new < t.seqs.unit_tokens ? t.seqs.max_new : t.seqs.unit_tokens) * t.seqs.group;
     auto go = [&](auto cluster) {
         constexpr int C = decltype(cluster)::value;
         if (t.d == 128) return rows <= 16 ? launch<128, 1, C, TREE>(t, a, stream) : launch<128, 2, C, TREE>(t, a, stream);

@@ -30,6 +30,7 @@ struct KeepArgs {
     uint4 *k, *v;
     int64_t page_stride, layer_stride;     // in 16-byte pieces
     int pieces, groups;                    // pieces of a token; blocks of a sequence
+    int page_shift;                        // log2 of the page size
     int64_t items, per;                    // pieces of a token in all layers' keys and values; of a block
     unsigned *status;
 };
@@ -38,6 +39,7 @@ __global__ void __launch_bounds__(kThreads) paged_keep_kernel(const KeepArgs a) 
     const PagedSeqs &sq = a.seqs;
     __shared__ short parents[kTreeMost], chain[kTreeMost];     // chain: the path from its end up
     __shared__ int64_t from[kTreeMost], to[kTreeMost];         // moved nodes' pieces in the pool
+    __shared__ int pages[kTreeMost / 16 + 1];                  // of the places behind `before`
     __shared__ int s_m, s_stay;
     pdl_wait();
     const int s = blockIdx.x / a.groups, group = blockIdx.x % a.groups;
@@ -49,6 +51,11 @@ __global__ void __launch_bounds__(kThreads) paged_keep_kernel(const KeepArgs a) 
     const bool none = last < 0 || last >= n || before < 0;
     if (!none)
         for (int i = threadIdx.x; i <= last; i += kThreads) parents[i] = (short)tree_parent(sq.parents, c0, i, bad);
+    // (the table beside the parents: one latency, and no entry without a place of the tree's)
+    const int64_t page0 = before >> a.page_shift;
+    if (!none)
+        for (int64_t i = threadIdx.x; page0 + i <= (before + last) >> a.page_shift; i += kThreads)
+            pages[i] = page0 + i < sq.max_pages ? sq.table[(size_t)s * sq.max_pages + page0 + i] : -1;
     __syncthreads();
     if (threadIdx.x == 0) {
         int m = 0;
@@ -64,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) paged_keep_kernel(const KeepArgs a) 
     if (group == 0 && a.path)
         for (int i = threadIdx.x; i < n_new; i += kThreads) a.path[c0 + i] = i < m ? c0 + chain[m - 1 - i] : -1;
     auto place = [&](int64_t pos) -> int64_t {
-        const int id = pos / sq.page < sq.max_pages ? sq.table[(size_t)s * sq.max_pages + pos / sq.page] : -1;
+        const int id = pages[(pos >> a.page_shift) - page0];
         if ((unsigned)id < (unsigned)sq.n_pages) return (int64_t)id * a.page_stride + (pos & (sq.page - 1)) * a.pieces;
         bad = true;
         return -1;
@@ -147,6 +154,7 @@ extern "C" ra_status ra_paged_keep_path(void *k_pages, void *v_pages, const int3
     a.layer_stride = layer_stride / 8;
     a.pieces = (int)(H_kv * d / 8);
     a.items = n_layers * 2 * a.pieces;
+    while ((int64_t)1 << a.page_shift < page_size) ++a.page_shift;
     a.status = static_cast<unsigned *>(workspace);
     // a piece to a thread while the blocks are few, more where sequences fill the SMs
     int64_t groups = (a.items + kThreads - 1) / kThreads;

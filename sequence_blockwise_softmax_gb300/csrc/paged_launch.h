@@ -22,7 +22,7 @@ struct TokensLaunch {
     void *o;
     float *lse;
     bool o_bf16, whole_pairs;
-    int d, ctas, cluster;
+    int d, ctas, cluster, row_blocks;
     float scale_log2;
     unsigned *status;
     unsigned long long *counters;   // kPagedTokensCtas
@@ -106,6 +106,17 @@ inline int tree_streams(int64_t H_kv) {
     int n = 8;
     while (H_kv % n) --n;
     return n;
+}
+
+// Whether a call of 17 to 32 rows to a pair runs there: with two row tiles a warp of the
+// few-row form takes 2.3 us for 16 keys at d = 128 (1.2 at d = 64), which holds that form to 4.3
+// TB/s.  8 nodes, in us, few-row form against runs, 32 / 8 heads, d = 128: one sequence of
+// 1000 keys 10 / 14, 2000: 13 / 14, 4000: 16 / 15, 16000: 45 / 24; 4 of 2000-4000: 22 / 23; 16 of
+// 200-1000: 24 / 24, of 2000-4000: 74 / 46; 64 of 100-300: 36 / 36, of 1000-2000: 111 / 83; 8 / 2
+// heads, d = 64: one of 8000: 13 / 14, 16000: 22 / 16; 16 of 2000-4000: 15 / 18, 64 of 1000-2000:
+// 29 / 28.
+inline bool tree_in_runs(int64_t pairs, int64_t keys, int d) {
+    return keys * d > 400000 || (double)pairs * (double)(keys * d) > 1.6e7;
 }
 
 struct TreeLaunch {

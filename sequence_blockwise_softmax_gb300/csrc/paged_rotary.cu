@@ -14,7 +14,9 @@
 // H_kv) d 2 bytes a token.  The call is one list of items, each two 16-byte
 // pieces of a head: the two that hold its pairs, or two to copy.  A block takes a
 // run of the list, finds its tokens' places and computes their cosines once for
-// all heads, while its first items are on their way.
+// all heads, while its first items are on their way.  One item of a thread at a time and five
+// blocks to an SM: two at a time take the registers of one block, and were slower (20589
+// tokens of 32 / 8 heads, d = 128: 84 us, 6.0 TB/s, against 90).
 #include "paged_checks.h"
 #include "ra_device.cuh"
 #include "ra_launch.h"
@@ -23,7 +25,8 @@
 namespace ra {
 namespace {
 
-constexpr int kThreads = 256, kTokens = 32, kAhead = 2;   // tokens a block meets at most, items of a thread at once
+constexpr int kThreads = 256, kTokens = 32;   // tokens a block meets at most
+constexpr int kSeqs = kThreads - 1;      // sequences whose rows and lengths a block reads at once
 constexpr int kSms = 152;
 // cosines and sines of 8 pairs: 16 floats and 4 between them and the next, so
 // that the 16-byte reads of 8 neighbouring threads meet in no bank
@@ -39,6 +42,8 @@ struct RotaryArgs {
     int turned;                 // items of a head that are turned (rot / 16)
     int pairs;                  // neighbouring columns are a pair
     int items, chunk;           // items of a token, of a block
+    unsigned inverse;           // floor(2^32 / items): a division by items without one
+    int shift, page_shift;      // log2 of per_head, of the page size
     unsigned *status;
 };
 
@@ -50,10 +55,11 @@ __device__ __forceinline__ unsigned long long turn_fraction(float f) {
 
 __device__ __forceinline__ float2 bf16x2(uint32_t x) { return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)); }
 
-__global__ void __launch_bounds__(kThreads) paged_append_rotary_kernel(const RotaryArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) paged_append_rotary_kernel(const RotaryArgs a) {
     const PagedSeqs &sq = a.seqs;
     __shared__ int64_t place[kTokens];       // a token's first piece in the pool, -1: not written
     __shared__ int position[kTokens];
+    __shared__ int rows[kThreads], lens[kThreads];
     __shared__ unsigned live;                // tokens that belong to a sequence
     __shared__ unsigned long long fraction[64];
     __shared__ __align__(16) float turns[kTokens * 8 * kGroup];
@@ -70,65 +76,75 @@ __global__ void __launch_bounds__(kThreads) paged_append_rotary_kernel(const Rot
     };
     auto item_of = [&](int64_t e) {
         const unsigned in = (unsigned)(e - (int64_t)t0 * a.items);     // (a block's list is short)
-        const int tok = (int)(in / (unsigned)a.items), r = (int)(in - (unsigned)tok * a.items);
-        const int head = r / a.per_head;
-        return Item{tok, head, r - head * a.per_head};
+        unsigned tok = __umulhi(in, a.inverse), r = in - tok * a.items;     // one too few at most
+        if (r >= (unsigned)a.items) {
+            r -= a.items;
+            ++tok;
+        }
+        return Item{(int)tok, (int)(r >> a.shift), (int)(r & ((1u << a.shift) - 1))};
     };
     auto turned = [&](const Item &x) { return x.head < a.H + a.Hkv && x.i < a.turned; };
     // the item's first piece in its head, and from there to its second
     auto piece = [&](const Item &x) { return turned(x) && !a.pairs ? x.i : 2 * x.i; };
     auto second = [&](const Item &x) { return turned(x) && !a.pairs ? a.turned : 1; };
-    uint4 x[kAhead][2];
-    auto load = [&](int64_t e0) {
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int64_t e = e0 + j * kThreads;
-            if (e >= end) continue;
-            const Item it = item_of(e);
-            const int64_t t = t0 + it.tok;
-            const int in_head = piece(it);
-            const uint4 *src = it.head < a.H ? a.q + t * a.q_stride + it.head * (2 * a.per_head)
-                               : it.head < a.H + a.Hkv ? a.k + t * a.new_stride + (it.head - a.H) * (2 * a.per_head)
-                                                       : a.v + t * a.new_stride + (it.head - a.H - a.Hkv) * (2 * a.per_head);
-            x[j][0] = __ldcs(src + in_head);
-            x[j][1] = __ldcs(src + in_head + second(it));
-        }
+    uint4 x[2];
+    auto load = [&](const Item &it) {
+        const int64_t t = t0 + it.tok;
+        const int in_head = piece(it);
+        const uint4 *src = it.head < a.H ? a.q + t * a.q_stride + it.head * (2 * a.per_head)
+                           : it.head < a.H + a.Hkv ? a.k + t * a.new_stride + (it.head - a.H) * (2 * a.per_head)
+                                                   : a.v + t * a.new_stride + (it.head - a.H - a.Hkv) * (2 * a.per_head);
+        x[0] = __ldcs(src + in_head);
+        x[1] = __ldcs(src + in_head + second(it));
     };
-    load(first + threadIdx.x);
+    if (first + threadIdx.x < end) load(item_of(first + threadIdx.x));     // on its way while the places are found
 
     // ---- the tokens' places and positions, the frequencies
+    // Few sequences: all their rows and lengths at once; many: by search.
+    const bool few = sq.n_seqs <= kSeqs;
+    if (few) {
+        if ((int)threadIdx.x <= sq.n_seqs) rows[threadIdx.x] = paged_bound(sq, threadIdx.x);
+        if ((int)threadIdx.x < sq.n_seqs) lens[threadIdx.x] = sq.seq_lens[threadIdx.x];
+    }
+    if (threadIdx.x >= kThreads - 64) {
+        const int m = threadIdx.x - (kThreads - 64);
+        if (m < a.turned * 8) fraction[m] = turn_fraction(a.inv_freq[m]);
+    }
+    if (few) __syncthreads();
     if (warp == 0) {
-        // the first token's sequence, 32 probes at a time, then for each lane's
-        // token how many of the next 32 sequences begin at it or before
-        int lo = 0, hi = sq.n_seqs;
-        while (hi - lo > 1) {
-            const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-            const bool below = at < hi && (lane == 0 || paged_bound(sq, at) <= t0);
-            const int last = 31 - __clz(__ballot_sync(0xffffffffu, below));
-            lo += last * step;
-            hi = min(hi, lo + step);
-        }
         const int t = t0 + lane;
-        const int next = lo + 1 + lane < sq.n_seqs ? paged_bound(sq, lo + 1 + lane) : 0x7fffffff;
-        int s = lo;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s += __shfl_sync(0xffffffffu, next, i) <= t ? 1 : 0;
-        if (s == lo + 32)
-            for (hi = sq.n_seqs; hi - s > 1;) {
-                const int mid = (s + hi) >> 1;
-                if (paged_bound(sq, mid) <= t) s = mid;
-                else hi = mid;
+        int s = 0, hi = sq.n_seqs;
+        if (!few) {
+            // the first token's sequence, 32 probes at a time, then for each lane's
+            // token how many of the next 32 sequences begin at it or before
+            while (hi - s > 1) {
+                const int step = (hi - s + 31) / 32, at = s + lane * step;
+                const bool below = at < hi && (lane == 0 || paged_bound(sq, at) <= t0);
+                const int last = 31 - __clz(__ballot_sync(0xffffffffu, below));
+                s += last * step;
+                hi = min(hi, s + step);
             }
-        const int c0 = paged_bound(sq, s), c1 = paged_bound(sq, s + 1);
+            const int lo = s, next = lo + 1 + lane < sq.n_seqs ? paged_bound(sq, lo + 1 + lane) : 0x7fffffff;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s += __shfl_sync(0xffffffffu, next, i) <= t ? 1 : 0;
+            hi = s == lo + 32 ? sq.n_seqs : s;
+        }
+        while (hi - s > 1) {
+            const int mid = (s + hi) >> 1;
+            if ((few ? rows[mid] : paged_bound(sq, mid)) <= t) s = mid;
+            else hi = mid;
+        }
+        const int c0 = few ? rows[s] : paged_bound(sq, s), c1 = few ? rows[s + 1] : paged_bound(sq, s + 1);
         bool in = lane < n_tok && t >= c0 && t < c1;
         int64_t dst = -1, p = 0;
         if (in) {
             const int i = t - c0;
-            const int64_t before = (int64_t)sq.seq_lens[s] - (c1 - c0), pos = before + i;
+            const int64_t before = (int64_t)(few ? lens[s] : sq.seq_lens[s]) - (c1 - c0), pos = before + i;
             p = pos;
             int id = -1;
             bool bad = false;
-            if (pos >= 0 && pos / sq.page < sq.max_pages) id = sq.table[(size_t)s * sq.max_pages + pos / sq.page];
+            const int64_t nth = pos >> a.page_shift;
+            if (pos >= 0 && nth < sq.max_pages) id = sq.table[(size_t)s * sq.max_pages + nth];
             if (sq.parents) {
                 if (i < kTreeMost) {
                     int depth = 0;
@@ -147,9 +163,6 @@ __global__ void __launch_bounds__(kThreads) paged_append_rotary_kernel(const Rot
         position[lane] = (int)p;
         const unsigned all = __ballot_sync(0xffffffffu, in);
         if (lane == 0) live = all;
-    } else if (threadIdx.x < 32 + 64) {
-        const int m = threadIdx.x - 32;
-        if (m < a.turned * 8) fraction[m] = turn_fraction(a.inv_freq[m]);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < n_tok * a.turned * 8; e += kThreads) {
@@ -163,51 +176,45 @@ __global__ void __launch_bounds__(kThreads) paged_append_rotary_kernel(const Rot
     }
     __syncthreads();
 
-    for (int64_t e0 = first + threadIdx.x; e0 < end; e0 += kAhead * kThreads) {
-        if (e0 != first + threadIdx.x) load(e0);
+    for (int64_t e = first + threadIdx.x; e < end; e += kThreads) {
+        const Item it = item_of(e);
+        if (e >= first + kThreads) load(it);
+        if (!((live >> it.tok) & 1u)) continue;
+        if (turned(it)) {
+            const float4 *cs = reinterpret_cast<const float4 *>(turns + (it.tok * 8 + it.i) * kGroup);
+            float c[8], s[8];
+            *reinterpret_cast<float4 *>(c) = cs[0];
+            *reinterpret_cast<float4 *>(c + 4) = cs[1];
+            *reinterpret_cast<float4 *>(s) = cs[2];
+            *reinterpret_cast<float4 *>(s + 4) = cs[3];
+            uint32_t *w0 = reinterpret_cast<uint32_t *>(&x[0]), *w1 = reinterpret_cast<uint32_t *>(&x[1]);
+            if (a.pairs) {
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int64_t e = e0 + j * kThreads;
-            if (e >= end) continue;
-            const Item it = item_of(e);
-            if (!((live >> it.tok) & 1u)) continue;
-            const bool turn = turned(it);
-            if (turn) {
-                const float4 *cs = reinterpret_cast<const float4 *>(turns + (it.tok * 8 + it.i) * kGroup);
-                float c[8], s[8];
-                *reinterpret_cast<float4 *>(c) = cs[0];
-                *reinterpret_cast<float4 *>(c + 4) = cs[1];
-                *reinterpret_cast<float4 *>(s) = cs[2];
-                *reinterpret_cast<float4 *>(s + 4) = cs[3];
-                uint32_t *w0 = reinterpret_cast<uint32_t *>(&x[j][0]), *w1 = reinterpret_cast<uint32_t *>(&x[j][1]);
-                if (a.pairs) {
+                for (int w = 0; w < 8; ++w) {
+                    uint32_t &word = w < 4 ? w0[w] : w1[w - 4];
+                    const float2 v = bf16x2(word);
+                    word = pack_bf16x2(v.x * c[w] - v.y * s[w], v.x * s[w] + v.y * c[w]);
+                }
+            } else {
 #pragma unroll
-                    for (int w = 0; w < 8; ++w) {
-                        uint32_t &word = w < 4 ? w0[w] : w1[w - 4];
-                        const float2 v = bf16x2(word);
-                        word = pack_bf16x2(v.x * c[w] - v.y * s[w], v.x * s[w] + v.y * c[w]);
-                    }
-                } else {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const float2 u = bf16x2(w0[w]), v = bf16x2(w1[w]);
-                        w0[w] = pack_bf16x2(u.x * c[2 * w] - v.x * s[2 * w], u.y * c[2 * w + 1] - v.y * s[2 * w + 1]);
-                        w1[w] = pack_bf16x2(u.x * s[2 * w] + v.x * c[2 * w], u.y * s[2 * w + 1] + v.y * c[2 * w + 1]);
-                    }
+                for (int w = 0; w < 4; ++w) {
+                    const float2 u = bf16x2(w0[w]), v = bf16x2(w1[w]);
+                    w0[w] = pack_bf16x2(u.x * c[2 * w] - v.x * s[2 * w], u.y * c[2 * w + 1] - v.y * s[2 * w + 1]);
+                    w1[w] = pack_bf16x2(u.x * s[2 * w] + v.x * c[2 * w], u.y * s[2 * w + 1] + v.y * c[2 * w + 1]);
                 }
             }
-            uint4 *dst;
-            if (it.head < a.H) {
-                dst = a.q_out + (int64_t)(t0 + it.tok) * a.out_stride + it.head * (2 * a.per_head);
-            } else {
-                if (place[it.tok] < 0) continue;
-                const bool key = it.head < a.H + a.Hkv;
-                dst = (key ? a.k_pages : a.v_pages) + place[it.tok] + (it.head - a.H - (key ? 0 : a.Hkv)) * (2 * a.per_head);
-            }
-            const int in_head = piece(it);
-            dst[in_head] = x[j][0];
-            dst[in_head + second(it)] = x[j][1];
         }
+        uint4 *dst;
+        if (it.head < a.H) {
+            dst = a.q_out + (int64_t)(t0 + it.tok) * a.out_stride + it.head * (2 * a.per_head);
+        } else {
+            if (place[it.tok] < 0) continue;
+            const bool key = it.head < a.H + a.Hkv;
+            dst = (key ? a.k_pages : a.v_pages) + place[it.tok] + (it.head - a.H - (key ? 0 : a.Hkv)) * (2 * a.per_head);
+        }
+        const int in_head = piece(it);
+        dst[in_head] = x[0];
+        dst[in_head + second(it)] = x[1];
     }
 }
 
@@ -271,6 +278,9 @@ extern "C" ra_status ra_paged_append_rotary(const void *q, const void *k_new, co
     a.turned = rot / 16;
     a.pairs = (flags & RA_FLAG_ROTARY_PAIRS) != 0;
     a.items = (int)((H + 2 * H_kv) * a.per_head);
+    a.inverse = (unsigned)(((int64_t)1 << 32) / a.items);
+    a.shift = d == 128 ? 3 : 2;
+    while ((int64_t)1 << a.page_shift < page_size) ++a.page_shift;
     a.status = static_cast<unsigned *>(workspace);
     // an item to a thread while that fills the SMs, then several, of no more tokens than a block holds
     const int64_t total = T * a.items;

@@ -134,23 +134,25 @@ RA_HD bool paged_needed(const RowKeys &first, int last_hi, int len, int k0, int 
 
 constexpr int kPagedChunk = 16;
 
-// The few-row form (attn_paged_tokens.cu): the 16-key chunks of sequence s's keys that its new tokens see, in order:
+// The few-row form (attn_paged_tokens.cu): the 16-key chunks of sequence s's keys that its new tokens (those of block number `block`) see, in order:
 // n_sink chunks from 0 on, then chunks from m0 on.  A sequence with new tokens
 // that see nothing keeps one (masked) chunk, so that its rows are written.
 struct PagedChunks {
     int n_sink, m0, count;
     int t0, n, p0, len;      // its new tokens, their first position, its length
+    int first;               // new tokens of the sequence before them
 };
-RA_HD PagedChunks paged_chunks(const PagedSeqs &q, int s) {
+RA_HD PagedChunks paged_chunks(const PagedSeqs &q, int s, int block = 0) {
     PagedChunks c;
-    const PagedUnit u = paged_unit(q, s, 0);
+    const PagedUnit u = paged_unit(q, s, block);
+    c.first = u.first;
     c.t0 = u.t0;
     c.n = u.n;
     c.p0 = u.p0;
     c.len = u.len;
     c.n_sink = c.m0 = c.count = 0;
     if (u.n <= 0) return c;
-    const RowKeys first = paged_row(q, u.p0);
+    const RowKeys first = paged_first_row(q, u);
     const int last = u.p0 + u.n;
     c.m0 = first.lo / kPagedChunk;
     const int m1 = (last + kPagedChunk - 1) / kPagedChunk;

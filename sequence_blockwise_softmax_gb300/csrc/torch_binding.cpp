@@ -200,28 +200,40 @@ struct Pool {
     void *k, *v;
     int64_t n_pages, page, Hkv, d, stride;
 };
-bool gapless(const at::Tensor &t) { return t.is_contiguous() || (t.size(0) > 0 && t.select(0, 0).is_contiguous()); }
+// Whether t[0] (t[0][0] with `from` 2) has no gaps.
+bool gapless(const at::Tensor &t, int64_t from = 1) {
+    int64_t next = 1;
+    for (int64_t i = t.dim() - 1; i >= from; --i) {
+        if (t.size(i) != 1 && t.stride(i) != next) return t.is_contiguous();     // (or is empty)
+        next *= t.size(i);
+    }
+    return t.size(0) > 0 || t.is_contiguous();
+}
 // ... and of the layers [layers, n_pages, page, H_kv, d] with one layer stride, or of one pool.
 struct Layers {
     Pool pool;
     int64_t n, stride;
 };
-Pool pool_of(const at::Tensor &k, const at::Tensor &v) {
-    if (k.dim() != 4 || v.sizes() != k.sizes())
-        refuse(PyExc_ValueError, "k_pages and v_pages must have one shape, [n_pages, page, H_kv, d]");
-    Pool p{k.data_ptr(), v.data_ptr(), k.size(0), k.size(1), k.size(2), k.size(3), 0};
-    p.stride = p.n_pages > 1 ? k.stride(0) : p.page * p.Hkv * p.d;
-    if (!gapless(k) || !gapless(v) || (p.n_pages > 1 && v.stride(0) != p.stride))
+// (`axis`: that of the pages)
+Pool pool_of(const at::Tensor &k, const at::Tensor &v, int64_t axis) {
+    Pool p{k.data_ptr(), v.data_ptr(), k.size(axis), k.size(axis + 1), k.size(axis + 2), k.size(axis + 3), 0};
+    p.stride = p.n_pages > 1 ? k.stride(axis) : p.page * p.Hkv * p.d;
+    if (!gapless(k, axis + 1) || !gapless(v, axis + 1) || (p.n_pages > 1 && v.stride(axis) != p.stride))
         refuse(PyExc_ValueError, "k_pages and v_pages: a page must be contiguous, and both pools have one page stride");
     return p;
 }
-Pool pool(PyObject *ko, PyObject *vo) { return pool_of(tensor(ko, "k_pages"), tensor(vo, "v_pages")); }
+Pool pool(PyObject *ko, PyObject *vo) {
+    const at::Tensor &k = tensor(ko, "k_pages"), &v = tensor(vo, "v_pages");
+    if (k.dim() != 4 || v.sizes() != k.sizes())
+        refuse(PyExc_ValueError, "k_pages and v_pages must have one shape, [n_pages, page, H_kv, d]");
+    return pool_of(k, v, 0);
+}
 Layers layers(PyObject *ko, PyObject *vo) {
     const at::Tensor &k = tensor(ko, "k_pages"), &v = tensor(vo, "v_pages");
-    if (k.dim() != 5) return {pool_of(k, v), 1, 0};
+    if (k.dim() != 5) return {pool(ko, vo), 1, 0};
     if (v.sizes() != k.sizes() || k.size(0) < 1 || (k.size(0) > 1 && v.stride(0) != k.stride(0)))
         refuse(PyExc_ValueError, "k_pages and v_pages must have one shape and layer stride, and a layer at least");
-    return {pool_of(k.select(0, 0), v.select(0, 0)), k.size(0), k.size(0) > 1 ? k.stride(0) : 0};
+    return {pool_of(k, v, 1), k.size(0), k.size(0) > 1 ? k.stride(0) : 0};
 }
 
 int pool_device(PyObject *first, const char *name, PyObject *ko, PyObject *vo) {
