@@ -32,6 +32,7 @@
 #include "ra_device.cuh"
 #include "ra_internal.h"
 #include "ra_paged.cuh"
+#include "ra_tree.cuh"
 
 namespace ra {
 
@@ -58,18 +59,6 @@ struct __align__(16) TreeCut {
     int t0, n, hk, more;
 };
 
-// A piece of a unit: `tiles` tiles of its walk from number i0 on (tiles < 0: the
-// queue's end).  The walk's n_main, last and s0 are TreeWalk's.
-struct __align__(16) TreeSegment {
-    int tiles, i0, n_main, last, s0;
-    int s, hk, t0, n, first;        // sequence, head, the unit's tokens (PagedUnit)
-    int before, len;                // the sequence's tokens before the new ones, and in all
-    int whole;                      // the piece is the unit
-    int begins, more;               // in the CTA's run; how many runs it goes on through
-    int places;                     // of the list
-};
-static_assert(sizeof(TreeSegment) == 64, "a quarter of a shared-memory line");
-
 template <int D>
 struct TreeSmem {
     static constexpr uint32_t kTile = 128u * D * 2u;     // 128 rows x d bf16
@@ -89,35 +78,6 @@ struct TreeSmem {
 };
 static_assert(TreeSmem<128>::kBytes <= 232448, "what a CTA may have");
 
-// A sequence as a run meets it: rows [c0, c1), len tokens in the cache, and the blocks
-// (units of one head) of its rows.
-struct TreeSeq {
-    int s, c0, c1, len, blocks;
-};
-__device__ __forceinline__ TreeSeq tree_seq(const PagedSeqs &q, int s) {
-    TreeSeq t;
-    t.s = s;
-    t.c0 = paged_bound(q, s);
-    t.c1 = paged_bound(q, s + 1);
-    t.len = paged_len(q, s);
-    const int n = min(t.c1 - t.c0, q.max_new);
-    t.blocks = n > 0 ? (n + q.unit_tokens - 1) / q.unit_tokens : 0;
-    return t;
-}
-__device__ __forceinline__ PagedUnit tree_unit(const PagedSeqs &q, const TreeSeq &t, int b) {
-    return paged_unit_of(q, t.s, t.c0, t.c1, t.len, b);
-}
-// Tiles of a block; one that sees no key takes one place in the list all the same,
-// so that its rows are written.
-__device__ __forceinline__ int tree_block_cost(const PagedSeqs &q, const TreeSeq &t, int b) {
-    return max(paged_walk(q, tree_unit(q, t, b)).end, 1);
-}
-__device__ __forceinline__ long long tree_head_cost(const PagedSeqs &q, const TreeSeq &t) {
-    long long sum = 0;
-    for (int b = 0; b < t.blocks; ++b) sum += tree_block_cost(q, t, b);
-    return sum;
-}
-
 __device__ __forceinline__ void st_shared_f4(uint32_t addr, const float4 &x) {
     asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w) : "memory");
 }
@@ -126,16 +86,6 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(addr) : "memory");
     return x;
 }
-// a / b for b > 0, a >= 0
-__device__ __forceinline__ long long div_pos(long long a, long long b) {
-    return (a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
-}
-// Key tile number j of a segment (TreeWalk's order).
-__device__ __forceinline__ int tree_tile(const TreeSegment &e, int j) {
-    const int i = e.i0 + j;
-    return i < e.n_main ? e.last - i : e.s0 + (i - e.n_main);
-}
-
 // The denominator's range in which the exponentials' reference stays (see
 // attn_fwd_kernel.cuh).
 constexpr float kTreeSumLo = 0x1p-32f, kTreeSumHi = 0x1p32f;
@@ -154,33 +104,6 @@ __device__ __forceinline__ void tree_store8(const TreeArgs &a, size_t to, int c0
 }
 __device__ __forceinline__ void tree_store_lse(const TreeArgs &a, size_t tok, int head, float top, float l) {
     if (a.lse) a.lse[(size_t)head * a.seqs.T + tok] = l > 0.f ? (top + lg2(l)) * 0.6931471805599453f : -INFINITY;
-}
-
-// The part of block b of a sequence from tile i0 of it on that lies in a run, whose places from
-// `pos` on it takes.
-__device__ __forceinline__ TreeSegment tree_segment(const PagedSeqs &q, const TreeSeq &t, int head, int b, int i0,
-                                                    long long pos, long long end, long long per, int run) {
-    const PagedUnit u = tree_unit(q, t, b);
-    const TreeWalk w = tree_walk(paged_walk(q, u));
-    const int cost = max(w.end, 1), i1 = (int)min((long long)cost, i0 + (end - pos));
-    TreeSegment e;
-    e.places = i1 - i0;
-    e.i0 = min(i0, w.end);
-    e.tiles = min(i1, w.end) - e.i0;
-    e.n_main = w.n_main;
-    e.last = w.last;
-    e.s0 = w.s0;
-    e.s = u.s;
-    e.hk = head;
-    e.t0 = u.t0;
-    e.n = u.n;
-    e.first = u.first;
-    e.before = u.p0 - u.first;
-    e.len = u.len;
-    e.begins = i0 == 0;
-    e.whole = i0 == 0 && i1 == cost;
-    e.more = i1 == cost ? 0 : (int)div_pos(pos - i0 + cost - 1, per) - run;
-    return e;
 }
 
 template <int D>
@@ -328,10 +251,7 @@ __global__ void __launch_bounds__(384, 1)
         TreeSegment e{};
         e.tiles = -1;
         if (pos < end) {
-            const int head = (int)div_pos(off, head_cost);
-            int i0 = (int)(off - head * head_cost), b = 0;
-            for (int c; b + 1 < seq.blocks && i0 >= (c = tree_block_cost(sq, seq, b)); ++b) i0 -= c;
-            e = tree_segment(sq, seq, head0 + head, b, i0, pos, end, per, run);
+            e = tree_first_segment(sq, seq, head_cost, head0, off, pos, end, per, run);
         }
         if (lane == 0) segs[0] = e;
     }
@@ -611,23 +531,14 @@ __global__ void __launch_bounds__(384, 1)
         };
         if (lane == 0) mbar_arrive(BAR(B_SEGFULL));      // (of the first segment)
         TreeSegment e = segs[0];
-        int seg = 1, b = e.first / sq.unit_tokens;
+        int seg = 1;
         bool ok = post_parents(0, e);
         TreeCut cut{0, 0, 0, 0};
         while (true) {
             pos += e.places;
             if (!e.whole && e.begins) cut = TreeCut{e.t0, e.n, e.hk, e.more};
             if (!ok || pos >= end) break;
-            int head = e.hk;
-            if (++b == seq.blocks) {
-                b = 0;
-                if (++head == head0 + args.heads) {
-                    head = head0;
-                    do seq = tree_seq(sq, seq.s + 1);
-                    while (seq.blocks == 0);
-                }
-            }
-            e = tree_segment(sq, seq, head, b, 0, pos, end, per, run);
+            e = tree_next_segment(sq, seq, e, head0, args.heads, pos, end, per, run);
             ok = post(seg++, e);
         }
         if (lane == 0) args.cuts[blockIdx.x] = cut;

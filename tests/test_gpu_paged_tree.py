@@ -287,3 +287,98 @@ def test_binding_refuses(ralib, gpu):
             call(**kw)
     with pytest.raises(ralib.RAError):
         call(new=1025)
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(9, 3, 128), (10, 5, 64), (7, 7, 128), (22, 11, 64), (24, 12, 128), (40, 1, 64)])
+def test_head_counts(ralib, gpu, H, Hkv, d):
+    """Key/value heads whose lists do not divide the GPU evenly, or are several heads long."""
+    new, lens = [33, 40, 2, 60], [700, 4000, 300, 61]
+    c = Cache(lens, 32, Hkv, d, 43)
+    c.fill_all()
+    q = randn_bf16((sum(new), H, d), 44).cuda()
+    trees = trees_of(new, "levels")
+    o, lse, _ = attend(ralib, c, q, cu_of(new), trees, torch.bfloat16)
+    assert_trees(c, q, o, lse, trees, 0, 0)
+
+
+@pytest.mark.parametrize("n,longest,new_max", [(40, 900, 40), (500, 200, 40), (1200, 60, 3), (33, 9000, 8)])
+def test_many_sequences_in_runs(ralib, gpu, n, longest, new_max):
+    """More sequences than a warp or a block has threads, most of them without new tokens."""
+    r = random.Random(n)
+    new = [r.choice([0, 0, r.randint(1, new_max)]) for _ in range(n)]
+    new[n // 2] = new_max
+    lens = [x + r.randint(0, longest) for x in new]
+    c = Cache(lens, 16, 4, 64, 73)
+    c.fill_all()
+    q = randn_bf16((sum(new), 16, 64), 5).cuda()
+    trees = trees_of(new, "forest")
+    for max_len in (max(lens), 1 << 22):
+        o, lse, _ = attend(ralib, c, q, cu_of(new), trees, torch.bfloat16, max_len=max_len)
+        assert_trees(c, q, o, lse, trees, 0, 0)
+
+
+def test_sequences_that_see_nothing_among_others(ralib, gpu):
+    """A sequence shorter than its new tokens in the middle of a run: its rows before place 0 are
+    empty, the others are the definition's."""
+    new, lens, H, d = [40, 50, 33], [900, 50, 1200], 8, 64
+    c = Cache(lens, 16, 2, d, 47)
+    c.fill_all()
+    q = randn_bf16((sum(new), H, d), 3).cuda()
+    trees = trees_of(new, "star")
+    c.seq_lens[1] = 0
+    o, lse, _ = attend(ralib, c, q, cu_of(new), trees, torch.bfloat16, check=False)
+    assert bool((o[40:90] == 0).all()) and bool(torch.isneginf(lse[:, 40:90]).all())
+    good = Cache.__new__(Cache)
+    for s, at in ((0, 0), (2, 90)):
+        good.lens, good.ks, good.vs = [lens[s]], [c.ks[s]], [c.vs[s]]
+        rows = slice(at, at + new[s])
+        assert_trees(good, q[rows], o[rows], lse[:, rows], [trees[s]], 0, 0)
+
+
+@pytest.mark.parametrize("n", [8, 40])
+def test_two_graphs_share_a_workspace(ralib, gpu, n):
+    """Two captured calls of different sizes, replayed in turns on one workspace, and an eager one between."""
+    shapes = [([n, n], [5000, 700], 8, 2, 128), ([n], [20000], 16, 4, 64)]
+    ws = ralib.new_workspace(64 << 20)
+    work = []
+    for new, lens, H, Hkv, d in shapes:
+        c = Cache(lens, 32, Hkv, d, 51)
+        c.fill_all()
+        q = randn_bf16((sum(new), H, d), 7).cuda()
+        trees = trees_of(new, "levels")
+        o, lse = torch.empty_like(q), torch.empty((H, sum(new)), device="cuda")
+        args = (q, c.k, c.v, c.table, c.seq_lens, cu_of(new), flat(trees), o, lse, max(new), max(lens))
+        ralib.ra_paged_tree_attn_fwd(*args, workspace=ws)
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            ralib.ra_paged_tree_attn_fwd(*args, workspace=ws)
+        work.append((c, q, o, lse, trees, graph, args))
+    for i in range(6):
+        c, q, o, lse, trees, graph, args = work[i % 2]
+        o.fill_(NAN)
+        graph.replay()
+        if i > 2:
+            ralib.ra_paged_tree_attn_fwd(*work[1 - i % 2][6], workspace=ws)
+        ralib.ra_check_status(ws)
+        assert_trees(c, q, o, lse, trees, 0, 0)
+
+
+@pytest.mark.parametrize("n", [8, 40])
+def test_two_streams_two_workspaces(ralib, gpu, n):
+    new, lens = [n] * 3, [20000, 300, 7000]
+    c = Cache(lens, 64, 2, 128, 83)
+    c.fill_all()
+    q = randn_bf16((3 * n, 8, 128), 4).cuda()
+    trees = trees_of(new, "bush")
+    want, want_lse, _ = attend(ralib, c, q, cu_of(new), trees, torch.bfloat16)
+    cu, parents = cu_of(new), flat(trees)
+    outs = [(torch.cuda.Stream(), torch.empty_like(want), torch.empty_like(want_lse), ralib.new_workspace(48 << 20)) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, o, lse, ws in outs:
+            ralib.ra_paged_tree_attn_fwd(q, c.k, c.v, c.table, c.seq_lens, cu, parents, o, lse, n, max(lens), workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for _, o, lse, ws in outs:
+        ralib.ra_check_status(ws)
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)

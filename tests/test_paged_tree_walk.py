@@ -1,4 +1,4 @@
-"""The tree attention's own units, walks, chains and chunks, counted on the host (tests/tree_probe.cu),
+"""The tree attention's own units, runs, chains and chunks, counted on the host (tests/tree_probe.cu),
 and what the calls on trees refuse."""
 import ctypes
 import os
@@ -70,19 +70,22 @@ def test_every_pair_once(probe, new, lens, page, max_pages, window, sinks, shape
     cu, sl = _ints(np.concatenate([[0], np.cumsum(new)])), _ints(lens)
     parents = _ints([x for t in trees for x in t] + [-9, 77])
     p = lambda a: ctypes.c_void_p(a.ctypes.data)
-    for group, unit, splits, share in ((1, 256, 1, 0), (4, 64, 3, 0), (5, 50, 2, 100), (128, 2, 9, 0)):
-        cnt = np.zeros((T, cap), dtype=np.int32)
-        assert probe.ra_test_tree_tiles(p(sl), p(cu), p(parents), len(new), T, max_pages, page, group, unit, max(new), window,
-                                        sinks, splits, share, p(cnt)) == 0
-        assert np.array_equal(cnt, want), (group, splits)
+    # group, heads, tokens of a unit, lists, runs of each, places of a run at least
+    for group, heads, unit, streams, runs, least in ((1, 1, 256, 1, 1, 4), (4, 3, 32, 3, 50, 4), (5, 2, 25, 1, 7, 1),
+                                                     (128, 2, 1, 2, 76, 4), (16, 8, 8, 8, 19, 2)):
+        cnt = np.zeros((T, heads, cap), dtype=np.int32)
+        assert probe.ra_test_tree_runs(p(sl), p(cu), p(parents), len(new), T, max_pages, page, group, heads, unit, max(new),
+                                       window, sinks, streams, runs, least, p(cnt)) == 0, (group, runs)
+        assert np.array_equal(cnt, np.broadcast_to(want[:, None], cnt.shape)), (group, runs)
     if max(new) <= 32:
-        cnt = np.zeros((T, cap), dtype=np.int32)
-        assert probe.ra_test_tree_chunks(p(sl), p(cu), p(parents), len(new), T, max_pages, page, max(new), window, sinks,
-                                         p(cnt)) == 0
-        assert np.array_equal(cnt, want)
+        for block in (max(new), 4, 1):
+            cnt = np.zeros((T, cap), dtype=np.int32)
+            assert probe.ra_test_tree_chunks(p(sl), p(cu), p(parents), len(new), T, max_pages, page, max(new), window, sinks,
+                                             block, p(cnt)) == 0
+            assert np.array_equal(cnt, want), block
 
 
-@pytest.mark.parametrize("form", ["tiles", "chunks"])
+@pytest.mark.parametrize("form", ["runs", "chunks"])
 def test_what_is_no_tree_stays_inside(probe, form):
     """Parents of any value: a node out of its range counts as a root, nothing is read outside."""
     new, lens, page, max_pages = [8, 24], [60, 200], 16, 16
@@ -96,10 +99,10 @@ def test_what_is_no_tree_stays_inside(probe, form):
         trees = [[int(x) if -1 <= x < i else -1 for i, x in enumerate(raw[a:b])] for a, b in ((0, 8), (8, 32))]
         want = _want(trees, lens, cap, T)(0, 0)
         cnt = np.zeros((T, cap), dtype=np.int32)
-        if form == "tiles":
-            rc = probe.ra_test_tree_tiles(p(sl), p(cu), p(raw), 2, T, max_pages, page, 4, 64, 24, 0, 0, 1, 0, p(cnt))
+        if form == "runs":
+            rc = probe.ra_test_tree_runs(p(sl), p(cu), p(raw), 2, T, max_pages, page, 4, 1, 32, 24, 0, 0, 1, 3, 1, p(cnt))
         else:
-            rc = probe.ra_test_tree_chunks(p(sl), p(cu), p(raw), 2, T, max_pages, page, 24, 0, 0, p(cnt))
+            rc = probe.ra_test_tree_chunks(p(sl), p(cu), p(raw), 2, T, max_pages, page, 24, 0, 0, 4, p(cnt))
         assert rc == 0 and np.array_equal(cnt, want)
 
 

@@ -1,8 +1,11 @@
 // Test helper, not part of the library: runs on the host what the tree forms of
-// paged attention run (ra_paged.cuh): the tensor-core form's units, splits, walk
-// and chains, and the few-row form's chunks and windows, counting for every new
-// token and place of the cache how often the pair is let through.
+// paged attention run (ra_paged.cuh, ra_tree.cuh): the tensor-core form's units,
+// runs, walk and chains, and the few-row form's blocks, chunks and windows, counting
+// for every new token and place of the cache how often the pair is let through.
+#include <vector>
+
 #include "ra_paged.cuh"
+#include "ra_tree.cuh"
 
 namespace {
 
@@ -30,95 +33,134 @@ ra::PagedSeqs seqs(const int *seq_lens, const int *cu_q, const int *parents, int
 
 extern "C" {
 
-// cnt[t * cap + place], cap = max_pages * page.  Returns 0, or what went wrong.
-int ra_test_tree_tiles(const int *seq_lens, const int *cu_q, const int *parents, int n_seqs, int T, int max_pages, int page,
-                       int H, int unit_tokens, int max_new, int window, int sinks, int num_splits, int tail_share, int *cnt) {
-    ra::PagedSeqs q = seqs(seq_lens, cu_q, parents, n_seqs, T, max_pages, page, H, max_new, window, sinks);
+// cnt[(t * Hkv + head) * cap + place], cap = max_pages * page: `streams` lists of Hkv / streams
+// heads, `runs` runs of each, of min_run places at least.  Returns 0, or what went wrong.
+int ra_test_tree_runs(const int *seq_lens, const int *cu_q, const int *parents, int n_seqs, int T, int max_pages, int page,
+                      int group, int Hkv, int unit_tokens, int max_new, int window, int sinks, int streams, int runs,
+                      int min_run, int *cnt) {
+    ra::PagedSeqs q = seqs(seq_lens, cu_q, parents, n_seqs, T, max_pages, page, group * Hkv, max_new, window, sinks);
+    q.Hkv = Hkv;
+    q.group = group;
     q.unit_tokens = unit_tokens;
-    q.num_splits = num_splits;
-    q.tail_share = tail_share;
     const size_t cap = (size_t)max_pages * page;
-    const int64_t units = ra::paged_units(T, n_seqs, unit_tokens);
+    const int heads = Hkv / streams;
     static short node_parent[ra::kTreeMost];
-    for (int u = 0; u < units; ++u) {
-        const int s = ra::paged_find_seq(q, u);
-        const ra::PagedUnit pu = ra::paged_unit(q, s, u - ra::paged_first_unit(q, s));
-        if (pu.n <= 0) continue;
-        bool bad = false;
-        if (pu.first + pu.n > ra::kTreeMost) return 1;
-        for (int i = 0; i < pu.first + pu.n; ++i)
-            node_parent[i] = (short)ra::tree_parent(parents, pu.t0 - pu.first, i, bad);
-        const int before = pu.p0 - pu.first;
-        const ra::RowKeys first = ra::paged_first_row(q, pu);
-        const ra::TreeWalk whole = ra::tree_walk(ra::paged_walk(q, pu));
-        const int parts = ra::paged_split_count(q, whole.end), per = ra::paged_split_tiles(q, whole.end);
-        for (int part = 0; part < parts; ++part) {
-            for (int i = 0; i < pu.n; ++i) {
-                const int node = pu.first + i;
-                int depth = 0;
-                if (window > 0)
-                    for (int p = node_parent[node]; p >= 0; p = node_parent[p]) ++depth;
-                const ra::RowKeys r = ra::tree_row(q, before + depth, before);
-                ra::TreeChain chain;
-                chain.start(node, depth, before, window, sinks);
-                ra::TreeWalk w = whole;
-                if (num_splits > 1) {
-                    w.i = part * per;
-                    w.end = w.end < w.i + per ? w.end : w.i + per;
-                }
-                for (w.start_step(); w.valid(); w.next()) {
-                    if (w.tile < 0) return 2;
-                    uint32_t drafted[4] = {0, 0, 0, 0};
-                    if (w.tile * 128 + 128 > before) chain.tile(node_parent, w.tile * 128 - before, drafted);
-                    for (int c = 0; c < 128; ++c) {
-                        const int k = w.tile * 128 + c;
-                        const bool bit = (drafted[c >> 5] >> (c & 31)) & 1;
-                        const bool old = (k >= r.lo && k < r.hi) || (k >= r.slo && k < r.shi);
-                        if (bit && old) return 3;
-                        if (!bit && !old) continue;
-                        if (!ra::paged_needed(first, pu.p0 + pu.n, pu.len, k, 1) || (size_t)k >= cap) return 4;
-                        ++cnt[(size_t)(pu.t0 + i) * cap + k];
+    std::vector<int> stored((size_t)T * Hkv);       // how often a row's unit was begun
+    for (int stream = 0; stream < streams; ++stream) {
+        const int head0 = stream * heads;
+        long long total = 0;
+        for (int s = 0; s < n_seqs; ++s) total += ra::tree_head_cost(q, ra::tree_seq(q, s)) * heads;
+        const long long each = (total + runs - 1) / runs, per = each > min_run ? each : min_run;
+        struct {
+            int more, run, t0, hk;
+        } open{0, 0, 0, 0};        // the unit that the run before left, and in how many runs it goes on
+        for (int run = 0; run < runs; ++run) {
+            long long pos = run * per;
+            const long long end = pos + per < total ? pos + per : total;
+            if (pos >= total) break;
+            long long off = pos;
+            int s = 0;
+            for (long long c; off >= (c = ra::tree_head_cost(q, ra::tree_seq(q, s)) * heads); ++s) off -= c;
+            ra::TreeSeq seq = ra::tree_seq(q, s);
+            ra::TreeSegment e = ra::tree_first_segment(q, seq, ra::tree_head_cost(q, seq), head0, off, pos, end, per, run);
+            int cuts = 0;
+            for (bool first_of_run = true;; first_of_run = false) {
+                if (e.tiles < 0 || e.places < 1 || e.n < 1 || e.hk < head0 || e.hk >= head0 + heads) return 1;
+                if (e.t0 < 0 || e.t0 + e.n > T || e.first + e.n > ra::kTreeMost) return 2;
+                if (!first_of_run && !e.begins) return 3;
+                if (!e.begins) {
+                    // the unit left open, until its note's last run
+                    if (open.t0 != e.t0 || open.hk != e.hk || run > open.run + open.more) return 4;
+                    if ((e.more > 0) != (run < open.run + open.more)) return 5;
+                } else {
+                    if (first_of_run && run > 0 && open.run + open.more >= run) return 6;
+                    for (int i = 0; i < e.n; ++i) ++stored[(size_t)(e.t0 + i) * Hkv + e.hk];
+                    if (!e.whole) {
+                        open = {e.more, run, e.t0, e.hk};
+                        if (++cuts > 1 || e.more < 1) return 7;
                     }
                 }
+                if (e.whole != (e.begins && e.more == 0)) return 8;
+                bool bad = false;
+                for (int i = 0; i < e.first + e.n; ++i)
+                    node_parent[i] = (short)ra::tree_parent(parents, e.t0 - e.first, i, bad);
+                const ra::RowKeys first = ra::paged_row(q, e.before);
+                for (int i = 0; i < e.n; ++i) {
+                    const int node = e.first + i;
+                    int depth = 0;
+                    if (window > 0)
+                        for (int p = node_parent[node]; p >= 0; p = node_parent[p]) ++depth;
+                    const ra::RowKeys r = ra::tree_row(q, e.before + depth, e.before);
+                    if (r.hi != e.before && e.before >= 0) return 9;
+                    ra::TreeChain chain;
+                    chain.start(node, depth, e.before, window, sinks);
+                    for (int j = 0; j < e.tiles; ++j) {
+                        const int tile = ra::tree_tile(e, j);
+                        if (tile < 0) return 10;
+                        uint32_t drafted[4] = {0, 0, 0, 0};
+                        if (tile * 128 + 128 > e.before) chain.tile(node_parent, tile * 128 - e.before, drafted);
+                        for (int c = 0; c < 128; ++c) {
+                            const int k = tile * 128 + c;
+                            const bool bit = (drafted[c >> 5] >> (c & 31)) & 1;
+                            // (as the kernel masks: the sinks from 0 up to shi)
+                            const bool old = (k >= r.lo && k < e.before) || k < r.shi;
+                            if (bit && old) return 11;
+                            if (!bit && !old) continue;
+                            if (!ra::paged_needed(first, e.before + e.first + e.n, e.len, k, 1) || (size_t)k >= cap) return 12;
+                            ++cnt[((size_t)(e.t0 + i) * Hkv + e.hk) * cap + k];
+                        }
+                    }
+                }
+                pos += e.places;
+                if (pos > end) return 13;
+                if (pos == end) break;
+                e = ra::tree_next_segment(q, seq, e, head0, heads, pos, end, per, run);
             }
         }
     }
+    for (int s = 0; s < n_seqs; ++s)
+        for (int t = cu_q[s]; t < cu_q[s + 1] && t < cu_q[s] + max_new; ++t)
+            for (int h = 0; h < Hkv; ++h)
+                if (stored[(size_t)t * Hkv + h] != 1) return 14;
     return 0;
 }
 
 // The few-row form: chunks of 16 keys, chains as 32 bits.
 int ra_test_tree_chunks(const int *seq_lens, const int *cu_q, const int *parents, int n_seqs, int T, int max_pages, int page,
-                        int max_new, int window, int sinks, int *cnt) {
+                        int max_new, int window, int sinks, int block, int *cnt) {
     ra::PagedSeqs q = seqs(seq_lens, cu_q, parents, n_seqs, T, max_pages, page, 1, max_new, window, sinks);
-    q.unit_tokens = q.max_new;
+    q.unit_tokens = block;
+    const int blocks = (q.max_new + block - 1) / block;
     if (q.max_new > 32) return 1;
     const size_t cap = (size_t)max_pages * page;
-    for (int s = 0; s < n_seqs; ++s) {
-        const ra::PagedChunks cl = ra::paged_chunks(q, s);
+    for (int v = 0; v < n_seqs * blocks; ++v) {
+        const ra::PagedChunks cl = ra::paged_chunks(q, v / blocks, v % blocks);
         if (cl.n <= 0) continue;
         bool bad = false;
         uint32_t chain[32];
-        const ra::RowKeys f = ra::tree_row(q, cl.p0, cl.p0), l = ra::paged_row(q, cl.p0 + cl.n - 1);
+        const int before = cl.p0 - cl.first;
+        const ra::RowKeys f = ra::tree_row(q, before, before), l = ra::paged_row(q, cl.p0 + cl.n - 1);
         const int all_lo = l.lo, all_hi = f.hi, all_shi = f.shi > f.slo ? f.shi : 0;
-        for (int i = 0; i < cl.n; ++i) {
-            const int p = ra::tree_parent(parents, cl.t0, i, bad);
+        for (int i = 0; i < cl.first + cl.n; ++i) {
+            const int p = ra::tree_parent(parents, cl.t0 - cl.first, i, bad);
             chain[i] = (1u << i) | (p >= 0 ? chain[p] : 0u);
+            if (i < cl.first) continue;
             int depth = -1;
             for (uint32_t x = chain[i]; x; x &= x - 1) ++depth;
-            const uint32_t seen = window > 0 && depth >= window ? ra::tree_window(chain[i], window, sinks - cl.p0) : chain[i];
-            const ra::RowKeys r = ra::tree_row(q, cl.p0 + depth, cl.p0);
+            const uint32_t seen = window > 0 && depth >= window ? ra::tree_window(chain[i], window, sinks - before) : chain[i];
+            const ra::RowKeys r = ra::tree_row(q, before + depth, before);
             for (int c = 0; c < cl.count; ++c) {
                 const int k0 = ra::paged_chunk_key(cl, c);
                 const bool whole = (k0 >= all_lo && k0 + 16 <= all_hi) || k0 + 16 <= all_shi;
                 for (int k = k0; k < k0 + 16; ++k) {
-                    const int node = k - cl.p0;
+                    const int node = k - before;
                     const bool bit = node >= 0 && node < 32 && ((seen >> node) & 1);
                     const bool old = (k >= r.lo && k < r.hi) || (k >= r.slo && k < r.shi);
                     if (whole && !bit && !old) return 2;
                     if (bit && old) return 3;
                     if (!bit && !old) continue;
                     if ((size_t)k >= cap || k >= cl.len) return 4;
-                    ++cnt[(size_t)(cl.t0 + i) * cap + k];
+                    ++cnt[(size_t)(cl.t0 + i - cl.first) * cap + k];
                 }
             }
         }
