@@ -5,11 +5,6 @@
 
 namespace ra {
 
-unsigned long long next_call_tag() {
-    static std::atomic<unsigned long long> calls{0};
-    return call_tag(calls.fetch_add(1, std::memory_order_relaxed));
-}
-
 ra_status launch_paged_tokens(const TokensLaunch &t, cudaStream_t stream) {
     TokensArgs a{};
     a.seqs = t.seqs;
@@ -25,7 +20,8 @@ ra_status launch_paged_tokens(const TokensLaunch &t, cudaStream_t stream) {
     a.row_blocks = t.row_blocks;
     a.scale_log2 = t.scale_log2;
     a.status = t.status;
-    a.call = next_call_tag();
+    static std::atomic<unsigned long long> calls{0};
+    a.call = call_tag(calls.fetch_add(1, std::memory_order_relaxed));
     a.counters = t.counters;
     a.part_o = t.part_o;
     a.part_ml = t.part_ml;

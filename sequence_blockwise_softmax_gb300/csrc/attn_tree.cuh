@@ -122,7 +122,10 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t s_base = smem_u32(smem);
     if ((s_base & 1023u) != 0u) {
         pdl_wait();
-        if (threadIdx.x == 0) atomicOr(args.status, RA_DEV_SMEM_ALIGN_BIT);
+        if (threadIdx.x == 0) {
+            atomicOr(args.status, RA_DEV_SMEM_ALIGN_BIT);
+            args.cuts[blockIdx.x] = TreeCut{0, 0, 0, 0};
+        }
         return;
     }
     auto BAR = [&](int i) -> uint32_t { return s_base + L::kBars + 8u * (uint32_t)i; };
@@ -386,7 +389,7 @@ __global__ void __launch_bounds__(384, 1)
     } else if (warp == 1) {
         // ================================================= S products
         regs_shrink<56>();
-        const uint64_t dq[2] = {sdesc_sw128(s_base + L::kQ, 16, 1024), sdesc_sw128(s_base + L::kQ + L::kTile, 16, 1024)};
+        const uint64_t dq0 = sdesc_sw128(s_base + L::kQ, 16, 1024), dq1 = sdesc_sw128(s_base + L::kQ + L::kTile, 16, 1024);
         const uint64_t dk0 = sdesc_sw128(ring, 16, KT::kGroup);
         auto issue_s = [&](int g, uint64_t a0, int slot) {
             const uint64_t b0 = dk0 + (uint64_t)(slot * (L::kTile >> 4));
@@ -405,32 +408,37 @@ __global__ void __launch_bounds__(384, 1)
             tc_commit_elect(BAR(B_SFULL + g));
         };
         uint32_t k_parity = 0;   // bit s: parity of the next K load of slot s
-        int n[2] = {0, 0};       // products issued per group
+        int n0 = 0, n1 = 0;      // products issued per group
         bool ok = true;
         int t = 0, q_loads = 0;
         TreeSegment e;
         for (int seg = 0; ok && next_segment(seg, e, ok); ++seg) {
-            if (e.tiles > 0) ok = warp_wait(BAR(B_QFULL), q_loads++ & 1, abort_flag);
+            const int tiles = e.tiles;
+            const bool second = e.n > args.tile_tokens;      // two: there is a second Q tile
+            if (tiles > 0) ok = warp_wait(BAR(B_QFULL), q_loads++ & 1, abort_flag);
 #pragma unroll 1
-            for (int j = 0; ok && j < e.tiles; ++j, ++t) {
+            for (int j = 0; ok && j < tiles; ++j, ++t) {
                 const int sl = k_load(t) % nsl;
                 ok = warp_wait(BAR(B_KF + sl), (k_parity >> sl) & 1u, abort_flag);
                 k_parity ^= 1u << sl;
                 if (!ok) break;
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    if (!ok || !takes(e, g, j)) continue;
-                    if (n[g] > 0 && !(ok = warp_wait(BAR(B_SFREE + g), (n[g] - 1) & 1, abort_flag))) continue;
+                if (two || !(j & 1)) {
+                    if (n0 > 0 && !(ok = warp_wait(BAR(B_SFREE + 0), (n0 - 1) & 1, abort_flag))) break;
                     tc_fence_after();
-                    issue_s(g, two ? dq[g] : dq[0], sl);
-                    ++n[g];
+                    issue_s(0, dq0, sl);
+                    ++n0;
                     __syncwarp();
                 }
-                if (!ok) break;
+                if (two ? second : (j & 1)) {
+                    if (n1 > 0 && !(ok = warp_wait(BAR(B_SFREE + 1), (n1 - 1) & 1, abort_flag))) break;
+                    tc_fence_after();
+                    issue_s(1, two ? dq1 : dq0, sl);
+                    ++n1;
+                }
                 tc_commit_elect(BAR(B_SLOTE + sl));
                 __syncwarp();
             }
-            if (ok && e.tiles > 0) tc_commit_elect(BAR(B_QFREE));
+            if (ok && tiles > 0) tc_commit_elect(BAR(B_QFREE));
         }
         if (!ok) timed_out();
         // every product this warp issued has finished before tensor memory is freed
@@ -442,10 +450,10 @@ __global__ void __launch_bounds__(384, 1)
     } else if (warp == 3) {
         // ================================================= PV products
         regs_shrink<56>();
-        const uint64_t dp[2] = {sdesc_sw128(s_base + L::kP, 16, 1024), sdesc_sw128(s_base + L::kP + 2 * L::kBox, 16, 1024)};
+        const uint64_t dp0 = sdesc_sw128(s_base + L::kP, 16, 1024), dp1 = sdesc_sw128(s_base + L::kP + 2 * L::kBox, 16, 1024);
         const uint64_t dv0 = sdesc_sw128(ring, KT::kHalf, KT::kGroup);
-        auto issue_pv = [&](int g, int slot, bool first) {
-            const uint64_t a0 = dp[g], b0 = dv0 + (uint64_t)(slot * (L::kTile >> 4));
+        auto issue_pv = [&](int g, uint64_t a0, int slot, bool first) {
+            const uint64_t b0 = dv0 + (uint64_t)(slot * (L::kTile >> 4));
             const uint32_t d = tmem + 256 + g * D;
             constexpr uint32_t vs = KT::kStep, hb = L::kBox >> 4;
             if constexpr (P_IN_TMEM) {
@@ -471,32 +479,35 @@ __global__ void __launch_bounds__(384, 1)
             tc_commit_elect(BAR(B_PVDONE + g));
         };
         uint32_t v_parity = 0;   // bit s: parity of the next V load of slot s
-        int n[2] = {0, 0};       // products issued per group
+        int n0 = 0, n1 = 0;      // products issued per group
         bool ok = true;
         int t = 0;
         TreeSegment e;
         for (int seg = 0; ok && next_segment(seg, e, ok); ++seg) {
+            const int tiles = e.tiles;
+            const bool second = e.n > args.tile_tokens;
             TreeWalk w = walk_of(e);
-            bool began[2] = {false, false};
 #pragma unroll 1
-            for (int j = 0; ok && j < e.tiles; ++j, ++t, w.next()) {
+            for (int j = 0; ok && j < tiles; ++j, ++t, w.next()) {
                 const int sl = v_load(t) % nsl;
                 ok = warp_wait(BAR(B_VF + sl), (v_parity >> sl) & 1u, abort_flag);
                 v_parity ^= 1u << sl;
                 if (!ok) break;
                 // what lies behind the last token may be NaN, which a weight of 0 would not remove
                 zero_rows<D, KT>(ring + sl * L::kTile, e.len - w.tile * 128, lane);
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    if (!ok || !takes(e, g, j)) continue;
-                    if (!(ok = warp_wait(BAR(B_PFULL + g), n[g] & 1, abort_flag))) continue;
+                if (two || !(j & 1)) {
+                    if (!(ok = warp_wait(BAR(B_PFULL + 0), n0 & 1, abort_flag))) break;
                     tc_fence_after();
-                    issue_pv(g, sl, !began[g]);
-                    began[g] = true;
-                    ++n[g];
+                    issue_pv(0, dp0, sl, j == 0);
+                    ++n0;
                     __syncwarp();
                 }
-                if (!ok) break;
+                if (two ? second : (j & 1)) {
+                    if (!(ok = warp_wait(BAR(B_PFULL + 1), n1 & 1, abort_flag))) break;
+                    tc_fence_after();
+                    issue_pv(1, dp1, sl, j <= 1 - args.two);
+                    ++n1;
+                }
                 tc_commit_elect(BAR(B_SLOTE + sl));
                 __syncwarp();
             }
