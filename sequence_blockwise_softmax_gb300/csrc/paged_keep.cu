@@ -126,13 +126,24 @@ extern "C" ra_status ra_paged_keep_path(void *k_pages, void *v_pages, const int3
     }
     if (n_seqs == 0) return RA_OK;
     if ((st = check_pointers({workspace}, {seq_lens, cu_new, last, new_lens})) != RA_OK) return st;
-    if (new_lens == seq_lens) return set_error(RA_ERR_INVALID_ARG, "new_lens must not be seq_lens: its blocks read them all along");
     if (!aligned(path, 4)) return set_error(RA_ERR_ALIGNMENT, "the int32 and fp32 vectors must be 4-byte aligned");
-    const bool any = T > 0 && n_layers > 0;
-    if (any) {
+    if (T > 0) {
+        // (the path is walked and its pages looked up without layers too)
         if (n_pages == 0 || max_pages == 0) return set_error(RA_ERR_SHAPE, "new tokens need pages to lie in");
-        if ((st = check_pointers({k_pages, v_pages}, {block_table, parents})) != RA_OK) return st;
+        if ((st = check_pointers({}, {block_table, parents})) != RA_OK) return st;
+        if (n_layers > 0 && (st = check_pointers({k_pages, v_pages}, {})) != RA_OK) return st;
     }
+    // a sequence's blocks read what the call is given all along
+    const struct Words { const int32_t *at; int64_t n; } out[] = {{new_lens, n_seqs}, {path, path ? T : 0}},
+        in[] = {{seq_lens, n_seqs}, {cu_new, n_seqs + 1}, {last, n_seqs}, {parents, T}, {block_table, n_seqs * max_pages}};
+    auto meet = [](const Words &x, const Words &y) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(x.at), b = reinterpret_cast<uintptr_t>(y.at);
+        return x.n > 0 && y.n > 0 && a < b + 4 * (uintptr_t)y.n && b < a + 4 * (uintptr_t)x.n;
+    };
+    for (const Words &x : out)
+        for (const Words &y : in)
+            if (meet(x, y)) return set_error(RA_ERR_INVALID_ARG, "new_lens and path must not overlap what the call reads");
+    if (meet(out[0], out[1])) return set_error(RA_ERR_INVALID_ARG, "new_lens and path must not overlap");
     if (workspace_bytes < RA_WORKSPACE_MIN_BYTES)
         return set_error(RA_ERR_INVALID_ARG, "workspace smaller than RA_WORKSPACE_MIN_BYTES");
     KeepArgs a{};

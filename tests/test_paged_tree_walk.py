@@ -194,3 +194,17 @@ def test_keep_path_refuses(ralib, kw, status):
 
 def test_keep_path_nothing_to_do(ralib):
     assert _keep(ralib.lib(), n=0, kp=0, par=0, last=0, lens=0, new_lens=0, path=0, ws=0) == 0
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(layers=0, par=0), 1),                                             # a path is walked without layers too
+    (dict(layers=0, n_pages=0), 2), (dict(layers=0, max_pages=0), 2),
+    (dict(new_lens=3 * FAKE + 4), 1), (dict(new_lens=3 * FAKE - 4), 1),     # into last, seq_lens ..
+    (dict(path=4 * FAKE), 1), (dict(path=4 * FAKE - 28), 1), (dict(path=4 * FAKE + 28), 1),    # .. parents ..
+    (dict(path=2 * FAKE), 1), (dict(path=2 * FAKE + 4), 1),                 # .. the other output
+])
+def test_keep_path_outputs_apart(ralib, kw, status):
+    """(the block table, cu_new and the values' pages are at FAKE)"""
+    a = dict(lens=6 * FAKE, last=3 * FAKE, par=4 * FAKE, path=5 * FAKE)
+    assert _keep(ralib.lib(), **dict(a, **kw)) == status
+    assert _keep(ralib.lib(), **dict(a, wsb=16)) == 1 and "workspace" in ralib.lib().ra_last_error().decode()
