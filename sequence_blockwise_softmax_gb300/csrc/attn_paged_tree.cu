@@ -38,10 +38,10 @@ ra_status launch_tree(const TreeLaunch &t, const CUtensorMap &q, const CUtensorM
         return launched(launch_dependent(join, (unsigned)(many ? kTreeCtas : 3 * kTreeCtas), 256, 0, stream, a, t.ctas));
     };
     if (t.d == 128)
-        return go(paged_tree_kernel<128>, many ? paged_tree_join_kernel<128, 10> : paged_tree_join_kernel<128, 4>,
-                  (int)TreeSmem<128>::kBytes);
-    return go(paged_tree_kernel<64>, many ? paged_tree_join_kernel<64, 10> : paged_tree_join_kernel<64, 4>,
-              (int)TreeSmem<64>::kBytes);
+        return go(t.two ? paged_tree_kernel<128, true> : paged_tree_kernel<128, false>,
+                  many ? paged_tree_join_kernel<128, 10> : paged_tree_join_kernel<128, 4>, (int)TreeSmem<128>::kBytes);
+    return go(t.two ? paged_tree_kernel<64, true> : paged_tree_kernel<64, false>,
+              many ? paged_tree_join_kernel<64, 10> : paged_tree_join_kernel<64, 4>, (int)TreeSmem<64>::kBytes);
 }
 
 }  // namespace ra

@@ -23,9 +23,12 @@
 // Warps (384 threads): 0 loads (TMA), 1 issues S, 3 issues PV, 2 finds the
 // segments (pieces of units) of the CTA's run and posts them in a queue of two with their
 // sequence's parents; 4-7 and 8-11 are two softmax groups, a thread to a row.
-// Where units have two Q tiles each group has one of them; where they have one
+// Where units have two Q tiles (TWO) each group has one of them; where they have one
 // (calls of at most 128 rows a unit) the groups take the key tiles in turn and add their
 // rows at the end, which keeps both at work and halves the chain of a tile.
+// One kernel for both kept their counts and slots in registers that the softmax
+// lacks: 512 nodes over 32768 keys, 16 / 4 heads, 129 us at d = 128 and 102 at d = 64
+// against 107 and 84 as two kernels.
 #pragma once
 #include "kv_tile.cuh"
 #include "paged_launch.h"
@@ -106,7 +109,7 @@ __device__ __forceinline__ void tree_store_lse(const TreeArgs &a, size_t tok, in
     if (a.lse) a.lse[(size_t)head * a.seqs.T + tok] = l > 0.f ? (top + lg2(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <int D>
+template <int D, bool TWO>
 __global__ void __launch_bounds__(384, 1)
     paged_tree_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ TreeArgs args) {
@@ -142,9 +145,14 @@ __global__ void __launch_bounds__(384, 1)
     int *run_seq = reinterpret_cast<int *>(smem + L::kMisc + 8);
     short *parents = reinterpret_cast<short *>(smem + L::kParents);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool two = args.two != 0;
-    const int nsl = L::slots(two);
+    constexpr bool two = TWO;
+    constexpr int nsl = L::slots(two);
     const uint32_t ring = s_base + L::ring(two);
+    // load i's slot, and how many loads that slot has had before.  (Both depend on TWO alone: as
+    // divisions by a variable they held up loads and products, 64 sequences of 500-12000
+    // keys 296 us against 287.)
+    auto round_of = [](unsigned i) -> unsigned { return i / nsl; };
+    auto slot_of = [](unsigned i) -> int { return (int)(i % nsl); };
 
     // ---- setup (nothing here reads what the kernel before may still write)
     if (threadIdx.x == 32) {
@@ -309,8 +317,8 @@ __global__ void __launch_bounds__(384, 1)
         regs_shrink<56>();
         uint32_t k_loads = 0, v_loads = 0;   // bit s: slot s has had a load of the kind, bit 8 + s: the parity of its last
         auto load = [&](unsigned i, int page, int tile, int head, bool is_k) -> bool {
-            const int sl = i % nsl;
-            if (i >= (unsigned)nsl && !warp_wait(BAR(B_SLOTE + sl), ((i / nsl) - 1) & 1, abort_flag)) return false;
+            const int sl = slot_of(i);
+            if (i >= (unsigned)nsl && !warp_wait(BAR(B_SLOTE + sl), (round_of(i) - 1) & 1, abort_flag)) return false;
             const uint32_t full = BAR((is_k ? B_KF : B_VF) + sl);
             uint32_t &loads = is_k ? k_loads : v_loads;
             loads = (loads & (1u << sl)) ? loads ^ (256u << sl) : loads | (1u << sl);
@@ -418,7 +426,7 @@ __global__ void __launch_bounds__(384, 1)
             if (tiles > 0) ok = warp_wait(BAR(B_QFULL), q_loads++ & 1, abort_flag);
 #pragma unroll 1
             for (int j = 0; ok && j < tiles; ++j, ++t) {
-                const int sl = k_load(t) % nsl;
+                const int sl = slot_of(k_load(t));
                 ok = warp_wait(BAR(B_KF + sl), (k_parity >> sl) & 1u, abort_flag);
                 k_parity ^= 1u << sl;
                 if (!ok) break;
@@ -489,7 +497,7 @@ __global__ void __launch_bounds__(384, 1)
             TreeWalk w = walk_of(e);
 #pragma unroll 1
             for (int j = 0; ok && j < tiles; ++j, ++t, w.next()) {
-                const int sl = v_load(t) % nsl;
+                const int sl = slot_of(v_load(t));
                 ok = warp_wait(BAR(B_VF + sl), (v_parity >> sl) & 1u, abort_flag);
                 v_parity ^= 1u << sl;
                 if (!ok) break;
@@ -505,7 +513,7 @@ __global__ void __launch_bounds__(384, 1)
                 if (two ? second : (j & 1)) {
                     if (!(ok = warp_wait(BAR(B_PFULL + 1), n1 & 1, abort_flag))) break;
                     tc_fence_after();
-                    issue_pv(1, dp1, sl, j <= 1 - args.two);
+                    issue_pv(1, dp1, sl, j <= 1 - (int)two);
                     ++n1;
                 }
                 tc_commit_elect(BAR(B_SLOTE + sl));
@@ -584,8 +592,11 @@ __global__ void __launch_bounds__(384, 1)
         // A segment's rows: what they see of the tokens before the new ones, their
         // chains, whether they are stored (others see what the last token sees, so that no
         // tile is masked for their sake).
-        int see_lo = 0, see_sinks = 0;       // [see_lo, before) and, of a window's sinks, [0, see_sinks)
-        TreeChain chain;
+        // (counted from the first new token)
+        int see_lo = 0, see_sinks = 0;       // [see_lo, 0) and, of a window's sinks, all below see_sinks
+        // The row's chain (TreeChain) and its bits in the last tile with new tokens.
+        int chain_at = -1, chain_steps = 0, chain_far = 0;
+        uint32_t drafted[4] = {0u, 0u, 0u, 0u};
         bool live = false;
         // (a segment's fields are read from shared memory as they are needed, to keep them
         // out of the tile loop's registers)
@@ -599,9 +610,13 @@ __global__ void __launch_bounds__(384, 1)
             if (sq.window > 0)
                 for (int p = parents[node]; p >= 0; p = parents[p]) ++depth;
             const RowKeys rk = tree_row(sq, e.before + depth, e.before);
-            see_lo = rk.lo;
-            see_sinks = rk.shi;
+            see_lo = rk.lo - e.before;
+            see_sinks = rk.shi - e.before;
+            TreeChain chain;
             chain.start(node, depth, e.before, sq.window, sq.sinks);
+            chain_at = chain.at;
+            chain_steps = chain.steps;
+            chain_far = chain.far;
             return true;
         };
         bool more = begin(0);
@@ -616,10 +631,11 @@ __global__ void __launch_bounds__(384, 1)
             };
             float m_ref = 0.f, l = 0.f, lr = 0.f;   // reference (log2 units), sum, sum of the rounded weights
             int mine = 0;                           // tiles of this segment taken
-            for (int j = 0; j < e.tiles; ++j) {
-                const int first_key = tree_tile(e, j) * 128;
-                if (holds && first_key + 128 <= e.before) let_go();
-                if (!takes(e, g, j)) continue;
+            // The group's tiles j, and the first key of one, counted from the first new token.
+            const int step = two ? 1 : 2, tiles_end = two && g == 1 && e.n <= args.tile_tokens ? 0 : e.tiles;
+            int j = two ? 0 : g, first_new = tree_tile(e, j) * 128 - e.before;
+            while (j < tiles_end) {
+                if (holds && first_new + 128 <= 0) let_go();
                 if (!(ok = warp_wait(BAR(B_SFULL + g), n & 1, abort_flag))) break;
                 if (!warp_live) {
                     mbar_arrive(BAR(B_SFREE + g));
@@ -628,15 +644,28 @@ __global__ void __launch_bounds__(384, 1)
                     mbar_arrive(BAR(B_PFULL + g));
                     ++mine;
                     ++n;
+                    j += step;
+                    first_new = tree_tile(e, j) * 128 - e.before;
                     continue;
                 }
                 tc_fence_after();
                 // columns [lim_lo, lim), the sinks up to sk_hi and the new tokens' bits are seen
-                const int lim = e.before - first_key, lim_lo = see_lo - first_key;
-                const int sk_hi = see_sinks - first_key;
+                const int lim = -first_new, lim_lo = see_lo - first_new, sk_hi = see_sinks - first_new;
                 const bool partial = lim < 128 || lim_lo > 0;
-                uint32_t drafted[4] = {0u, 0u, 0u, 0u};
-                if (holds) chain.tile(parents, first_key - e.before, drafted);
+                bool any_drafted = false;
+                if (holds) {
+                    TreeChain chain;
+                    chain.start(chain_at, 0, 0, sq.window, 0);
+                    chain.steps = chain_steps;
+                    chain.far = chain_far;
+                    uint32_t word[4];
+                    chain.tile(parents, first_new, word);
+                    chain_at = chain.at;
+                    chain_steps = chain.steps;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) drafted[q] = word[q];
+                    any_drafted = (word[0] | word[1] | word[2] | word[3]) != 0u;
+                }
                 uint32_t sr[4][32];
                 auto load_s = [&]() {
 #pragma unroll
@@ -651,7 +680,7 @@ __global__ void __launch_bounds__(384, 1)
                         for (int q = 0; q < 4; ++q) {
                             if (32 * q >= lo_max && 32 * q + 32 <= hi_min) continue;
                             const uint32_t seen = (low_bits(lim - 32 * q) & ~low_bits(lim_lo - 32 * q)) |
-                                                  low_bits(sk_hi - 32 * q) | drafted[q];
+                                                  low_bits(sk_hi - 32 * q) | (holds ? drafted[q] : 0u);
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
                                 if (!(seen & (1u << c))) s[32 * q + c] = -INFINITY;
@@ -696,8 +725,7 @@ __global__ void __launch_bounds__(384, 1)
                     const float ln = l + lt;
                     // (a row may see no column of a tile that its unit visits)
                     const bool bad = !(ln >= kTreeSumLo && ln <= kTreeSumHi) && live &&
-                                     (max(lim_lo, 0) < min(lim, 128) || sk_hi > 0 ||
-                                      (drafted[0] | drafted[1] | drafted[2] | drafted[3]) != 0u);
+                                     (max(lim_lo, 0) < min(lim, 128) || sk_hi > 0 || any_drafted);
                     if (__builtin_expect(__any_sync(0xffffffffu, bad), 0)) {
                         load_s();
                         const float *s = reinterpret_cast<const float *>(&sr[0][0]);
@@ -738,6 +766,9 @@ __global__ void __launch_bounds__(384, 1)
                 lr += lrt;
                 tc_fence_before();
                 mbar_arrive(BAR(B_SFREE + g));
+                j += step;
+                first_new -= 128 * step;
+                if (sq.window > 0) first_new = tree_tile(e, j) * 128 - e.before;    // (the sinks' tiles)
                 // P_g's place is free once the product before has read it, and a segment's first
                 // product may write O once both groups have read the last one's
                 if (!settle()) break;
