@@ -146,9 +146,15 @@ void plan_tree(const Paged &a, Plan &p) {
     const int64_t tiles = (keys + 127) / 128 + 1;
     // no more units than this have rows
     auto most = [&](int tokens) { return (a.T / tokens + active) * a.H_kv; };
-    // a unit of two Q tiles takes 1.85 times as long as one of one
+    // Two Q tiles a unit where SMs have two such tiles each at least, and either they waste
+    // little (a unit of two takes 1.85 times as long as one of one) or the cache's bytes
+    // count.  One against two, in us, 32 / 8 heads, d = 128: 60 nodes over 1000 keys 13.5 /
+    // 14.9, 4000: 17.0 / 19.3, 8192: 24.6 / 22.7, 32000: 51 / 41; 200 nodes over 8192: 41.7 /
+    // 43.5, 32000: 143 / 106; 128 nodes, 16 / 4 heads, d = 64, over 4000: 17.6 / 16.7, 32000:
+    // 36.8 / 32.7.
     const int64_t ones = (a.max_new + p.tile_tokens - 1) / p.tile_tokens;
-    p.two = (ones + 1) / 2 * 50 <= ones * 27;
+    const double load = (double)most(2 * p.tile_tokens) * (double)tiles / kTreeCtas;
+    p.two = ones > 1 && load >= 2 && ((ones + 1) / 2 * 50 <= ones * 27 || load >= 20);
     const int64_t streams = tree_streams(a.H_kv);
     p.units = most((p.two ? 2 : 1) * p.tile_tokens);
     int64_t runs = (p.units * tiles / streams + kTreeMinRun - 1) / kTreeMinRun;

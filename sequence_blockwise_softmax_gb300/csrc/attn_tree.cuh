@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(384, 1)
     const int run = blockIdx.x / args.streams, runs = gridDim.x / args.streams;
     const int head0 = (blockIdx.x - run * args.streams) * args.heads;     // the stream's heads
     long long pos = 0, end = 0, per = 1, off = 0, head_cost = 1;
+    int pad = 1;
     TreeSeq seq{};
     if (sq.n_seqs > 32) {
         // consecutive sequences to a thread, and the sum of what lies before them
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(384, 1)
             if (w < warp) inc += warp_sums[w];
             total += warp_sums[w];
         }
-        per = max(div_pos(total + runs - 1, runs), (long long)args.min_run);
+        per = tree_per(total, runs, args.min_run, two);
         pos = run * per;
         end = min(pos + per, total);
         if (inc - mine <= pos && pos < inc) {
@@ -237,15 +238,24 @@ __global__ void __launch_bounds__(384, 1)
         // a sequence to a lane
         const TreeSeq t = tree_seq(sq, min(lane, sq.n_seqs - 1));
         if (blockIdx.x == 0 && paged_bad_counts(sq, t.s)) atomicOr(args.status, RA_DEV_PAGE_BIT);
-        const long long of_head = lane < sq.n_seqs ? tree_head_cost(sq, t) : 0, mine = of_head * args.heads;
-        long long inc = mine;
+        const int units = (int)__reduce_add_sync(0xffffffffu, lane < sq.n_seqs ? (unsigned)t.blocks : 0u);
+        long long of_head, mine, inc, total;
+#pragma unroll 1
+        while (true) {
+            of_head = lane < sq.n_seqs ? tree_head_cost(sq, t, pad) : 0;
+            mine = inc = of_head * args.heads;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long up = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += up;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += up;
+            }
+            total = __shfl_sync(0xffffffffu, inc, 31);
+            if (pad > 1) break;
+            per = tree_per(total, runs, args.min_run, two);
+            pad = tree_pad((long long)units * args.heads, total, runs, per, two ? 1 : 2);
+            if (pad == 1) break;
+            per = pad;
         }
-        const long long total = __shfl_sync(0xffffffffu, inc, 31);
-        per = max(div_pos(total + runs - 1, runs), (long long)args.min_run);
         pos = run * per;
         end = min(pos + per, total);
         const unsigned found = __ballot_sync(0xffffffffu, inc - mine <= pos && pos < inc);
@@ -262,7 +272,7 @@ __global__ void __launch_bounds__(384, 1)
         TreeSegment e{};
         e.tiles = -1;
         if (pos < end) {
-            e = tree_first_segment(sq, seq, head_cost, head0, off, pos, end, per, run);
+            e = tree_first_segment(sq, seq, head_cost, head0, off, pos, end, per, run, pad);
         }
         if (lane == 0) segs[0] = e;
     }
@@ -557,7 +567,7 @@ __global__ void __launch_bounds__(384, 1)
             pos += e.places;
             if (!e.whole && e.begins) cut = TreeCut{e.t0, e.n, e.hk, e.more};
             if (!ok || pos >= end) break;
-            e = tree_next_segment(sq, seq, e, head0, args.heads, pos, end, per, run);
+            e = tree_next_segment(sq, seq, e, head0, args.heads, pos, end, per, run, pad);
             ok = post(seg++, e);
         }
         if (lane == 0) args.cuts[blockIdx.x] = cut;

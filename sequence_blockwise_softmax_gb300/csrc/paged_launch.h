@@ -99,7 +99,7 @@ ra_status launch_paged_few(const PagedFewLaunch &t, cudaStream_t stream);
 
 // Tree attention's tensor-core form (attn_tree.cuh).
 constexpr int kTreeCtas = 152;              // one to each SM of a GB300
-constexpr int kTreeMinRun = 4;              // tiles of a run at least
+constexpr int kTreeMinRun = 2;              // tiles of a run at least
 
 // The lists of tiles side by side: as many of the key/value heads as divide them, up to eight.
 inline int tree_streams(int64_t H_kv) {
@@ -110,11 +110,12 @@ inline int tree_streams(int64_t H_kv) {
 
 // Whether a call of 17 to 32 rows to a pair runs there: with two row tiles a warp of the
 // few-row form takes 2.3 us for 16 keys at d = 128 (1.2 at d = 64), which holds that form to 4.3
-// TB/s.  8 nodes, in us, few-row form against runs, 32 / 8 heads, d = 128: one sequence of
-// 1000 keys 10 / 14, 2000: 13 / 14, 4000: 16 / 15, 16000: 45 / 24; 4 of 2000-4000: 22 / 23; 16 of
-// 200-1000: 24 / 24, of 2000-4000: 74 / 46; 64 of 100-300: 36 / 36, of 1000-2000: 111 / 83; 8 / 2
-// heads, d = 64: one of 8000: 13 / 14, 16000: 22 / 16; 16 of 2000-4000: 15 / 18, 64 of 1000-2000:
-// 29 / 28.
+// TB/s.  8 nodes, in us, few-row form (in blocks of 16 rows where clusters hold them, see plan in
+// attn_paged.cu) against runs, 32 / 8 heads, d = 128: one sequence of 1000 keys 8.9 / 13.7,
+// 2000: 10.4 / 13.7, 3000: 12.2 / 13.8, 4000: 16 / 13.9, 16000: 45 / 24; 4 of 1000: 10.6 / 14.1, of
+// 2000-4000: 22 / 23; 16 of 200-1000: 24 / 24, of 2000-4000: 74 / 45; 64 of 100-300: 36 / 35, of
+// 1000-2000: 111 / 82; 8 / 2 heads, d = 64: one of 4000: 8.2 / 12.5, 8000: 13 / 13.5, 16000: 22 /
+// 15.5; 16 of 2000-4000: 15.3 / 18.0, 64 of 1000-2000: 29 / 26.
 inline bool tree_in_runs(int64_t pairs, int64_t keys, int d) {
     return keys * d > 400000 || (double)pairs * (double)(keys * d) > 1.6e7;
 }

@@ -3,7 +3,11 @@
 // Plain integer arithmetic callable from host and device (tests/tree_probe.cu
 // runs it on the CPU).  A list has the units of some key/value heads, sequence by
 // sequence, head by head, block of rows by block, and each unit as many places
-// as it has key tiles; a run is `per` places in a row.
+// as it has key tiles; a run is `per` places in a row.  A run that ends one unit and
+// begins another pays for both ends (about 3.5 us), so where there are runs enough each
+// unit is cut on its own: it then has places for whole runs, `pad` at a time (tree_pad).
+// 60 nodes over 1100 keys, 32 / 8 heads, d = 128: 17.2 us cut anywhere, 14.7 so; 3
+// sequences of 1500-3500: 25.2 and 21.8; for about 0.5 us where it changes nothing.
 #pragma once
 #include "ra_paged.cuh"
 
@@ -51,24 +55,46 @@ RA_HD TreeSeq tree_seq(const PagedSeqs &q, int s) {
 RA_HD PagedUnit tree_unit(const PagedSeqs &q, const TreeSeq &t, int b) {
     return paged_unit_of(q, t.s, t.c0, t.c1, t.len, b);
 }
-// Tiles of a block; one that sees no key takes one place in the list all the same,
-// so that its rows are written.
-RA_HD int tree_block_cost(const PagedSeqs &q, const TreeSeq &t, int b) {
-    return tree_max(paged_walk(q, tree_unit(q, t, b)).end, 1);
+// Places of a unit of so many tiles; one that sees no key takes some all the
+// same, so that its rows are written.
+RA_HD int tree_places(int tiles, int pad) {
+    const int n = tree_max(tiles, 1);
+    return pad > 1 ? (n + pad - 1) / pad * pad : n;
 }
-RA_HD long long tree_head_cost(const PagedSeqs &q, const TreeSeq &t) {
+RA_HD int tree_block_cost(const PagedSeqs &q, const TreeSeq &t, int b, int pad = 1) {
+    return tree_places(paged_walk(q, tree_unit(q, t, b)).end, pad);
+}
+RA_HD long long tree_head_cost(const PagedSeqs &q, const TreeSeq &t, int pad = 1) {
     long long sum = 0;
-    for (int b = 0; b < t.blocks; ++b) sum += tree_block_cost(q, t, b);
+    for (int b = 0; b < t.blocks; ++b) sum += tree_block_cost(q, t, b, pad);
     return sum;
+}
+// How long the pieces are when each unit is cut on its own: per, or `step` tiles more where that is
+// little, as it takes that the runs suffice whatever the units' lengths; 1 where they do not or
+// there is one unit.  (No division: this stands before a CTA's first load.)
+RA_HD int tree_pad(long long units, long long total, int runs, long long per, int step) {
+    if (units == 1 || units * 2 > runs || total > (1 << 28)) return 1;
+    for (int k = 0; k < (per < 6 ? 1 : 2); ++k, per += step)
+        if (total + units * (per - 1) < (runs + 1) * per) return (int)per;
+    return 1;
+}
+
+// A run's places: an equal share of the list, and where two groups take a unit's tiles in turn 4
+// instead of 3, which take as long (30 nodes over 5000 keys, 32 / 8 heads, d = 128: 16.6 us
+// against 17.8; but 6 for 5 lose 2, of two sequences of up to 8000).
+RA_HD long long tree_per(long long total, int runs, int least, bool two) {
+    long long per = div_pos(total + runs - 1, runs);
+    if (per < least) per = least;
+    return !two && per == 3 ? 4 : per;
 }
 
 // The part of block b of a sequence from tile i0 of it on that lies in a run, whose places from
 // `pos` on it takes.
 RA_HD TreeSegment tree_segment(const PagedSeqs &q, const TreeSeq &t, int head, int b, int i0, long long pos, long long end,
-                               long long per, int run) {
+                               long long per, int run, int pad = 1) {
     const PagedUnit u = tree_unit(q, t, b);
     const TreeWalk w = tree_walk(paged_walk(q, u));
-    const int cost = tree_max(w.end, 1), i1 = cost < i0 + (end - pos) ? cost : (int)(i0 + (end - pos));
+    const int cost = tree_places(w.end, pad), i1 = cost < i0 + (end - pos) ? cost : (int)(i0 + (end - pos));
     TreeSegment e;
     e.places = i1 - i0;
     e.i0 = i0 < w.end ? i0 : w.end;
@@ -92,15 +118,15 @@ RA_HD TreeSegment tree_segment(const PagedSeqs &q, const TreeSeq &t, int head, i
 // The first segment of a run that begins `off` places behind a sequence's first head's
 // first block; head_cost: the places of one head's blocks.
 RA_HD TreeSegment tree_first_segment(const PagedSeqs &q, const TreeSeq &t, long long head_cost, int head0, long long off,
-                                     long long pos, long long end, long long per, int run) {
+                                     long long pos, long long end, long long per, int run, int pad = 1) {
     const int head = (int)div_pos(off, head_cost);
     int i0 = (int)(off - head * head_cost), b = 0;
-    for (int c; b + 1 < t.blocks && i0 >= (c = tree_block_cost(q, t, b)); ++b) i0 -= c;
-    return tree_segment(q, t, head0 + head, b, i0, pos, end, per, run);
+    for (int c; b + 1 < t.blocks && i0 >= (c = tree_block_cost(q, t, b, pad)); ++b) i0 -= c;
+    return tree_segment(q, t, head0 + head, b, i0, pos, end, per, run, pad);
 }
 // The one after segment e, of the list of heads [head0, head0 + heads); t: e's sequence, then its own.
 RA_HD TreeSegment tree_next_segment(const PagedSeqs &q, TreeSeq &t, const TreeSegment &e, int head0, int heads, long long pos,
-                                    long long end, long long per, int run) {
+                                    long long end, long long per, int run, int pad = 1) {
     int head = e.hk, b = e.first / q.unit_tokens + 1;
     if (b == t.blocks) {
         b = 0;
@@ -110,7 +136,7 @@ RA_HD TreeSegment tree_next_segment(const PagedSeqs &q, TreeSeq &t, const TreeSe
             while (t.blocks == 0);
         }
     }
-    return tree_segment(q, t, head, b, 0, pos, end, per, run);
+    return tree_segment(q, t, head, b, 0, pos, end, per, run, pad);
 }
 
 }  // namespace ra

@@ -70,13 +70,16 @@ def test_every_pair_once(probe, new, lens, page, max_pages, window, sinks, shape
     cu, sl = _ints(np.concatenate([[0], np.cumsum(new)])), _ints(lens)
     parents = _ints([x for t in trees for x in t] + [-9, 77])
     p = lambda a: ctypes.c_void_p(a.ctypes.data)
-    # group, heads, tokens of a unit, lists, runs of each, places of a run at least
-    for group, heads, unit, streams, runs, least in ((1, 1, 256, 1, 1, 4), (4, 3, 32, 3, 50, 4), (5, 2, 25, 1, 7, 1),
-                                                     (128, 2, 1, 2, 76, 4), (16, 8, 8, 8, 19, 2)):
+    # group, heads, tokens of a unit, lists, runs of each, places of a run at least, whether two Q tiles
+    alone = ctypes.c_int(0)
+    for group, heads, unit, streams, runs, least, two in ((1, 1, 256, 1, 1, 4, 1), (4, 3, 32, 3, 50, 4, 0), (5, 2, 25, 1, 7, 1, 0),
+                                                          (128, 2, 1, 2, 76, 4, 0), (16, 8, 8, 8, 19, 2, 0),
+                                                          (4, 4, 64, 2, 76, 2, 1), (1, 4, 512, 1, 60, 1, 1)):
         cnt = np.zeros((T, heads, cap), dtype=np.int32)
         assert probe.ra_test_tree_runs(p(sl), p(cu), p(parents), len(new), T, max_pages, page, group, heads, unit, max(new),
-                                       window, sinks, streams, runs, least, p(cnt)) == 0, (group, runs)
+                                       window, sinks, streams, runs, least, two, ctypes.byref(alone), p(cnt)) == 0, (group, runs)
         assert np.array_equal(cnt, np.broadcast_to(want[:, None], cnt.shape)), (group, runs)
+    assert alone.value > 0          # units were cut on their own in some of them
     if max(new) <= 32:
         for block in (max(new), 4, 1):
             cnt = np.zeros((T, cap), dtype=np.int32)
@@ -100,7 +103,8 @@ def test_what_is_no_tree_stays_inside(probe, form):
         want = _want(trees, lens, cap, T)(0, 0)
         cnt = np.zeros((T, cap), dtype=np.int32)
         if form == "runs":
-            rc = probe.ra_test_tree_runs(p(sl), p(cu), p(raw), 2, T, max_pages, page, 4, 1, 32, 24, 0, 0, 1, 3, 1, p(cnt))
+            rc = probe.ra_test_tree_runs(p(sl), p(cu), p(raw), 2, T, max_pages, page, 4, 1, 32, 24, 0, 0, 1, 3, 1, 0,
+                                         ctypes.byref(ctypes.c_int(0)), p(cnt))
         else:
             rc = probe.ra_test_tree_chunks(p(sl), p(cu), p(raw), 2, T, max_pages, page, 24, 0, 0, 4, p(cnt))
         assert rc == 0 and np.array_equal(cnt, want)

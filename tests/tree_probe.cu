@@ -34,10 +34,11 @@ ra::PagedSeqs seqs(const int *seq_lens, const int *cu_q, const int *parents, int
 extern "C" {
 
 // cnt[(t * Hkv + head) * cap + place], cap = max_pages * page: `streams` lists of Hkv / streams
-// heads, `runs` runs of each, of min_run places at least.  Returns 0, or what went wrong.
+// heads, `runs` runs of each, of min_run places at least; two: the units have two Q tiles; tried: receives how often
+// units were cut on their own.  Returns 0, or what went wrong.
 int ra_test_tree_runs(const int *seq_lens, const int *cu_q, const int *parents, int n_seqs, int T, int max_pages, int page,
                       int group, int Hkv, int unit_tokens, int max_new, int window, int sinks, int streams, int runs,
-                      int min_run, int *cnt) {
+                      int min_run, int two, int *tried, int *cnt) {
     ra::PagedSeqs q = seqs(seq_lens, cu_q, parents, n_seqs, T, max_pages, page, group * Hkv, max_new, window, sinks);
     q.Hkv = Hkv;
     q.group = group;
@@ -50,7 +51,16 @@ int ra_test_tree_runs(const int *seq_lens, const int *cu_q, const int *parents, 
         const int head0 = stream * heads;
         long long total = 0;
         for (int s = 0; s < n_seqs; ++s) total += ra::tree_head_cost(q, ra::tree_seq(q, s)) * heads;
-        const long long each = (total + runs - 1) / runs, per = each > min_run ? each : min_run;
+        long long per = ra::tree_per(total, runs, min_run, two), units = 0;
+        for (int s = 0; s < n_seqs; ++s) units += ra::tree_seq(q, s).blocks;
+        const int pad = ra::tree_pad(units * heads, total, runs, per, two ? 1 : 2);
+        if (pad > 1) {
+            per = pad;
+            total = 0;
+            for (int s = 0; s < n_seqs; ++s) total += ra::tree_head_cost(q, ra::tree_seq(q, s), pad) * heads;
+            if (total > runs * per) return 15;
+            ++*tried;
+        }
         struct {
             int more, run, t0, hk;
         } open{0, 0, 0, 0};        // the unit that the run before left, and in how many runs it goes on
@@ -60,14 +70,15 @@ int ra_test_tree_runs(const int *seq_lens, const int *cu_q, const int *parents, 
             if (pos >= total) break;
             long long off = pos;
             int s = 0;
-            for (long long c; off >= (c = ra::tree_head_cost(q, ra::tree_seq(q, s)) * heads); ++s) off -= c;
+            for (long long c; off >= (c = ra::tree_head_cost(q, ra::tree_seq(q, s), pad) * heads); ++s) off -= c;
             ra::TreeSeq seq = ra::tree_seq(q, s);
-            ra::TreeSegment e = ra::tree_first_segment(q, seq, ra::tree_head_cost(q, seq), head0, off, pos, end, per, run);
+            ra::TreeSegment e = ra::tree_first_segment(q, seq, ra::tree_head_cost(q, seq, pad), head0, off, pos, end, per, run, pad);
             int cuts = 0;
             for (bool first_of_run = true;; first_of_run = false) {
                 if (e.tiles < 0 || e.places < 1 || e.n < 1 || e.hk < head0 || e.hk >= head0 + heads) return 1;
                 if (e.t0 < 0 || e.t0 + e.n > T || e.first + e.n > ra::kTreeMost) return 2;
-                if (!first_of_run && !e.begins) return 3;
+                if (!first_of_run && (!e.begins || pad > 1)) return 3;
+                if (e.tiles == 0 && e.i0 > 0) return 16;
                 if (!e.begins) {
                     // the unit left open, until its note's last run
                     if (open.t0 != e.t0 || open.hk != e.hk || run > open.run + open.more) return 4;
@@ -114,7 +125,7 @@ int ra_test_tree_runs(const int *seq_lens, const int *cu_q, const int *parents, 
                 pos += e.places;
                 if (pos > end) return 13;
                 if (pos == end) break;
-                e = ra::tree_next_segment(q, seq, e, head0, heads, pos, end, per, run);
+                e = ra::tree_next_segment(q, seq, e, head0, heads, pos, end, per, run, pad);
             }
         }
     }
