@@ -188,7 +188,7 @@ Plan plan(Paged a) {
         if (a.tree && a.max_new * group > 16 && group <= 16) {
             // blocks of 16 rows while clusters for all of them stand side by side: half the
             // products to a warp, the keys twice from L2.  8 nodes over 1000 keys, 32 / 8
-            // heads, d = 128: 10.0 us as one block, 8.0 as two.
+            // heads, d = 128: 10.6 us as one block, 8.9 as two.
             const int64_t blocks = (a.max_new + 16 / group - 1) / (16 / group);
             if (paged_tokens_cluster(active0 * blocks * a.H_kv, seen)) p.row_blocks = (int)blocks;
         }

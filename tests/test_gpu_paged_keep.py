@@ -6,6 +6,7 @@ import torch
 
 import tree_reference as tr
 from synthetic_inputs import randn_bf16
+from test_gpu_readme import snippet
 from test_gpu_paged import NAN, Cache, cu_of
 from test_gpu_paged_rotary import frequencies, rotated
 from test_gpu_paged_tree import assert_trees
@@ -279,3 +280,33 @@ def test_rounds_of_drafting_replayed(ralib, gpu, H, Hkv, d, n_draft):
             assert torch.equal(c.k[old], c.ks[s]) and torch.equal(c.v[old], c.vs[s])
             c.ks[s] = c.k[c.places(s, 0, c.lens[s])]
             c.vs[s] = c.v[c.places(s, 0, c.lens[s])]
+
+
+def test_a_server_follows_the_readme(ralib, gpu):
+    """The README's snippet, as it stands there."""
+    n, H, H_kv, d, page, new = 3, 8, 4, 128, 16, [12, 1, 30]
+    lens = [1000, 40, 300]
+    c = Cache(lens, page, H_kv, d, 11)
+    for s, (x, length) in enumerate(zip(new, lens)):
+        c.fill(s, 0, length - x)
+    trees = [tr.random_tree(x, tr.SHAPES[s], s) for s, x in enumerate(new)]
+    T = sum(new)
+    names = dict(ra=ralib, T=T, n=n, H=H, H_kv=H_kv, d=d, max_new=max(new), max_len=max(lens), k_pages=c.k, v_pages=c.v,
+                 block_table=c.table, seq_lens=c.seq_lens, cu=cu_of(new), parents=ints([x for t in trees for x in t]),
+                 q=randn_bf16((T, H, d), 5).cuda(), k_new=randn_bf16((T, H_kv, d), 6).cuda(),
+                 v_new=randn_bf16((T, H_kv, d), 7).cuda(), inv_freq=frequencies(d // 2), last=ints([x - 1 for x in new]),
+                 o=torch.empty((T, H, d), dtype=torch.bfloat16, device="cuda"), lse=torch.empty((H, T), device="cuda"),
+                 q_rot=torch.empty((T, H, d), dtype=torch.bfloat16, device="cuda"), new_lens=ints([0] * n), path=ints([0] * T))
+    lines = snippet("ra_paged_keep_path").split("# last: ")
+    exec(lines[0], names)
+    ks, vs = ([x[c.places(s, 0, m)] for s, m in enumerate(lens)] for x in (c.k, c.v))
+    full = Cache.__new__(Cache)
+    full.lens, full.ks, full.vs = lens, ks, vs
+    assert_trees(full, names["q_rot"], names["o"], names["lse"], trees, 0, 0)
+    exec("# " + lines[1], names)
+    ralib.ra_check_status(names["ws"])
+    for s, (x, m) in enumerate(zip(new, lens)):
+        at = [m - x + a for a in tr.path(trees[s], x - 1)]
+        assert int(names["new_lens"][s]) == m - x + len(at)
+        now = c.places(s, m - x, m - x + len(at))
+        assert torch.equal(c.k[now], ks[s][at]) and torch.equal(c.v[now], vs[s][at])
