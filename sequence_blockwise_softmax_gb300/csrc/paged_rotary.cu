@@ -248,6 +248,8 @@ extern "C" ra_status ra_paged_append_rotary(const void *q, const void *k_new, co
     if (n_pages == 0 || max_pages == 0) return set_error(RA_ERR_SHAPE, "new tokens need pages to lie in");
     if ((st = check_pointers({k_new, v_new, k_pages, v_pages, workspace}, {block_table, seq_lens, cu_new, inv_freq})) != RA_OK) return st;
     if (H > 0 && (st = check_pointers({q, q_out}, {})) != RA_OK) return st;
+    if (H > 0 && q == q_out && q_stride != q_out_stride && T > 1)
+        return set_error(RA_ERR_INVALID_ARG, "queries rotated in place keep their token stride");
     if (!aligned(parents, 4)) return set_error(RA_ERR_ALIGNMENT, "the int32 and fp32 vectors must be 4-byte aligned");
     if (workspace_bytes < RA_WORKSPACE_MIN_BYTES)
         return set_error(RA_ERR_INVALID_ARG, "workspace smaller than RA_WORKSPACE_MIN_BYTES");

@@ -171,6 +171,13 @@ def test_append_rotary_refuses(ralib, kw, status):
     assert ralib.lib().ra_last_error().decode()
 
 
+def test_append_rotary_in_place_keeps_the_stride(ralib):
+    kw = dict(q=2 * FAKE, qo=2 * FAKE, wsb=128)
+    assert _rotary(ralib.lib(), **kw) == 1 and "workspace" in ralib.lib().ra_last_error().decode()
+    assert _rotary(ralib.lib(), qs=1280, **kw) == 1 and "in place" in ralib.lib().ra_last_error().decode()
+    assert _rotary(ralib.lib(), qs=1280, T=1, **kw) == 1 and "workspace" in ralib.lib().ra_last_error().decode()
+
+
 def test_append_rotary_nothing_to_do(ralib):
     for kw in (dict(T=0), dict(n=0)):
         assert _rotary(ralib.lib(), q=0, k=0, qo=0, kp=0, freq=0, ws=0, **kw) == 0
