@@ -202,12 +202,13 @@ struct Pool {
 };
 // Whether t[0] (t[0][0] with `from` 2) has no gaps.
 bool gapless(const at::Tensor &t, int64_t from = 1) {
+    if (t.is_contiguous()) return true;
     int64_t next = 1;
     for (int64_t i = t.dim() - 1; i >= from; --i) {
-        if (t.size(i) != 1 && t.stride(i) != next) return t.is_contiguous();     // (or is empty)
+        if (t.size(i) != 1 && t.stride(i) != next) return false;
         next *= t.size(i);
     }
-    return t.size(0) > 0 || t.is_contiguous();
+    return t.size(0) > 0;
 }
 // ... and of the layers [layers, n_pages, page, H_kv, d] with one layer stride, or of one pool.
 struct Layers {
