@@ -528,8 +528,8 @@ RA_API ra_status ra_paged_append_rotary(const void *q, const void *k_new, const 
  * layers have one block table.  Pages with new rows belong to one sequence each.
  * A last[s] outside -1 .. n - 1, or a page outside the pool, moves nothing (of that
  * row), and ra_check_status() returns RA_ERR_INVALID_ARG.  new_lens and path
- * must overlap neither what the call reads nor each other.  workspace: RA_WORKSPACE_MIN_BYTES bytes, zero-filled before
- * its first use.
+ * must overlap neither what the call reads nor each other.  workspace:
+ * RA_WORKSPACE_MIN_BYTES bytes, zero-filled before its first use.
  */
 RA_API ra_status ra_paged_keep_path(void *k_pages, void *v_pages, const int32_t *block_table,
                                     const int32_t *seq_lens, const int32_t *cu_new, const int32_t *parents,
