@@ -496,8 +496,8 @@ RA_API size_t ra_paged_tree_attn_workspace_bytes(int64_t T, int64_t n_seqs, int6
  *   (x cos(p f) - y sin(p f), x sin(p f) + y cos(p f)),  f = inv_freq[m],
  * the pair being columns m and m + rot / 2, or 2 m and 2 m + 1 with
  * RA_FLAG_ROTARY_PAIRS; the other columns, and the values, are copied.  The angle
- * is taken modulo one turn exactly enough for any position (off by 1e-7 of a
- * radian at most for f <= 1), the rotation computed in fp32 and rounded once.
+ * is taken modulo one turn, off by 1e-7 of a radian at most at any position for f up to
+ * 2^55 of either sign; the rotation is computed in fp32 and rounded once.
  * p is the token's place, seq_lens[s] - n + i, or with parents (else NULL) its
  * position in a tree.
  * q: bf16 [T, H, d] with q_stride elements from token to token, q_out: bf16 [T, H,

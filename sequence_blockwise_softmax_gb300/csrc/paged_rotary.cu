@@ -5,10 +5,7 @@
 // `rot` columns by the angle p f_m:
 //   x' = x cos - y sin,  y' = x sin + y cos,
 // the pair being columns m and m + rot / 2, or 2 m and 2 m + 1.  The angle is
-// taken in turns: f_m / 2 pi as a 64-bit fraction of a turn, times p modulo 2^64,
-// so that whole turns fall away exactly.  The fraction is off by 2^-53 of f_m /
-// 2 pi at most (it passes through 64-bit floating point), the angle at p = 2^29 and f = 1
-// by 6e-8 of a radian; the top 32 bits go to sincospif.
+// taken in turns modulo one (ra_rotary.cuh) and goes to sincospif.
 //
 // Bound by the bytes: each of q, k and v is read once and written once, 2 (H + 2
 // H_kv) d 2 bytes a token.  The call is one list of items, each two 16-byte
@@ -21,6 +18,7 @@
 #include "ra_device.cuh"
 #include "ra_launch.h"
 #include "ra_paged.cuh"
+#include "ra_rotary.cuh"
 
 namespace ra {
 namespace {
@@ -46,12 +44,6 @@ struct RotaryArgs {
     int shift, page_shift;      // log2 of per_head, of the page size
     unsigned *status;
 };
-
-// The turns of a frequency as a fraction of 2^64.
-__device__ __forceinline__ unsigned long long turn_fraction(float f) {
-    const double t = (double)f * 0.15915494309189535;
-    return __double2ull_rd((t - floor(t)) * 18446744073709551616.0);
-}
 
 __device__ __forceinline__ float2 bf16x2(uint32_t x) { return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)); }
 
@@ -167,9 +159,8 @@ __global__ void __launch_bounds__(kThreads, 5) paged_append_rotary_kernel(const 
     __syncthreads();
     for (int e = threadIdx.x; e < n_tok * a.turned * 8; e += kThreads) {
         const int tok = e / (a.turned * 8), m = e - tok * a.turned * 8;
-        const unsigned long long phase = (unsigned long long)(long long)position[tok] * fraction[m];
         float s, c;
-        sincospif((float)(int)(phase >> 32) * 0x1p-31f, &s, &c);
+        sincospif(half_turns(position[tok], fraction[m]), &s, &c);
         float *to = turns + (tok * 8 + (m >> 3)) * kGroup + (m & 7);
         to[0] = c;
         to[8] = s;
