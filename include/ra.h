@@ -501,9 +501,11 @@ RA_API size_t ra_paged_tree_attn_workspace_bytes(int64_t T, int64_t n_seqs, int6
  * p is the token's place, seq_lens[s] - n + i, or with parents (else NULL) its
  * position in a tree.
  * q: bf16 [T, H, d] with q_stride elements from token to token, q_out: bf16 [T, H,
- * d] with q_out_stride, or q itself with q's; rows of no sequence are left as they were.  H
- * = 0: no queries (q, q_out may be NULL).  inv_freq: fp32 [rot / 2] on the device,
- * finite; rot: a multiple of 16, at most d.  flags: 0 or RA_FLAG_ROTARY_PAIRS.
+ * d] with q_out_stride, or q itself with q's; rows of no sequence are left as they were.
+ * q_out's rows must overlap neither k_new's nor v_new's, nor q's but as q itself
+ * (columns of one projection may lie side by side).  H = 0: no queries (q, q_out may
+ * be NULL).  inv_freq: fp32 [rot / 2] on the device, finite; rot: a multiple of 16,
+ * at most d.  flags: 0 or RA_FLAG_ROTARY_PAIRS.
  * The rest as ra_paged_append.
  */
 RA_API ra_status ra_paged_append_rotary(const void *q, const void *k_new, const void *v_new, void *q_out,

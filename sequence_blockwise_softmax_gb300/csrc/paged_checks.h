@@ -47,4 +47,32 @@ inline ra_status check_pointers(std::initializer_list<const void *> tensors, std
     return RA_OK;
 }
 
+// T rows of `width` elements (of 2 bytes), `stride` apart.
+struct TokenRows {
+    const void *at;
+    int64_t stride, width;
+};
+// Whether a row of x and a row of y share an element; rows no wider than their strides.
+inline bool rows_meet(const TokenRows &x, const TokenRows &y, int64_t T) {
+    using Wide = __int128;       // (the largest T and strides reach 2^63 between them)
+    const int64_t a = (int64_t)(reinterpret_cast<uintptr_t>(x.at) / 2), b = (int64_t)(reinterpret_cast<uintptr_t>(y.at) / 2);
+    if (a + (Wide)(T - 1) * x.stride + x.width <= b || b + (Wide)(T - 1) * y.stride + y.width <= a) return false;
+    if (T == 1) return true;
+    if (x.stride == y.stride) {
+        // y's row j begins in x's row j + k or behind it (`in` elements from where that row does), before row j + k + 1
+        int64_t k = (b - a) / x.stride, in = (b - a) % x.stride;
+        if (in < 0) in += x.stride, --k;
+        return (in < x.width && -T < k && k < T) || (in + y.width > x.stride && -T < k + 1 && k + 1 < T);
+    }
+    for (int64_t i = 0; i < T; ++i) {
+        // the last row of y that begins before this row of x ends
+        const Wide from = a + (Wide)i * x.stride, to = from + x.width;
+        if (to <= b) continue;
+        Wide j = (to - 1 - b) / y.stride;
+        if (j > T - 1) j = T - 1;
+        if (b + j * y.stride + y.width > from) return true;
+    }
+    return false;
+}
+
 }  // namespace ra

@@ -242,6 +242,14 @@ extern "C" ra_status ra_paged_append_rotary(const void *q, const void *k_new, co
     if (H > 0 && q == q_out && q_stride != q_out_stride && T > 1)
         return set_error(RA_ERR_INVALID_ARG, "queries rotated in place keep their token stride");
     if (!aligned(parents, 4)) return set_error(RA_ERR_ALIGNMENT, "the int32 and fp32 vectors must be 4-byte aligned");
+    if (H > 0) {
+        // rotated queries go out while other blocks still read (q itself apart, which
+        // each thread reads where it writes)
+        const TokenRows from{q, q_stride, H * d}, to{q_out, q_out_stride, H * d};
+        if ((q != q_out && rows_meet(from, to, T)) || rows_meet({k_new, new_stride, H_kv * d}, to, T) ||
+            rows_meet({v_new, new_stride, H_kv * d}, to, T))
+            return set_error(RA_ERR_INVALID_ARG, "q_out must overlap neither k_new nor v_new, nor q unless it is q");
+    }
     if (workspace_bytes < RA_WORKSPACE_MIN_BYTES)
         return set_error(RA_ERR_INVALID_ARG, "workspace smaller than RA_WORKSPACE_MIN_BYTES");
     RotaryArgs a{};
