@@ -418,6 +418,7 @@ ra_status launch_paged(const Paged &a, const int *table, const int *seq_lens, co
         t.tile_tokens = p.tile_tokens;
         t.page_box = (int)(a.page < 128 ? a.page : 128);
         t.two = p.two;
+        t.in_parts = tree_in_parts(a.max_pages * a.page, t.seqs.max_new, t.seqs.window, t.seqs.sinks);
         t.units = p.units;
         t.ctas = p.ctas;
         t.streams = tree_streams(a.H_kv);

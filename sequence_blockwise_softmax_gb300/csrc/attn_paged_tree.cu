@@ -1,6 +1,7 @@
 // attn_paged_tree.cu -- the launches of tree attention: the few-row form
 // (attn_paged_tokens.cuh) and the tensor-core form (attn_tree.cuh).  The entry
-// point, its checks and its plan are in attn_paged.cu.
+// point, its checks and its plan are in attn_paged.cu; the kernels in parts in
+// attn_paged_tree_long.cu, to be compiled beside these.
 #include "attn_paged_tokens.cuh"
 #include "attn_tree.cuh"
 
@@ -37,11 +38,12 @@ ra_status launch_tree(const TreeLaunch &t, const CUtensorMap &q, const CUtensorM
         if (st != RA_OK || t.ctas == t.streams) return st;       // one run to a stream cuts no unit
         return launched(launch_dependent(join, (unsigned)(many ? kTreeCtas : 3 * kTreeCtas), 256, 0, stream, a, t.ctas));
     };
+    const TreeKernel parts = t.in_parts ? tree_kernel_in_parts(t.d, t.two) : nullptr;
     if (t.d == 128)
-        return go(t.two ? paged_tree_kernel<128, true> : paged_tree_kernel<128, false>,
-                  many ? paged_tree_join_kernel<128, 10> : paged_tree_join_kernel<128, 4>, (int)TreeSmem<128>::kBytes);
-    return go(t.two ? paged_tree_kernel<64, true> : paged_tree_kernel<64, false>,
-              many ? paged_tree_join_kernel<64, 10> : paged_tree_join_kernel<64, 4>, (int)TreeSmem<64>::kBytes);
+        return go(parts ? parts : t.two ? paged_tree_kernel<128, true, false> : paged_tree_kernel<128, false, false>,
+                  many ? paged_tree_join_kernel<128, 10> : paged_tree_join_kernel<128, 4>, (int)TreeSmem<128, true>::kBytes);
+    return go(parts ? parts : t.two ? paged_tree_kernel<64, true, false> : paged_tree_kernel<64, false, false>,
+              many ? paged_tree_join_kernel<64, 10> : paged_tree_join_kernel<64, 4>, (int)TreeSmem<64, true>::kBytes);
 }
 
 }  // namespace ra

@@ -62,7 +62,33 @@ struct __align__(16) TreeCut {
     int t0, n, hk, more;
 };
 
-template <int D>
+// A kernel in PARTS works on a segment by at most kTreePart (1024) tiles at a time, whose rows are added
+// in fp32 where the segment's piece has its place in the workspace.  The tensor cores cut
+// off what lies below 2^-21 of a sum that they add to, at each of a tile's eight products: where
+// values are alike O comes out short by 3e-4 after 1024 tiles, by 5e-3 after 2^20 keys and by a quarter
+// after 2^26.  It also keeps segments well inside the waits' limit of two seconds, which one
+// of 2^28 keys passes.  The code costs d = 64 up to 5 % (500 nodes 43.8 to 45.9 us) and d = 128
+// 0.3 %, so calls whose units cannot be longer (tree_in_parts) do without.
+struct TreePart : TreeSegment {
+    int earlier;            // the segment had parts before
+    int left;               // its tiles behind this part
+    __device__ __forceinline__ void take(int n) {
+        tiles = min(n, kTreePart);
+        left = n - tiles;
+    }
+};
+
+// What goes through the queue of segments.
+template <bool PARTS>
+struct TreeQueued {
+    using Type = TreeSegment;
+};
+template <>
+struct TreeQueued<true> {
+    using Type = TreePart;
+};
+
+template <int D, bool PARTS>
 struct TreeSmem {
     static constexpr uint32_t kTile = 128u * D * 2u;     // 128 rows x d bf16
     static constexpr uint32_t kBox = 128u * 128u;        // 128 rows x 64 columns
@@ -75,11 +101,11 @@ struct TreeSmem {
     static constexpr uint32_t kBars = 224u * 1024;
     static constexpr int kNumBars = 2 + 3 * kMostSlots + 8 + 4 + 2 + 2;
     static constexpr uint32_t kSegs = (kBars + kNumBars * 8 + 15) / 16 * 16;
-    static constexpr uint32_t kMisc = kSegs + 2 * sizeof(TreeSegment);   // tensor memory's address, flags, the scan's sums
+    static constexpr uint32_t kMisc = kSegs + 2 * sizeof(typename TreeQueued<PARTS>::Type);   // tensor memory's address, flags, the scan's sums
     static constexpr uint32_t kParents = kMisc + 128;
     static constexpr uint32_t kBytes = kParents + kTreeMost * 2;
 };
-static_assert(TreeSmem<128>::kBytes <= 232448, "what a CTA may have");
+static_assert(TreeSmem<128, true>::kBytes <= 232448, "what a CTA may have");
 
 __device__ __forceinline__ void st_shared_f4(uint32_t addr, const float4 &x) {
     asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w) : "memory");
@@ -109,11 +135,12 @@ __device__ __forceinline__ void tree_store_lse(const TreeArgs &a, size_t tok, in
     if (a.lse) a.lse[(size_t)head * a.seqs.T + tok] = l > 0.f ? (top + lg2(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <int D, bool TWO>
+template <int D, bool TWO, bool PARTS>
 __global__ void __launch_bounds__(384, 1)
     paged_tree_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ TreeArgs args) {
-    using L = TreeSmem<D>;
+    using L = TreeSmem<D, PARTS>;
+    using Queued = typename TreeQueued<PARTS>::Type;
     using KT = KvTile<D, D == 128>;
     constexpr int HALVES = D / 64, MOST = L::kMostSlots;
     constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, false), IDESC_O = idesc_bf16_f32(128, D, true);
@@ -137,7 +164,7 @@ __global__ void __launch_bounds__(384, 1)
                   B_SEGFREE = B_SEGFULL + 2, B_PARFULL = B_SEGFREE + 2, B_PARFREE = B_PARFULL + 1, B_MEET = B_PARFREE + 1,
                   B_FINAL = B_MEET + 1;
     static_assert(B_FINAL + 1 == L::kNumBars, "one place for each barrier");
-    TreeSegment *segs = reinterpret_cast<TreeSegment *>(smem + L::kSegs);
+    Queued *segs = reinterpret_cast<Queued *>(smem + L::kSegs);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
     long long *warp_sums = reinterpret_cast<long long *>(smem + L::kMisc + 16);      // 12
@@ -269,10 +296,11 @@ __global__ void __launch_bounds__(384, 1)
         head_cost = __shfl_sync(0xffffffffu, of_head, at);
     }
     if (warp == 2) {
-        TreeSegment e{};
+        Queued e{};
         e.tiles = -1;
         if (pos < end) {
-            e = tree_first_segment(sq, seq, head_cost, head0, off, pos, end, per, run, pad);
+            static_cast<TreeSegment &>(e) = tree_first_segment(sq, seq, head_cost, head0, off, pos, end, per, run, pad);
+            if constexpr (PARTS) e.take(e.tiles);
         }
         if (lane == 0) segs[0] = e;
     }
@@ -549,7 +577,7 @@ __global__ void __launch_bounds__(384, 1)
             mbar_arrive(BAR(B_PARFULL));
             return true;
         };
-        auto post = [&](int seg, const TreeSegment &e) -> bool {
+        auto post = [&](int seg, const Queued &e) -> bool {
             if (seg >= 2 && !warp_wait(BAR(B_SEGFREE + (seg & 1)), ((seg >> 1) - 1) & 1, abort_flag)) return false;
             if (lane == 0) {
                 segs[seg & 1] = e;
@@ -559,15 +587,26 @@ __global__ void __launch_bounds__(384, 1)
             return e.tiles < 0 || post_parents(seg, e);
         };
         if (lane == 0) mbar_arrive(BAR(B_SEGFULL));      // (of the first segment)
-        TreeSegment e = segs[0];
+        Queued e = segs[0];
         int seg = 1;
         bool ok = post_parents(0, e);
         TreeCut cut{0, 0, 0, 0};
         while (true) {
+            if constexpr (PARTS)
+                while (ok && e.left > 0) {
+                    e.earlier = 1;
+                    e.i0 += e.tiles;
+                    e.take(e.left);
+                    ok = post(seg++, e);
+                }
             pos += e.places;
             if (!e.whole && e.begins) cut = TreeCut{e.t0, e.n, e.hk, e.more};
             if (!ok || pos >= end) break;
-            e = tree_next_segment(sq, seq, e, head0, args.heads, pos, end, per, run, pad);
+            static_cast<TreeSegment &>(e) = tree_next_segment(sq, seq, e, head0, args.heads, pos, end, per, run, pad);
+            if constexpr (PARTS) {
+                e.earlier = 0;
+                e.take(e.tiles);
+            }
             ok = post(seg++, e);
         }
         if (lane == 0) args.cuts[blockIdx.x] = cut;
@@ -612,7 +651,7 @@ __global__ void __launch_bounds__(384, 1)
         // out of the tile loop's registers)
         auto begin = [&](int seg) -> bool {
             ok = seg == 0 || warp_wait(BAR(B_SEGFULL + (seg & 1)), (seg >> 1) & 1, abort_flag);
-            const TreeSegment &e = segs[seg & 1];
+            const Queued &e = segs[seg & 1];
             if (!ok || e.tiles < 0 || !(ok = warp_wait(BAR(B_PARFULL), seg & 1, abort_flag))) return false;
             live = r / sq.group < args.tile_tokens && my_tok < e.n;
             const int node = e.first + min(my_tok, e.n - 1);
@@ -631,7 +670,7 @@ __global__ void __launch_bounds__(384, 1)
         };
         bool more = begin(0);
         for (int seg = 0; ok && more; ++seg) {
-            const TreeSegment &e = segs[seg & 1];
+            const Queued &e = segs[seg & 1];
             const bool warp_live = __any_sync(0xffffffffu, live);
             bool holds = true;        // the parents are still needed
             auto let_go = [&]() {
@@ -811,12 +850,14 @@ __global__ void __launch_bounds__(384, 1)
             }
             let_go();
             if (!ok) break;
-            // ---- the rows go out: final ones, or a piece of them to the workspace
-            const float m_out = l > 0.f ? m_ref : -INFINITY;
+            // ---- the rows go out: final ones, or to the workspace, as a piece or a segment's parts so far
+            float m_out = l > 0.f ? m_ref : -INFINITY;
             const size_t tok = (size_t)e.t0 + my_tok;
             const int head = e.hk * sq.group + my_head, tiles = e.tiles;
             const size_t to = (tok * sq.H + head) * D;
-            const bool final = e.whole != 0, stored = live;
+            bool final = e.whole != 0;
+            if constexpr (PARTS) final = final && e.left == 0;
+            const bool stored = live;
             const size_t slot = ((size_t)blockIdx.x * 2 + (e.begins ? 1 : 0)) * 2;
             // the next segment is made ready while the last products run
             more = begin(seg + 1);
@@ -826,6 +867,36 @@ __global__ void __launch_bounds__(384, 1)
             }
             if (!ok) break;
             float4 *part_o = args.part_o + slot * (D / 4) * 128 + r, *part_ml = args.part_ml + slot * 128 + r;
+            if constexpr (PARTS) {
+                if (e.earlier != 0 && warp_live && (two || g == 0)) {
+                    // the parts before are added to this one's O.  (Where the groups share the rows, each
+                    // wrote half of the columns; they have met since.)
+                    const float4 before = part_ml[g * 128];
+                    const float top = fmaxf(m_out, before.x);
+                    const float mine_f = m_out > -INFINITY ? ex2(m_out - top) : 0.f;
+                    const float before_f = before.x > -INFINITY ? ex2(before.x - top) : 0.f;
+                    m_out = top;
+                    l = l * mine_f + before.y * before_f;
+                    lr = lr * mine_f + before.z * before_f;
+#pragma unroll 1
+                    for (int q = 0; q < D / 16; ++q) {
+                        uint32_t o[16];
+                        tmem_ld16(tO + q * 16, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 16; c += 4) {
+                            const float4 y = part_o[((two ? g * (D / 4) : 0) + 4 * q + c / 4) * 128];
+                            o[c] = __float_as_uint(__uint_as_float(o[c]) * mine_f + y.x * before_f);
+                            o[c + 1] = __float_as_uint(__uint_as_float(o[c + 1]) * mine_f + y.y * before_f);
+                            o[c + 2] = __float_as_uint(__uint_as_float(o[c + 2]) * mine_f + y.z * before_f);
+                            o[c + 3] = __float_as_uint(__uint_as_float(o[c + 3]) * mine_f + y.w * before_f);
+                        }
+                        tmem_st16(tO + q * 16, o);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+            }
             auto rows16 = [&](int gg, int q, bool there, float (&x)[16]) {     // columns 16 q .. of group gg's O
                 uint32_t o[16];
                 if (there) {
@@ -909,6 +980,10 @@ __global__ void __launch_bounds__(384, 1)
         tmem_dealloc(tmem, 512);
     }
 }
+
+// The main kernel for units that may be longer than kTreePart tiles (attn_paged_tree_long.cu).
+using TreeKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, TreeArgs);
+TreeKernel tree_kernel_in_parts(int d, bool two);
 
 // The rows of cut units from their pieces, in their order: m = max m_i, l = sum l_i
 // 2^(m_i - m), O = sum O_i 2^(m_i - m) / lr.  The blocks find the units that are cut in the

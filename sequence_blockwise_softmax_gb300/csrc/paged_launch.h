@@ -120,10 +120,20 @@ inline bool tree_in_runs(int64_t pairs, int64_t keys, int d) {
     return keys * d > 400000 || (double)pairs * (double)(keys * d) > 1.6e7;
 }
 
+// Whether a unit may be longer than the kTreePart key tiles that are summed at a time: its table row can hold
+// more, and its window, if any, sees more.
+constexpr int kTreePart = 1024;
+inline bool tree_in_parts(int64_t capacity, int64_t max_new, int64_t window, int64_t sinks) {
+    const int64_t all = (capacity + 127) / 128;
+    const int64_t seen = window > 0 ? (window + max_new) / 128 + sinks / 128 + 4 : all;
+    return (seen < all ? seen : all) > kTreePart;
+}
+
 struct TreeLaunch {
     PagedSeqs seqs;                         // unit_tokens: tokens of a unit
     int64_t units;                          // at most
     int tile_tokens, page_box, two, ctas, streams, d;
+    bool in_parts;
     void *o;
     float *lse;
     bool o_bf16;
