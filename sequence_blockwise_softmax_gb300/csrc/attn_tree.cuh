@@ -851,7 +851,8 @@ __global__ void __launch_bounds__(384, 1)
             let_go();
             if (!ok) break;
             // ---- the rows go out: final ones, or to the workspace, as a piece or a segment's parts so far
-            float m_out = l > 0.f ? m_ref : -INFINITY;
+            // (a sum that is NaN keeps its reference, so that what it is added to becomes NaN too)
+            float m_out = l == 0.f ? -INFINITY : m_ref;
             const size_t tok = (size_t)e.t0 + my_tok;
             const int head = e.hk * sq.group + my_head, tiles = e.tiles;
             const size_t to = (tok * sq.H + head) * D;
