@@ -28,7 +28,8 @@
 // rows at the end, which keeps both at work and halves the chain of a tile.
 // One kernel for both kept their counts and slots in registers that the softmax
 // lacks: 512 nodes over 32768 keys, 16 / 4 heads, 129 us at d = 128 and 102 at d = 64
-// against 107 and 84 as two kernels.
+// against 107 and 84 as two kernels.  (They spill up to 28 bytes all the same, the two-tile
+// one at d = 64 none.)
 #pragma once
 #include "kv_tile.cuh"
 #include "paged_launch.h"
@@ -42,7 +43,7 @@ namespace ra {
 struct TreeArgs {
     PagedSeqs seqs;             // unit_tokens: tokens of a unit
     int tile_tokens, page_box;  // tokens of a Q tile; keys of a copy
-    int two;                    // units have two Q tiles
+    int two;                    // units have two Q tiles (for the join: the main kernel is one for each)
     int min_run;                // tiles of a run at least
     int streams, heads;         // lists side by side, of this many key/value heads each
     float scale_log2;
@@ -336,13 +337,8 @@ __global__ void __launch_bounds__(384, 1)
         w.n_main = e.n_main;
         w.last = e.last;
         w.s0 = e.s0;
-        w.j = 0;
         w.seek();
         return w;
-    };
-    // whether softmax group g takes tile number j of a segment
-    auto takes = [&](const TreeSegment &e, int g, int j) -> bool {
-        return two ? g == 0 || e.n > args.tile_tokens : (j & 1) == g;
     };
     // K and V tiles go to the slots in the order K(0), K(1), V(0), K(2), V(1), ..
     // over all segments: K(t) is load 2 t - 1 (K(0) load 0), V(t) load 2 t + 2 (at a

@@ -257,10 +257,9 @@ struct TreeChain {
 // the sinks'.
 struct TreeWalk {
     int i, end, n_main, last, s0;
-    int tile, j;
+    int tile;
 
     RA_HD_STEP void seek() { tile = i < n_main ? last - i : s0 + (i - n_main); }
-    RA_HD_STEP void start_step() { seek(); }
     RA_HD_STEP bool valid() const { return i < end; }
     RA_HD_STEP void next() {
         ++i;
@@ -274,7 +273,7 @@ RA_HD TreeWalk tree_walk(const RangeWalk &r) {
     w.n_main = r.end - r.n_sink;
     w.last = r.m0 + w.n_main - 1;
     w.s0 = r.s0;
-    w.tile = w.j = 0;
+    w.tile = 0;
     return w;
 }
 
