@@ -471,6 +471,9 @@ RA_API ra_status ra_paged_append(const void *k_new, const void *v_new, void *k_p
  * max_new is at most 1024 (else RA_ERR_UNSUPPORTED).  A row whose place is
  * negative (more new rows than the sequence is long) sees what of its ancestors
  * lies in the cache; one that sees nothing gets O = 0 and LSE = -inf.
+ * The weights enter the product with V as two bf16 values each where a key/value
+ * head has at most 16 rows (new tokens times query heads of max_new), or at most 32 over a
+ * short cache; else as one, which is off by up to 2^-8 of a weight.
  * workspace: ra_paged_tree_attn_workspace_bytes() bytes, under the terms of
  * ra_paged_attn_fwd's.
  */
