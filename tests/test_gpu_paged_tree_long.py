@@ -6,7 +6,8 @@ import torch
 import tree_reference as tr
 import window_reference as ref
 from synthetic_inputs import randn_bf16
-from test_gpu_paged import NAN, cu_of
+from test_gpu_paged import NAN, Cache, cu_of
+from test_gpu_paged_tree import CASES, assert_trees, attend, trees_of
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +108,16 @@ def test_values_of_one(ralib, gpu, n_seqs, n, H, d):
     ralib.ra_paged_tree_attn_fwd(q, k, v, table, lens, cu_of([n] * n_seqs), parents, o, None, n, length, workspace=ws)
     ralib.ra_check_status(ws)
     assert (o - 1).abs().max().item() <= 2.0 ** -9 + 1e-6
+
+
+@pytest.mark.parametrize("new,lens,H,Hkv,d,page,window,sinks", CASES)
+@pytest.mark.parametrize("shape", ["levels", "chain"])
+def test_tables_that_could_hold_more(ralib, gpu, new, lens, H, Hkv, d, page, window, sinks, shape):
+    """Ordinary contexts in tables for more tokens than are summed in one part."""
+    c = Cache(lens, page, Hkv, d, sum(lens) + H)
+    c.fill_all()
+    c.table = torch.nn.functional.pad(c.table, (0, 140000 // page), value=-1).contiguous()
+    q = randn_bf16((sum(new), H, d), 99 + H).cuda()
+    trees = trees_of(new, shape)
+    o, lse, _ = attend(ralib, c, q, cu_of(new), trees, torch.bfloat16 if shape == "chain" else torch.float32, window, sinks)
+    assert_trees(c, q, o, lse, trees, window, sinks)
